@@ -57,6 +57,14 @@ def load() -> ctypes.CDLL:
     lib.attn_fwd_varlen.restype = i
     lib.attn_fwd_paged.argtypes = [vp] * 6 + [i, vp, vp] + [i] * 8 + [f, vp, vp, sz, vp]
     lib.attn_fwd_paged.restype = i
+    lib.attn_fwd_paged_fp8kv.argtypes = [vp] * 8 + [i, vp, vp] + [i] * 8 + [f, vp, vp, sz, vp]
+    lib.attn_fwd_paged_fp8kv.restype = i
+    lib.attn_paged_slots.argtypes = [vp] * 5 + [i] * 6 + [vp] * 7
+    lib.attn_paged_slots.restype = i
+    lib.attn_qk_norm_rope.argtypes = [vp] * 4 + [i, f] + [vp] * 3 + [i] * 5 + [vp]
+    lib.attn_qk_norm_rope.restype = i
+    lib.attn_qk_norm_rope_paged.argtypes = [vp] * 5 + [i, f] + [vp] * 5 + [i] + [vp] * 3 + [i] * 8 + [vp]
+    lib.attn_qk_norm_rope_paged.restype = i
     lib.attn_varlen_workspace_size.argtypes = [i] * 4
     lib.attn_varlen_workspace_size.restype = sz
     lib.attn_paged_workspace_size.argtypes = [i] * 7
@@ -77,6 +85,18 @@ class Options(ctypes.Structure):
     """gqa_options of include/gqa_attn.h."""
     _fields_ = [("window_left", ctypes.c_int), ("window_right", ctypes.c_int), ("softcap", ctypes.c_float),
                 ("sinks", ctypes.c_void_p), ("dtype", ctypes.c_int)]
+
+
+class HeadRows(ctypes.Structure):
+    """gqa_head_rows of include/gqa_attn.h."""
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """gqa_rope of include/gqa_attn.h."""
+    _fields_ = [("cos_sin", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("max_pos", ctypes.c_int),
+                ("rot", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int),
+                ("pair_axis", ctypes.c_char_p)]
 
 
 def status_name(code: int) -> str:

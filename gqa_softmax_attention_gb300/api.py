@@ -394,6 +394,289 @@ def attn_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table
     return out, lse
 
 
+def _on(device, fn, *args):
+    """fn(*args) with `device` current (the library works on the current device)."""
+    if device.index == torch.cuda.current_device():
+        return fn(*args)
+    with torch.cuda.device(device):
+        return fn(*args)
+
+
+def _check_plain(name, t, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype and shape on `device` (None in shape: any size)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise ValueError("%s must be a %s CUDA tensor" % (name, dtype))
+    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cache_seqlens, block_table, causal=True,
+                         scale=None, out=None, lse=None, window_left=-1, window_right=-1, softcap=None, sinks=None,
+                         workspace=None, split_decode=True):
+    """attn_fwd_paged over float8_e4m3fn key/value caches: prefill chunks and
+    decode steps in one call.
+
+    q [total_q, Hq, D] bfloat16 or float16, D 128 or 256; k_cache / v_cache
+    [num_pages, page_size, Hkv, D] torch.float8_e4m3fn (or uint8 holding e4m3fn
+    codes), contiguous; k_scale / v_scale [B, Hkv] float32 CUDA tensors or None (ones):
+    key t of KV head r in request b is K * k_scale[b, r], its value V *
+    v_scale[b, r].  Every scale must be finite and positive; they stay on the
+    GPU and are not checked.  Other arguments as attn_fwd_paged.
+    Returns (o [total_q, Hq, D] like q, lse [total_q, Hq] float32).
+    """
+    _check_16_cuda("q", q, 3)
+    dev = q.device
+    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4 or \
+                t.dtype not in (torch.float8_e4m3fn, torch.uint8):
+            raise ValueError("%s must be a 4-D float8_e4m3fn (or uint8) CUDA tensor" % n)
+    total_q, Hq, D = q.shape
+    num_pages, page_size, Hkv, Dk = k_cache.shape
+    if Dk != D or v_cache.shape != k_cache.shape:
+        raise ValueError("cache shape mismatch: k %s, v %s, D %d" % (tuple(k_cache.shape), tuple(v_cache.shape), D))
+    if Hkv == 0 or Hq % Hkv != 0:
+        raise ValueError("Hq (%d) must be divisible by Hkv (%d)" % (Hq, Hkv))
+    if not isinstance(cache_seqlens, torch.Tensor) or cache_seqlens.dim() != 1:
+        raise ValueError("cache_seqlens must be [B]")
+    B = cache_seqlens.shape[0]
+    kc = _check_plain("k_cache", k_cache, k_cache.dtype, k_cache.shape, dev)
+    vc = _check_plain("v_cache", v_cache, v_cache.dtype, k_cache.shape, dev)
+    cq = _check_plain("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev)
+    sl = _check_plain("cache_seqlens", cache_seqlens, torch.int32, (B,), dev)
+    bt = _check_plain("block_table", block_table, torch.int32, (B, None), dev)
+    max_pages = block_table.shape[1]
+    ks = _check_plain("k_scale", k_scale, torch.float32, (B, Hkv), dev) if k_scale is not None else None
+    vs = _check_plain("v_scale", v_scale, torch.float32, (B, Hkv), dev) if v_scale is not None else None
+    q = q.contiguous()
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=dev)
+    po = _check_plain("out", out, q.dtype, q.shape, dev)
+    pl = _check_plain("lse", lse, torch.float32, (total_q, Hq), dev)
+    lib = _lib.load()
+    if workspace is None:
+        if split_decode:
+            need = _on(dev, lib.attn_paged_workspace_size, B, total_q, Hq, Hkv, D, page_size, max_pages)
+        else:
+            need = lib.attn_varlen_workspace_size(B, total_q, Hq, Hkv)
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    opt, _keep = _options(window_left, window_right, softcap, sinks, Hq, dev, _DTYPES[q.dtype])
+    st = _on(dev, lib.attn_fwd_paged_fp8kv, q.data_ptr(), kc, vc, ks, vs, cq, sl, bt, page_size, po, pl, B, total_q,
+             Hq, Hkv, D, num_pages, max_pages, int(bool(causal)), resolve_scale(scale, D),
+             ctypes.byref(opt) if opt is not None else None, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _raise(st, "attn_fwd_paged_fp8kv")
+    return out, lse
+
+
+def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, num_pages, max_tokens, free_start=None,
+                     out=None):
+    """Metadata of one serving step, built on the GPU from the requests' lengths.
+
+    past_lens / new_lens [B] int32: tokens each request holds and brings;
+    block_table [B, max_pages] int32, updated in place: the pages the new tokens
+    need are entered behind the past ones; free_pages [n] int32 ids handed out
+    in request order, from index free_start (an int32 CUDA tensor of one value)
+    on; max_tokens: rows of the packed batch, padding included.
+    Returns (cu_seqlens_q [B + 1], cache_seqlens [B], slots [max_tokens],
+    positions [max_tokens], requests [max_tokens], counts [3]) int32: slots are
+    cache rows page * page_size + offset (-1 for padding and for tokens without
+    a page), counts the tokens and pages asked for and the next free_start.
+    out: the six tensors of an earlier call, written again (the buffers of a
+    captured graph).  Nothing is read back: counts[0] > max_tokens, or
+    counts[2] > n, tells the caller later that rows or pages ran out.
+    """
+    if not isinstance(past_lens, torch.Tensor) or past_lens.dim() != 1:
+        raise ValueError("past_lens must be [B]")
+    dev, i32, B = past_lens.device, torch.int32, past_lens.shape[0]
+    pp = _check_plain("past_lens", past_lens, i32, (B,), dev)
+    pn = _check_plain("new_lens", new_lens, i32, (B,), dev)
+    pt = _check_plain("block_table", block_table, i32, (B, None), dev)
+    pf = _check_plain("free_pages", free_pages, i32, (None,), dev)
+    fs = _check_plain("free_start", free_start, i32, (1,), dev) if free_start is not None else None
+    T = int(max_tokens)
+    if T < 0:
+        raise ValueError("max_tokens must be >= 0, got %d" % T)
+    sizes = (B + 1, B, T, T, T, 3)
+    if out is None:
+        out = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
+    elif len(out) != 6:
+        raise ValueError("out must hold six tensors")
+    outs = [_check_plain(name, t, i32, (n,), dev) for name, t, n in
+            zip(("out cu_seqlens_q", "out cache_seqlens", "out slots", "out positions", "out requests", "out counts"),
+                out, sizes)]
+    st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, block_table.shape[1], int(page_size),
+             int(num_pages), free_pages.shape[0], T, *outs, torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _raise(st, "attn_paged_slots")
+    return tuple(out)
+
+
+def _head_rows(t, T):
+    """gqa_head_rows of t [..., H, D] with T rows: strides as they are where the
+    kernels take them, else of a copy (returned to keep it alive)."""
+    if t.dim() == 4:
+        t = t.reshape(T, t.shape[2], t.shape[3])      # a view where the rows have one stride
+    # the stride of an axis of one element says nothing
+    ts, hs, ds = [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
+    if ds != 1 or ts % 8 or hs % 8 or t.data_ptr() % 16:
+        t = t.clone(memory_format=torch.contiguous_format)
+        ts, hs, ds = t.stride()
+    return _lib.HeadRows(t.data_ptr(), ts, hs), t
+
+
+def _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axes):
+    """Checks and C arguments shared by attn_qk_norm_rope and its paged form."""
+    nd = q.dim() if isinstance(q, torch.Tensor) else 0
+    if nd not in (3, 4):
+        raise ValueError("q must be a CUDA tensor [T, Hq, D] or [B, S, Hq, D]")
+    _check_16_cuda("q", q, nd)
+    dev, lead, D = q.device, q.shape[:-2], q.shape[-1]
+    T = lead.numel()
+    for n, t in (("k", k), ("v", v)):
+        if t is not None:
+            _check_16_cuda(n, t, nd, (q.dtype,))
+            if t.device != dev or t.shape[:-2] != lead or t.shape[-1] != D or t.shape[-2] != k.shape[-2]:
+                raise ValueError("shape mismatch: q %s, %s %s (k %s), all on one device"
+                                 % (tuple(q.shape), n, tuple(t.shape), tuple(k.shape)))
+    wt = torch.float32 if any(w is not None and w.dtype == torch.float32 for w in (q_weight, k_weight)) else q.dtype
+    pw = [_check_plain(n, w, wt, (D,), dev) if w is not None else None
+          for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
+    rope = None
+    if cos_sin is not None:
+        pc = _check_plain("cos_sin", cos_sin, torch.float32, (None, None), dev)
+        rot = cos_sin.shape[1]
+        if rot > D or rot % 16:
+            raise ValueError("cos_sin must be [max_pos, rot] with rot <= D and a multiple of 16, got %s"
+                             % (tuple(cos_sin.shape),))
+        if axes is None:
+            n_axes, pa, shape = 1, None, lead
+        else:
+            if len(axes) != rot // 2 or not isinstance(positions, torch.Tensor) or positions.dim() < 2:
+                raise ValueError("axes must name the axis of each of the rot / 2 = %d pairs, positions be "
+                                 "[n_axes, ...]" % (rot // 2))
+            n_axes = positions.shape[0]
+            if any(not 0 <= int(x) < min(n_axes, 4) for x in axes):
+                raise ValueError("axes must lie in [0, n_axes = %d), at most four axes" % n_axes)
+            pa, shape = bytes(axes), (n_axes, *lead)
+        pp = _check_plain("positions", positions, torch.int32, shape, dev)
+        rope = _lib.Rope(pc, pp, cos_sin.shape[0], rot, int(bool(interleaved)), n_axes, pa)
+    elif positions is not None or axes is not None:
+        raise ValueError("positions and axes need cos_sin")
+    return dev, T, D, pw, int(wt == torch.float32), rope
+
+
+def _rope_out(name, out, like):
+    """`out` (checked) or a new contiguous tensor like `like`."""
+    if out is None:
+        out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    return out, _check_plain(name, out, like.dtype, like.shape, like.device)
+
+
+def attn_qk_norm_rope(q, k, cos_sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, axes=None,
+                      out=None):
+    """RMS norm of each query and key head and rotation by position, in one pass.
+
+    q [T, Hq, D] or [B, S, Hq, D], k likewise with Hkv heads: bfloat16 or
+    float16 CUDA tensors, D 64, 128 or 256; slices of a fused projection are
+    read in place (strides of multiples of 8), other layouts are copied first.
+    cos_sin [max_pos, rot] float32: cosines of the rot / 2 pairs, then their
+    sines (rope_table), or None for no rotation; positions int32 of q's leading
+    shape.  A pair is dims (j, j + rot / 2), or (2j, 2j + 1) with interleaved; dims
+    past rot pass through.  axes: the position axis of each pair (rot / 2 ints),
+    positions then [n_axes, *leading] with up to four axes.
+    q_weight / k_weight [D] (q's dtype, or both float32) or None for no norm of
+    that side.  FP32 throughout, rounded once.
+    out: (q_out, k_out), contiguous; q_out may be q and k_out k.
+    Returns (q_out, k_out).
+    """
+    if not isinstance(k, torch.Tensor):
+        raise ValueError("k must be a CUDA tensor")
+    dev, T, D, (pqw, pkw), wf, rope = _rope_args(q, k, None, cos_sin, positions, q_weight, k_weight, interleaved,
+                                                 axes)
+    oq, pq = _rope_out("out q", out[0] if out is not None else None, q)
+    ok, pk = _rope_out("out k", out[1] if out is not None else None, k)
+    rq, _kq = _head_rows(q, T)
+    rk, _kk = _head_rows(k, T)
+    st = _on(dev, _lib.load().attn_qk_norm_rope, ctypes.byref(rq), ctypes.byref(rk), pqw, pkw, wf, float(eps),
+             ctypes.byref(rope) if rope is not None else None, pq, pk, T, q.shape[-2], k.shape[-2], D,
+             _DTYPES[q.dtype], torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _raise(st, "attn_qk_norm_rope")
+    return oq, ok
+
+
+def attn_qk_norm_rope_paged(q, k, v, cos_sin, positions, slots, k_cache, v_cache, q_weight=None, k_weight=None,
+                            eps=1e-6, interleaved=False, axes=None, k_scale=None, v_scale=None, requests=None,
+                            out=None):
+    """attn_qk_norm_rope with the keys, and the values as they are, written into
+    paged caches.
+
+    v like k; slots int32 of q's leading shape (attn_paged_slots): the cache row
+    page * page_size + offset of each token; a token with a slot outside the
+    pool is padding: its rows of the result and the caches stay as they were.
+    k_cache / v_cache [num_pages, page_size, Hkv, D], contiguous, written in
+    place: q's dtype, or torch.float8_e4m3fn (or uint8 codes).  For e4m3 caches,
+    k_scale / v_scale [B, Hkv] float32 (or None: ones) divide what is stored,
+    with requests (int32 like slots) naming each token's row of them.
+    Other arguments as attn_qk_norm_rope.  Returns q_out.
+    """
+    if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
+        raise ValueError("k and v must be CUDA tensors")
+    dev, T, D, (pqw, pkw), wf, rope = _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axes)
+    Hkv = k.shape[-2]
+    lead = q.shape[:-2]
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
+        raise ValueError("k_cache must be a CUDA tensor [num_pages, page_size, Hkv, D]")
+    e4m3 = k_cache.dtype in (torch.float8_e4m3fn, torch.uint8)
+    num_pages, page_size = k_cache.shape[:2]
+    ct = k_cache.dtype if e4m3 else q.dtype
+    pkc = _check_plain("k_cache", k_cache, ct, (None, None, Hkv, D), dev)
+    pvc = _check_plain("v_cache", v_cache, ct, k_cache.shape, dev)
+    ps = _check_plain("slots", slots, torch.int32, lead, dev)
+    B, scales, pr = 0, [None, None], None
+    for i, (n, t) in enumerate((("k_scale", k_scale), ("v_scale", v_scale))):
+        if t is not None:
+            if not e4m3:
+                raise ValueError("%s needs float8_e4m3fn caches" % n)
+            scales[i] = _check_plain(n, t, torch.float32, (B or None, Hkv), dev)
+            B = t.shape[0]
+    if B:
+        pr = _check_plain("requests", requests, torch.int32, lead, dev)
+    elif requests is not None:
+        raise ValueError("requests needs k_scale or v_scale")
+    oq, pq = _rope_out("out", out, q)
+    rq, _kq = _head_rows(q, T)
+    rk, _kk = _head_rows(k, T)
+    rv, _kv = _head_rows(v, T)
+    st = _on(dev, _lib.load().attn_qk_norm_rope_paged, ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv), pqw, pkw,
+             wf, float(eps), ctypes.byref(rope) if rope is not None else None, pq, ps, pkc, pvc, int(e4m3),
+             scales[0], scales[1], pr, B, T, q.shape[-2], Hkv, D, num_pages, page_size, _DTYPES[q.dtype],
+             torch.cuda.current_stream(dev).cuda_stream)
+    if st != 0:
+        _raise(st, "attn_qk_norm_rope_paged")
+    return oq
+
+
+def rope_table(max_pos, rot, base=10000.0, device="cuda"):
+    """cos_sin [max_pos, rot] float32 of attn_qk_norm_rope with the angles
+    p * base^(-2j / rot), formed in 64 bits."""
+    if rot <= 0 or rot % 2:
+        raise ValueError("rot must be positive and even, got %r" % (rot,))
+    freq = float(base) ** (-torch.arange(rot // 2, dtype=torch.float64) / (rot // 2))
+    angle = torch.arange(max_pos, dtype=torch.float64)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float().to(device)
+
+
 def attn_validate_paged(real_seqlen_kv, block_table, Sq, page_size, num_pages, causal=True):
     """Host-side range check of paged metadata (synchronises the stream)."""
     B, max_pages = block_table.shape

@@ -551,16 +551,24 @@ static SideStream* side_stream(cudaStream_t caller) {
     return &ss;
 }
 
-gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* cu_seqlens_q,
-                          const int32_t* cache_seqlens, const int32_t* block_table, int page_size, void* o,
-                          float* lse, int B, int total_q, int Hq, int Hkv, int D, int num_pages, int max_pages,
-                          int causal, float scale, const gqa_options* opts, void* workspace,
-                          size_t workspace_bytes, gqa_stream_t stream) {
+// Packed queries over a paged cache: 16-bit, or (fp8) e4m3fn bytes with scales.
+static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_cache, bool fp8, const float* k_scale,
+                            const float* v_scale, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+                            const int32_t* block_table, int page_size, void* o, float* lse, int B, int total_q,
+                            int Hq, int Hkv, int D, int num_pages, int max_pages, int causal, float scale,
+                            const gqa_options* opts, void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
     PrefillArgs a{};
     CUtensorMap tq, tk, tv, to;
     if (page_size <= 0 || num_pages <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
     if ((long)max_pages * page_size >= kMaxSeq) return GQA_ERR_INVALID_ARG;
     if ((long)num_pages * page_size >= (1L << 31)) return GQA_ERR_UNSUPPORTED;
+    if (fp8) {
+        if (!k_cache || !v_cache || !cache_seqlens || !block_table) return GQA_ERR_INVALID_ARG;
+        if (!aligned16(k_cache) || !aligned16(v_cache) || !aligned4(cache_seqlens) || !aligned4(block_table) ||
+            !aligned4(k_scale) || !aligned4(v_scale))
+            return GQA_ERR_MISALIGNED;
+        if (D == 64) return GQA_ERR_UNSUPPORTED;
+    }
     gqa_status st = varlen_common(q, o, lse, cu_seqlens_q, B, total_q, Hq, Hkv, D, causal, scale, opts, workspace,
                                   workspace_bytes, &a, &tq, &to);
     if (st != GQA_OK) return st;
@@ -576,7 +584,12 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
     a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.num_pages = num_pages;
-    if (page_size % 8 == 0) {
+    if (fp8) {
+        // rows read with plain loads (no K or V map)
+        a.q = q;
+        a.k_scale = k_scale;
+        a.v_scale = v_scale;
+    } else if (page_size % 8 == 0) {
         // pages move as 8-row TMA blocks
         a.bt_k = gcd_int(page_size, 128);
         a.bt_v = gcd_int(page_size, vkeys);
@@ -611,12 +624,17 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
                                 (long)max_pages * page_size, ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e,
                                 s, route, false, side ? a.num_sms : 0) != cudaSuccess)
         return GQA_ERR_CUDA;
+    const long items = (long)max_e * Hkv;
+    auto launch_chunks = [&](cudaStream_t on) {
+        return fp8 ? gqa::launch_varlen_paged_fp8(to, a, items, on)
+                   : gqa::launch_varlen_paged(tq, tk, tv, to, a, items, on);
+    };
     if (side) {
         // fork after the plan: the chunks (highest priority, so their CTAs
         // take their SMs first) and the decode steps become ready together
         if (cudaEventRecord(side->fork, s) != cudaSuccess || cudaStreamWaitEvent(side->s, side->fork, 0) != cudaSuccess)
             return GQA_ERR_CUDA;
-        if (gqa::launch_varlen_paged(tq, tk, tv, to, a, (long)max_e * Hkv, side->s) != cudaSuccess ||
+        if (launch_chunks(side->s) != cudaSuccess ||
             cudaEventRecord(side->join, side->s) != cudaSuccess)
             return GQA_ERR_CUDA;
     }
@@ -637,14 +655,179 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
         da.q_rows = cu_seqlens_q;
         da.q_total = total_q;
         const int box = gqa::decode_box_tokens(D, page_size);
-        CUtensorMap dk, dv;
-        const bool use_tma = box > 0 && make_cache_map(&dk, k_cache, rows, Hkv, D, box, a.f16) &&
-                             make_cache_map(&dv, v_cache, rows, Hkv, D, box, a.f16);
-        if (gqa::launch_decode(da, use_tma ? &dk : nullptr, use_tma ? &dv : nullptr, box, s) != cudaSuccess)
-            return GQA_ERR_CUDA;
+        CUtensorMap dk{}, dv{};
+        if (fp8) {
+            da.k_scale = k_scale;
+            da.v_scale = v_scale;
+            if (box > 0 && (!make_cache_map_fp8(&dk, k_cache, rows, Hkv, D, box) ||
+                            !make_cache_map_fp8(&dv, v_cache, rows, Hkv, D, box)))
+                return GQA_ERR_CUDA;
+            if (gqa::launch_decode_fp8(da, dk, dv, box, s) != cudaSuccess) return GQA_ERR_CUDA;
+        } else {
+            const bool use_tma = box > 0 && make_cache_map(&dk, k_cache, rows, Hkv, D, box, a.f16) &&
+                                 make_cache_map(&dv, v_cache, rows, Hkv, D, box, a.f16);
+            if (gqa::launch_decode(da, use_tma ? &dk : nullptr, use_tma ? &dv : nullptr, box, s) != cudaSuccess)
+                return GQA_ERR_CUDA;
+        }
     }
     if (side) return cudaStreamWaitEvent(s, side->join, 0) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;   // join
-    return gqa::launch_varlen_paged(tq, tk, tv, to, a, (long)max_e * Hkv, s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    return launch_chunks(s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cache, const int32_t* cu_seqlens_q,
+                          const int32_t* cache_seqlens, const int32_t* block_table, int page_size, void* o,
+                          float* lse, int B, int total_q, int Hq, int Hkv, int D, int num_pages, int max_pages,
+                          int causal, float scale, const gqa_options* opts, void* workspace,
+                          size_t workspace_bytes, gqa_stream_t stream) {
+    return fwd_paged(q, k_cache, v_cache, false, nullptr, nullptr, cu_seqlens_q, cache_seqlens, block_table, page_size,
+                     o, lse, B, total_q, Hq, Hkv, D, num_pages, max_pages, causal, scale, opts, workspace,
+                     workspace_bytes, stream);
+}
+
+gqa_status attn_fwd_paged_fp8kv(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                const float* v_scale, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+                                const int32_t* block_table, int page_size, void* o, float* lse, int B, int total_q,
+                                int Hq, int Hkv, int D, int num_pages, int max_pages, int causal, float scale,
+                                const gqa_options* opts, void* workspace, size_t workspace_bytes,
+                                gqa_stream_t stream) {
+    return fwd_paged(q, k_cache, v_cache, true, k_scale, v_scale, cu_seqlens_q, cache_seqlens, block_table, page_size,
+                     o, lse, B, total_q, Hq, Hkv, D, num_pages, max_pages, causal, scale, opts, workspace,
+                     workspace_bytes, stream);
+}
+
+// ---------------------------------------------------------------- step metadata
+gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
+                            const int32_t* free_pages, const int32_t* free_start, int B, int max_pages,
+                            int page_size, int num_pages, int num_free, int max_tokens, int32_t* cu_seqlens_q,
+                            int32_t* cache_seqlens, int32_t* slots, int32_t* positions, int32_t* requests,
+                            int32_t* counts, gqa_stream_t stream) {
+    if (B <= 0 || max_pages <= 0 || page_size <= 0 || num_pages < 0 || num_free < 0 || max_tokens < 0)
+        return GQA_ERR_INVALID_ARG;
+    if ((long)max_pages * page_size >= kMaxSeq || max_tokens >= kMaxSeq) return GQA_ERR_INVALID_ARG;
+    if ((long)num_pages * page_size >= (1L << 31)) return GQA_ERR_UNSUPPORTED;
+    if (!past_lens || !new_lens || !block_table || (num_free > 0 && !free_pages) || !cu_seqlens_q ||
+        !cache_seqlens || !counts || (max_tokens > 0 && (!slots || !positions || !requests)))
+        return GQA_ERR_INVALID_ARG;
+    for (const void* p : {(const void*)past_lens, (const void*)new_lens, (const void*)block_table,
+                          (const void*)free_pages, (const void*)free_start, (const void*)cu_seqlens_q,
+                          (const void*)cache_seqlens, (const void*)slots, (const void*)positions,
+                          (const void*)requests, (const void*)counts})
+        if (!aligned4(p)) return GQA_ERR_MISALIGNED;
+    // every block reads the lengths and free_start while block 0 writes its results
+    for (const void* r : {(const void*)past_lens, (const void*)new_lens, (const void*)free_start})
+        for (const void* w : {(const void*)cu_seqlens_q, (const void*)cache_seqlens, (const void*)counts})
+            if (r && r == w) return GQA_ERR_INVALID_ARG;
+    if (free_start && free_start > counts && free_start < counts + 3) return GQA_ERR_INVALID_ARG;
+    gqa::SlotArgs a{};
+    a.past_lens = past_lens; a.new_lens = new_lens;
+    a.block_table = block_table; a.free_pages = free_pages; a.free_start = free_start;
+    a.B = B; a.max_pages = max_pages; a.page_size = page_size; a.num_pages = num_pages;
+    a.num_free = num_free; a.max_tokens = max_tokens;
+    a.cu_seqlens_q = cu_seqlens_q; a.cache_seqlens = cache_seqlens;
+    a.slots = slots; a.positions = positions; a.requests = requests; a.counts = counts;
+    return gqa::launch_paged_slots(a, sm_count(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------- norm and rotation
+// Checks shared by the two calls and the kernel form of their common arguments.
+static gqa_status rope_common(const gqa_head_rows* q, const gqa_head_rows* k, const void* q_weight,
+                              const void* k_weight, int weight_f32, float eps, const gqa_rope* rope, void* q_out,
+                              int T, int Hq, int Hkv, int D, int dtype, gqa::RopeArgs* a) {
+    if (T < 0 || T >= kMaxSeq || Hq <= 0 || Hkv <= 0 || !q || !k) return GQA_ERR_INVALID_ARG;
+    if (dtype != GQA_BF16 && dtype != GQA_FP16) return GQA_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 0.f) return GQA_ERR_INVALID_ARG;
+    if (!head_dim_ok(D)) return GQA_ERR_UNSUPPORTED;
+    if ((long)T * ((long)Hq + 2L * Hkv) >= (1L << 32)) return GQA_ERR_UNSUPPORTED;
+    a->rot = 0;
+    a->n_axes = 1;
+    if (rope) {
+        if (rope->rot < 0 || rope->rot > D || rope->max_pos <= 0 || rope->n_axes < 1 || rope->n_axes > 4)
+            return GQA_ERR_INVALID_ARG;
+        if (rope->rot % 16 != 0) return GQA_ERR_UNSUPPORTED;
+        if (rope->n_axes > 1 && !rope->pair_axis) return GQA_ERR_INVALID_ARG;
+        if (rope->rot > 0 && T > 0 && (!rope->cos_sin || !rope->positions)) return GQA_ERR_INVALID_ARG;
+        if (!aligned16(rope->cos_sin) || !aligned4(rope->positions)) return GQA_ERR_MISALIGNED;
+        a->cos_sin = rope->cos_sin;
+        a->positions = rope->positions;
+        a->max_pos = rope->max_pos;
+        a->rot = rope->rot;
+        a->interleaved = rope->interleaved ? 1 : 0;
+        a->n_axes = rope->n_axes;
+        if (rope->pair_axis)
+            for (int j = 0; j < rope->rot / 2; ++j) {
+                if (rope->pair_axis[j] >= rope->n_axes) return GQA_ERR_INVALID_ARG;
+                a->pair_axis[j / 16] |= (uint32_t)rope->pair_axis[j] << (2 * (j % 16));
+            }
+    }
+    if (T == 0) return GQA_OK;
+    if (!q->data || !k->data || !q_out) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(q_out) || !aligned16(q_weight) ||
+        !aligned16(k_weight))
+        return GQA_ERR_MISALIGNED;
+    for (const gqa_head_rows* r : {q, k}) {
+        if (r->token_stride < 0 || r->head_stride < 0) return GQA_ERR_INVALID_ARG;
+        if (r->token_stride % 8 || r->head_stride % 8) return GQA_ERR_MISALIGNED;
+    }
+    a->q = q->data; a->q_ts = q->token_stride; a->q_hs = q->head_stride;
+    a->k = k->data; a->k_ts = k->token_stride; a->k_hs = k->head_stride;
+    a->q_weight = q_weight; a->k_weight = k_weight;
+    a->weight_f32 = weight_f32 ? 1 : 0;
+    a->eps = eps;
+    a->T = T; a->Hq = Hq; a->Hkv = Hkv;
+    a->q_out = q_out;
+    return GQA_OK;
+}
+
+gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, const void* q_weight,
+                             const void* k_weight, int weight_f32, float eps, const gqa_rope* rope, void* q_out,
+                             void* k_out, int T, int Hq, int Hkv, int D, int dtype, gqa_stream_t stream) {
+    gqa::RopeArgs a{};
+    const gqa_status st =
+        rope_common(q, k, q_weight, k_weight, weight_f32, eps, rope, q_out, T, Hq, Hkv, D, dtype, &a);
+    if (st != GQA_OK || T == 0) return st;
+    if (!k_out) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(k_out)) return GQA_ERR_MISALIGNED;
+    a.k_out = k_out;
+    return gqa::launch_qk_norm_rope(a, D, dtype == GQA_FP16, false, sm_count(),
+                                    reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* k, const gqa_head_rows* v,
+                                   const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                                   const gqa_rope* rope, void* q_out, const int32_t* slots, void* k_cache,
+                                   void* v_cache, int e4m3, const float* k_scale, const float* v_scale,
+                                   const int32_t* requests, int B, int T, int Hq, int Hkv, int D, int num_pages,
+                                   int page_size, int dtype, gqa_stream_t stream) {
+    gqa::RopeArgs a{};
+    const gqa_status st =
+        rope_common(q, k, q_weight, k_weight, weight_f32, eps, rope, q_out, T, Hq, Hkv, D, dtype, &a);
+    if (st != GQA_OK) return st;
+    if (!v || num_pages < 0 || page_size <= 0) return GQA_ERR_INVALID_ARG;
+    if ((long)num_pages * page_size >= (1L << 31)) return GQA_ERR_UNSUPPORTED;
+    if (!e4m3 && (k_scale || v_scale)) return GQA_ERR_INVALID_ARG;      // scales belong to e4m3 caches
+    if ((k_scale || v_scale) && (B <= 0 || (T > 0 && !requests))) return GQA_ERR_INVALID_ARG;
+    if (T == 0) return GQA_OK;
+    if (!v->data || !slots || (num_pages > 0 && (!k_cache || !v_cache))) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(v->data) || !aligned16(k_cache) || !aligned16(v_cache)) return GQA_ERR_MISALIGNED;
+    if (!aligned4(slots) || !aligned4(requests) || !aligned4(k_scale) || !aligned4(v_scale)) return GQA_ERR_MISALIGNED;
+    if (v->token_stride < 0 || v->head_stride < 0) return GQA_ERR_INVALID_ARG;
+    if (v->token_stride % 8 || v->head_stride % 8) return GQA_ERR_MISALIGNED;
+    a.v = v->data; a.v_ts = v->token_stride; a.v_hs = v->head_stride;
+    a.slots = slots;
+    a.requests = requests;
+    a.k_scale = k_scale; a.v_scale = v_scale;
+    a.k_cache = k_cache; a.v_cache = v_cache;
+    a.num_slots = (long)num_pages * page_size;
+    a.e4m3 = e4m3 ? 1 : 0;
+    a.B = B;
+    return gqa::launch_qk_norm_rope(a, D, dtype == GQA_FP16, true, sm_count(),
+                                    reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
 }
 
 gqa_status attn_validate_paged(const int32_t* real_seqlen_kv, const int32_t* block_table, int B, int Sq,
@@ -690,10 +873,11 @@ gqa_status gqa_device_error(void) {
     const int e2 = gqa::prefill_d256_take_device_error();
     const int v1 = gqa::varlen_packed_take_device_error();
     const int v2 = gqa::varlen_paged_take_device_error();
+    const int v3 = gqa::varlen_paged_fp8_take_device_error();
     const int d = gqa::decode_take_device_error();
     const int t = gqa::decode_tc_take_device_error();
-    if (e < 0 || e2 < 0 || v1 < 0 || v2 < 0 || d < 0 || t < 0) return GQA_ERR_CUDA;
-    return (e || e2 || v1 || v2 || d || t) ? GQA_ERR_TIMEOUT : GQA_OK;
+    if (e < 0 || e2 < 0 || v1 < 0 || v2 < 0 || v3 < 0 || d < 0 || t < 0) return GQA_ERR_CUDA;
+    return (e || e2 || v1 || v2 || v3 || d || t) ? GQA_ERR_TIMEOUT : GQA_OK;
 }
 
 const char* gqa_version(void) { return "gqa_attn 0.1 sm_103a"; }

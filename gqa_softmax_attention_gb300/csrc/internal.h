@@ -45,6 +45,11 @@ struct PrefillArgs {
     const void* k_cache;
     const void* v_cache;
     int num_pages;
+    // paged, float8_e4m3fn caches (attn_fwd_paged_fp8kv): dequantization
+    // scales [B, Hkv], nullptr meaning 1
+    const float* k_scale;
+    const float* v_scale;
+    const void* q;            // [total_q, Hq, D]: its rows are read by plain loads there
 };
 
 // Launches the tcgen05 prefill kernel.  The tensor maps describe q, k, v as
@@ -94,8 +99,13 @@ cudaError_t launch_varlen_packed(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  const CUtensorMap& tm_o, const PrefillArgs& a, long max_items, cudaStream_t stream);
 cudaError_t launch_varlen_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                 const CUtensorMap& tm_o, const PrefillArgs& a, long max_items, cudaStream_t stream);
+// Paged over float8_e4m3fn caches (varlen_paged_fp8.cu): the caches are read
+// through a.k_cache / a.v_cache; tm_o as above; D is 128 or 256.
+cudaError_t launch_varlen_paged_fp8(const CUtensorMap& tm_o, const PrefillArgs& a, long max_items,
+                                    cudaStream_t stream);
 int varlen_packed_take_device_error();
 int varlen_paged_take_device_error();
+int varlen_paged_fp8_take_device_error();
 
 struct DecodeArgs {
     const void* q;          // [B, Sq, Hq, D]
@@ -180,5 +190,47 @@ cudaError_t launch_decode_tc(const CUtensorMap& tm_k, const CUtensorMap& tm_v, c
 cudaError_t launch_decode_tc_fp8(const CUtensorMap& tm_k, const CUtensorMap& tm_v, const DecodeArgs& a,
                                  int box_tokens, cudaStream_t stream);
 int decode_tc_take_device_error();
+
+// Block tables, offsets and slot map of one serving step (paged_slots.cu; see
+// attn_paged_slots).
+struct SlotArgs {
+    const int32_t* past_lens;   // [B]
+    const int32_t* new_lens;    // [B]
+    int32_t* block_table;       // [B, max_pages], fresh pages entered
+    const int32_t* free_pages;  // [num_free]
+    const int32_t* free_start;  // [1] or nullptr (0)
+    int B, max_pages, page_size, num_pages, num_free, max_tokens;
+    int32_t* cu_seqlens_q;      // [B + 1]
+    int32_t* cache_seqlens;     // [B]
+    int32_t* slots;             // [max_tokens]
+    int32_t* positions;         // [max_tokens]
+    int32_t* requests;          // [max_tokens]
+    int32_t* counts;            // [3]
+};
+cudaError_t launch_paged_slots(const SlotArgs& a, int num_sms, cudaStream_t stream);
+
+// Per-head norm and rotation (qk_norm_rope.cu; see attn_qk_norm_rope and
+// attn_qk_norm_rope_paged).  Strides in elements.
+struct RopeArgs {
+    const void *q, *k, *v;          // [T, Hq / Hkv, D], token stride *_ts, head stride *_hs
+    long q_ts, q_hs, k_ts, k_hs, v_ts, v_hs;
+    const void *q_weight, *k_weight;   // [D] or nullptr
+    int weight_f32;                 // the weights are FP32 (else of the inputs' type)
+    float eps;
+    const float* cos_sin;           // [max_pos, rot]: rot / 2 cosines, then rot / 2 sines
+    const int32_t* positions;       // [n_axes, T]
+    int max_pos, rot, interleaved, n_axes;
+    uint32_t pair_axis[8];          // axis of pair j: bits 2 (j % 16), +1 of word j / 16
+    int T, Hq, Hkv;
+    void *q_out, *k_out;            // [T, Hq, D], [T, Hkv, D] (k_out: unpaged only)
+    // paged: rows of the caches [num_slots, Hkv, D]
+    const int32_t* slots;           // [T]
+    const int32_t* requests;        // [T]: row of the scales
+    const float *k_scale, *v_scale; // [B, Hkv] or nullptr (1)
+    void *k_cache, *v_cache;
+    long num_slots;
+    int e4m3, B;
+};
+cudaError_t launch_qk_norm_rope(const RopeArgs& a, int D, bool f16, bool paged, int num_sms, cudaStream_t stream);
 
 }  // namespace gqa

@@ -12,8 +12,11 @@
 //            cu_seqlens name;
 //   kPaged   packed queries over a paged cache (TileOPs GQAPagedFwdOp):
 //            k / v [pages, page_size, Hkv, D] read through block_table, the
-//            cache length of a request counting its query tokens.
-// In the two packed layouts an item is a row block of one (request, KV
+//            cache length of a request counting its query tokens;
+//   kPaged8  kPaged over float8_e4m3fn caches with one scale per (request,
+//            KV head): the products run in float16 on exactly widened keys
+//            and values, and the scales join the softmax scale and 1 / l.
+// In the packed layouts an item is a row block of one (request, KV
 // head): the g = Hq / Hkv query heads of the group are packed into the tile
 // rows (row r = query q0 + r / g, head hkv * g + r % g; floor(128 / g)
 // queries per block), so every key and value a request reads serves all g
@@ -72,7 +75,7 @@ namespace ot {
 
 using namespace pf;
 
-enum Mode : int { kBSHD = 0, kPacked = 1, kPaged = 2 };
+enum Mode : int { kBSHD = 0, kPacked = 1, kPaged = 2, kPaged8 = 3 };
 
 constexpr int NUM_THREADS = 384;
 constexpr int WARP_EPI0 = 4;
@@ -100,7 +103,7 @@ struct Cfg {
     static constexpr int VKEYS = BN / CV;               // keys per V chunk
     static constexpr int K_CHUNK = BN * 128 * KSL_C;    // bytes
     static constexpr int V_CHUNK = VKEYS * 128 * KSL;
-    static constexpr bool GROUPED = MODE == kPaged;
+    static constexpr bool GROUPED = MODE == kPaged || MODE == kPaged8;
     static constexpr int K_SLICE = GROUPED ? 1024 : BN * 128;
     static constexpr int K_GROUP = GROUPED ? KSL_C * 1024 : 1024;
     static constexpr int V_SLICE = GROUPED ? 1024 : VKEYS * 128;
@@ -122,6 +125,154 @@ struct Cfg {
 };
 constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
 
+// kPaged8: one item's Q rows and e4m3 key and value rows, by three warps.
+// The Q block (bfloat16 or float16 rows q_row0 .. of the packed batch, packed
+// r = query * g + head) is widened or copied to float16 rows; rows past the
+// block are zero.  A 128-byte stretch of a cache row goes to eight lanes, 16
+// bytes each; a warp takes every third group of 512 bytes of a ring slot (32
+// groups a slot) and holds the next slot's groups in registers while it widens
+// this one's, so 11 loads a warp stay in flight.  Rows past the request's end
+// and pages outside the pool give zeros.  The widened row has 256 bytes, the
+// lane's 16 codes becoming two 16-byte chunks of the swizzled tile; lanes 4-7
+// of eight write the odd chunk first, so that the eight lanes of a store cover
+// eight different bank groups.
+template <int D, bool F16, class C>
+__device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t r_full0, uint32_t r_empty0,
+                                         uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
+                                         int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
+                                         int lane, int& nc, int& nq) {
+    constexpr int NG = 11;                        // groups of a slot a warp takes at most
+    const uint32_t sb = smem_u32(smem);
+    uint32_t buf[NG][4];
+    auto find_row = [&](int key) -> int {
+        if (key >= skv) return -1;
+        const int page = __ldg(a.table + (size_t)b * a.max_pages + key / a.page_size);
+        return page >= 0 && page < a.num_pages ? page * a.page_size + key % a.page_size : -1;
+    };
+    auto find_rows = [&](int tile) -> int4 {
+        const int key = tile * BN + lane;
+        return make_int4(find_row(key), find_row(key + 32), find_row(key + 64), find_row(key + 96));
+    };
+    auto pick = [](bool first_one, const int4& p, const int4& q) -> int4 {
+        return make_int4(first_one ? p.x : q.x, first_one ? p.y : q.y, first_one ? p.z : q.z, first_one ? p.w : q.w);
+    };
+    // group gi of chunk ch of a K tile (V: of a V tile): the lane's row in the
+    // tile and its 16-byte column of the cache row
+    auto place = [&](bool v, int ch, int gi, int& row, int& col) {
+        if (D == 256 && v) {
+            row = C::VKEYS * ch + 2 * gi + lane / 16;
+            col = lane % 16;
+        } else {
+            row = 4 * gi + lane / 8;
+            col = (D == 256 ? 8 * ch : 0) + lane % 8;
+        }
+    };
+    const size_t row_bytes = (size_t)a.Hkv * D;
+    auto load = [&](bool v, int ch, int j, const int4& rows) {
+        const int gi = wid + 3 * j;
+        if (gi >= 32) return;
+        int row, col;
+        place(v, ch, gi, row, col);
+        const int x = __shfl_sync(0xffffffffu, row, 0) / 32;        // uniform: a group lies within 32 rows
+        const int have = x == 0 ? rows.x : (x == 1 ? rows.y : (x == 2 ? rows.z : rows.w));
+        const int src = __shfl_sync(0xffffffffu, have, row % 32);
+        uint4 d = make_uint4(0u, 0u, 0u, 0u);
+        if (src >= 0)
+            d = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache) +
+                                                     (size_t)src * row_bytes + (size_t)hkv * D) + col);
+        buf[j][0] = d.x; buf[j][1] = d.y; buf[j][2] = d.z; buf[j][3] = d.w;
+    };
+    auto store = [&](bool v, int ch, int j, uint8_t* dst) {
+        const int gi = wid + 3 * j;
+        if (gi >= 32) return;
+        int row, col;
+        place(v, ch, gi, row, col);
+        const int lr = v ? row % C::VKEYS : row;
+        const int c16 = 2 * (v ? col : col % 8);
+        uint8_t* p = dst + (lr / 8) * (v ? C::V_GROUP : C::K_GROUP) + (c16 >> 3) * 1024 + (lr % 8) * 128;
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(buf[j][e], h[2 * e], h[2 * e + 1]);
+        const uint4 even = make_uint4(h[0], h[1], h[2], h[3]), odd = make_uint4(h[4], h[5], h[6], h[7]);
+        const int sw = (lane >> 2) & 1;
+        const int q0 = (c16 + sw) & 7, q1 = (c16 + 1 - sw) & 7;
+        *reinterpret_cast<uint4*>(p + ((q0 ^ (lr % 8)) << 4)) = sw ? odd : even;
+        *reinterpret_cast<uint4*>(p + ((q1 ^ (lr % 8)) << 4)) = sw ? even : odd;
+    };
+    // Widens the slot held in buf while loading the next one of the stream.
+    auto turn = [&](bool v, int ch, bool more, bool nv, int nch, const int4& nrows) -> bool {
+        const int s = nc % C::NS;
+        if (!__all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * s, ((nc / C::NS) & 1) ^ 1, abort_flag))) return false;
+        uint8_t* dst = smem + C::OFF_RING + s * SLOT;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            store(v, ch, j, dst);
+            if (more) load(nv, nch, j, nrows);
+        }
+        fence_proxy_async_smem();                 // the tensor core reads what the warp wrote
+        __syncwarp();
+        if (lane == 0) mbar_arrive(r_full0 + 8u * s);
+        ++nc;
+        return true;
+    };
+
+    const int c = n_tiles - first;
+    // cache rows of tiles i, i + 1 and i + 2: lane l holds keys l + 32 x
+    int4 rows_v = find_rows(first), rows_k = make_int4(-1, -1, -1, -1), rows_n = rows_k;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) load(false, 0, j, rows_v);
+    if (c > 1) rows_k = find_rows(first + 1);
+    // the Q block
+    if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
+    {
+        const int n_rows = nq_rows * g;
+        for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += 96) {
+            const int r = idx / (D / 8), c8 = idx % (D / 8);
+            uint4 d = make_uint4(0u, 0u, 0u, 0u);
+            if (r < n_rows) {
+                d = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                         (((size_t)q_row0 + r / g) * a.Hq + hkv * g + r % g) * D) + c8);
+                if constexpr (!F16) {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(&d);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+                }
+            }
+            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) = d;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(q_full);
+        ++nq;
+    }
+    // K of tile 0, then (K of tile i + 1, V of tile i) for each tile i
+    for (int ch = 0; ch < C::CK; ++ch) {
+        const bool last = ch + 1 == C::CK;
+        const bool v_next = last && c == 1;       // K of tile 1, or V of tile 0 when it is the only one
+        if (!turn(false, ch, true, v_next, last ? 0 : ch + 1, pick(last && c > 1, rows_k, rows_v))) return false;
+    }
+    for (int i = 0; i < c; ++i) {
+        if (i + 2 < c) rows_n = find_rows(first + i + 2);
+        if (i + 1 < c)
+            for (int ch = 0; ch < C::CK; ++ch) {
+                const bool last = ch + 1 == C::CK;
+                if (!turn(false, ch, true, last, last ? 0 : ch + 1, pick(last, rows_v, rows_k))) return false;
+            }
+        for (int ch = 0; ch < C::CV; ++ch) {
+            const bool last = ch + 1 == C::CV;
+            // after V of tile i: K of tile i + 2, or V of tile i + 1 when that is the last tile
+            const bool k_next = last && i + 2 < c, v_last = last && i + 2 == c;
+            if (!turn(true, ch, !last || k_next || v_last, !k_next, last ? 0 : ch + 1,
+                      pick(!last, rows_v, pick(k_next, rows_n, rows_k))))
+                return false;
+        }
+        rows_v = rows_k;
+        rows_k = rows_n;
+    }
+    return true;
+}
+
 template <int D, int MODE, bool OPTS, bool F16>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
 onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -132,8 +283,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     if (a.g_eff != nullptr && (int)blockIdx.x >= *a.g_eff) return;
     using C = Cfg<D, MODE>;
     constexpr bool PACKED = MODE != kBSHD;
-    constexpr uint32_t IDESC_QK = make_idesc_16<F16>(BM, BN, false, false);
-    constexpr uint32_t IDESC_PV = make_idesc_16<F16>(BM, D, false, true);
+    constexpr bool KV8 = MODE == kPaged8;
+    constexpr bool MF16 = KV8 || F16;            // the MMAs' operand type is float16 (F16: the call's type)
+    constexpr uint32_t IDESC_QK = make_idesc_16<MF16>(BM, BN, false, false);
+    constexpr uint32_t IDESC_PV = make_idesc_16<MF16>(BM, D, false, true);
     const int wl = OPTS ? a.x.wl : -1;
     const int wr = OPTS ? a.x.wr : -1;
     const float cap_in = OPTS ? a.x.cap_in : 0.f;
@@ -262,9 +415,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, 1);
+        constexpr int FILL = KV8 ? 3 : 1;           // arrivals that fill a slot: TMA, or one per widening warp
+        mbar_init(q_full, FILL);
         mbar_init(q_empty, 1);
-        for (int s = 0; s < C::NS; ++s) { mbar_init(r_full(s), 1); mbar_init(r_empty(s), 1); }
+        for (int s = 0; s < C::NS; ++s) { mbar_init(r_full(s), FILL); mbar_init(r_empty(s), 1); }
         for (int k = 0; k < 2; ++k) { mbar_init(s_full(k), 1); mbar_init(p_full(k), BM); }
         mbar_init(o_ready, 1);
         mbar_init(o_final, 1);
@@ -274,12 +428,13 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         mbar_init(drain, 1);
         for (int k = 0; k < 2; ++k) {
             mbar_init(item_full(k), 1);
-            mbar_init(item_empty(k), 1 + 8);   // the MMA warp and the eight softmax / epilogue warps
+            // the MMA warp, the eight softmax / epilogue warps, and the widening warps but the claiming one
+            mbar_init(item_empty(k), 1 + 8 + (KV8 ? 2 : 0));
         }
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if constexpr (PACKED) {
+    if constexpr (PACKED && !KV8) {
         // Q rows past g * qpb are never loaded: zero them once (finite rows,
         // their results are never stored)
         const int rows = a.g * a.qpb;
@@ -300,7 +455,23 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 
     if (warp >= WARP_LOAD) {
         regs_dec<kRegsOther>();
-        if (warp == WARP_LOAD) {
+        if (KV8 && warp != WARP_MMA) {
+            if constexpr (KV8) {
+                const int wid = warp == WARP_LOAD ? 0 : warp - WARP_MMA;      // 0, 1, 2
+                const uint32_t ring_bar = r_full(0), ring_free = r_empty(0);
+                int nc = 0, nq = 0;
+                for (int r = 0;; ++r) {
+                    const int w = wid == 0 ? claim_item(r) : next_item(r);
+                    if (w < 0) break;
+                    const Item it = describe(w);
+                    if (it.t.n_tiles == it.first) continue;
+                    if (!fp8_item<D, F16, C>(a, smem, ring_bar, ring_free, q_full, q_empty, abort_flag, it.b, it.hkv,
+                                             it.qs + it.t.q0, it.t.rows_valid, it.skv, it.first, it.t.n_tiles, g, wid,
+                                             lane, nc, nq))
+                        break;
+                }
+            }
+        } else if (!KV8 && warp == WARP_LOAD) {
             // ------------------------------------------------------------ producer
             int nc = 0, nq = 0;                     // ring chunks and Q blocks issued (lane 0's count)
             bool ok = true;
@@ -575,8 +746,8 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             if (ok) ok = issue_pv(g_t + i, false);
                         }
                         if (ok) mma_commit(q_empty);               // every S of the item is issued
-                        // BSHD: no value row to zero, lane 0 issues the last P V too
-                        if (!PACKED && ok) ok = issue_pv(g_t + c - 1, c == 1);
+                        // BSHD, kPaged8: no value row to zero, lane 0 issues the last P V too
+                        if ((!PACKED || KV8) && ok) ok = issue_pv(g_t + c - 1, c == 1);
                     } else {
                         ok = wait_o_empty(n_item);
                     }
@@ -585,7 +756,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 nc = __shfl_sync(0xffffffffu, nc, 0);
                 nq = __shfl_sync(0xffffffffu, nq, 0);
                 oe = __shfl_sync(0xffffffffu, oe, 0);
-                if (PACKED && ok && c > 0) {
+                if (PACKED && !KV8 && ok && c > 0) {
                     // the item's last P V, by the whole warp
                     const int gi = g_t + c - 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(p_full(gi & 1), (gi >> 1) & 1, abort_flag));
@@ -631,7 +802,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         // ------------------------------------------------------------ softmax warps 0-3
         const int r = warp * 32 + lane;                        // row of the tile == TMEM lane
         const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
-        const float sl = a.scale_log2;
+        float sl = a.scale_log2, cap_i = cap_in;
         const int rq = r / g;                                  // query of this row within the block
         int gt = 0;                  // visited tiles so far
         int n = 0;                   // items finished
@@ -642,6 +813,11 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const Item itm = describe(w);
             const TileInfo ti = itm.t;
             const uint8_t* mrow = itm.mrow;
+            if constexpr (KV8) {
+                const float ks = a.k_scale ? a.k_scale[itm.b * a.Hkv + itm.hkv] : 1.f;
+                sl = a.scale_log2 * ks;
+                cap_i = cap_in * ks;
+            }
             const long p_row = (long)ti.q0 + rq + itm.skv - itm.sq;
             const int lim = (int)key_hi(p_row, itm.skv, a.causal, wr);   // visible keys: [lo, lim)
             const int lo = (int)key_lo(p_row, itm.skv, wl);
@@ -703,7 +879,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                         for (int c = 0; c < BN; ++c) {
                             const float x = ((vis[c / 32] >> (c % 32)) & 1u)
-                                                ? softcap_log2(s[c], cap_in, cap_out) : -INFINITY;
+                                                ? softcap_log2(s[c], cap_i, cap_out) : -INFINITY;
                             s[c] = x;
                             mx8[c & 7] = fmaxf(mx8[c & 7], x);
                         }
@@ -728,7 +904,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                 const float fa = fast ? sl : 1.f;
                 uint32_t pk[BN / 2];
-                const float rs = exp_row<F16>(s, fa, m_use, pk);
+                const float rs = exp_row<MF16>(s, fa, m_use, pk);
                 tmem_st64(tmem + lane_addr + col_s, pk);          // P over the first 64 columns of S
                 l_run = l_run * alpha + rs;
 
@@ -810,6 +986,8 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     lse2 = M + log2f(l_tot);
                 }
             }
+            if constexpr (KV8)
+                if (a.v_scale) inv *= a.v_scale[itm.b * a.Hkv + itm.hkv];
             // Whole blocks go out with TMA; a packed block cut by its request's
             // end is written row by row (its box would reach the next request).
             // The choice is the same for every thread of the item.

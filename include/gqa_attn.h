@@ -331,6 +331,149 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
                           int max_pages, int causal, float scale, const gqa_options* opts,
                           void* workspace, size_t workspace_bytes, gqa_stream_t stream);
 
+/*
+ * attn_fwd_paged over float8_e4m3fn caches (TileOPs "Attention Operators",
+ * GQAPagedFwdOp over the FP8 caches of GQADenseFwdOp stage 2): key t of KV head
+ * r in request b is K * k_scale[b * Hkv + r], its value V * v_scale[b * Hkv + r].
+ *
+ *   k_cache, v_cache, k_scale, v_scale  as for attn_decode_paged_fp8kv (scales
+ *                     [B, Hkv] or NULL for ones; finite and positive, a caller
+ *                     obligation; NaN codes must not occur in slots a request
+ *                     reads)
+ *   other arguments   as attn_fwd_paged, q and o 16-bit; the same workspaces
+ *                     and streams (with attn_paged_workspace_size bytes the
+ *                     one-query requests run on the split decode kernel of
+ *                     attn_decode_paged_fp8kv, beside the chunks)
+ *
+ * Keys and values are widened exactly to float16 and the products run in
+ * float16 with FP32 accumulation: Q is rounded to float16 once, so a bfloat16
+ * Q must stay below 65504 (attn_decode_paged_fp8kv).  D = 128 or 256
+ * (GQA_ERR_UNSUPPORTED otherwise), any page size at one speed.
+ */
+gqa_status attn_fwd_paged_fp8kv(const void* q, const void* k_cache, const void* v_cache,
+                                const float* k_scale, const float* v_scale,
+                                const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
+                                const int32_t* block_table, int page_size, void* o, float* lse,
+                                int B, int total_q, int Hq, int Hkv, int D, int num_pages,
+                                int max_pages, int causal, float scale, const gqa_options* opts,
+                                void* workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * Metadata of one serving step, built on the device from the requests'
+ * lengths: what attn_qk_norm_rope_paged and the paged attention calls take.
+ *
+ *   past_lens    [B] int32: tokens request b already holds in its pages
+ *   new_lens     [B] int32: tokens it brings in this step (0 allowed)
+ *   block_table  [B, max_pages] int32: row b holds the pages of the past
+ *                tokens; the pages that the new tokens need beyond them are
+ *                entered behind (no other entry is written)
+ *   free_pages   [num_free] int32 page ids, handed out in request order from
+ *                index *free_start on (free_start: one device int32, or NULL
+ *                for 0; it must not be part of counts)
+ *   max_tokens   rows of the packed batch, padding included
+ *   cu_seqlens_q [B + 1] (written): min(sum of new_lens before b, max_tokens)
+ *   cache_seqlens [B] (written): min(past + new, max_pages * page_size)
+ *   slots, positions, requests  [max_tokens] (written): for token t of request
+ *                b the row page * page_size + position % page_size of the
+ *                cache, the position past + i, and b; rows past the last token
+ *                get -1, 0 and -1
+ *   counts       [3] (written): tokens asked for, fresh pages asked for, and
+ *                *free_start plus the latter (the next call's free_start)
+ *
+ * Negative lengths count as 0, past_lens are clamped to the table's capacity.
+ * A token has slot -1 where its request runs past the capacity, the free list
+ * is exhausted (the table entry is then -1 too) or the page id lies outside
+ * [0, num_pages).  Tokens past max_tokens are counted, but get no row and no
+ * page: counts[0] > max_tokens asks for another call with more rows.  The call
+ * changes nothing it reads, so it may be repeated or replayed.  One launch, no
+ * workspace, no host read-back.
+ */
+gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
+                            const int32_t* free_pages, const int32_t* free_start, int B, int max_pages,
+                            int page_size, int num_pages, int num_free, int max_tokens,
+                            int32_t* cu_seqlens_q, int32_t* cache_seqlens, int32_t* slots,
+                            int32_t* positions, int32_t* requests, int32_t* counts,
+                            gqa_stream_t stream);
+
+/* Rows [T, heads, D] of 16-bit values, D contiguous; strides in elements,
+ * multiples of 8 (a slice of a fused projection needs no copy). */
+typedef struct {
+    const void* data;
+    int64_t token_stride;
+    int64_t head_stride;
+} gqa_head_rows;
+
+/*
+ * Rotation by position.  Pair j of the first rot dims (rot <= D, a multiple of
+ * 16; dims past it are not rotated) is dims (j, j + rot / 2), or (2j, 2j + 1)
+ * with interleaved, and turns by the angle whose cosine and sine stand in
+ * cos_sin[p, j] and cos_sin[p, rot / 2 + j] for the token's position p on the
+ * pair's axis.
+ *   cos_sin    [max_pos, rot] float, DEVICE, 16-byte aligned
+ *   positions  [n_axes, T] int32, DEVICE; values outside [0, max_pos) are a
+ *              caller error and read as the nearest table row
+ *   n_axes     1 to 4 (time, height, width, ...)
+ *   pair_axis  rot / 2 bytes, HOST, read during the call: axis of each pair;
+ *              NULL with one axis
+ */
+typedef struct {
+    const float* cos_sin;
+    const int32_t* positions;
+    int max_pos;
+    int rot;
+    int interleaved;
+    int n_axes;
+    const uint8_t* pair_axis;
+} gqa_rope;
+
+/*
+ * Norm of each query and key head and rotation, in one pass:
+ *     n_d = x_d / sqrt(mean_d(x_d^2) + eps) * w_d        (n = x without a weight)
+ *     y   = n with each rotary pair (n_0, n_1) turned into
+ *           (n_0 cos - n_1 sin, n_1 cos + n_0 sin)
+ * in FP32, rounded once.
+ *
+ *   q [T, Hq, D], k [T, Hkv, D]   bfloat16 or float16 (dtype, gqa_dtype)
+ *   q_weight, k_weight  [D] of the same type, or float with weight_f32; NULL
+ *                       for no norm of that side; 16-byte aligned
+ *   rope                NULL for no rotation
+ *   q_out [T, Hq, D], k_out [T, Hkv, D]   contiguous, of the same type
+ *                       (written); q_out may be q and k_out k where those are
+ *                       contiguous, any other overlap is a caller error
+ *
+ * D = 64, 128 or 256.  T = 0 does nothing.
+ */
+gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, const void* q_weight,
+                             const void* k_weight, int weight_f32, float eps, const gqa_rope* rope,
+                             void* q_out, void* k_out, int T, int Hq, int Hkv, int D, int dtype,
+                             gqa_stream_t stream);
+
+/*
+ * attn_qk_norm_rope with the keys and the values (as they are) written into
+ * paged caches, for the attention call that follows.
+ *
+ *   v            [T, Hkv, D]
+ *   slots        [T] int32: cache row (page * page_size + offset) of each
+ *                token.  A token whose slot lies outside [0, num_pages *
+ *                page_size) is padding: nothing of it is read, its rows of
+ *                q_out and the caches stay as they were.  Two tokens with one
+ *                slot are a caller error (either may win, value by value)
+ *   k_cache, v_cache  [num_pages, page_size, Hkv, D] (written at the slots):
+ *                the inputs' type, or float8_e4m3fn with e4m3
+ *   k_scale, v_scale  [B, Hkv] float, or NULL for ones; e4m3 only: the stored
+ *                code is x / scale rounded to nearest even, +-448 beyond the
+ *                range (x from FP32, not through 16 bits); finite and positive
+ *                scales are a caller obligation
+ *   requests     [T] int32: the token's row of the scales (not read without
+ *                scales); a token whose row lies outside [0, B) is padding
+ */
+gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* k, const gqa_head_rows* v,
+                                   const void* q_weight, const void* k_weight, int weight_f32, float eps,
+                                   const gqa_rope* rope, void* q_out, const int32_t* slots, void* k_cache,
+                                   void* v_cache, int e4m3, const float* k_scale, const float* v_scale,
+                                   const int32_t* requests, int B, int T, int Hq, int Hkv, int D,
+                                   int num_pages, int page_size, int dtype, gqa_stream_t stream);
+
 /* Workspace bytes of attn_fwd_varlen / attn_fwd_paged (0 for invalid sizes). */
 size_t attn_varlen_workspace_size(int B, int total_q, int Hq, int Hkv);
 

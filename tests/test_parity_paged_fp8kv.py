@@ -1,0 +1,289 @@
+"""Packed queries over a float8_e4m3fn paged cache on the GPU (chunks and decode
+steps in one call) against the FP64 oracle, request by request; unread slots
+hold the NaN code.
+
+Every output is held to what its roundings allow: half a step of the output
+type (eps / 2 of the value), and half a step of a float16 weight, 2^-11 of each
+p, so at most 2^-11 max|v| of the weighted mean; the FP32 scores and
+exponentials add less than 2^-13 max|v| (128 to 256 products of 2^-24 each on
+scores of a few units, and 2^-22 of an exponential).  The absolute 2e-2 of
+parity.compare does not fit here: a row that sees one key returns its value, up
+to 5.5 x 2 with scales up to 2, and half a bfloat16 step between 8 and 16 is
+2^-5 = 3.1e-2.  The LSE limit (1e-3) and the empty rows are those of compare.
+"""
+import pytest
+import torch
+
+import oracle
+from gqa_softmax_attention_gb300 import workloads as W
+
+from parity import TOL_LSE
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+
+
+@pytest.fixture(scope="module")
+def g():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA GPU")
+    from gqa_softmax_attention_gb300 import build
+    build.build()
+    import gqa_softmax_attention_gb300 as m
+    yield m
+    m.gqa_device_error()          # no kernel wait may have timed out
+
+
+def inputs(ql, L, Hq, Hkv, D, ps, seed=0, dtype=torch.bfloat16, scale_range=(0.25, 1.0)):
+    """varlen_paged_inputs with e4m3 caches and scales; slots no request owns hold NaN codes."""
+    p = W.varlen_paged_inputs(ql, L, Hq, Hkv, D, ps, seed=seed)
+    p["q"] = p["q"].to(dtype)
+    gen = torch.Generator().manual_seed(seed + 77)
+    lo, hi = scale_range
+    p["k_scale"], p["v_scale"] = (lo + (hi - lo) * torch.rand(len(ql), Hkv, generator=gen) for _ in range(2))
+    owned = torch.zeros(p["num_pages"] * ps, dtype=torch.bool)
+    for b, n in enumerate(L):
+        t = torch.arange(n)
+        owned[p["block_table"][b].long()[t // ps] * ps + t % ps] = True
+    for n in ("k_cache", "v_cache"):
+        c = p[n].float().to(torch.float8_e4m3fn).view(torch.uint8)
+        c.view(-1, Hkv, D)[~owned] = 0x7F
+        p[n] = c.view(torch.float8_e4m3fn)
+    return p
+
+
+NAMES = ("q", "k_cache", "v_cache", "k_scale", "v_scale", "cu_seqlens_q", "cache_seqlens", "block_table")
+
+
+def run(g, p, **kw):
+    o, lse = g.attn_fwd_paged_fp8kv(*[p[n].cuda() for n in NAMES], **kw)
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu()
+
+
+def check(p, o, lse, label="", requests=None, **kw):
+    cu, D = p["cu_seqlens_q"].tolist(), p["q"].shape[2]
+    for b in range(len(cu) - 1) if requests is None else requests:
+        a, z = cu[b], cu[b + 1]
+        if a == z:
+            continue
+        one = slice(b, b + 1)
+        ro, rl = oracle.attn_paged_fp8kv(p["q"][None, a:z], p["k_cache"], p["v_cache"], p["k_scale"][one],
+                                         p["v_scale"][one], p["cache_seqlens"][one], p["block_table"][one], **kw)
+        ro, rl, go, gl = ro[0], rl[0], o[a:z], lse[a:z]
+        top = torch.isposinf(rl)                       # heads with a +inf sink
+        assert bool(torch.isposinf(gl[top]).all()) and bool((go.float()[top] == 0).all()), label
+        ro, rl, go, gl = ro[~top], rl[~top], go[~top], gl[~top]
+        empty = torch.isneginf(rl)
+        assert torch.equal(torch.isneginf(gl), empty) and bool((go.float()[empty] == 0).all()), label
+        assert bool(((gl.double() - rl)[~empty].abs() <= TOL_LSE).all()), "%s request %d: LSE" % (label, b)
+        vmax = 5.5 * float(p["v_scale"][b].max())          # N(0, 1) draws of this size stay below 5.5
+        tol = torch.finfo(o.dtype).eps / 2 * ro.abs() + (2.0 ** -11 + 2.0 ** -13) * vmax
+        off = (go.double() - ro).abs()
+        assert bool((off <= tol).all()), "%s request %d: %.3g of its tolerance" % (label, b, float((off / tol).max()))
+
+
+CASES = [
+    # q lengths, cache lengths (query tokens included), Hq, Hkv, D, page_size
+    ([2], [2], 4, 2, 128, 16), ([1], [1], 4, 2, 128, 16), ([7], [300], 4, 4, 256, 8),
+    ([1, 300, 0, 4, 1, 129], [1000, 800, 50, 333, 1, 129], 8, 2, 128, 16),
+    ([1, 1, 1, 1, 2, 200], [17, 4000, 129, 640, 2, 200], 32, 8, 128, 64),
+    ([4, 4, 1, 64], [3000, 17, 700, 64], 24, 2, 256, 16),
+    ([3, 100, 1], [77, 100, 1000], 4, 2, 128, 8),
+    ([1, 40, 2], [500, 300, 2], 8, 2, 128, 24),
+    ([5, 1, 130], [900, 600, 130], 16, 2, 256, 256),
+    ([1, 1, 20, 1], [0, 700, 40, 1], 8, 2, 128, 16),                       # a decode step with an empty cache
+    ([1, 37, 3], [300, 200, 3], 8, 2, 128, 1),
+    ([2, 1, 150], [41, 500, 400], 8, 2, 128, 3),
+    ([1, 129, 4], [777, 129, 260], 24, 2, 256, 5),
+    ([200, 1, 1], [1000, 13, 1200], 32, 8, 128, 12),
+    ([20, 1, 6], [20, 300, 1111], 33, 1, 128, 16),                         # g = 33: decode steps stay packed
+    ([9, 1], [2000, 130], 128, 1, 128, 64), ([40, 3], [500, 260], 12, 12, 128, 64),   # g = 128, g = 1
+    ([128, 127, 129, 256], [128, 255, 257, 512], 8, 8, 128, 128),          # whole tiles and their neighbours
+]
+
+
+@pytest.mark.parametrize("split_decode", [True, False], ids=["split_decode", "packed_only"])
+@pytest.mark.parametrize("case", CASES, ids=[str(c[:2]) + "/%d/%d/D%d/ps%d" % c[2:] for c in CASES])
+def test_matches_oracle(g, case, split_decode):
+    p = inputs(*case, seed=sum(case[1]) % 97)
+    check(p, *run(g, p, split_decode=split_decode))
+
+
+@pytest.mark.parametrize("split_decode", [True, False], ids=["split_decode", "packed_only"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("geometry", [(24, 2, 256, 32), (32, 8, 128, 64)], ids=str)
+def test_options(g, geometry, dtype, split_decode):
+    Hq = geometry[0]
+    p = inputs([1, 200, 4, 1, 300], [2000, 450, 40, 90, 1500], *geometry, seed=5, dtype=dtype, scale_range=(0.05, 2.0))
+    sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(9)) * 2
+    sinks[0], sinks[-1] = -INF, INF
+    for kw in (dict(window_left=300, softcap=20.0, sinks=sinks), dict(window_left=0), dict(softcap=5.0),
+               dict(window_left=129, window_right=0, scale=0.03), dict(scale=-0.1), dict(scale=0.0)):
+        check(p, *run(g, p, split_decode=split_decode, **kw), label=str(kw), **kw)
+
+
+def test_noncausal_and_two_sided_window(g):
+    p = inputs([60, 200, 1, 5], [300, 200, 77, 90], 6, 3, 128, 16, seed=12)
+    check(p, *run(g, p, causal=False), causal=False)
+    kw = dict(causal=False, window_left=40, window_right=17)
+    check(p, *run(g, p, **kw), **kw)
+
+
+def test_rows_without_a_key(g):
+    """More queries than cached tokens (leading rows see nothing) and no cache at all: zeros and -inf."""
+    p = inputs([5, 130, 1, 40], [2, 100, 0, 0], 8, 2, 128, 16, seed=3)
+    p["block_table"] = p["block_table"].contiguous()
+    o, lse = run(g, p)
+    check(p, o, lse)
+    assert bool(torch.isneginf(lse[:3]).all()) and bool((o[:3].float() == 0).all())
+    assert bool(torch.isneginf(lse[-41:]).all()) and bool((o[-41:].float() == 0).all())
+
+
+def test_every_code(g):
+    """Every finite e4m3 code among keys and values, subnormals included: one
+    visible key gives its value exactly (scales are powers of two)."""
+    D, Hkv, T = 128, 2, 4
+    codes = torch.arange(256, dtype=torch.uint8)
+    codes[(codes & 0x7F) == 0x7F] = 0
+    cache = codes.repeat(4)[:T * Hkv * D].view(1, T, Hkv, D)
+    q = torch.zeros(2 * T, 2 * Hkv, D, dtype=torch.float16)
+    cu = torch.tensor([0, 2, 4, 6, 8], dtype=torch.int32)
+    lens = torch.ones(T, dtype=torch.int32)
+    pool = cache.view(T, 1, Hkv, D).contiguous()
+    table = torch.arange(T, dtype=torch.int32)[:, None].contiguous()
+    vs = torch.full((T, Hkv), 0.5)
+    o, lse = g.attn_fwd_paged_fp8kv(q.cuda(), pool.cuda(), pool.cuda(), None, vs.cuda(), cu.cuda(), lens.cuda(),
+                                    table.cuda())
+    want = (oracle.e4m3_decode(pool)[:, 0] * 0.5).repeat_interleave(2, dim=1)
+    assert torch.equal(o[1::2].double().cpu(), want)               # row 1 of each request sees its one key
+    assert bool((lse[1::2] == 0).all()) and bool(torch.isneginf(lse[0::2]).all())
+
+
+def test_unit_scales_equal_the_16bit_call(g):
+    """Codes are float16 values: with unit scales the 16-bit call on the widened cache has the same inputs."""
+    p = inputs([100, 1, 30], [900, 400, 30], 8, 2, 128, 16, seed=6, dtype=torch.float16)
+    kc, vc = (p[n].float().nan_to_num(0).half().cuda() for n in ("k_cache", "v_cache"))
+    o, lse = g.attn_fwd_paged_fp8kv(p["q"].cuda(), p["k_cache"].cuda(), p["v_cache"].view(torch.uint8).cuda(), None,
+                                    None, *[p[n].cuda() for n in NAMES[5:]])
+    o2, lse2 = g.attn_fwd_paged(p["q"].cuda(), kc, vc, *[p[n].cuda() for n in NAMES[5:]])
+    tol = (2.0 ** -11 * o2.float().abs() + 2 * (2.0 ** -11 + 2.0 ** -13) * 5.5)
+    assert bool(((o.float() - o2.float()).abs() <= tol).all())
+    assert bool(((lse - lse2).abs() <= 1e-4).all())
+
+
+def test_bad_page_ids_read_as_zeros_and_stay_in_the_pool(g):
+    p = inputs([150, 20], [400, 100], 8, 2, 128, 16, seed=8)
+    p["block_table"][0, 3] = 2**31 - 1
+    p["block_table"][0, 5] = -9
+    p["block_table"][1, 0] = p["num_pages"]
+    o, lse = run(g, p)
+    assert bool(o.isfinite().all()) and bool(lse.isfinite().all())
+    # the same call with those pages zeroed
+    z = dict(p, block_table=p["block_table"].clone())
+    spare = sorted(set(range(p["num_pages"])) - set(p["block_table"].flatten().tolist()))[:1]
+    for b, j in ((0, 3), (0, 5), (1, 0)):
+        z["block_table"][b, j] = spare[0]
+    for n in ("k_cache", "v_cache"):
+        z[n] = p[n].view(torch.uint8).clone()
+        z[n][spare[0]] = 0
+        z[n] = z[n].view(torch.float8_e4m3fn)
+    o2, lse2 = run(g, z)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_rows_outside_the_requests_stay(g):
+    p = inputs([3, 140, 1], [50, 300, 70], 8, 2, 128, 16, seed=4)
+    q = torch.cat([p["q"], torch.full((9, 8, 128), float("nan"), dtype=p["q"].dtype)])
+    out = torch.full_like(q, 3.0).cuda()
+    lse = torch.full((q.shape[0], 8), 5.0, device="cuda")
+    g.attn_fwd_paged_fp8kv(q.cuda(), *[p[n].cuda() for n in NAMES[1:]], out=out, lse=lse)
+    check(p, out[:144].cpu(), lse[:144].cpu())
+    assert bool((out[144:] == 3).all()) and bool((lse[144:] == 5).all())
+
+
+def test_many_requests(g):
+    gen = torch.Generator().manual_seed(21)
+    B = 1200
+    ql = torch.randint(0, 3, (B,), generator=gen).tolist()
+    L = [max(n, int(x)) for n, x in zip(ql, torch.randint(1, 200, (B,), generator=gen))]
+    p = inputs(ql, L, 4, 2, 128, 8, seed=3)
+    check(p, *run(g, p), requests=range(0, B, 37))
+
+
+def test_long_cache_and_mixed_batch(g):
+    """A serving-sized mix: 30 decode steps and two chunks over long caches, sampled."""
+    gen = torch.Generator().manual_seed(4)
+    L = [int(x) for x in torch.randint(1024, 9000, (32,), generator=gen)]
+    ql = [1] * 32
+    ql[5], ql[20] = 700, 1024
+    p = inputs(ql, L, 32, 8, 128, 64, seed=11)
+    o, lse = run(g, p)
+    assert bool(o.isfinite().all()) and bool(lse.isfinite().all())
+    check(p, o, lse, requests=(0, 17, 31))
+    for b in (5, 20):
+        a, n = int(p["cu_seqlens_q"][b]), ql[b]
+        for i in (0, 1, 31, 32, 511, n - 1):
+            r = dict(p, q=p["q"][a + i:a + i + 1], cu_seqlens_q=torch.tensor([0, 1], dtype=torch.int32),
+                     cache_seqlens=p["cache_seqlens"][b:b + 1] - n + i + 1, block_table=p["block_table"][b:b + 1],
+                     k_scale=p["k_scale"][b:b + 1], v_scale=p["v_scale"][b:b + 1])
+            check(r, o[a + i:a + i + 1], lse[a + i:a + i + 1], "request %d row %d" % (b, i))
+
+
+def test_graph_replay_with_new_lengths_and_scales(g):
+    p = inputs([1, 300, 1, 4], [1500, 700, 50, 1000], 32, 8, 128, 64, seed=9)
+    for n, c in zip(("k_cache", "v_cache"), (p["k_cache"], p["v_cache"])):      # any slot may be read below
+        p[n] = torch.where(c.view(torch.uint8) == 0x7F, 0, c.view(torch.uint8)).to(torch.uint8).view(torch.float8_e4m3fn)
+    dev = {n: p[n].cuda() for n in NAMES}
+    out = torch.empty_like(dev["q"])
+    lse = torch.empty((p["q"].shape[0], 32), device="cuda")
+    call = lambda: g.attn_fwd_paged_fp8kv(*[dev[n] for n in NAMES], out=out, lse=lse)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens, cu in (([900, 301, 20, 700], [0, 1, 301, 302, 306]), ([1500, 305, 30, 10], [0, 0, 300, 302, 306])):
+        p["cache_seqlens"], p["cu_seqlens_q"] = (torch.tensor(x, dtype=torch.int32) for x in (lens, cu))
+        p["k_scale"], p["v_scale"] = p["v_scale"].flip(0), p["k_scale"].flip(0)
+        for n in ("cache_seqlens", "cu_seqlens_q", "k_scale", "v_scale"):
+            dev[n].copy_(p[n])
+        graph.replay()
+        torch.cuda.synchronize()
+        check(p, out.cpu(), lse.cpu(), "replay %s" % lens)
+
+
+def test_other_stream_and_repeat(g):
+    p = inputs([1, 600, 1, 300], [3000, 1800, 40, 700], 32, 8, 128, 64, seed=6)
+    dev = [p[n].cuda() for n in NAMES]
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    copies = []
+    with torch.cuda.stream(st):
+        for _ in range(3):
+            o, lse = g.attn_fwd_paged_fp8kv(*dev)
+            copies.append((o.clone(), lse.clone()))          # queued behind the call
+    torch.cuda.synchronize()
+    check(p, copies[0][0].cpu(), copies[0][1].cpu())
+    for o, lse in copies[1:]:
+        assert torch.equal(o, copies[0][0]) and torch.equal(lse, copies[0][1])
+
+
+def test_refusals(g):
+    p = inputs([2, 3], [20, 30], 8, 2, 128, 16)
+    d = {n: p[n].cuda() for n in NAMES}
+    for bad in (dict(q=d["q"].float()), dict(q=d["q"][..., :64]), dict(k_cache=d["k_cache"].half()),
+                dict(k_cache=d["k_cache"][:, ::2]), dict(v_cache=d["v_cache"][1:]), dict(k_scale=d["k_scale"][:1]),
+                dict(v_scale=d["v_scale"].double()), dict(cu_seqlens_q=d["cu_seqlens_q"].long()),
+                dict(cu_seqlens_q=d["cu_seqlens_q"][:2]), dict(cache_seqlens=d["cache_seqlens"].cpu()),
+                dict(block_table=d["block_table"][:1]), dict(block_table=d["block_table"].t().contiguous().t()),
+                dict(q=d["q"][:, :7]), dict(window_left=-2), dict(softcap=-1.0), dict(softcap=float("nan")),
+                dict(scale=float("inf")), dict(sinks=torch.zeros(3)), dict(out=torch.empty(5, 8, 128, device="cuda")),
+                dict(lse=torch.empty(5, 9, device="cuda")),
+                dict(workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(ValueError):
+            g.attn_fwd_paged_fp8kv(**{**d, **bad})
+    d64 = {n: p[n].cuda() for n in NAMES}
+    d64["q"], d64["k_cache"], d64["v_cache"] = (d64[n][..., :64].contiguous() for n in ("q", "k_cache", "v_cache"))
+    with pytest.raises(ValueError):
+        g.attn_fwd_paged_fp8kv(**d64)                                     # D = 64
