@@ -89,6 +89,18 @@ constexpr int kRegsSoftmax = 208;
 constexpr int kRegsEpi = 152;
 constexpr int kRegsOther = 144;
 static_assert((kRegsSoftmax + kRegsEpi + kRegsOther) * 128 <= kRegsLaunch * NUM_THREADS, "register split");
+// kPaged8: warps 8-11 widen keys, 12-14 values, 15 issues the MMAs.  128
+// registers per thread at launch (four warps on each SM sub-partition); softmax
+// 208, epilogue 96, the other two warpgroups 104 each.
+constexpr int NUM_THREADS8 = 512;
+constexpr int WARP_V8 = 12;
+constexpr int WARP_MMA8 = 15;
+constexpr int TEAM_K8 = 4, TEAM_V8 = 3;        // warps of a widening team
+constexpr int kFill8 = TEAM_K8 * TEAM_V8;      // arrivals that fill a ring slot, whichever team fills it
+constexpr int kRegsEpi8 = 96;
+constexpr int kRegsOther8 = 104;
+static_assert((kRegsSoftmax + kRegsEpi8 + 2 * kRegsOther8) * 128 <= 128 * NUM_THREADS8, "register split");
+constexpr int num_threads(int mode) { return mode == kPaged8 ? NUM_THREADS8 : NUM_THREADS; }
 
 constexpr int BOX = BM * 128;      // one 64-column box of 128 rows (16 KB)
 constexpr int SLOT = 32768;        // one ring slot
@@ -125,156 +137,137 @@ struct Cfg {
 };
 constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
 
-// kPaged8: one item's Q rows and e4m3 key and value rows, by three warps.
-// The Q block (bfloat16 or float16 rows q_row0 .. of the packed batch, packed
-// r = query * g + head) is widened or copied to float16 rows; rows past the
-// block are zero.  A 128-byte stretch of a cache row goes to eight lanes, 16
-// bytes each; a warp takes every third group of 512 bytes of a ring slot (32
-// groups a slot) and holds the next slot's groups in registers while it widens
-// this one's, so 11 loads a warp stay in flight.  Rows past the request's end
-// and pages outside the pool give zeros.  The widened row has 256 bytes, the
-// lane's 16 codes becoming two 16-byte chunks of the swizzled tile; lanes 4-7
-// of eight write the odd chunk first, so that the eight lanes of a store cover
-// eight different bank groups.
-template <int D, bool F16, class C>
+// kPaged8: one item's e4m3 key (V: value) rows, by a team of four (three)
+// warps, as float16 tiles in the ring slots that hold its keys (values).  A
+// 128-byte stretch of a cache row goes to eight lanes, 16 bytes each, so a
+// warp's load covers 512 bytes, and a slot takes 32 of them.  The loads of the
+// next slot are issued when this one's are widened and stored: their latency
+// runs beside the wait for the slot.  Rows past the request's end and pages
+// outside the pool give zeros.  The lane's 16 codes become two 16-byte chunks
+// of the swizzled tile; lanes 4-7 of eight write the odd chunk first, so that
+// the eight lanes of a store cover eight different bank groups.  Nothing here
+// may spill: the streaming loads evict local memory from the small L1 beside
+// 227 KB of shared memory, and every reload then goes to L2 (10.6 ms instead of
+// RESULT on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128).
+// The key team also writes the Q block (rows q_row0 .. of the packed batch,
+// packed r = query * g + head, bfloat16 rounded to float16), zeros past it.
+template <int D, bool F16, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t r_full0, uint32_t r_empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
                                          int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
-                                         int lane, int& nc, int& nq) {
-    constexpr int NG = 11;                        // groups of a slot a warp takes at most
-    const uint32_t sb = smem_u32(smem);
-    uint32_t buf[NG][4];
-    auto find_row = [&](int key) -> int {
-        if (key >= skv) return -1;
-        const int page = __ldg(a.table + (size_t)b * a.max_pages + key / a.page_size);
-        return page >= 0 && page < a.num_pages ? page * a.page_size + key % a.page_size : -1;
+                                         int lane, int nc, int& nq) {
+    static_assert(C::CV == C::CK, "slot positions");
+    constexpr int NCH = C::CK;                    // slots per tile
+    constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
+    constexpr int LPR = WIDE ? 16 : 8;            // lanes per row
+    constexpr int TEAM = V ? TEAM_V8 : TEAM_K8;
+    constexpr int NL = (32 + TEAM - 1) / TEAM;    // a warp's loads of a slot
+    constexpr int STEP = TEAM * (32 / LPR);       // rows between a warp's loads
+    constexpr int GROUP = V ? C::V_GROUP : C::K_GROUP;
+    const int row0 = wid * (32 / LPR) + lane / LPR;      // this lane's row of the first load
+    const int col = lane % LPR;                          // its 16-byte column
+    // where the first of its two chunks of row r goes (the second: bit 4 flipped)
+    const int sw = (lane >> 2) & 1;
+    auto place = [&](int r) -> uint32_t {
+        return (r / 8) * GROUP + (col >> 2) * 1024 + (r % 8) * 128 + ((((2 * col) & 7) + sw) ^ (r % 8)) * 16;
     };
-    auto find_rows = [&](int tile) -> int4 {
-        const int key = tile * BN + lane;
-        return make_int4(find_row(key), find_row(key + 32), find_row(key + 64), find_row(key + 96));
+    const uint32_t to = place(row0);
+    const uint8_t* cache = static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + (size_t)hkv * D + 16 * col;
+    const uint32_t row_bytes = (uint32_t)a.Hkv * D;
+    const int32_t* table = a.table + (size_t)b * a.max_pages;
+    // No load stands in a branch: what a branch loads may be moved to its
+    // register at the branch's end, which waits out the load's latency.
+    // Cache rows of a tile: lane l holds keys l, l + 32, l + 64, l + 96 (-1: no row).
+    auto find_rows = [&](int tile, bool any) -> int4 {
+        int r[4], page[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            r[x] = tile * BN + 32 * x + lane;
+            page[x] = __ldg(table + min(r[x], skv - 1) / a.page_size);
+        }
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            r[x] = any && r[x] < skv && page[x] >= 0 && page[x] < a.num_pages
+                       ? page[x] * a.page_size + r[x] % a.page_size : -1;
+        return make_int4(r[0], r[1], r[2], r[3]);
     };
-    auto pick = [](bool first_one, const int4& p, const int4& q) -> int4 {
-        return make_int4(first_one ? p.x : q.x, first_one ? p.y : q.y, first_one ? p.z : q.z, first_one ? p.w : q.w);
-    };
-    // group gi of chunk ch of a K tile (V: of a V tile): the lane's row in the
-    // tile and its 16-byte column of the cache row
-    auto place = [&](bool v, int ch, int gi, int& row, int& col) {
-        if (D == 256 && v) {
-            row = C::VKEYS * ch + 2 * gi + lane / 16;
-            col = lane % 16;
-        } else {
-            row = 4 * gi + lane / 8;
-            col = (D == 256 ? 8 * ch : 0) + lane % 8;
+    uint32_t buf[NL][4];
+    auto load = [&](int ch, const int4& rows) {
+        auto part = [&](int x) { return x == 0 ? rows.x : (x == 1 ? rows.y : (x == 2 ? rows.z : rows.w)); };
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int at = (WIDE ? 64 * ch : 0) + j * STEP;             // + row0 < STEP: the lane's row of the tile
+            int src = __shfl_sync(0xffffffffu, part(at / 32), at % 32 + row0);
+            if (at % 32 + STEP > 32 && at < 96) {                       // the warps' rows straddle two parts
+                const int next = __shfl_sync(0xffffffffu, part(at / 32 + 1), at % 32 + row0);
+                src = at % 32 + row0 >= 32 ? next : src;
+            }
+            if (32 % TEAM && j == NL - 1 && wid + TEAM * j >= 32) src = -1;
+            ldg16_or_zero(buf[j], cache + (size_t)max(src, 0) * row_bytes + (D == 256 && !V ? 128 * ch : 0), src >= 0);
         }
     };
-    const size_t row_bytes = (size_t)a.Hkv * D;
-    auto load = [&](bool v, int ch, int j, const int4& rows) {
-        const int gi = wid + 3 * j;
-        if (gi >= 32) return;
-        int row, col;
-        place(v, ch, gi, row, col);
-        const int x = __shfl_sync(0xffffffffu, row, 0) / 32;        // uniform: a group lies within 32 rows
-        const int have = x == 0 ? rows.x : (x == 1 ? rows.y : (x == 2 ? rows.z : rows.w));
-        const int src = __shfl_sync(0xffffffffu, have, row % 32);
-        uint4 d = make_uint4(0u, 0u, 0u, 0u);
-        if (src >= 0)
-            d = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(v ? a.v_cache : a.k_cache) +
-                                                     (size_t)src * row_bytes + (size_t)hkv * D) + col);
-        buf[j][0] = d.x; buf[j][1] = d.y; buf[j][2] = d.z; buf[j][3] = d.w;
-    };
-    auto store = [&](bool v, int ch, int j, uint8_t* dst) {
-        const int gi = wid + 3 * j;
-        if (gi >= 32) return;
-        int row, col;
-        place(v, ch, gi, row, col);
-        const int lr = v ? row % C::VKEYS : row;
-        const int c16 = 2 * (v ? col : col % 8);
-        uint8_t* p = dst + (lr / 8) * (v ? C::V_GROUP : C::K_GROUP) + (c16 >> 3) * 1024 + (lr % 8) * 128;
-        uint32_t h[8];
+    auto store = [&](uint8_t* dst) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(buf[j][e], h[2 * e], h[2 * e + 1]);
-        const uint4 even = make_uint4(h[0], h[1], h[2], h[3]), odd = make_uint4(h[4], h[5], h[6], h[7]);
-        const int sw = (lane >> 2) & 1;
-        const int q0 = (c16 + sw) & 7, q1 = (c16 + 1 - sw) & 7;
-        *reinterpret_cast<uint4*>(p + ((q0 ^ (lr % 8)) << 4)) = sw ? odd : even;
-        *reinterpret_cast<uint4*>(p + ((q1 ^ (lr % 8)) << 4)) = sw ? even : odd;
-    };
-    // Widens the slot held in buf while loading the next one of the stream.
-    auto turn = [&](bool v, int ch, bool more, bool nv, int nch, const int4& nrows) -> bool {
-        const int s = nc % C::NS;
-        if (!__all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * s, ((nc / C::NS) & 1) ^ 1, abort_flag))) return false;
-        uint8_t* dst = smem + C::OFF_RING + s * SLOT;
+        for (int j = 0; j < NL; ++j) {
+            if (32 % TEAM && j == NL - 1 && wid + TEAM * j >= 32) break;
+            uint32_t h[8];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            store(v, ch, j, dst);
-            if (more) load(nv, nch, j, nrows);
+            for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(buf[j][e], h[2 * e], h[2 * e + 1]);
+            const uint4 even = make_uint4(h[0], h[1], h[2], h[3]), odd = make_uint4(h[4], h[5], h[6], h[7]);
+            const uint32_t p = STEP % 8 == 0 ? to + j * (STEP / 8) * GROUP : place(j * STEP + row0);
+            *reinterpret_cast<uint4*>(dst + p) = sw ? odd : even;
+            *reinterpret_cast<uint4*>(dst + (p ^ 16)) = sw ? even : odd;
         }
-        fence_proxy_async_smem();                 // the tensor core reads what the warp wrote
-        __syncwarp();
-        if (lane == 0) mbar_arrive(r_full0 + 8u * s);
-        ++nc;
-        return true;
     };
 
     const int c = n_tiles - first;
-    // cache rows of tiles i, i + 1 and i + 2: lane l holds keys l + 32 x
-    int4 rows_v = find_rows(first), rows_k = make_int4(-1, -1, -1, -1), rows_n = rows_k;
-#pragma unroll
-    for (int j = 0; j < NG; ++j) load(false, 0, j, rows_v);
-    if (c > 1) rows_k = find_rows(first + 1);
-    // the Q block
-    if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
-    {
+    int4 rows = find_rows(first, true), rows_n = find_rows(first + 1, c > 1);
+    load(0, rows);
+    if constexpr (!V) {
+        if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
         const int n_rows = nq_rows * g;
-        for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += 96) {
-            const int r = idx / (D / 8), c8 = idx % (D / 8);
-            uint4 d = make_uint4(0u, 0u, 0u, 0u);
-            if (r < n_rows) {
-                d = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
-                                                         (((size_t)q_row0 + r / g) * a.Hq + hkv * g + r % g) * D) + c8);
-                if constexpr (!F16) {
-                    uint32_t* w = reinterpret_cast<uint32_t*>(&d);
+#pragma unroll 2
+        for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += TEAM * 32) {
+            const int r = idx / (D / 8), c8 = idx % (D / 8), rr = min(r, n_rows - 1);
+            uint32_t w[4];
+            ldg16_or_zero(w, static_cast<const uint16_t*>(a.q) +
+                                 (((size_t)q_row0 + rr / g) * a.Hq + hkv * g + rr % g) * D + 8 * c8, r < n_rows);
+            if constexpr (!F16) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-                }
+                for (int e = 0; e < 4; ++e)
+                    w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
             }
-            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) = d;
+            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         ++nq;
     }
-    // K of tile 0, then (K of tile i + 1, V of tile i) for each tile i
-    for (int ch = 0; ch < C::CK; ++ch) {
-        const bool last = ch + 1 == C::CK;
-        const bool v_next = last && c == 1;       // K of tile 1, or V of tile 0 when it is the only one
-        if (!turn(false, ch, true, v_next, last ? 0 : ch + 1, pick(last && c > 1, rows_k, rows_v))) return false;
-    }
     for (int i = 0; i < c; ++i) {
-        if (i + 2 < c) rows_n = find_rows(first + i + 2);
-        if (i + 1 < c)
-            for (int ch = 0; ch < C::CK; ++ch) {
-                const bool last = ch + 1 == C::CK;
-                if (!turn(false, ch, true, last, last ? 0 : ch + 1, pick(last, rows_v, rows_k))) return false;
-            }
-        for (int ch = 0; ch < C::CV; ++ch) {
-            const bool last = ch + 1 == C::CV;
-            // after V of tile i: K of tile i + 2, or V of tile i + 1 when that is the last tile
-            const bool k_next = last && i + 2 < c, v_last = last && i + 2 == c;
-            if (!turn(true, ch, !last || k_next || v_last, !k_next, last ? 0 : ch + 1,
-                      pick(!last, rows_v, pick(k_next, rows_n, rows_k))))
+        // the slots' order is K(0), then K(i + 1), V(i) for each tile i
+        const int pos = V ? min(2 * i + 2, 2 * c - 1) : max(2 * i - 1, 0);
+#pragma unroll
+        for (int ch = 0; ch < NCH; ++ch) {
+            const int n = nc + pos * NCH + ch, s = n % C::NS;
+            if (!__all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * s, ((n / C::NS) & 1) ^ 1, abort_flag)))
                 return false;
+            store(smem + C::OFF_RING + s * SLOT);
+            fence_proxy_async_smem();             // the tensor core reads what the warp wrote
+            __syncwarp();
+            if (lane == 0) mbar_arrive_n(r_full0 + 8u * s, kFill8 / TEAM);
+            // past the last tile: no row, no load
+            load(ch + 1 < NCH ? ch + 1 : 0, ch + 1 < NCH ? rows : rows_n);
         }
-        rows_v = rows_k;
-        rows_k = rows_n;
+        rows = rows_n;
+        rows_n = find_rows(first + min(i + 2, c), i + 2 < c);
     }
     return true;
 }
 
 template <int D, int MODE, bool OPTS, bool F16>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __launch_bounds__(num_threads(MODE), 1)
 onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                const PrefillArgs a, int n_qtiles) {
@@ -284,6 +277,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     using C = Cfg<D, MODE>;
     constexpr bool PACKED = MODE != kBSHD;
     constexpr bool KV8 = MODE == kPaged8;
+    constexpr int WMMA = KV8 ? WARP_MMA8 : WARP_MMA;
     constexpr bool MF16 = KV8 || F16;            // the MMAs' operand type is float16 (F16: the call's type)
     constexpr uint32_t IDESC_QK = make_idesc_16<MF16>(BM, BN, false, false);
     constexpr uint32_t IDESC_PV = make_idesc_16<MF16>(BM, D, false, true);
@@ -415,8 +409,8 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        constexpr int FILL = KV8 ? 3 : 1;           // arrivals that fill a slot: TMA, or one per widening warp
-        mbar_init(q_full, FILL);
+        constexpr int FILL = KV8 ? kFill8 : 1;      // arrivals that fill a slot: the widening team's, or TMA
+        mbar_init(q_full, KV8 ? TEAM_K8 : 1);
         mbar_init(q_empty, 1);
         for (int s = 0; s < C::NS; ++s) { mbar_init(r_full(s), FILL); mbar_init(r_empty(s), 1); }
         for (int k = 0; k < 2; ++k) { mbar_init(s_full(k), 1); mbar_init(p_full(k), BM); }
@@ -429,7 +423,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         for (int k = 0; k < 2; ++k) {
             mbar_init(item_full(k), 1);
             // the MMA warp, the eight softmax / epilogue warps, and the widening warps but the claiming one
-            mbar_init(item_empty(k), 1 + 8 + (KV8 ? 2 : 0));
+            mbar_init(item_empty(k), 1 + 8 + (KV8 ? TEAM_K8 + TEAM_V8 - 1 : 0));
         }
         *abort_flag = 0;
         fence_mbar_init();
@@ -444,7 +438,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         fence_proxy_async_smem();
     }
-    if (warp == WARP_MMA) {
+    if (warp == WMMA) {
         tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish();
     }
@@ -454,21 +448,27 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     const uint32_t tmem = *tmem_slot;
 
     if (warp >= WARP_LOAD) {
-        regs_dec<kRegsOther>();
-        if (KV8 && warp != WARP_MMA) {
+        regs_dec<KV8 ? kRegsOther8 : kRegsOther>();
+        if (KV8 && warp != WMMA) {
             if constexpr (KV8) {
-                const int wid = warp == WARP_LOAD ? 0 : warp - WARP_MMA;      // 0, 1, 2
-                const uint32_t ring_bar = r_full(0), ring_free = r_empty(0);
-                int nc = 0, nq = 0;
+                const bool team_v = warp >= WARP_V8;
+                const int wid = warp % 4;
+                int nc = 0, nq = 0;                 // ring slots and Q blocks of the items so far
                 for (int r = 0;; ++r) {
-                    const int w = wid == 0 ? claim_item(r) : next_item(r);
+                    const int w = warp == WARP_LOAD ? claim_item(r) : next_item(r);
                     if (w < 0) break;
                     const Item it = describe(w);
                     if (it.t.n_tiles == it.first) continue;
-                    if (!fp8_item<D, F16, C>(a, smem, ring_bar, ring_free, q_full, q_empty, abort_flag, it.b, it.hkv,
-                                             it.qs + it.t.q0, it.t.rows_valid, it.skv, it.first, it.t.n_tiles, g, wid,
-                                             lane, nc, nq))
-                        break;
+                    const int q_row = it.qs + it.t.q0;
+                    const bool done =
+                        team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(0), r_empty(0), q_full, q_empty, abort_flag,
+                                                           it.b, it.hkv, q_row, it.t.rows_valid, it.skv, it.first,
+                                                           it.t.n_tiles, g, wid, lane, nc, nq)
+                               : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
+                                                            abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
+                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq);
+                    if (!done) break;
+                    nc += 2 * C::CK * (it.t.n_tiles - it.first);
                 }
             }
         } else if (!KV8 && warp == WARP_LOAD) {
@@ -658,7 +658,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
             }
-        } else if (warp == WARP_MMA) {
+        } else if (warp == WMMA) {
             // ------------------------------------------------------------ MMA issuer
             // Lane 0 alone issues every MMA of an item but its last P V (a
             // single polling lane keeps the issue loop short); the whole warp
@@ -944,7 +944,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         named_bar_arrive(2, 8 * 32 + 32);
     } else {
-        regs_dec<kRegsEpi>();
+        regs_dec<KV8 ? kRegsEpi8 : kRegsEpi>();
         // ------------------------------------------------------------ epilogue warps 4-7
         const int r = (warp - WARP_EPI0) * 32 + lane;
         const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
@@ -992,7 +992,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // end is written row by row (its box would reach the next request).
             // The choice is the same for every thread of the item.
             const bool boxed = !PACKED || ti.rows_valid == qpb;
-            constexpr int HALF = D < 128 ? D : 128;     // O columns read per pass
+            constexpr int HALF = KV8 || D < 128 ? 64 : 128;     // O columns read per pass
             // O / l packed to 16 bits, HALF columns at a time; O is free once the
             // last columns are read
             auto read_o = [&](int half, uint32_t* ow) {
@@ -1082,7 +1082,7 @@ cudaError_t launch_onetile(const CUtensorMap& tm_q, const CUtensorMap& tm_k, con
     const long sms = a.num_sms > 0 ? a.num_sms : 148;
     const long grid = max_items < sms ? max_items : sms;    // persistent: one CTA per SM
     if (grid <= 0) return cudaSuccess;
-    onetile_kernel<D, MODE, OPTS, F16><<<(unsigned)grid, NUM_THREADS, C::SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v,
+    onetile_kernel<D, MODE, OPTS, F16><<<(unsigned)grid, num_threads(MODE), C::SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v,
                                                                                               tm_o, a, n_qtiles);
     return cudaGetLastError();
 }
