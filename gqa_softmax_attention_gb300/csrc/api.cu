@@ -589,6 +589,10 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
         a.q = q;
         a.k_scale = k_scale;
         a.v_scale = v_scale;
+        // division by a constant as a multiplication (Granlund and Montgomery,
+        // "Division by Invariant Integers using Multiplication", 1994)
+        while ((1L << a.ps_shift) < page_size) ++a.ps_shift;
+        a.ps_mul = (uint32_t)(((1ull << 32) * ((1ull << a.ps_shift) - page_size)) / page_size + 1);
     } else if (page_size % 8 == 0) {
         // pages move as 8-row TMA blocks
         a.bt_k = gcd_int(page_size, 128);

@@ -50,6 +50,7 @@ struct PrefillArgs {
     const float* k_scale;
     const float* v_scale;
     const void* q;            // [total_q, Hq, D]: its rows are read by plain loads there
+    uint32_t ps_mul, ps_shift;   // n / page_size = (umulhi(n, ps_mul) + n) >> ps_shift for 0 <= n < 2^31
 };
 
 // Launches the tcgen05 prefill kernel.  The tensor maps describe q, k, v as

@@ -142,8 +142,7 @@ constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
 // 128-byte stretch of a cache row goes to eight lanes, 16 bytes each, so a
 // warp's load covers 512 bytes, and a slot takes 32 of them.  The loads of the
 // next slot are issued when this one's are widened and stored: their latency
-// runs beside the wait for the slot.  Rows past the request's end and pages
-// outside the pool give zeros.  The lane's 16 codes become two 16-byte chunks
+// runs beside the wait for the slot.  The lane's 16 codes become two 16-byte chunks
 // of the swizzled tile; lanes 4-7 of eight write the odd chunk first, so that
 // the eight lanes of a store cover eight different bank groups.  Nothing here
 // may spill: the streaming loads evict local memory from the small L1 beside
@@ -175,38 +174,63 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     const uint8_t* cache = static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + (size_t)hkv * D + 16 * col;
     const uint32_t row_bytes = (uint32_t)a.Hkv * D;
     const int32_t* table = a.table + (size_t)b * a.max_pages;
-    // No load stands in a branch: what a branch loads may be moved to its
-    // register at the branch's end, which waits out the load's latency.
-    // Cache rows of a tile: lane l holds keys l, l + 32, l + 64, l + 96 (-1: no row).
-    auto find_rows = [&](int tile, bool any) -> int4 {
-        int r[4], page[4];
+    // Keys of a tile, lane l holding l, l + 32, l + 64 and l + 96: their pages
+    // and places in them; and, once the pages have arrived, their cache rows.  A
+    // key past the request's end takes the last key's row (its score is masked
+    // and its weight 0), one of a page outside the pool row 0, marked to be
+    // zeroed.  No load stands in a branch: what a branch loads may be moved to
+    // its register at the branch's end, which waits out the load's latency.
+    struct Pages {
+        int page[4], off[4];
+    };
+    auto find_pages = [&](int tile) -> Pages {
+        Pages p;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            r[x] = tile * BN + 32 * x + lane;
-            page[x] = __ldg(table + min(r[x], skv - 1) / a.page_size);
+            const uint32_t key = (uint32_t)min(tile * BN + 32 * x + lane, skv - 1);
+            const uint32_t n = (__umulhi(key, a.ps_mul) + key) >> a.ps_shift;       // key / page_size
+            p.page[x] = ldg_int(table + n);
+            p.off[x] = (int)(key - n * (uint32_t)a.page_size);
         }
+        return p;
+    };
+    uint32_t bad[4];                               // keys of the tile (32 a word) to be zeroed
+    auto find_rows = [&](const Pages& p) -> int4 {
+        int r[4];
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-            r[x] = any && r[x] < skv && page[x] >= 0 && page[x] < a.num_pages
-                       ? page[x] * a.page_size + r[x] % a.page_size : -1;
+        for (int x = 0; x < 4; ++x) {
+            const bool in = (uint32_t)p.page[x] < (uint32_t)a.num_pages;
+            bad[x] = __ballot_sync(0xffffffffu, !in);
+            r[x] = in ? p.page[x] * a.page_size + p.off[x] : 0;
+        }
         return make_int4(r[0], r[1], r[2], r[3]);
     };
     uint32_t buf[NL][4];
     auto load = [&](int ch, const int4& rows) {
         auto part = [&](int x) { return x == 0 ? rows.x : (x == 1 ? rows.y : (x == 2 ? rows.z : rows.w)); };
+        int src[NL];
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             const int at = (WIDE ? 64 * ch : 0) + j * STEP;             // + row0 < STEP: the lane's row of the tile
-            int src = __shfl_sync(0xffffffffu, part(at / 32), at % 32 + row0);
+            src[j] = __shfl_sync(0xffffffffu, part(at / 32), at % 32 + row0);
             if (at % 32 + STEP > 32 && at < 96) {                       // the warps' rows straddle two parts
                 const int next = __shfl_sync(0xffffffffu, part(at / 32 + 1), at % 32 + row0);
-                src = at % 32 + row0 >= 32 ? next : src;
+                src[j] = at % 32 + row0 >= 32 ? next : src[j];
             }
-            if (32 % TEAM && j == NL - 1 && wid + TEAM * j >= 32) src = -1;
-            ldg16_or_zero(buf[j], cache + (size_t)max(src, 0) * row_bytes + (D == 256 && !V ? 128 * ch : 0), src >= 0);
         }
+#pragma unroll
+        for (int j = 0; j < NL; ++j)               // a team's surplus load repeats some row, and is not stored
+            ldg16(buf[j], cache + (size_t)(uint32_t)src[j] * row_bytes + (D == 256 && !V ? 128 * ch : 0));
     };
-    auto store = [&](uint8_t* dst) {
+    auto store = [&](int ch, uint8_t* dst) {
+        if (bad[0] | bad[1] | bad[2] | bad[3]) {   // uniform; pages outside the pool
+#pragma unroll
+            for (int j = 0; j < NL; ++j) {
+                const int r = (WIDE ? 64 * ch : 0) + j * STEP + row0, x = r / 32;
+                const uint32_t w = x == 0 ? bad[0] : (x == 1 ? bad[1] : (x == 2 ? bad[2] : bad[3]));
+                if ((w >> (r % 32)) & 1u) buf[j][0] = buf[j][1] = buf[j][2] = buf[j][3] = 0u;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
             if (32 % TEAM && j == NL - 1 && wid + TEAM * j >= 32) break;
@@ -221,8 +245,9 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     };
 
     const int c = n_tiles - first;
-    int4 rows = find_rows(first, true), rows_n = find_rows(first + 1, c > 1);
+    int4 rows = find_rows(find_pages(first));
     load(0, rows);
+    Pages pages = find_pages(first + 1);          // a tile ahead of their use
     if constexpr (!V) {
         if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
         const int n_rows = nq_rows * g;
@@ -253,15 +278,14 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
             const int n = nc + pos * NCH + ch, s = n % C::NS;
             if (!__all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * s, ((n / C::NS) & 1) ^ 1, abort_flag)))
                 return false;
-            store(smem + C::OFF_RING + s * SLOT);
+            store(ch, smem + C::OFF_RING + s * SLOT);
             fence_proxy_async_smem();             // the tensor core reads what the warp wrote
             __syncwarp();
             if (lane == 0) mbar_arrive_n(r_full0 + 8u * s, kFill8 / TEAM);
-            // past the last tile: no row, no load
-            load(ch + 1 < NCH ? ch + 1 : 0, ch + 1 < NCH ? rows : rows_n);
+            if (ch + 1 == NCH) rows = find_rows(pages);
+            load(ch + 1 < NCH ? ch + 1 : 0, rows);           // past the last tile: the last key's row again
         }
-        rows = rows_n;
-        rows_n = find_rows(first + min(i + 2, c), i + 2 < c);
+        pages = find_pages(first + i + 2);
     }
     return true;
 }

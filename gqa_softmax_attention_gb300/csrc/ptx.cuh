@@ -456,7 +456,21 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     else return pack_bf16x2(lo, hi);
 }
 
-// 16 bytes of read-only global memory, or zeros without a load where !ok.
+// A read-only 32-bit load that stays where it stands.
+__device__ __forceinline__ int ldg_int(const int* p) {
+    int v;
+    asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// 16 bytes of read-only global memory that will not be read again from L1.
+__device__ __forceinline__ void ldg16(uint32_t* r, const void* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p));
+}
+
+// The same, or zeros without a load where !ok.
 __device__ __forceinline__ void ldg16_or_zero(uint32_t* r, const void* p, bool ok) {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
