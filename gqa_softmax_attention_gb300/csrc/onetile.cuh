@@ -154,7 +154,7 @@ template <int D, bool F16, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t r_full0, uint32_t r_empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
                                          int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
-                                         int lane, int nc, int& nq) {
+                                         int lane, int nc, int& nq, int& last) {
     static_assert(C::CV == C::CK, "slot positions");
     constexpr int NCH = C::CK;                    // slots per tile
     constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
@@ -276,8 +276,18 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
 #pragma unroll
         for (int ch = 0; ch < NCH; ++ch) {
             const int n = nc + pos * NCH + ch, s = n % C::NS;
-            if (!__all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * s, ((n / C::NS) & 1) ^ 1, abort_flag)))
-                return false;
+            // A parity tells a slot's uses apart only one apart: the use before
+            // the awaited one must have been released.  Slots are released in
+            // order, so a team's waits may lie NS positions apart at most; where
+            // the other team's positions make a wider gap, wait in between.
+            bool free = true;
+            for (int p = last + C::NS; p < n + C::NS && free; p += C::NS) {
+                const int w = min(p, n);
+                free = __all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * (w % C::NS), ((w / C::NS) & 1) ^ 1,
+                                                         abort_flag));
+            }
+            if (!free) return false;
+            last = n;
             store(ch, smem + C::OFF_RING + s * SLOT);
             fence_proxy_async_smem();             // the tensor core reads what the warp wrote
             __syncwarp();
@@ -478,6 +488,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const bool team_v = warp >= WARP_V8;
                 const int wid = warp % 4;
                 int nc = 0, nq = 0;                 // ring slots and Q blocks of the items so far
+                int last = -1;                      // position of the team's last slot
                 for (int r = 0;; ++r) {
                     const int w = warp == WARP_LOAD ? claim_item(r) : next_item(r);
                     if (w < 0) break;
@@ -487,10 +498,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const bool done =
                         team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(0), r_empty(0), q_full, q_empty, abort_flag,
                                                            it.b, it.hkv, q_row, it.t.rows_valid, it.skv, it.first,
-                                                           it.t.n_tiles, g, wid, lane, nc, nq)
+                                                           it.t.n_tiles, g, wid, lane, nc, nq, last)
                                : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
                                                             abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq);
+                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq, last);
                     if (!done) break;
                     nc += 2 * C::CK * (it.t.n_tiles - it.first);
                 }
