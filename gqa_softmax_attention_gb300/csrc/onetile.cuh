@@ -96,7 +96,6 @@ constexpr int NUM_THREADS8 = 512;
 constexpr int WARP_V8 = 12;
 constexpr int WARP_MMA8 = 15;
 constexpr int TEAM_K8 = 4, TEAM_V8 = 3;        // warps of a widening team
-constexpr int kFill8 = TEAM_K8 * TEAM_V8;      // arrivals that fill a ring slot, whichever team fills it
 constexpr int kRegsEpi8 = 96;
 constexpr int kRegsOther8 = 104;
 static_assert((kRegsSoftmax + kRegsEpi8 + 2 * kRegsOther8) * 128 <= 128 * NUM_THREADS8, "register split");
@@ -121,6 +120,11 @@ struct Cfg {
     static constexpr int V_SLICE = GROUPED ? 1024 : VKEYS * 128;
     static constexpr int V_GROUP = GROUPED ? KSL * 1024 : 1024;
     static constexpr int NS = D == 256 ? 4 : 5;         // ring slots
+    // kPaged8: two rings, slots [0, NK8) for keys and [NK8, NS) for values, each
+    // filled by one team: with one ring, a team could come to a slot whose use
+    // before last was still to be released, and a parity would not tell.  V P
+    // follows its keys' S by a tile, so values get the odd slot.
+    static constexpr int NK8 = 2, NV8 = NS - NK8;
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_RING = OFF_Q + KSL * BOX;
     static constexpr int OFF_STAGE = OFF_RING + NS * SLOT;   // 2 output boxes
@@ -151,12 +155,12 @@ constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
 // The key team also writes the Q block (rows q_row0 .. of the packed batch,
 // packed r = query * g + head, bfloat16 rounded to float16), zeros past it.
 template <int D, bool F16, class C, bool V>
-__device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t r_full0, uint32_t r_empty0,
+__device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t full0, uint32_t empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
                                          int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
-                                         int lane, int nc, int& nq, int& last) {
-    static_assert(C::CV == C::CK, "slot positions");
-    constexpr int NCH = C::CK;                    // slots per tile
+                                         int lane, int& nc, int& nq) {
+    constexpr int NCH = V ? C::CV : C::CK;        // slots per tile
+    constexpr int NR = V ? C::NV8 : C::NK8;       // slots of this team's ring
     constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
     constexpr int LPR = WIDE ? 16 : 8;            // lanes per row
     constexpr int TEAM = V ? TEAM_V8 : TEAM_K8;
@@ -271,27 +275,14 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
         ++nq;
     }
     for (int i = 0; i < c; ++i) {
-        // the slots' order is K(0), then K(i + 1), V(i) for each tile i
-        const int pos = V ? min(2 * i + 2, 2 * c - 1) : max(2 * i - 1, 0);
 #pragma unroll
-        for (int ch = 0; ch < NCH; ++ch) {
-            const int n = nc + pos * NCH + ch, s = n % C::NS;
-            // A parity tells a slot's uses apart only one apart: the use before
-            // the awaited one must have been released.  Slots are released in
-            // order, so a team's waits may lie NS positions apart at most; where
-            // the other team's positions make a wider gap, wait in between.
-            bool free = true;
-            for (int p = last + C::NS; p < n + C::NS && free; p += C::NS) {
-                const int w = min(p, n);
-                free = __all_sync(0xffffffffu, mbar_wait(r_empty0 + 8u * (w % C::NS), ((w / C::NS) & 1) ^ 1,
-                                                         abort_flag));
-            }
-            if (!free) return false;
-            last = n;
-            store(ch, smem + C::OFF_RING + s * SLOT);
+        for (int ch = 0; ch < NCH; ++ch, ++nc) {
+            const int s = nc % NR;
+            if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8u * s, ((nc / NR) & 1) ^ 1, abort_flag))) return false;
+            store(ch, smem + C::OFF_RING + ((V ? C::NK8 : 0) + s) * SLOT);
             fence_proxy_async_smem();             // the tensor core reads what the warp wrote
             __syncwarp();
-            if (lane == 0) mbar_arrive_n(r_full0 + 8u * s, kFill8 / TEAM);
+            if (lane == 0) mbar_arrive(full0 + 8u * s);
             if (ch + 1 == NCH) rows = find_rows(pages);
             load(ch + 1 < NCH ? ch + 1 : 0, rows);           // past the last tile: the last key's row again
         }
@@ -443,10 +434,12 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        constexpr int FILL = KV8 ? kFill8 : 1;      // arrivals that fill a slot: the widening team's, or TMA
         mbar_init(q_full, KV8 ? TEAM_K8 : 1);
         mbar_init(q_empty, 1);
-        for (int s = 0; s < C::NS; ++s) { mbar_init(r_full(s), FILL); mbar_init(r_empty(s), 1); }
+        for (int s = 0; s < C::NS; ++s) {
+            mbar_init(r_full(s), !KV8 ? 1 : (s < C::NK8 ? TEAM_K8 : TEAM_V8));     // TMA, or the widening team
+            mbar_init(r_empty(s), 1);
+        }
         for (int k = 0; k < 2; ++k) { mbar_init(s_full(k), 1); mbar_init(p_full(k), BM); }
         mbar_init(o_ready, 1);
         mbar_init(o_final, 1);
@@ -487,8 +480,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if constexpr (KV8) {
                 const bool team_v = warp >= WARP_V8;
                 const int wid = warp % 4;
-                int nc = 0, nq = 0;                 // ring slots and Q blocks of the items so far
-                int last = -1;                      // position of the team's last slot
+                int nc = 0, nq = 0;                 // slots of the team's ring and Q blocks filled
                 for (int r = 0;; ++r) {
                     const int w = warp == WARP_LOAD ? claim_item(r) : next_item(r);
                     if (w < 0) break;
@@ -496,14 +488,13 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (it.t.n_tiles == it.first) continue;
                     const int q_row = it.qs + it.t.q0;
                     const bool done =
-                        team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(0), r_empty(0), q_full, q_empty, abort_flag,
-                                                           it.b, it.hkv, q_row, it.t.rows_valid, it.skv, it.first,
-                                                           it.t.n_tiles, g, wid, lane, nc, nq, last)
+                        team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(C::NK8), r_empty(C::NK8), q_full, q_empty,
+                                                           abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
+                                                           it.first, it.t.n_tiles, g, wid, lane, nc, nq)
                                : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
                                                             abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq, last);
+                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq);
                     if (!done) break;
-                    nc += 2 * C::CK * (it.t.n_tiles - it.first);
                 }
             }
         } else if (!KV8 && warp == WARP_LOAD) {
@@ -699,31 +690,42 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // single polling lane keeps the issue loop short); the whole warp
             // takes the last P V, whose value rows past the request's end it
             // zeroes first (packed layouts).
-            int nc = 0, nq = 0;     // ring chunks and Q blocks consumed
+            int nc = 0, nq = 0;     // ring chunks (kPaged8: of the key ring) and Q blocks consumed
+            int nv = 0;             // kPaged8: chunks of the value ring consumed
             int g_t = 0;            // visited tiles of earlier items (S buffer / p_full parity)
             int oe = 0;             // o_empty phases waited
             bool ok = true;
-            auto chunk_addr = [&](int k) { return sb + C::OFF_RING + ((nc + k) % C::NS) * SLOT; };
-            auto take = [&](int n) -> bool {        // lane 0: the next n ring chunks have landed
+            // slot and phase of the k-th next chunk (v: of values)
+            auto slot_of = [&](bool v, int k) -> int {
+                if constexpr (KV8) return v ? C::NK8 + (nv + k) % C::NV8 : (nc + k) % C::NK8;
+                else return (nc + k) % C::NS;
+            };
+            auto phase_of = [&](bool v, int k) -> uint32_t {
+                if constexpr (KV8) return (v ? (nv + k) / C::NV8 : (nc + k) / C::NK8) & 1;
+                else return ((nc + k) / C::NS) & 1;
+            };
+            auto chunk_addr = [&](bool v, int k) { return sb + C::OFF_RING + slot_of(v, k) * SLOT; };
+            auto take = [&](bool v, int n) -> bool {        // lane 0: the next n ring chunks have landed
                 for (int k = 0; k < n; ++k)
-                    if (!mbar_wait(r_full((nc + k) % C::NS), ((nc + k) / C::NS) & 1, abort_flag)) return false;
+                    if (!mbar_wait(r_full(slot_of(v, k)), phase_of(v, k), abort_flag)) return false;
                 tc_fence_after();
                 return true;
             };
-            auto release = [&](int n) {             // lane 0
-                for (int k = 0; k < n; ++k) mma_commit(r_empty((nc + k) % C::NS));
-                nc += n;
+            auto release = [&](bool v, int n) {             // lane 0
+                for (int k = 0; k < n; ++k) mma_commit(r_empty(slot_of(v, k)));
+                if (KV8 && v) nv += n;
+                else nc += n;
             };
             // S of visited tile gi = Q K^T over D / 16 steps of 16 columns (lane 0)
             auto issue_qk = [&](int gi) -> bool {
-                if (!take(C::CK)) return false;
+                if (!take(false, C::CK)) return false;
                 const uint32_t d = tmem + COL_S0 + (gi & 1) * BN;
                 // descriptors of the Q tile and of each K chunk, advanced by
                 // constant offsets (>> 4) per step
                 const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
                 uint64_t kdesc[C::CK];
 #pragma unroll
-                for (int c = 0; c < C::CK; ++c) kdesc[c] = make_sdesc_sw128(chunk_addr(c), 16, C::K_GROUP);
+                for (int c = 0; c < C::CK; ++c) kdesc[c] = make_sdesc_sw128(chunk_addr(false, c), 16, C::K_GROUP);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     constexpr int PER = D / 16 / C::CK;       // steps per K chunk
@@ -733,7 +735,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mma_bf16_ss(d, qdesc + (qoff >> 4), kdesc[kk / PER] + (koff >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(s_full(gi & 1));
-                release(C::CK);
+                release(false, C::CK);
                 return true;
             };
             // O (+)= P V of visited tile gi: 8 steps of 16 keys (lane 0)
@@ -741,7 +743,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const uint32_t p = tmem + COL_S0 + (gi & 1) * BN;
                 uint64_t vdesc[C::CV];
 #pragma unroll
-                for (int c = 0; c < C::CV; ++c) vdesc[c] = make_sdesc_sw128(chunk_addr(c), C::V_SLICE, C::V_GROUP);
+                for (int c = 0; c < C::CV; ++c) vdesc[c] = make_sdesc_sw128(chunk_addr(true, c), C::V_SLICE, C::V_GROUP);
 #pragma unroll
                 for (int kk = 0; kk < BN / 16; ++kk) {
                     constexpr int PER = BN / 16 / C::CV;       // steps per V chunk
@@ -749,12 +751,12 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mma_bf16_ts(tmem + COL_O, p + kk * 8, vdesc[kk / PER] + (((kc / 8) * C::V_GROUP) >> 4), IDESC_PV,
                                 (!fresh || kk > 0) ? 1u : 0u);
                 }
-                release(C::CV);
+                release(true, C::CV);
                 mma_commit(o_ready);
             };
             auto issue_pv = [&](int gi, bool fresh) -> bool {      // lane 0
                 if (!mbar_wait(p_full(gi & 1), (gi >> 1) & 1, abort_flag)) return false;
-                if (!take(C::CV)) return false;
+                if (!take(true, C::CV)) return false;
                 mma_pv(gi, fresh);
                 return true;
             };
@@ -806,7 +808,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                 const int key = nvalid + idx / (8 * C::KSL);
                                 const int s = (idx / 8) % C::KSL, q = idx % 8;
                                 const int kc = key % C::VKEYS;
-                                const uint32_t off = chunk_addr(key / C::VKEYS) - sb + s * C::V_SLICE +
+                                const uint32_t off = chunk_addr(true, key / C::VKEYS) - sb + s * C::V_SLICE +
                                                      (kc / 8) * C::V_GROUP + (kc % 8) * 128 + q * 16;
                                 *reinterpret_cast<uint4*>(smem + off) = make_uint4(0u, 0u, 0u, 0u);
                             }
