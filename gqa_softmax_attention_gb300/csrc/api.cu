@@ -626,7 +626,7 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
     if (side) a.g_eff = ws + 2;
     if (gqa::launch_varlen_plan(cu_seqlens_q, cache_seqlens, true, B, a.qpb, a.g, a.causal, total_q,
                                 (long)max_pages * page_size, ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e,
-                                s, route, false, side ? a.num_sms : 0) != cudaSuccess)
+                                s, route, false, side ? a.num_sms : 0, fp8) != cudaSuccess)
         return GQA_ERR_CUDA;
     const long items = (long)max_e * Hkv;
     auto launch_chunks = [&](cudaStream_t on) {

@@ -86,11 +86,11 @@ int prefill_d256_take_device_error();
 // two-Q-tile kernel.  With skip_single, n_entries[2] receives how many of
 // `grid` persistent CTAs the listed blocks should keep so that they and the
 // left-out decode steps, run at the same time, end together (grid when there
-// is no decode step).
+// is no decode step); fp8: the caches are e4m3 bytes.
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single = false, bool pairs = false,
-                               int grid = 0);
+                               int grid = 0, bool fp8 = false);
 // tm_q / tm_o: {D, Hq, total_q} with a {64, g, qpb} box.  Packed: tm_k / tm_v
 // {D, Hkv, total_kv} with {64, 1, 128} and {64, 1, 128 or 64 (D = 256)} boxes.
 // Paged: the caches as {64, 8, D / 64, pages * page_size / 8, Hkv} with

@@ -12,11 +12,14 @@
 // its heads.  Sums and products are FP32, rounded once to the output's type.
 //
 // Bound by HBM: every head row is read once and written once.  D / 8 lanes
-// share a row, 16 bytes each; a warp holds 32 / (D / 8) rows at a time and
-// loads U of those ahead before it reduces the first.  A warp's rows are of one
-// kind (queries, keys or values), so nothing diverges.  The mate of a lane's
-// chunk sits rot / 16 lanes away (rot a multiple of 16) and comes by shuffle as
-// packed 16-bit pairs, before the norm is applied.
+// share a row; a lane holds two pieces of four values, chosen so that the mates
+// of a piece lie in the lane itself: pieces 4l and rot/2 + 4l (mates in the
+// other piece), or 4l and D/2 + 4l interleaved (mates in the same piece), so
+// that only the sum of squares crosses lanes, and each load of a warp still
+// covers whole 64-byte stretches.  A warp holds 32 / (D / 8) rows at a time
+// and loads U of those ahead before it works on U; its rows are of one kind
+// (queries, keys or values), so nothing diverges.  Arithmetic goes in pairs
+// (f32x2).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,20 +34,25 @@ constexpr int U = 4;               // row groups a warp loads ahead
 
 enum Kind : int { kQ = 0, kK = 1, kV = 2 };
 
+// Two 16-bit values -> a pair of floats.
 template <bool F16>
-__device__ __forceinline__ void unpack8(const uint4& v, float* f) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (F16) {
-            const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-            f[2 * i] = p.x;
-            f[2 * i + 1] = p.y;
-        } else {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-        }
+__device__ __forceinline__ uint64_t widen2(uint32_t w) {
+    if constexpr (F16) {
+        const float2 p = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        return f32x2(p.x, p.y);
+    } else {
+        return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
+}
+__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t swap2(uint64_t v) {
+    float lo, hi;
+    f32x2_split(v, lo, hi);
+    return f32x2(hi, lo);
 }
 
 // Two FP32 values -> two e4m3fn codes (round to nearest even, +-448 beyond the
@@ -55,33 +63,38 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-template <bool F16>
-__device__ __forceinline__ uint4 pack8(const float* f) {
-    return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
+// y / s given inv, the rounded 1 / s: the product corrected by its remainder
+// (Markstein 1990), which is the rounded quotient where it matters; beyond the
+// e4m3 range, where the remainder could overflow, the product alone.  Scales
+// whose reciprocal leaves the normal range are divided by.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+    if (s < 0x1p-120f || s > 0x1p120f) return __fdiv_rn(y, s);
+    const float q = y * inv;
+    const float c = fmaf(fmaf(-q, s, y), inv, q);
+    return fabsf(q) < 1024.f ? c : q;
 }
 
-// Eight weights of dims d .. d + 7 (ones without a norm).
+// Four weights of dims d .. d + 3 (ones without a norm).
 template <bool F16>
 __device__ __forceinline__ void load_w(const void* w, int f32, int d, float* out) {
     if (!w) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) out[i] = 1.f;
+        out[0] = out[1] = out[2] = out[3] = 1.f;
     } else if (f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(w) + d);
-        const float4 x = __ldg(p), y = __ldg(p + 1);
+        const float4 x = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + d));
         out[0] = x.x; out[1] = x.y; out[2] = x.z; out[3] = x.w;
-        out[4] = y.x; out[5] = y.y; out[6] = y.z; out[7] = y.w;
     } else {
-        unpack8<F16>(__ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(w) + d)), out);
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(w) + d));
+        f32x2_split(widen2<F16>(x.x), out[0], out[1]);
+        f32x2_split(widen2<F16>(x.y), out[2], out[3]);
     }
 }
 
-template <int D, bool F16, bool PAGED>
+template <int D, bool F16, bool PAGED, bool NEXT>
 __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int nq, int nk, int rows_per_warp) {
     constexpr int LPH = D / 8;              // lanes per head row
     constexpr int HPW = 32 / LPH;           // rows of a warp at a time
     const int lane = threadIdx.x % 32;
-    const int c = lane % LPH, sub = lane / LPH;
+    const int l = lane % LPH, sub = lane / LPH;
     const long task = (long)blockIdx.x * (NT / 32) + threadIdx.x / 32;
     const int per_token = nq + nk + (PAGED ? nk : 0);
     const long t = task / per_token;
@@ -92,147 +105,195 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
     const int H = kind == kQ ? a.Hq : a.Hkv;
     const int h_end = min(H, h0 + rows_per_warp);
 
-    long slot = 0;
-    float kv_scale = 1.f;
-    const float* scales = nullptr;
-    int req = 0;
-    if constexpr (PAGED) {
-        slot = a.slots[t];
-        if (slot < 0 || slot >= a.num_slots) return;       // a padding row
-        if (a.k_scale || a.v_scale) {
-            req = a.requests[t];
-            if (req < 0 || req >= a.B) return;
-            scales = kind == kQ ? nullptr : (kind == kK ? a.k_scale : a.v_scale);
-        }
-    }
-    const uint16_t* src = static_cast<const uint16_t*>(kind == kQ ? a.q : (kind == kK ? a.k : a.v)) +
-                          t * (kind == kQ ? a.q_ts : (kind == kK ? a.k_ts : a.v_ts)) + 8 * c;
-    const long hs = kind == kQ ? a.q_hs : (kind == kK ? a.k_hs : a.v_hs);
+    // this lane's two pieces
+    const int pairs = a.rot / 8;            // lanes that hold rotated pieces (mates in halves)
+    const int p0 = NEXT ? 4 * l : (l < pairs ? 4 * l : a.rot + 8 * (l - pairs));
+    const int p1 = NEXT ? D / 2 + 4 * l : (l < pairs ? a.rot / 2 + 4 * l : p0 + 4);
+    const bool rot0 = p0 < a.rot, rot1 = p1 < a.rot;
 
-    uint4 raw[U];
+    const uint16_t* src = static_cast<const uint16_t*>(kind == kQ ? a.q : (kind == kK ? a.k : a.v)) +
+                          t * (kind == kQ ? a.q_ts : (kind == kK ? a.k_ts : a.v_ts));
+    const long hs = kind == kQ ? a.q_hs : (kind == kK ? a.k_hs : a.v_hs);
+    uint2 raw[U][2];
     auto load = [&](int h) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int hh = h + u * HPW + sub;
-            raw[u] = hh < h_end ? *reinterpret_cast<const uint4*>(src + hh * hs) : make_uint4(0u, 0u, 0u, 0u);
+            const int hh = min(h + u * HPW + sub, h_end - 1);      // a surplus row repeats the last, and is not stored
+            raw[u][0] = *reinterpret_cast<const uint2*>(src + hh * hs + p0);
+            raw[u][1] = *reinterpret_cast<const uint2*>(src + hh * hs + p1);
         }
     };
     load(h0);
+    long slot = 0;
+    int req = 0;
+    if constexpr (PAGED) {
+        slot = a.slots[t];
+        if (a.k_scale || a.v_scale) req = a.requests[t];
+    }
+    int pos[4] = {0, 0, 0, 0};
+    if (kind != kV && a.rot > 0) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+            if (x < a.n_axes) pos[x] = min(max(a.positions[(size_t)x * a.T + t], 0), a.max_pos - 1);
+    }
+    if constexpr (PAGED) {
+        if (slot < 0 || slot >= a.num_slots) return;               // a padding row
+        if ((a.k_scale || a.v_scale) && (req < 0 || req >= a.B)) return;
+    }
 
-    // A and B of this lane's eight dims
+    // A and B of the two pieces
     const bool normed = kind == kQ ? a.q_weight != nullptr : (kind == kK && a.k_weight != nullptr);
-    float A[8], Bm[8];
-    int mate = lane;
+    uint64_t A[2][2], B[2][2];
     if (kind != kV) {
         const void* w = kind == kQ ? a.q_weight : a.k_weight;
-        load_w<F16>(w, a.weight_f32, 8 * c, A);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) Bm[i] = 0.f;
-        if (8 * c < a.rot) {
-            const int half = a.rot / 2;
-            int pos[4];
-#pragma unroll
-            for (int x = 0; x < 4; ++x) pos[x] = x < a.n_axes ? min(max(a.positions[(size_t)x * a.T + t], 0), a.max_pos - 1) : 0;
-            // the table row of pair j
-            auto row = [&](int j) -> const float* {
-                if (a.n_axes == 1) return a.cos_sin + (size_t)pos[0] * a.rot;
+        const int half = a.rot / 2;
+        float wp[2][4], co[2][4], si[2][4];
+        load_w<F16>(w, a.weight_f32, p0, wp[0]);
+        load_w<F16>(w, a.weight_f32, p1, wp[1]);
+        // the table row of pair j
+        auto row = [&](int j) -> const float* {
+            int p = pos[0];
+            if (a.n_axes > 1) {
                 const int ax = (a.pair_axis[j >> 4] >> (2 * (j & 15))) & 3;
-                const int p = ax == 0 ? pos[0] : (ax == 1 ? pos[1] : (ax == 2 ? pos[2] : pos[3]));
-                return a.cos_sin + (size_t)p * a.rot;
-            };
-            if (a.interleaved) {
+                p = ax == 0 ? pos[0] : (ax == 1 ? pos[1] : (ax == 2 ? pos[2] : pos[3]));
+            }
+            return a.cos_sin + (size_t)p * a.rot;
+        };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int j = 4 * c + i;
-                    const float* r = row(j);
-                    const float co = __ldg(r + j), si = __ldg(r + half + j);
-                    const float w0 = A[2 * i], w1 = A[2 * i + 1];
-                    A[2 * i] = w0 * co;
-                    Bm[2 * i] = -w1 * si;
-                    A[2 * i + 1] = w1 * co;
-                    Bm[2 * i + 1] = w0 * si;
-                }
-            } else {
-                const int hc = a.rot / 16;                  // chunks of a half
-                const bool low = c < hc;
-                mate = low ? lane + hc : lane - hc;
-                float wm[8];
-                load_w<F16>(w, a.weight_f32, 8 * (low ? c + hc : c - hc), wm);
-                const int j0 = 8 * (low ? c : c - hc);
+        for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float* r = row(j0 + i);
-                    const float co = __ldg(r + j0 + i), si = __ldg(r + half + j0 + i);
-                    A[i] *= co;
-                    Bm[i] = low ? -wm[i] * si : wm[i] * si;
-                }
+            for (int i = 0; i < 4; ++i) {
+                co[k][i] = 1.f;
+                si[k][i] = 0.f;
             }
         }
+        if constexpr (NEXT) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k == 0 ? rot0 : rot1) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int j = (k == 0 ? p0 : p1) / 2 + i;
+                        const float* r = row(j);
+                        co[k][2 * i] = co[k][2 * i + 1] = __ldg(r + j);
+                        si[k][2 * i] = si[k][2 * i + 1] = __ldg(r + half + j);
+                    }
+                }
+            }
+        } else if (rot0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float* r = row(p0 + i);
+                co[0][i] = co[1][i] = __ldg(r + p0 + i);
+                si[0][i] = si[1][i] = __ldg(r + half + p0 + i);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            float b[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                b[i] = NEXT ? (i & 1 ? wp[k][i ^ 1] * si[k][i] : -wp[k][i ^ 1] * si[k][i])
+                            : (k == 1 ? wp[0][i] * si[k][i] : -wp[1][i] * si[k][i]);
+            A[k][0] = f32x2(wp[k][0] * co[k][0], wp[k][1] * co[k][1]);
+            A[k][1] = f32x2(wp[k][2] * co[k][2], wp[k][3] * co[k][3]);
+            B[k][0] = f32x2(b[0], b[1]);
+            B[k][1] = f32x2(b[2], b[3]);
+        }
     }
-    const bool rotated = 8 * c < a.rot;
 
     for (int h = h0; h < h_end; h += U * HPW) {
-        uint4 cur[U];
+        uint2 cur[U][2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) cur[u] = raw[u];
+        for (int u = 0; u < U; ++u) {
+            cur[u][0] = raw[u][0];
+            cur[u][1] = raw[u][1];
+        }
         if (h + U * HPW < h_end) load(h + U * HPW);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int hh = h + u * HPW + sub;
-            float y[8];
-            unpack8<F16>(cur[u], y);
+            uint64_t y[2][2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                y[k][0] = widen2<F16>(cur[u][k].x);
+                y[k][1] = widen2<F16>(cur[u][k].y);
+            }
             if (kind != kV) {
                 float r = 1.f;
                 if (normed) {
-                    float s = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) s = fmaf(y[i], y[i], s);
+                    uint64_t s2 = fmul2(y[0][0], y[0][0]);
+                    s2 = ffma2(y[0][1], y[0][1], s2);
+                    s2 = ffma2(y[1][0], y[1][0], s2);
+                    s2 = ffma2(y[1][1], y[1][1], s2);
+                    float s, s1;
+                    f32x2_split(s2, s, s1);
+                    s += s1;
 #pragma unroll
                     for (int o = LPH / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
                     r = rsqrtf(s * (1.f / D) + a.eps);
                 }
-                float m[8];
-                if (a.interleaved) {
+                uint64_t m[2][2];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) m[i] = y[i ^ 1];
-                } else {
-                    uint4 o;
-                    o.x = __shfl_sync(0xffffffffu, cur[u].x, mate);
-                    o.y = __shfl_sync(0xffffffffu, cur[u].y, mate);
-                    o.z = __shfl_sync(0xffffffffu, cur[u].z, mate);
-                    o.w = __shfl_sync(0xffffffffu, cur[u].w, mate);
-                    unpack8<F16>(o, m);
+                for (int i = 0; i < 2; ++i) {
+                    m[0][i] = NEXT ? swap2(y[0][i]) : y[1][i];
+                    m[1][i] = NEXT ? swap2(y[1][i]) : y[0][i];
                 }
+                if (a.rot < D) {                           // an unrotated value has no mate: inf * 0 would be NaN
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    // an unrotated dim has no mate: inf * 0 would make it NaN
-                    const float v = rotated ? fmaf(y[i], A[i], m[i] * Bm[i]) : y[i] * A[i];
-                    y[i] = v * r;
+                    for (int i = 0; i < 2; ++i) {
+                        m[0][i] = rot0 ? m[0][i] : 0ull;
+                        m[1][i] = rot1 ? m[1][i] : 0ull;
+                    }
                 }
+                const uint64_t r2 = f32x2(r, r);
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        y[k][i] = fmul2(ffma2(y[k][i], A[k][i], fmul2(m[k][i], B[k][i])), r2);
             }
             if (hh >= h_end) continue;
-            if (kind == kQ) {
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.q_out) + ((size_t)t * a.Hq + hh) * D)[c] =
-                    pack8<F16>(y);
-            } else if (!PAGED) {
-                reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.k_out) + ((size_t)t * a.Hkv + hh) * D)[c] =
-                    pack8<F16>(y);
+            if (kind == kQ || !PAGED) {
+                uint16_t* dst = static_cast<uint16_t*>(kind == kQ ? a.q_out : a.k_out) +
+                                ((size_t)t * (kind == kQ ? a.Hq : a.Hkv) + hh) * D;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float f[4];
+                    f32x2_split(y[k][0], f[0], f[1]);
+                    f32x2_split(y[k][1], f[2], f[3]);
+                    *reinterpret_cast<uint2*>(dst + (k == 0 ? p0 : p1)) =
+                        make_uint2(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]));
+                }
             } else {
                 void* cache = kind == kK ? a.k_cache : a.v_cache;
                 const size_t at = ((size_t)slot * a.Hkv + hh) * D;
-                if (a.e4m3) {
-                    if (scales) {
-                        kv_scale = __ldg(scales + (size_t)req * a.Hkv + hh);
+                float f[2][4];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(y[i], kv_scale);
+                for (int k = 0; k < 2; ++k) {
+                    f32x2_split(y[k][0], f[k][0], f[k][1]);
+                    f32x2_split(y[k][1], f[k][2], f[k][3]);
+                }
+                if (a.e4m3) {
+                    const float* scales = kind == kK ? a.k_scale : a.v_scale;
+                    if (scales) {
+                        const float s = __ldg(scales + (size_t)req * a.Hkv + hh);
+                        const float inv = __frcp_rn(s);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) f[k][i] = quotient(f[k][i], s, inv);
                     }
-                    uint2 o;
-                    o.x = e4m3x2(y[0], y[1]) | (e4m3x2(y[2], y[3]) << 16);
-                    o.y = e4m3x2(y[4], y[5]) | (e4m3x2(y[6], y[7]) << 16);
-                    reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at)[c] = o;
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(cache) + at + (k == 0 ? p0 : p1)) =
+                            e4m3x2(f[k][0], f[k][1]) | (e4m3x2(f[k][2], f[k][3]) << 16);
                 } else {
-                    reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + at)[c] =
-                        kind == kV ? cur[u] : pack8<F16>(y);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)            // values go as they came
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(cache) + at + (k == 0 ? p0 : p1)) =
+                            kind == kV ? cur[u][k]
+                                       : make_uint2(pack2<F16>(f[k][0], f[k][1]), pack2<F16>(f[k][2], f[k][3]));
                 }
             }
         }
@@ -253,7 +314,10 @@ cudaError_t launch_t(const RopeArgs& a, int num_sms, cudaStream_t stream) {
     while (rows < most && tasks() / 2 >= enough) rows *= 2;
     const long blocks = (tasks() + NT / 32 - 1) / (NT / 32);
     if (blocks >= (1L << 31)) return cudaErrorInvalidValue;
-    qk_norm_rope_kernel<D, F16, PAGED><<<(unsigned)blocks, NT, 0, stream>>>(a, parts(a.Hq), parts(a.Hkv), rows);
+    if (a.interleaved)
+        qk_norm_rope_kernel<D, F16, PAGED, true><<<(unsigned)blocks, NT, 0, stream>>>(a, parts(a.Hq), parts(a.Hkv), rows);
+    else
+        qk_norm_rope_kernel<D, F16, PAGED, false><<<(unsigned)blocks, NT, 0, stream>>>(a, parts(a.Hq), parts(a.Hkv), rows);
     return cudaGetLastError();
 }
 

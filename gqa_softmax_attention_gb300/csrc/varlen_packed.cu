@@ -26,6 +26,11 @@ constexpr int NBUCKET = 2048;
 // fill the SMs the chunks leave (measured on the mixed serving batch: 0.622,
 // 0.606 and 0.683 ms at 0.009, 0.0126 and 0.016).
 constexpr double kDecPerKey = 0.011;
+// Over e4m3 caches a cached key is half the bytes and the split kernel is bound by
+// its instructions: the mixed batch (60 steps, 4 chunks) took 0.57, 0.55, 0.55,
+// 0.59 and 0.67 ms at 0.002, 0.004, 0.006, 0.008 and 0.011, one chunk beside the
+// steps 0.30, 0.30, 0.33, 0.39 and 0.43.
+constexpr double kDecPerKey8 = 0.005;
 
 __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb, int g, int causal) {
     const int q0 = e0.y, sq = e0.w, L = e1.y;
@@ -40,7 +45,8 @@ __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb,
 __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, const int32_t* kv, int paged,
                                                           int B, int qpb, int g, int causal, int total_q,
                                                           long kv_cap, int32_t* tmp, int32_t* entries,
-                                                          int32_t* n_entries, int max_entries, int grid) {
+                                                          int32_t* n_entries, int max_entries, int grid,
+                                                          double dec_per_key) {
     __shared__ int warp_sum[32];
     __shared__ unsigned long long pre_cost, dec_keys;   // listed blocks' cost; decode steps' cached keys
     __shared__ int base;
@@ -185,10 +191,10 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         // so that both end together.  A cost unit is half a 128-key tile of a
         // full 128-row block (128 x 128 x D x 2 FLOP per KV head); a cached key
         // of a decode step is 4 D bytes per KV head (16-bit K and V); D and
-        // Hkv cancel, and kDecPerKey converts the second into the first.
+        // Hkv cancel, and dec_per_key converts the second into the first.
         int ge = grid;
         if (grid > 0 && pre_cost > 0 && dec_keys > 0) {
-            const double tp = (double)pre_cost, td = (double)dec_keys * kDecPerKey;
+            const double tp = (double)pre_cost, td = (double)dec_keys * dec_per_key;
             ge = (int)lrint((double)grid * tp / (tp + td));
             ge = min(grid, max(ge, min(grid, 8)));
         }
@@ -200,12 +206,14 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
 
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
-                               int max_entries, cudaStream_t stream, bool skip_single, bool pairs, int grid) {
+                               int max_entries, cudaStream_t stream, bool skip_single, bool pairs, int grid,
+                               bool fp8) {
     // flags: bit 0 paged (kv holds cache lengths), bit 1 skip single-query
     // requests, bit 2 pairs of row blocks
     const int flags = (paged ? 1 : 0) | (skip_single ? 2 : 0) | (pairs ? 4 : 0);
     varlen_plan_kernel<<<1, 1024, 0, stream>>>(cu_q, kv, flags, B, qpb, g, causal, total_q, kv_cap, tmp,
-                                               entries, n_entries, max_entries, grid);
+                                               entries, n_entries, max_entries, grid,
+                                               fp8 ? kDecPerKey8 : kDecPerKey);
     return cudaGetLastError();
 }
 

@@ -455,8 +455,8 @@ gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, con
  *   v            [T, Hkv, D]
  *   slots        [T] int32: cache row (page * page_size + offset) of each
  *                token.  A token whose slot lies outside [0, num_pages *
- *                page_size) is padding: nothing of it is read, its rows of
- *                q_out and the caches stay as they were.  Two tokens with one
+ *                page_size) is padding: its row of q_out and the caches stay
+ *                as they were.  Two tokens with one
  *                slot are a caller error (either may win, value by value)
  *   k_cache, v_cache  [num_pages, page_size, Hkv, D] (written at the slots):
  *                the inputs' type, or float8_e4m3fn with e4m3

@@ -346,3 +346,18 @@ def test_refusals(g):
                 dict(k_scale=s, v_scale=torch.ones(2, 2, device="cuda"), requests=slots)):
         with pytest.raises(ValueError):
             g.attn_qk_norm_rope_paged(q, k, v, table, pos, slots, k8, k8.clone(), qw, kw, **bad)
+
+
+def test_extreme_scales(g):
+    """Scales at the ends of the normal and subnormal range divide like any other."""
+    T, Hkv, D = 4, 1, 64
+    v = torch.tensor([0.0, 1.0, -3.5, 1e-30, 3e38, -1e20, 7e-39, 240.0], dtype=torch.bfloat16).repeat(T * Hkv * D // 8)
+    v = v.view(T, Hkv, D).cuda()
+    z = torch.zeros_like(v)
+    vs = torch.tensor([[1e-45], [2.0 ** -126], [2.0 ** 127], [1e30]], device="cuda")
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    kc = torch.zeros(1, T, Hkv, D, dtype=torch.float8_e4m3fn, device="cuda")
+    vc = kc.clone()
+    g.attn_qk_norm_rope_paged(z, z, v, None, None, slots, kc, vc, v_scale=vs, requests=slots)
+    want = (v.float().cpu() / vs.cpu()[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
+    assert torch.equal(vc.view(T, Hkv, D).cpu().float(), want.float())
