@@ -402,17 +402,34 @@ def _on(device, fn, *args):
         return fn(*args)
 
 
-def _check_plain(name, t, dtype, shape, device):
-    """A contiguous CUDA tensor of this dtype and shape on `device` (None in shape: any size)."""
+def _raw_stream(device):
+    """Handle of the current stream of `device`."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _data(name, t, dtype, shape, device):
+    """Address of a contiguous CUDA tensor of this dtype and shape on `device`.
+    The test that every good argument passes comes first: these calls are
+    launched for a few microseconds of work."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise ValueError("%s must be a %s CUDA tensor" % (name, dtype))
-    if t.dim() != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if t.device != device:
         raise ValueError("%s must be on %s, got %s" % (name, device, t.device))
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return t.data_ptr()
+    raise ValueError("%s must be contiguous" % name)
+
+
+def _size(name, t, ndim, axis):
+    """Size of an axis of a tensor of ndim dimensions."""
+    if not isinstance(t, torch.Tensor) or t.dim() != ndim:
+        raise ValueError("%s must be a CUDA tensor of %d dimensions" % (name, ndim))
+    return t.shape[axis]
 
 
 def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, cache_seqlens, block_table, causal=True,
@@ -430,35 +447,32 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
     Returns (o [total_q, Hq, D] like q, lse [total_q, Hq] float32).
     """
     _check_16_cuda("q", q, 3)
-    dev = q.device
-    for n, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4 or \
-                t.dtype not in (torch.float8_e4m3fn, torch.uint8):
-            raise ValueError("%s must be a 4-D float8_e4m3fn (or uint8) CUDA tensor" % n)
+    dev, i32, f32 = q.device, torch.int32, torch.float32
     total_q, Hq, D = q.shape
-    num_pages, page_size, Hkv, Dk = k_cache.shape
-    if Dk != D or v_cache.shape != k_cache.shape:
-        raise ValueError("cache shape mismatch: k %s, v %s, D %d" % (tuple(k_cache.shape), tuple(v_cache.shape), D))
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or not isinstance(v_cache, torch.Tensor):
+        raise ValueError("k_cache and v_cache must be 4-D float8_e4m3fn (or uint8) CUDA tensors")
+    num_pages, page_size, Hkv, Dk = shape = k_cache.shape
+    if Dk != D or v_cache.shape != shape:
+        raise ValueError("cache shape mismatch: k %s, v %s, D %d" % (tuple(shape), tuple(v_cache.shape), D))
     if Hkv == 0 or Hq % Hkv != 0:
         raise ValueError("Hq (%d) must be divisible by Hkv (%d)" % (Hq, Hkv))
-    if not isinstance(cache_seqlens, torch.Tensor) or cache_seqlens.dim() != 1:
-        raise ValueError("cache_seqlens must be [B]")
-    B = cache_seqlens.shape[0]
-    kc = _check_plain("k_cache", k_cache, k_cache.dtype, k_cache.shape, dev)
-    vc = _check_plain("v_cache", v_cache, v_cache.dtype, k_cache.shape, dev)
-    cq = _check_plain("cu_seqlens_q", cu_seqlens_q, torch.int32, (B + 1,), dev)
-    sl = _check_plain("cache_seqlens", cache_seqlens, torch.int32, (B,), dev)
-    bt = _check_plain("block_table", block_table, torch.int32, (B, None), dev)
-    max_pages = block_table.shape[1]
-    ks = _check_plain("k_scale", k_scale, torch.float32, (B, Hkv), dev) if k_scale is not None else None
-    vs = _check_plain("v_scale", v_scale, torch.float32, (B, Hkv), dev) if v_scale is not None else None
+    ct = torch.uint8 if k_cache.dtype == torch.uint8 else torch.float8_e4m3fn
+    B = _size("cache_seqlens", cache_seqlens, 1, 0)
+    max_pages = _size("block_table", block_table, 2, 1)
+    kc = _data("k_cache", k_cache, ct, shape, dev)
+    vc = _data("v_cache", v_cache, torch.uint8 if v_cache.dtype == torch.uint8 else torch.float8_e4m3fn, shape, dev)
+    cq = _data("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev)
+    sl = _data("cache_seqlens", cache_seqlens, i32, (B,), dev)
+    bt = _data("block_table", block_table, i32, (B, max_pages), dev)
+    ks = _data("k_scale", k_scale, f32, (B, Hkv), dev) if k_scale is not None else None
+    vs = _data("v_scale", v_scale, f32, (B, Hkv), dev) if v_scale is not None else None
     q = q.contiguous()
     if out is None:
         out = torch.empty_like(q)
     if lse is None:
-        lse = torch.empty((total_q, Hq), dtype=torch.float32, device=dev)
-    po = _check_plain("out", out, q.dtype, q.shape, dev)
-    pl = _check_plain("lse", lse, torch.float32, (total_q, Hq), dev)
+        lse = torch.empty((total_q, Hq), dtype=f32, device=dev)
+    po = _data("out", out, q.dtype, q.shape, dev)
+    pl = _data("lse", lse, f32, (total_q, Hq), dev)
     lib = _lib.load()
     if workspace is None:
         if split_decode:
@@ -470,9 +484,9 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     opt, _keep = _options(window_left, window_right, softcap, sinks, Hq, dev, _DTYPES[q.dtype])
     st = _on(dev, lib.attn_fwd_paged_fp8kv, q.data_ptr(), kc, vc, ks, vs, cq, sl, bt, page_size, po, pl, B, total_q,
-             Hq, Hkv, D, num_pages, max_pages, int(bool(causal)), resolve_scale(scale, D),
+             Hq, Hkv, D, num_pages, max_pages, 1 if causal else 0, resolve_scale(scale, D),
              ctypes.byref(opt) if opt is not None else None, workspace.data_ptr(),
-             workspace.numel() * workspace.element_size(), torch.cuda.current_stream(dev).cuda_stream)
+             workspace.numel() * workspace.element_size(), _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_fwd_paged_fp8kv")
     return out, lse
@@ -495,30 +509,29 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
     captured graph).  Nothing is read back: counts[0] > max_tokens, or
     counts[2] > n, tells the caller later that rows or pages ran out.
     """
-    if not isinstance(past_lens, torch.Tensor) or past_lens.dim() != 1:
-        raise ValueError("past_lens must be [B]")
-    dev, i32, B = past_lens.device, torch.int32, past_lens.shape[0]
-    pp = _check_plain("past_lens", past_lens, i32, (B,), dev)
-    pn = _check_plain("new_lens", new_lens, i32, (B,), dev)
-    pt = _check_plain("block_table", block_table, i32, (B, None), dev)
-    pf = _check_plain("free_pages", free_pages, i32, (None,), dev)
-    fs = _check_plain("free_start", free_start, i32, (1,), dev) if free_start is not None else None
-    T = int(max_tokens)
+    B = _size("past_lens", past_lens, 1, 0)
+    dev, i32, T = past_lens.device, torch.int32, int(max_tokens)
+    max_pages, n_free = _size("block_table", block_table, 2, 1), _size("free_pages", free_pages, 1, 0)
+    pp = _data("past_lens", past_lens, i32, (B,), dev)
+    pn = _data("new_lens", new_lens, i32, (B,), dev)
+    pt = _data("block_table", block_table, i32, (B, max_pages), dev)
+    pf = _data("free_pages", free_pages, i32, (n_free,), dev)
+    fs = _data("free_start", free_start, i32, (1,), dev) if free_start is not None else None
     if T < 0:
         raise ValueError("max_tokens must be >= 0, got %d" % T)
-    sizes = (B + 1, B, T, T, T, 3)
     if out is None:
-        out = torch.empty(sum(sizes), dtype=i32, device=dev).split(sizes)
+        out = torch.empty(2 * B + 3 * T + 4, dtype=i32, device=dev).split((B + 1, B, T, T, T, 3))
     elif len(out) != 6:
         raise ValueError("out must hold six tensors")
-    outs = [_check_plain(name, t, i32, (n,), dev) for name, t, n in
-            zip(("out cu_seqlens_q", "out cache_seqlens", "out slots", "out positions", "out requests", "out counts"),
-                out, sizes)]
-    st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, block_table.shape[1], int(page_size),
-             int(num_pages), free_pages.shape[0], T, *outs, torch.cuda.current_stream(dev).cuda_stream)
+    cu, lens, slots, positions, requests, counts = out
+    st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, max_pages, int(page_size), int(num_pages),
+             n_free, T, _data("out cu_seqlens_q", cu, i32, (B + 1,), dev), _data("out cache_seqlens", lens, i32, (B,), dev),
+             _data("out slots", slots, i32, (T,), dev), _data("out positions", positions, i32, (T,), dev),
+             _data("out requests", requests, i32, (T,), dev), _data("out counts", counts, i32, (3,), dev),
+             _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_paged_slots")
-    return tuple(out)
+    return cu, lens, slots, positions, requests, counts
 
 
 def _head_rows(t, T):
@@ -526,12 +539,18 @@ def _head_rows(t, T):
     kernels take them, else of a copy (returned to keep it alive)."""
     if t.dim() == 4:
         t = t.reshape(T, t.shape[2], t.shape[3])      # a view where the rows have one stride
+    _, H, D = t.shape
+    ts, hs, ds = t.stride()
     # the stride of an axis of one element says nothing
-    ts, hs, ds = [st if n > 1 else 0 for n, st in zip(t.shape, t.stride())]
-    if ds != 1 or ts % 8 or hs % 8 or t.data_ptr() % 16:
+    if T <= 1:
+        ts = 0
+    if H <= 1:
+        hs = 0
+    p = t.data_ptr()
+    if ds != 1 or ts % 8 or hs % 8 or p % 16:
         t = t.clone(memory_format=torch.contiguous_format)
-        ts, hs, ds = t.stride()
-    return _lib.HeadRows(t.data_ptr(), ts, hs), t
+        p, ts, hs = t.data_ptr(), H * D, D
+    return _lib.HeadRows(p, ts, hs), t
 
 
 def _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axes):
@@ -540,46 +559,47 @@ def _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axe
     if nd not in (3, 4):
         raise ValueError("q must be a CUDA tensor [T, Hq, D] or [B, S, Hq, D]")
     _check_16_cuda("q", q, nd)
-    dev, lead, D = q.device, q.shape[:-2], q.shape[-1]
+    dev, dt, lead, D = q.device, q.dtype, q.shape[:-2], q.shape[-1]
     T = lead.numel()
+    shape = k.shape
     for n, t in (("k", k), ("v", v)):
-        if t is not None:
-            _check_16_cuda(n, t, nd, (q.dtype,))
-            if t.device != dev or t.shape[:-2] != lead or t.shape[-1] != D or t.shape[-2] != k.shape[-2]:
-                raise ValueError("shape mismatch: q %s, %s %s (k %s), all on one device"
-                                 % (tuple(q.shape), n, tuple(t.shape), tuple(k.shape)))
-    wt = torch.float32 if any(w is not None and w.dtype == torch.float32 for w in (q_weight, k_weight)) else q.dtype
-    pw = [_check_plain(n, w, wt, (D,), dev) if w is not None else None
-          for n, w in (("q_weight", q_weight), ("k_weight", k_weight))]
+        if t is not None and (t.dtype is not dt or t.device != dev or t.shape != shape or t.dim() != nd or
+                              shape[:-2] != lead or shape[-1] != D):
+            raise ValueError("q, k and v must have one dtype, device, leading shape and head dim, k and v as many "
+                             "heads: q %s %s, %s %s %s" % (tuple(q.shape), dt, n, tuple(t.shape), t.dtype))
+    f32 = torch.float32
+    wt = f32 if any(w is not None and w.dtype == f32 for w in (q_weight, k_weight)) else dt
+    pqw = _data("q_weight", q_weight, wt, (D,), dev) if q_weight is not None else None
+    pkw = _data("k_weight", k_weight, wt, (D,), dev) if k_weight is not None else None
     rope = None
     if cos_sin is not None:
-        pc = _check_plain("cos_sin", cos_sin, torch.float32, (None, None), dev)
-        rot = cos_sin.shape[1]
+        max_pos, rot = _size("cos_sin", cos_sin, 2, 0), cos_sin.shape[1]
+        pc = _data("cos_sin", cos_sin, f32, (max_pos, rot), dev)
         if rot > D or rot % 16:
             raise ValueError("cos_sin must be [max_pos, rot] with rot <= D and a multiple of 16, got %s"
                              % (tuple(cos_sin.shape),))
         if axes is None:
-            n_axes, pa, shape = 1, None, lead
+            n_axes, pa, pshape = 1, None, lead
         else:
             if len(axes) != rot // 2 or not isinstance(positions, torch.Tensor) or positions.dim() < 2:
                 raise ValueError("axes must name the axis of each of the rot / 2 = %d pairs, positions be "
                                  "[n_axes, ...]" % (rot // 2))
             n_axes = positions.shape[0]
-            if any(not 0 <= int(x) < min(n_axes, 4) for x in axes):
+            if n_axes > 4 or (rot > 0 and not 0 <= min(axes) <= max(axes) < n_axes):
                 raise ValueError("axes must lie in [0, n_axes = %d), at most four axes" % n_axes)
-            pa, shape = bytes(axes), (n_axes, *lead)
-        pp = _check_plain("positions", positions, torch.int32, shape, dev)
-        rope = _lib.Rope(pc, pp, cos_sin.shape[0], rot, int(bool(interleaved)), n_axes, pa)
+            pa, pshape = bytes(axes), (n_axes, *lead)
+        pp = _data("positions", positions, torch.int32, pshape, dev)
+        rope = _lib.Rope(pc, pp, max_pos, rot, 1 if interleaved else 0, n_axes, pa)
     elif positions is not None or axes is not None:
         raise ValueError("positions and axes need cos_sin")
-    return dev, T, D, pw, int(wt == torch.float32), rope
+    return dev, T, D, (pqw, pkw), 1 if wt is f32 else 0, ctypes.byref(rope) if rope is not None else None
 
 
 def _rope_out(name, out, like):
-    """`out` (checked) or a new contiguous tensor like `like`."""
+    """`out` (checked) or a new contiguous tensor like `like`, and its address."""
     if out is None:
         out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
-    return out, _check_plain(name, out, like.dtype, like.shape, like.device)
+    return out, _data(name, out, like.dtype, like.shape, like.device)
 
 
 def attn_qk_norm_rope(q, k, cos_sin, positions, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, axes=None,
@@ -607,9 +627,8 @@ def attn_qk_norm_rope(q, k, cos_sin, positions, q_weight=None, k_weight=None, ep
     ok, pk = _rope_out("out k", out[1] if out is not None else None, k)
     rq, _kq = _head_rows(q, T)
     rk, _kk = _head_rows(k, T)
-    st = _on(dev, _lib.load().attn_qk_norm_rope, ctypes.byref(rq), ctypes.byref(rk), pqw, pkw, wf, float(eps),
-             ctypes.byref(rope) if rope is not None else None, pq, pk, T, q.shape[-2], k.shape[-2], D,
-             _DTYPES[q.dtype], torch.cuda.current_stream(dev).cuda_stream)
+    st = _on(dev, _lib.load().attn_qk_norm_rope, ctypes.byref(rq), ctypes.byref(rk), pqw, pkw, wf, eps, rope, pq, pk,
+             T, q.shape[-2], k.shape[-2], D, _DTYPES[q.dtype], _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_qk_norm_rope")
     return oq, ok
@@ -633,25 +652,22 @@ def attn_qk_norm_rope_paged(q, k, v, cos_sin, positions, slots, k_cache, v_cache
     if not isinstance(k, torch.Tensor) or not isinstance(v, torch.Tensor):
         raise ValueError("k and v must be CUDA tensors")
     dev, T, D, (pqw, pkw), wf, rope = _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axes)
-    Hkv = k.shape[-2]
-    lead = q.shape[:-2]
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
-        raise ValueError("k_cache must be a CUDA tensor [num_pages, page_size, Hkv, D]")
-    e4m3 = k_cache.dtype in (torch.float8_e4m3fn, torch.uint8)
-    num_pages, page_size = k_cache.shape[:2]
-    ct = k_cache.dtype if e4m3 else q.dtype
-    pkc = _check_plain("k_cache", k_cache, ct, (None, None, Hkv, D), dev)
-    pvc = _check_plain("v_cache", v_cache, ct, k_cache.shape, dev)
-    ps = _check_plain("slots", slots, torch.int32, lead, dev)
-    B, scales, pr = 0, [None, None], None
-    for i, (n, t) in enumerate((("k_scale", k_scale), ("v_scale", v_scale))):
-        if t is not None:
-            if not e4m3:
-                raise ValueError("%s needs float8_e4m3fn caches" % n)
-            scales[i] = _check_plain(n, t, torch.float32, (B or None, Hkv), dev)
-            B = t.shape[0]
-    if B:
-        pr = _check_plain("requests", requests, torch.int32, lead, dev)
+    i32, f32, Hkv, lead = torch.int32, torch.float32, k.shape[-2], q.shape[:-2]
+    num_pages, page_size = _size("k_cache", k_cache, 4, 0), k_cache.shape[1]
+    ct = k_cache.dtype
+    e4m3 = ct is torch.float8_e4m3fn or ct is torch.uint8
+    shape = (num_pages, page_size, Hkv, D)
+    pkc = _data("k_cache", k_cache, ct if e4m3 else q.dtype, shape, dev)
+    pvc = _data("v_cache", v_cache, ct if e4m3 else q.dtype, shape, dev)
+    ps = _data("slots", slots, i32, lead, dev)
+    B, pks, pvs, pr = 0, None, None, None
+    if k_scale is not None or v_scale is not None:
+        if not e4m3:
+            raise ValueError("k_scale and v_scale need float8_e4m3fn caches")
+        B = _size("k_scale" if k_scale is not None else "v_scale", k_scale if k_scale is not None else v_scale, 2, 0)
+        pks = _data("k_scale", k_scale, f32, (B, Hkv), dev) if k_scale is not None else None
+        pvs = _data("v_scale", v_scale, f32, (B, Hkv), dev) if v_scale is not None else None
+        pr = _data("requests", requests, i32, lead, dev)
     elif requests is not None:
         raise ValueError("requests needs k_scale or v_scale")
     oq, pq = _rope_out("out", out, q)
@@ -659,9 +675,8 @@ def attn_qk_norm_rope_paged(q, k, v, cos_sin, positions, slots, k_cache, v_cache
     rk, _kk = _head_rows(k, T)
     rv, _kv = _head_rows(v, T)
     st = _on(dev, _lib.load().attn_qk_norm_rope_paged, ctypes.byref(rq), ctypes.byref(rk), ctypes.byref(rv), pqw, pkw,
-             wf, float(eps), ctypes.byref(rope) if rope is not None else None, pq, ps, pkc, pvc, int(e4m3),
-             scales[0], scales[1], pr, B, T, q.shape[-2], Hkv, D, num_pages, page_size, _DTYPES[q.dtype],
-             torch.cuda.current_stream(dev).cuda_stream)
+             wf, eps, rope, pq, ps, pkc, pvc, 1 if e4m3 else 0, pks, pvs, pr, B, T, q.shape[-2], Hkv, D, num_pages,
+             page_size, _DTYPES[q.dtype], _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_qk_norm_rope_paged")
     return oq

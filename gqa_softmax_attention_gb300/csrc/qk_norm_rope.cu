@@ -17,7 +17,7 @@
 // other piece), or 4l and D/2 + 4l interleaved (mates in the same piece), so
 // that only the sum of squares crosses lanes, and each load of a warp still
 // covers whole 64-byte stretches.  A warp holds 32 / (D / 8) rows at a time
-// and loads U of those ahead before it works on U; its rows are of one kind
+// and loads U of those before it works on them; its rows are of one kind
 // (queries, keys or values), so nothing diverges.  Arithmetic goes in pairs
 // (f32x2).
 #include <cuda_bf16.h>
@@ -30,7 +30,7 @@ namespace gqa {
 namespace {
 
 constexpr int NT = 128;
-constexpr int U = 4;               // row groups a warp loads ahead
+constexpr int U = 4;               // row groups a warp loads at once
 
 enum Kind : int { kQ = 0, kK = 1, kV = 2 };
 
@@ -63,15 +63,17 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return r;
 }
 
-// y / s given inv, the rounded 1 / s: the product corrected by its remainder
-// (Markstein 1990), which is the rounded quotient where it matters; beyond the
-// e4m3 range, where the remainder could overflow, the product alone.  Scales
-// whose reciprocal leaves the normal range are divided by.
-__device__ __forceinline__ float quotient(float y, float s, float inv) {
-    if (s < 0x1p-120f || s > 0x1p120f) return __fdiv_rn(y, s);
-    const float q = y * inv;
-    const float c = fmaf(fmaf(-q, s, y), inv, q);
-    return fabsf(q) < 1024.f ? c : q;
+// Pairs y / s given inv, the rounded 1 / s: the product corrected by its
+// remainder (Markstein 1990), which is the rounded quotient where it matters;
+// beyond the e4m3 range, where the remainder could overflow, the product alone.
+__device__ __forceinline__ void quotient2(uint64_t y, float s, float inv, float& lo, float& hi) {
+    const uint64_t inv2 = f32x2(inv, inv), q = fmul2(y, inv2);
+    const uint64_t c = ffma2(ffma2(q, f32x2(-s, -s), y), inv2, q);
+    float q0, q1;
+    f32x2_split(q, q0, q1);
+    f32x2_split(c, lo, hi);
+    lo = fabsf(q0) < 1024.f ? lo : q0;
+    hi = fabsf(q1) < 1024.f ? hi : q1;
 }
 
 // Four weights of dims d .. d + 3 (ones without a norm).
@@ -89,41 +91,33 @@ __device__ __forceinline__ void load_w(const void* w, int f32, int d, float* out
     }
 }
 
-template <int D, bool F16, bool PAGED, bool NEXT>
-__global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int nq, int nk, int rows_per_warp) {
+// Rows h0 .. h_end - 1 of one kind of token t.
+template <int D, bool F16, bool PAGED, bool NEXT, int KIND>
+__device__ __forceinline__ void do_rows(const RopeArgs& a, long t, int h0, int h_end, int lane) {
     constexpr int LPH = D / 8;              // lanes per head row
     constexpr int HPW = 32 / LPH;           // rows of a warp at a time
-    const int lane = threadIdx.x % 32;
+    constexpr bool STORE8 = PAGED && KIND != kQ;
     const int l = lane % LPH, sub = lane / LPH;
-    const long task = (long)blockIdx.x * (NT / 32) + threadIdx.x / 32;
-    const int per_token = nq + nk + (PAGED ? nk : 0);
-    const long t = task / per_token;
-    if (t >= a.T) return;
-    const int part = (int)(task % per_token);
-    const int kind = part < nq ? kQ : (part < nq + nk ? kK : kV);
-    const int h0 = (kind == kQ ? part : (kind == kK ? part - nq : part - nq - nk)) * rows_per_warp;
-    const int H = kind == kQ ? a.Hq : a.Hkv;
-    const int h_end = min(H, h0 + rows_per_warp);
-
     // this lane's two pieces
     const int pairs = a.rot / 8;            // lanes that hold rotated pieces (mates in halves)
     const int p0 = NEXT ? 4 * l : (l < pairs ? 4 * l : a.rot + 8 * (l - pairs));
     const int p1 = NEXT ? D / 2 + 4 * l : (l < pairs ? a.rot / 2 + 4 * l : p0 + 4);
     const bool rot0 = p0 < a.rot, rot1 = p1 < a.rot;
 
-    const uint16_t* src = static_cast<const uint16_t*>(kind == kQ ? a.q : (kind == kK ? a.k : a.v)) +
-                          t * (kind == kQ ? a.q_ts : (kind == kK ? a.k_ts : a.v_ts));
-    const long hs = kind == kQ ? a.q_hs : (kind == kK ? a.k_hs : a.v_hs);
+    const long hs = KIND == kQ ? a.q_hs : (KIND == kK ? a.k_hs : a.v_hs);
+    const uint16_t* src = static_cast<const uint16_t*>(KIND == kQ ? a.q : (KIND == kK ? a.k : a.v)) +
+                          t * (KIND == kQ ? a.q_ts : (KIND == kK ? a.k_ts : a.v_ts)) + (h0 + sub) * hs;
+    const int n = h_end - h0;               // rows; this lane's are sub, sub + HPW, ...
     uint2 raw[U][2];
-    auto load = [&](int h) {
+    auto load = [&](int i) {                // rows i .. of the task; past its end the last row this lane has
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int hh = min(h + u * HPW + sub, h_end - 1);      // a surplus row repeats the last, and is not stored
-            raw[u][0] = *reinterpret_cast<const uint2*>(src + hh * hs + p0);
-            raw[u][1] = *reinterpret_cast<const uint2*>(src + hh * hs + p1);
+            const uint16_t* p = src + (i + u * HPW + sub < n ? i + u * HPW : (n - 1 - sub) / HPW * HPW) * hs;
+            raw[u][0] = *reinterpret_cast<const uint2*>(p + p0);
+            raw[u][1] = *reinterpret_cast<const uint2*>(p + p1);
         }
     };
-    load(h0);
+    if (sub < n) load(0);                   // a lane without a row works on whatever its registers hold
     long slot = 0;
     int req = 0;
     if constexpr (PAGED) {
@@ -131,7 +125,7 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
         if (a.k_scale || a.v_scale) req = a.requests[t];
     }
     int pos[4] = {0, 0, 0, 0};
-    if (kind != kV && a.rot > 0) {
+    if (KIND != kV && a.rot > 0) {
 #pragma unroll
         for (int x = 0; x < 4; ++x)
             if (x < a.n_axes) pos[x] = min(max(a.positions[(size_t)x * a.T + t], 0), a.max_pos - 1);
@@ -142,14 +136,21 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
     }
 
     // A and B of the two pieces
-    const bool normed = kind == kQ ? a.q_weight != nullptr : (kind == kK && a.k_weight != nullptr);
+    const void* w = KIND == kQ ? a.q_weight : a.k_weight;
     uint64_t A[2][2], B[2][2];
-    if (kind != kV) {
-        const void* w = kind == kQ ? a.q_weight : a.k_weight;
+    if constexpr (KIND != kV) {
         const int half = a.rot / 2;
         float wp[2][4], co[2][4], si[2][4];
         load_w<F16>(w, a.weight_f32, p0, wp[0]);
         load_w<F16>(w, a.weight_f32, p1, wp[1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                co[k][i] = 1.f;
+                si[k][i] = 0.f;
+            }
+        }
         // the table row of pair j
         auto row = [&](int j) -> const float* {
             int p = pos[0];
@@ -159,14 +160,6 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
             }
             return a.cos_sin + (size_t)p * a.rot;
         };
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                co[k][i] = 1.f;
-                si[k][i] = 0.f;
-            }
-        }
         if constexpr (NEXT) {
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -180,6 +173,13 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
                     }
                 }
             }
+        } else if (rot0 && a.n_axes == 1) {
+            // rot is a multiple of 16, so four cosines or sines are 16 aligned bytes
+            const float* r = row(0);
+            const float4 c4 = __ldg(reinterpret_cast<const float4*>(r + p0));
+            const float4 s4 = __ldg(reinterpret_cast<const float4*>(r + half + p0));
+            co[0][0] = co[1][0] = c4.x; co[0][1] = co[1][1] = c4.y; co[0][2] = co[1][2] = c4.z; co[0][3] = co[1][3] = c4.w;
+            si[0][0] = si[1][0] = s4.x; si[0][1] = si[1][1] = s4.y; si[0][2] = si[1][2] = s4.z; si[0][3] = si[1][3] = s4.w;
         } else if (rot0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -201,25 +201,34 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
             B[k][1] = f32x2(b[2], b[3]);
         }
     }
+    const bool normed = KIND != kV && w != nullptr;
+    const bool partial = a.rot < D;
+    const float* scale = nullptr;           // of this lane's first row
+    if constexpr (STORE8) {
+        scale = KIND == kK ? a.k_scale : a.v_scale;
+        if (scale) scale += (size_t)req * a.Hkv + h0 + sub;
+    }
+    // this lane's first output row, in elements
+    const size_t out = ((KIND != kQ && PAGED ? (size_t)slot : (size_t)t) * (KIND == kQ ? a.Hq : a.Hkv) + h0 + sub) * D;
 
-    for (int h = h0; h < h_end; h += U * HPW) {
-        uint2 cur[U][2];
+    for (int i = 0; i < n; i += U * HPW) {
+        if (i > 0 && sub < n) load(i);
+        float sc[U];
+        if constexpr (STORE8) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            cur[u][0] = raw[u][0];
-            cur[u][1] = raw[u][1];
+            for (int u = 0; u < U; ++u)
+                sc[u] = scale && i + u * HPW + sub < n ? __ldg(scale + i + u * HPW) : 1.f;
         }
-        if (h + U * HPW < h_end) load(h + U * HPW);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int hh = h + u * HPW + sub;
+            const int row = i + u * HPW;                           // + sub
             uint64_t y[2][2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                y[k][0] = widen2<F16>(cur[u][k].x);
-                y[k][1] = widen2<F16>(cur[u][k].y);
+                y[k][0] = widen2<F16>(raw[u][k].x);
+                y[k][1] = widen2<F16>(raw[u][k].y);
             }
-            if (kind != kV) {
+            if constexpr (KIND != kV) {
                 float r = 1.f;
                 if (normed) {
                     uint64_t s2 = fmul2(y[0][0], y[0][0]);
@@ -235,67 +244,95 @@ __global__ void __launch_bounds__(NT) qk_norm_rope_kernel(const RopeArgs a, int 
                 }
                 uint64_t m[2][2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    m[0][i] = NEXT ? swap2(y[0][i]) : y[1][i];
-                    m[1][i] = NEXT ? swap2(y[1][i]) : y[0][i];
+                for (int e = 0; e < 2; ++e) {
+                    m[0][e] = NEXT ? swap2(y[0][e]) : y[1][e];
+                    m[1][e] = NEXT ? swap2(y[1][e]) : y[0][e];
                 }
-                if (a.rot < D) {                           // an unrotated value has no mate: inf * 0 would be NaN
+                if (partial) {                             // an unrotated value has no mate: inf * 0 would be NaN
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        m[0][i] = rot0 ? m[0][i] : 0ull;
-                        m[1][i] = rot1 ? m[1][i] : 0ull;
+                    for (int e = 0; e < 2; ++e) {
+                        m[0][e] = rot0 ? m[0][e] : 0ull;
+                        m[1][e] = rot1 ? m[1][e] : 0ull;
                     }
                 }
                 const uint64_t r2 = f32x2(r, r);
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        y[k][i] = fmul2(ffma2(y[k][i], A[k][i], fmul2(m[k][i], B[k][i])), r2);
+                    for (int e = 0; e < 2; ++e)
+                        y[k][e] = fmul2(ffma2(y[k][e], A[k][e], fmul2(m[k][e], B[k][e])), r2);
             }
-            if (hh >= h_end) continue;
-            if (kind == kQ || !PAGED) {
-                uint16_t* dst = static_cast<uint16_t*>(kind == kQ ? a.q_out : a.k_out) +
-                                ((size_t)t * (kind == kQ ? a.Hq : a.Hkv) + hh) * D;
+            if (row + sub >= n) continue;
+            const size_t at = out + (size_t)row * D;
+            float f[2][4];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    float f[4];
-                    f32x2_split(y[k][0], f[0], f[1]);
-                    f32x2_split(y[k][1], f[2], f[3]);
-                    *reinterpret_cast<uint2*>(dst + (k == 0 ? p0 : p1)) =
-                        make_uint2(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]));
-                }
-            } else {
-                void* cache = kind == kK ? a.k_cache : a.v_cache;
-                const size_t at = ((size_t)slot * a.Hkv + hh) * D;
-                float f[2][4];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    f32x2_split(y[k][0], f[k][0], f[k][1]);
-                    f32x2_split(y[k][1], f[k][2], f[k][3]);
-                }
-                if (a.e4m3) {
-                    const float* scales = kind == kK ? a.k_scale : a.v_scale;
-                    if (scales) {
-                        const float s = __ldg(scales + (size_t)req * a.Hkv + hh);
+            for (int k = 0; k < 2; ++k) {
+                f32x2_split(y[k][0], f[k][0], f[k][1]);
+                f32x2_split(y[k][1], f[k][2], f[k][3]);
+            }
+            if (STORE8 && a.e4m3) {
+                if (scale) {
+                    const float s = sc[u];
+                    if (s > 0x1p-120f && s < 0x1p120f) {
                         const float inv = __frcp_rn(s);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            quotient2(y[k][0], s, inv, f[k][0], f[k][1]);
+                            quotient2(y[k][1], s, inv, f[k][2], f[k][3]);
+                        }
+                    } else {                               // no normal reciprocal
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) f[k][i] = quotient(f[k][i], s, inv);
+                            for (int e = 0; e < 4; ++e) f[k][e] = __fdiv_rn(f[k][e], s);
                     }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)
-                        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(cache) + at + (k == 0 ? p0 : p1)) =
-                            e4m3x2(f[k][0], f[k][1]) | (e4m3x2(f[k][2], f[k][3]) << 16);
+                }
+                uint8_t* dst = static_cast<uint8_t*>(KIND == kK ? a.k_cache : a.v_cache) + at;
+                *reinterpret_cast<uint32_t*>(dst + p0) = e4m3x2(f[0][0], f[0][1]) | (e4m3x2(f[0][2], f[0][3]) << 16);
+                *reinterpret_cast<uint32_t*>(dst + p1) = e4m3x2(f[1][0], f[1][1]) | (e4m3x2(f[1][2], f[1][3]) << 16);
+            } else {
+                uint16_t* dst = static_cast<uint16_t*>(KIND == kQ ? a.q_out
+                                                                  : (!PAGED ? a.k_out
+                                                                            : (KIND == kK ? a.k_cache : a.v_cache))) + at;
+                if constexpr (KIND == kV) {                        // values go as they came
+                    *reinterpret_cast<uint2*>(dst + p0) = raw[u][0];
+                    *reinterpret_cast<uint2*>(dst + p1) = raw[u][1];
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 2; ++k)            // values go as they came
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(cache) + at + (k == 0 ? p0 : p1)) =
-                            kind == kV ? cur[u][k]
-                                       : make_uint2(pack2<F16>(f[k][0], f[k][1]), pack2<F16>(f[k][2], f[k][3]));
+                    *reinterpret_cast<uint2*>(dst + p0) =
+                        make_uint2(pack2<F16>(f[0][0], f[0][1]), pack2<F16>(f[0][2], f[0][3]));
+                    *reinterpret_cast<uint2*>(dst + p1) =
+                        make_uint2(pack2<F16>(f[1][0], f[1][1]), pack2<F16>(f[1][2], f[1][3]));
                 }
             }
+        }
+    }
+}
+
+// A warp per task: up to rows_per_warp rows of one kind of one token.  All query
+// tasks come before the key tasks and those before the value tasks, so that a
+// block's warps take equally long (token by token, blocks held three warps of 8
+// rows until one of 64 was done: 180 instead of RESULT us at 16384 tokens, 64/8
+// heads, D = 128, e4m3 caches).
+template <int D, bool F16, bool PAGED, bool NEXT>
+__global__ void __launch_bounds__(NT, 8) qk_norm_rope_kernel(const RopeArgs a, int nq, int nk, int rows_per_warp) {
+    const int lane = threadIdx.x % 32;
+    long task = (long)blockIdx.x * (NT / 32) + threadIdx.x / 32;
+    if (task < (long)a.T * nq) {
+        const int h0 = (int)(task % nq) * rows_per_warp;
+        do_rows<D, F16, PAGED, NEXT, kQ>(a, task / nq, h0, min(a.Hq, h0 + rows_per_warp), lane);
+        return;
+    }
+    task -= (long)a.T * nq;
+    if (task < (long)a.T * nk) {
+        const int h0 = (int)(task % nk) * rows_per_warp;
+        do_rows<D, F16, PAGED, NEXT, kK>(a, task / nk, h0, min(a.Hkv, h0 + rows_per_warp), lane);
+        return;
+    }
+    if constexpr (PAGED) {
+        task -= (long)a.T * nk;
+        if (task < (long)a.T * nk) {
+            const int h0 = (int)(task % nk) * rows_per_warp;
+            do_rows<D, F16, PAGED, NEXT, kV>(a, task / nk, h0, min(a.Hkv, h0 + rows_per_warp), lane);
         }
     }
 }
