@@ -141,6 +141,89 @@ struct Cfg {
 };
 constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
 
+// tanh of two values of magnitude at most 1: y times a polynomial of degree 6 in
+// y^2, the minimax one for the relative error on [0, 1] (Remez exchange in 40
+// digits: 5.0e-8, with FP32 rounding 1.1e-7 absolute).
+__device__ __forceinline__ uint64_t tanh2_small(uint64_t y) {
+    auto both = [](float c) { return f32x2(c, c); };
+    const uint64_t u = fmul2(y, y);
+    uint64_t p = ffma2(u, both(1.0410225856812554e-3f), both(-6.203378982082121e-3f));
+    p = ffma2(u, p, both(2.0289980320438973e-2f));
+    p = ffma2(u, p, both(-5.345702954900354e-2f));
+    p = ffma2(u, p, both(1.3325204077205186e-1f));
+    p = ffma2(u, p, both(-3.333283915359491e-1f));
+    p = ffma2(u, p, both(9.999999502408815e-1f));
+    return fmul2(y, p);
+}
+
+// tanh(y) = 1 - 2 / (e^(2y) + 1)
+__device__ __forceinline__ float tanh_mufu(float y) {
+    return fmaf(-2.f, rcp_approx(fast_exp2(y * 2.8853900817779268f) + 1.f), 1.f);      // 2 log2(e)
+}
+
+// kPaged8: 32 raw scores -> tanh(to_y * s) (to_y = scale / softcap), in place.
+// Scores within the cap take a polynomial, 10 paired FP32 operations for two; a
+// warp with a larger one takes 1 - 2 / (e^(2y) + 1).  Warp-collective.
+__device__ __forceinline__ void tanh_32(float* s, float to_y) {
+    float am[2] = {0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < 32; c += 2) am[(c >> 1) & 1] = fmax3(am[(c >> 1) & 1], fabsf(s[c]), fabsf(s[c + 1]));
+    if (__all_sync(0xffffffffu, fmaxf(am[0], am[1]) * fabsf(to_y) <= 1.f)) {
+        const uint64_t k = f32x2(to_y, to_y);
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) f32x2_split(tanh2_small(fmul2(f32x2(s[c], s[c + 1]), k)), s[c], s[c + 1]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = tanh_mufu(s[c] * to_y);
+    }
+}
+
+// kPaged8: a row of raw scores in TMEM -> what the exponential scales, in
+// place, 32 columns a turn: tanh(to_y * s) with a softcap, else s * factor; -inf
+// outside [lo, lim).  Only tiles that need it take this pass (a mask, a scale
+// that is not positive); all others go straight to the maximum, so that the
+// code of the usual tile stays small: the roles of a CTA share one instruction
+// cache, and with the masked and capped forms unrolled over 128 columns 4.5
+// warps waited for instructions per issue (ncu, D = 256 with a softcap).
+__device__ __forceinline__ void prepare_scores(uint32_t taddr, bool capped, float to_y, float factor, int lo, int lim) {
+#pragma unroll 1
+    for (int c0 = 0; c0 < BN; c0 += 32) {
+        float s[32];
+        __syncwarp();
+        tmem_ld32(taddr + c0, s);
+        if (capped) {
+            tanh_32(s, to_y);
+        } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) s[c] *= factor;
+        }
+        const int l = lo - c0, h = lim - c0;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) s[c] = c >= l && c < h ? s[c] : -INFINITY;
+        __syncwarp();
+        tmem_st32(taddr + c0, reinterpret_cast<uint32_t*>(s));
+    }
+}
+
+// kPaged8: an unmasked row of raw scores in TMEM -> P = 2^(cap_out tanh(to_y s) - m)
+// over its first 64 columns, 32 scores a turn (the 16 columns that turn k
+// writes held scores of turn k / 2); returns the row's sum.
+__device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float cap_out, float m) {
+    float sum = 0.f;
+#pragma unroll 1
+    for (int k = 0; k < BN / 32; ++k) {
+        float s[32];
+        uint32_t pk[16];
+        __syncwarp();
+        tmem_ld32(taddr + 32 * k, s);
+        tanh_32(s, to_y);
+        sum += exp_row<true, 32>(s, cap_out, m, pk);
+        __syncwarp();
+        tmem_st16(taddr + 16 * k, pk);
+    }
+    return sum;
+}
+
 // kPaged8: one item's e4m3 key (V: value) rows, by a team of four (three)
 // warps, as float16 tiles in the ring slots that hold its keys (values).  A
 // 128-byte stretch of a cache row goes to eight lanes, 16 bytes each, so a
@@ -210,14 +293,16 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
         return make_int4(r[0], r[1], r[2], r[3]);
     };
     uint32_t buf[NL][4];
-    auto load = [&](int ch, const int4& rows) {
+    auto load = [&](int ch, const int4& all) {
+        // a wide slot holds half a tile's keys
+        const int4 rows = WIDE && ch ? make_int4(all.z, all.w, all.z, all.w) : all;
         auto part = [&](int x) { return x == 0 ? rows.x : (x == 1 ? rows.y : (x == 2 ? rows.z : rows.w)); };
         int src[NL];
 #pragma unroll
         for (int j = 0; j < NL; ++j) {
-            const int at = (WIDE ? 64 * ch : 0) + j * STEP;             // + row0 < STEP: the lane's row of the tile
+            const int at = j * STEP;                                    // + row0 < STEP: the lane's row of the slot
             src[j] = __shfl_sync(0xffffffffu, part(at / 32), at % 32 + row0);
-            if (at % 32 + STEP > 32 && at < 96) {                       // the warps' rows straddle two parts
+            if (at % 32 + STEP > 32 && at < (WIDE ? 32 : 96)) {                       // the warps' rows straddle two parts
                 const int next = __shfl_sync(0xffffffffu, part(at / 32 + 1), at % 32 + row0);
                 src[j] = at % 32 + row0 >= 32 ? next : src[j];
             }
@@ -275,7 +360,7 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
         ++nq;
     }
     for (int i = 0; i < c; ++i) {
-#pragma unroll
+#pragma unroll 1
         for (int ch = 0; ch < NCH; ++ch, ++nc) {
             const int s = nc % NR;
             if (!__all_sync(0xffffffffu, mbar_wait(empty0 + 8u * s, ((nc / NR) & 1) ^ 1, abort_flag))) return false;
@@ -774,6 +859,17 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (lane == 0) {
                     if (c > 0) {
                         ok = mbar_wait(q_full, nq++ & 1, abort_flag);
+                        if constexpr (KV8) {
+                            // the same order from two copies of each step (small code)
+                            if (ok) ok = issue_qk(g_t);
+                            for (int i = 0; i + 1 < c && ok; ++i) {
+                                ok = issue_qk(g_t + i + 1) && wait_o_empty(n_item);
+                                if (ok) ok = issue_pv(g_t + i, i == 0);
+                            }
+                            if (ok) mma_commit(q_empty);
+                            if (ok) ok = wait_o_empty(n_item);
+                            if (ok) ok = issue_pv(g_t + c - 1, c == 1);
+                        } else {
                         if (ok) ok = issue_qk(g_t);
                         if (ok && c > 1) ok = issue_qk(g_t + 1);
                         if (ok) ok = wait_o_empty(n_item);
@@ -783,8 +879,9 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             if (ok) ok = issue_pv(g_t + i, false);
                         }
                         if (ok) mma_commit(q_empty);               // every S of the item is issued
-                        // BSHD, kPaged8: no value row to zero, lane 0 issues the last P V too
-                        if ((!PACKED || KV8) && ok) ok = issue_pv(g_t + c - 1, c == 1);
+                        // BSHD: no value row to zero, lane 0 issues the last P V too
+                        if (!PACKED && ok) ok = issue_pv(g_t + c - 1, c == 1);
+                        }
                     } else {
                         ok = wait_o_empty(n_item);
                     }
@@ -890,12 +987,22 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 ok = __all_sync(0xffffffffu, mbar_wait(s_full(gt & 1), (gt >> 1) & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
+                const bool capped = cap_out != 0.f;
+                // kPaged8 (need_mask is the same for the whole warp): masked tiles and
+                // scales that are not positive are prepared in place; an unmasked
+                // capped tile takes its maximum from the raw scores and applies the
+                // cap with the exponential.  mul scales the row's values there.
+                const float to_y = cap_i * 0.34657359027997264f;         // scale / cap: ln(2) / 2
+                const bool prepare = KV8 && (need_mask || !(sl > 0.f));
+                const bool late_cap = KV8 && capped && !prepare;
+                const float mul = !KV8 ? sl : (capped ? cap_out : (sl > 0.f ? sl : 1.f));
+                if (prepare)
+                    prepare_scores(tmem + lane_addr + col_s, capped, to_y, sl > 0.f ? 1.f : sl, lo - kbase, lim - kbase);
                 uint32_t sr[BN];
                 tmem_ld128(tmem + lane_addr + col_s, sr);
                 float* s = reinterpret_cast<float*>(sr);
 
-                const bool capped = cap_out != 0.f;
-                const bool fast = !need_mask && sl > 0.f && !capped;
+                const bool fast = KV8 || (!need_mask && sl > 0.f && !capped);
                 float mx8[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
@@ -932,17 +1039,22 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
 #pragma unroll
                 for (int e = 0; e < 4; ++e) mx8[e] = fmaxf(mx8[e], mx8[e + 4]);
                 const float mx_raw = fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3]));
-                const float mx = fast ? mx_raw * sl : mx_raw;
+                const float mx = !fast ? mx_raw : (late_cap ? tanh_mufu(mx_raw * to_y) * mul : mx_raw * mul);
                 float alpha = 1.f;
                 if (mx > m_ref + kRescaleThreshold) {
                     alpha = fast_exp2(m_ref - mx);
                     m_ref = mx;
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-                const float fa = fast ? sl : 1.f;
-                uint32_t pk[BN / 2];
-                const float rs = exp_row<MF16>(s, fa, m_use, pk);
-                tmem_st64(tmem + lane_addr + col_s, pk);          // P over the first 64 columns of S
+                const float fa = fast ? mul : 1.f;
+                float rs;
+                if (late_cap) {
+                    rs = capped_exp(tmem + lane_addr + col_s, to_y, cap_out, m_use);
+                } else {
+                    uint32_t pk[BN / 2];
+                    rs = exp_row<MF16>(s, fa, m_use, pk);
+                    tmem_st64(tmem + lane_addr + col_s, pk);      // P over the first 64 columns of S
+                }
                 l_run = l_run * alpha + rs;
 
                 if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -1048,8 +1160,9 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     mbar_arrive(o_empty);
                 }
             };
+            constexpr int UNROLL = KV8 ? 1 : D / HALF;  // small code (see prepare_scores)
             if (cnt > 0 && boxed) {
-#pragma unroll
+#pragma unroll UNROLL
                 for (int half = 0; half < D / HALF; ++half) {
                     uint32_t ow[HALF / 2];
                     read_o(half, ow);
@@ -1078,7 +1191,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     }
                 }
             } else if (cnt > 0) {
-#pragma unroll
+#pragma unroll UNROLL
                 for (int half = 0; half < D / HALF; ++half) {
                     uint32_t ow[HALF / 2];
                     read_o(half, ow);

@@ -44,11 +44,6 @@ __device__ __forceinline__ uint64_t widen2(uint32_t w) {
         return f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
     }
 }
-__device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 __device__ __forceinline__ uint64_t swap2(uint64_t v) {
     float lo, hi;
     f32x2_split(v, lo, hi);
@@ -314,7 +309,7 @@ __device__ __forceinline__ void do_rows(const RopeArgs& a, long t, int h0, int h
 // rows until one of 64 was done: 180 instead of RESULT us at 16384 tokens, 64/8
 // heads, D = 128, e4m3 caches).
 template <int D, bool F16, bool PAGED, bool NEXT>
-__global__ void __launch_bounds__(NT, 8) qk_norm_rope_kernel(const RopeArgs a, int nq, int nk, int rows_per_warp) {
+__global__ void __launch_bounds__(NT, 7) qk_norm_rope_kernel(const RopeArgs a, int nq, int nk, int rows_per_warp) {
     const int lane = threadIdx.x % 32;
     long task = (long)blockIdx.x * (NT / 32) + threadIdx.x / 32;
     if (task < (long)a.T * nq) {
