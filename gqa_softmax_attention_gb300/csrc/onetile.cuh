@@ -140,6 +140,7 @@ struct Cfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
+constexpr float kSumLimit8 = 32768.f;          // kPaged8: P is float16
 
 // tanh of two values of magnitude at most 1: y times a polynomial of degree 6 in
 // y^2, the minimax one for the relative error on [0, 1] (Remez exchange in 40
@@ -257,7 +258,10 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     auto place = [&](int r) -> uint32_t {
         return (r / 8) * GROUP + (col >> 2) * 1024 + (r % 8) * 128 + ((((2 * col) & 7) + sw) ^ (r % 8)) * 16;
     };
-    const uint32_t to = place(row0);
+    constexpr int PER = STEP % 8 == 0 ? 1 : (STEP % 4 == 0 ? 2 : 4);      // loads after which r % 8 repeats
+    uint32_t to[PER];
+#pragma unroll
+    for (int k = 0; k < PER; ++k) to[k] = place(k * STEP + row0);
     const uint8_t* cache = static_cast<const uint8_t*>(V ? a.v_cache : a.k_cache) + (size_t)hkv * D + 16 * col;
     const uint32_t row_bytes = (uint32_t)a.Hkv * D;
     const int32_t* table = a.table + (size_t)b * a.max_pages;
@@ -327,7 +331,7 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(buf[j][e], h[2 * e], h[2 * e + 1]);
             const uint4 even = make_uint4(h[0], h[1], h[2], h[3]), odd = make_uint4(h[4], h[5], h[6], h[7]);
-            const uint32_t p = STEP % 8 == 0 ? to + j * (STEP / 8) * GROUP : place(j * STEP + row0);
+            const uint32_t p = to[j % PER] + (j / PER) * (PER * STEP / 8) * GROUP;
             *reinterpret_cast<uint4*>(dst + p) = sw ? odd : even;
             *reinterpret_cast<uint4*>(dst + (p ^ 16)) = sw ? even : odd;
         }
@@ -957,13 +961,16 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             const int lo = (int)key_lo(p_row, itm.skv, wl);
             float m_ref = -INFINITY;
             float l_run = 0.f;
+            bool has_ref = false;                      // kPaged8: every row of the warp has a reference max
             int it = 0;
             TileIter tiles(mrow, itm.first, ti.n_tiles, ti.kv_end, lane);
             auto fetch = [&](int j, uint8_t* mb) {
+                if constexpr (!KV8) {                  // kPaged8 has no padding mask
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int key = j * BN + q * 32 + lane;
-                    mb[q] = (mrow && j >= 0 && key < ti.kv_end) ? mrow[key] : (uint8_t)(mrow ? 0 : 1);
+                    for (int q = 0; q < 4; ++q) {
+                        const int key = j * BN + q * 32 + lane;
+                        mb[q] = (mrow && j >= 0 && key < ti.kv_end) ? mrow[key] : (uint8_t)(mrow ? 0 : 1);
+                    }
                 }
             };
             int j = tiles.next();
@@ -975,10 +982,12 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 fetch(jn, mbn);
                 uint32_t mw[4];
                 bool all_kept = true;
+                if constexpr (!KV8) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    mw[q] = __ballot_sync(0xffffffffu, mb[q] != 0);
-                    all_kept = all_kept && (mw[q] == 0xffffffffu);
+                    for (int q = 0; q < 4; ++q) {
+                        mw[q] = __ballot_sync(0xffffffffu, mb[q] != 0);
+                        all_kept = all_kept && (mw[q] == 0xffffffffu);
+                    }
                 }
                 const int kbase = j * BN;
                 const bool need_mask = (kbase + BN > ti.lim_first) || kbase < ti.lo_last || !all_kept;
@@ -1001,6 +1010,28 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 uint32_t sr[BN];
                 tmem_ld128(tmem + lane_addr + col_s, sr);
                 float* s = reinterpret_cast<float*>(sr);
+                if constexpr (KV8) {
+                    // Once every row of the warp has a reference max, a plain tile
+                    // is exponentiated against it without taking its own; a row
+                    // sum past kSumLimit8 (no P of the row can be larger, and
+                    // float16 holds it) sends the warp to the full step, the scores
+                    // being still in TMEM.
+                    if (has_ref && !prepare && !capped) {
+                        uint32_t pk[BN / 2];
+                        const float rs = exp_row<true>(s, mul, m_ref, pk);
+                        if (!__any_sync(0xffffffffu, rs > kSumLimit8)) {
+                            tmem_st64(tmem + lane_addr + col_s, pk);
+                            l_run += rs;
+                            tc_fence_before();
+                            mbar_arrive(p_full(gt & 1));
+                            ++it;
+                            ++gt;
+                            j = jn;
+                            continue;
+                        }
+                        tmem_ld128(tmem + lane_addr + col_s, sr);
+                    }
+                }
 
                 const bool fast = KV8 || (!need_mask && sl > 0.f && !capped);
                 float mx8[8];
@@ -1056,6 +1087,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     tmem_st64(tmem + lane_addr + col_s, pk);      // P over the first 64 columns of S
                 }
                 l_run = l_run * alpha + rs;
+                if constexpr (KV8) has_ref = __all_sync(0xffffffffu, m_ref != -INFINITY);
 
                 if (it > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
                     // PV of the previous tile must have completed before O is rescaled
