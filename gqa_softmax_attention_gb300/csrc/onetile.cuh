@@ -119,14 +119,20 @@ struct Cfg {
     static constexpr int K_GROUP = GROUPED ? KSL_C * 1024 : 1024;
     static constexpr int V_SLICE = GROUPED ? 1024 : VKEYS * 128;
     static constexpr int V_GROUP = GROUPED ? KSL * 1024 : 1024;
-    static constexpr int NS = D == 256 ? 4 : 5;         // ring slots
+    // kPaged8 at D = 128: Q lives in TMEM (64 columns beside S0, S1 and O), the A
+    // operand of S = Q K^T; shared memory then carries 160 KB a tile instead of
+    // 192 (K and V written by the wideners and read by the MMAs, and the loads
+    // through L1, which share its 128 bytes a clock), and a sixth slot
+    static constexpr bool TQ = MODE == kPaged8 && D == 128;
+    // threads at the barrier before TMEM is freed: softmax, epilogue, MMA and Q-writing warps
+    static constexpr int TMEM_USERS = 8 * 32 + 32 + (TQ ? TEAM_K8 * 32 : 0);
+    static constexpr int NS = TQ ? 6 : (D == 256 ? 4 : 5);         // ring slots
     // kPaged8: two rings, slots [0, NK8) for keys and [NK8, NS) for values, each
     // filled by one team: with one ring, a team could come to a slot whose use
-    // before last was still to be released, and a parity would not tell.  V P
-    // follows its keys' S by a tile, so values get the odd slot.
-    static constexpr int NK8 = 2, NV8 = NS - NK8;
+    // before last was still to be released, and a parity would not tell.
+    static constexpr int NK8 = NS / 2, NV8 = NS - NK8;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = OFF_Q + KSL * BOX;
+    static constexpr int OFF_RING = OFF_Q + (TQ ? 0 : KSL * BOX);
     static constexpr int OFF_STAGE = OFF_RING + NS * SLOT;   // 2 output boxes
     static constexpr int OFF_STATS = OFF_STAGE + 2 * BOX;    // m[128], l[128], visited-tile count
     static constexpr int OFF_BAR = OFF_STATS + 2 * BM * 4 + 16;
@@ -139,7 +145,7 @@ struct Cfg {
     static_assert(K_CHUNK <= SLOT && V_CHUNK <= SLOT, "ring slot");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
-constexpr uint32_t COL_S0 = 0, COL_O = 256, TMEM_COLS = 512;
+constexpr uint32_t COL_S0 = 0, COL_O = 256, COL_Q8 = 384, TMEM_COLS = 512;
 constexpr float kSumLimit8 = 32768.f;          // kPaged8: P is float16
 
 // tanh of two values of magnitude at most 1: y times a polynomial of degree 6 in
@@ -242,7 +248,7 @@ template <int D, bool F16, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t full0, uint32_t empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
                                          int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
-                                         int lane, int& nc, int& nq) {
+                                         int lane, uint32_t tmem, int& nc, int& nq) {
     constexpr int NCH = V ? C::CV : C::CK;        // slots per tile
     constexpr int NR = V ? C::NV8 : C::NK8;       // slots of this team's ring
     constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
@@ -344,10 +350,8 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     if constexpr (!V) {
         if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
         const int n_rows = nq_rows * g;
-#pragma unroll 2
-        for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += TEAM * 32) {
-            const int r = idx / (D / 8), c8 = idx % (D / 8), rr = min(r, n_rows - 1);
-            uint32_t w[4];
+        auto q_piece = [&](int r, int c8, uint32_t* w) {          // 8 dims of row r as float16
+            const int rr = min(r, n_rows - 1);
             ldg16_or_zero(w, static_cast<const uint16_t*>(a.q) +
                                  (((size_t)q_row0 + rr / g) * a.Hq + hkv * g + rr % g) * D + 8 * c8, r < n_rows);
             if constexpr (!F16) {
@@ -355,10 +359,30 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
                 for (int e = 0; e < 4; ++e)
                     w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
             }
-            *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) =
-                make_uint4(w[0], w[1], w[2], w[3]);
+        };
+        if constexpr (C::TQ) {
+            // TMEM lane = row: warp wid of the team holds rows 32 wid .. + 31
+            tc_fence_after();                     // the S MMAs that read the last Q are complete
+#pragma unroll 1
+            for (int half = 0; half < D / 64; ++half) {
+                uint32_t w[32];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q_piece(wid * 32 + lane, 8 * half + e, w + 4 * e);
+                __syncwarp();
+                tmem_st32(tmem + ((uint32_t)(wid * 32) << 16) + COL_Q8 + 32 * half, w);
+            }
+            tc_fence_before();
+        } else {
+#pragma unroll 2
+            for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += TEAM * 32) {
+                const int r = idx / (D / 8), c8 = idx % (D / 8);
+                uint32_t w[4];
+                q_piece(r, c8, w);
+                *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(q_full);
         ++nq;
@@ -579,12 +603,15 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const bool done =
                         team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(C::NK8), r_empty(C::NK8), q_full, q_empty,
                                                            abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                           it.first, it.t.n_tiles, g, wid, lane, nc, nq)
+                                                           it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq)
                                : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
                                                             abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                            it.first, it.t.n_tiles, g, wid, lane, nc, nq);
+                                                            it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq);
                     if (!done) break;
                 }
+                __syncwarp();
+                tc_fence_before();
+                if (C::TQ && !team_v) named_bar_arrive(2, C::TMEM_USERS);
             }
         } else if (!KV8 && warp == WARP_LOAD) {
             // ------------------------------------------------------------ producer
@@ -821,7 +848,12 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const int kl = kk % PER;
                     const uint32_t qoff = (kk / 4) * BOX + (kk % 4) * 32;
                     const uint32_t koff = (kl / 4) * C::K_SLICE + (kl % 4) * 32;
-                    mma_bf16_ss(d, qdesc + (qoff >> 4), kdesc[kk / PER] + (koff >> 4), IDESC_QK, kk > 0 ? 1u : 0u);
+                    if constexpr (C::TQ)
+                        mma_bf16_ts(d, tmem + COL_Q8 + 8 * kk, kdesc[kk / PER] + (koff >> 4), IDESC_QK,
+                                    kk > 0 ? 1u : 0u);
+                    else
+                        mma_bf16_ss(d, qdesc + (qoff >> 4), kdesc[kk / PER] + (koff >> 4), IDESC_QK,
+                                    kk > 0 ? 1u : 0u);
                 }
                 mma_commit(s_full(gi & 1));
                 release(false, C::CK);
@@ -931,7 +963,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mbar_drain(drain, 0);
             }
             __syncwarp();
-            named_bar_sync(2, 8 * 32 + 32);          // softmax and epilogue warps are done with TMEM
+            named_bar_sync(2, C::TMEM_USERS);        // softmax and epilogue (and Q-writing) warps are done with TMEM
             tc_fence_after();
             tmem_dealloc(tmem, TMEM_COLS);
         }
@@ -1123,7 +1155,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             mbar_arrive(stats_full);
             ++n;
         }
-        named_bar_arrive(2, 8 * 32 + 32);
+        named_bar_arrive(2, C::TMEM_USERS);
     } else {
         regs_dec<KV8 ? kRegsEpi8 : kRegsEpi>();
         // ------------------------------------------------------------ epilogue warps 4-7
@@ -1248,7 +1280,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         if (r == 0) bulk_wait_read_all();
         tc_fence_before();
-        named_bar_arrive(2, 8 * 32 + 32);
+        named_bar_arrive(2, C::TMEM_USERS);
     }
     if (threadIdx.x == 0 && *abort_flag) atomicExch(&g_onetile_error, (int)kErrPrefillWait);
 }
