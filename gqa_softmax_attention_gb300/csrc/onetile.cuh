@@ -148,18 +148,17 @@ struct Cfg {
 constexpr uint32_t COL_S0 = 0, COL_O = 256, COL_Q8 = 384, TMEM_COLS = 512;
 constexpr float kSumLimit8 = 32768.f;          // kPaged8: P is float16
 
-// tanh of two values of magnitude at most 1: y times a polynomial of degree 6 in
-// y^2, the minimax one for the relative error on [0, 1] (Remez exchange in 40
-// digits: 5.0e-8, with FP32 rounding 1.1e-7 absolute).
+// tanh of two values of magnitude at most 0.6: y times a polynomial of degree 4
+// in y^2, the minimax one for the relative error there (Remez exchange in 40
+// digits: 7.3e-08, with FP32 rounding 9.4e-08 absolute).
+constexpr float kTanhSmall = 0.6f;
 __device__ __forceinline__ uint64_t tanh2_small(uint64_t y) {
     auto both = [](float c) { return f32x2(c, c); };
     const uint64_t u = fmul2(y, y);
-    uint64_t p = ffma2(u, both(1.0410225856812554e-3f), both(-6.203378982082121e-3f));
-    p = ffma2(u, p, both(2.0289980320438973e-2f));
-    p = ffma2(u, p, both(-5.345702954900354e-2f));
-    p = ffma2(u, p, both(1.3325204077205186e-1f));
-    p = ffma2(u, p, both(-3.333283915359491e-1f));
-    p = ffma2(u, p, both(9.999999502408815e-1f));
+    uint64_t p = ffma2(u, both(0.01547542757f), both(-0.05210148018f));
+    p = ffma2(u, p, both(0.1331017366f));
+    p = ffma2(u, p, both(-0.3333230997f));
+    p = ffma2(u, p, both(0.9999999269f));
     return fmul2(y, p);
 }
 
@@ -168,20 +167,21 @@ __device__ __forceinline__ float tanh_mufu(float y) {
     return fmaf(-2.f, rcp_approx(fast_exp2(y * 2.8853900817779268f) + 1.f), 1.f);      // 2 log2(e)
 }
 
-// kPaged8: 32 raw scores -> tanh(to_y * s) (to_y = scale / softcap), in place.
-// Scores within the cap take a polynomial, 10 paired FP32 operations for two; a
-// warp with a larger one takes 1 - 2 / (e^(2y) + 1).  Warp-collective.
-__device__ __forceinline__ void tanh_32(float* s, float to_y) {
+// kPaged8: N raw scores -> tanh(to_y * s) (to_y = scale / softcap), in place.
+// Scores up to 0.6 of the cap take a polynomial, 7 paired FP32 operations for
+// two; a warp with a larger one takes 1 - 2 / (e^(2y) + 1).  Warp-collective.
+template <int N>
+__device__ __forceinline__ void tanh_cols(float* s, float to_y) {
     float am[2] = {0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < 32; c += 2) am[(c >> 1) & 1] = fmax3(am[(c >> 1) & 1], fabsf(s[c]), fabsf(s[c + 1]));
-    if (__all_sync(0xffffffffu, fmaxf(am[0], am[1]) * fabsf(to_y) <= 1.f)) {
+    for (int c = 0; c < N; c += 2) am[(c >> 1) & 1] = fmax3(am[(c >> 1) & 1], fabsf(s[c]), fabsf(s[c + 1]));
+    if (__all_sync(0xffffffffu, fmaxf(am[0], am[1]) * fabsf(to_y) <= kTanhSmall)) {
         const uint64_t k = f32x2(to_y, to_y);
 #pragma unroll
-        for (int c = 0; c < 32; c += 2) f32x2_split(tanh2_small(fmul2(f32x2(s[c], s[c + 1]), k)), s[c], s[c + 1]);
+        for (int c = 0; c < N; c += 2) f32x2_split(tanh2_small(fmul2(f32x2(s[c], s[c + 1]), k)), s[c], s[c + 1]);
     } else {
 #pragma unroll
-        for (int c = 0; c < 32; ++c) s[c] = tanh_mufu(s[c] * to_y);
+        for (int c = 0; c < N; ++c) s[c] = tanh_mufu(s[c] * to_y);
     }
 }
 
@@ -199,7 +199,7 @@ __device__ __forceinline__ void prepare_scores(uint32_t taddr, bool capped, floa
         __syncwarp();
         tmem_ld32(taddr + c0, s);
         if (capped) {
-            tanh_32(s, to_y);
+            tanh_cols<32>(s, to_y);
         } else {
 #pragma unroll
             for (int c = 0; c < 32; ++c) s[c] *= factor;
@@ -213,20 +213,20 @@ __device__ __forceinline__ void prepare_scores(uint32_t taddr, bool capped, floa
 }
 
 // kPaged8: an unmasked row of raw scores in TMEM -> P = 2^(cap_out tanh(to_y s) - m)
-// over its first 64 columns, 32 scores a turn (the 16 columns that turn k
-// writes held scores of turn k / 2); returns the row's sum.
+// over its first 64 columns, 64 scores a turn; returns the row's sum.
 __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float cap_out, float m) {
     float sum = 0.f;
 #pragma unroll 1
-    for (int k = 0; k < BN / 32; ++k) {
-        float s[32];
-        uint32_t pk[16];
+    for (int k = 0; k < BN / 64; ++k) {
+        float s[64];
+        uint32_t pk[32];
         __syncwarp();
-        tmem_ld32(taddr + 32 * k, s);
-        tanh_32(s, to_y);
-        sum += exp_row<true, 32>(s, cap_out, m, pk);
+        tmem_ld32(taddr + 64 * k, s);
+        tmem_ld32(taddr + 64 * k + 32, s + 32);
+        tanh_cols<64>(s, to_y);
+        sum += exp_row<true, 64>(s, cap_out, m, pk);
         __syncwarp();
-        tmem_st16(taddr + 16 * k, pk);
+        tmem_st32(taddr + 32 * k, pk);
     }
     return sum;
 }
