@@ -59,6 +59,8 @@ def load() -> ctypes.CDLL:
     lib.attn_fwd_paged.restype = i
     lib.attn_fwd_paged_fp8kv.argtypes = [vp] * 8 + [i, vp, vp] + [i] * 8 + [f, vp, vp, sz, vp]
     lib.attn_fwd_paged_fp8kv.restype = i
+    lib.attn_paged_fp8kv_workspace_size.argtypes = [i] * 7
+    lib.attn_paged_fp8kv_workspace_size.restype = sz
     lib.attn_paged_slots.argtypes = [vp] * 5 + [i] * 6 + [vp] * 7
     lib.attn_paged_slots.restype = i
     lib.attn_qk_norm_rope.argtypes = [vp] * 4 + [i, f] + [vp] * 3 + [i] * 5 + [vp]

@@ -443,7 +443,9 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
     codes), contiguous; k_scale / v_scale [B, Hkv] float32 CUDA tensors or None (ones):
     key t of KV head r in request b is K * k_scale[b, r], its value V *
     v_scale[b, r].  Every scale must be finite and positive; they stay on the
-    GPU and are not checked.  Other arguments as attn_fwd_paged.
+    GPU and are not checked.  Other arguments as attn_fwd_paged; the default
+    workspace (attn_paged_fp8kv_workspace_size bytes) also lets the call cut the
+    keys of few rows over long caches into parts for the idle SMs.
     Returns (o [total_q, Hq, D] like q, lse [total_q, Hq] float32).
     """
     _check_16_cuda("q", q, 3)
@@ -476,7 +478,7 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
     lib = _lib.load()
     if workspace is None:
         if split_decode:
-            need = _on(dev, lib.attn_paged_workspace_size, B, total_q, Hq, Hkv, D, page_size, max_pages)
+            need = _on(dev, lib.attn_paged_fp8kv_workspace_size, B, total_q, Hq, Hkv, D, page_size, max_pages)
         else:
             need = lib.attn_varlen_workspace_size(B, total_q, Hq, Hkv)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
@@ -490,6 +492,12 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
     if st != 0:
         _raise(st, "attn_fwd_paged_fp8kv")
     return out, lse
+
+
+def attn_paged_fp8kv_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages):
+    """Workspace bytes of attn_fwd_paged_fp8kv with everything split that may be
+    (at least attn_paged_workspace_size)."""
+    return int(_lib.load().attn_paged_fp8kv_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages))
 
 
 def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, num_pages, max_tokens, free_start=None,

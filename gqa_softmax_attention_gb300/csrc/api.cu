@@ -432,6 +432,24 @@ size_t attn_paged_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int
     return (v + 255) / 256 * 256 + p.workspace_bytes;
 }
 
+// Key-split partials of an e4m3 call's row blocks: a part for every SM at most.
+static size_t fp8_parts_bytes(int D) { return (size_t)sm_count() * 128 * (D + 1) * sizeof(float); }
+
+// Whether some split of these sizes into requests leaves so few row blocks that
+// their keys would be cut (at most half as many as SMs): a lower bound of the
+// blocks, those of total_q - B queries, which no B single queries can be.
+static bool fp8_may_split(int B, int total_q, int Hq, int Hkv) {
+    const int qpb = 128 / (Hq / Hkv);
+    const long least = ((long)(total_q > B ? total_q - B : 0) + qpb - 1) / qpb;
+    return least * Hkv * 2 <= sm_count();
+}
+
+size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    const size_t w = attn_paged_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
+    if (w == 0 || !fp8_may_split(B, total_q, Hq, Hkv)) return w;
+    return (w + 255) / 256 * 256 + fp8_parts_bytes(D);
+}
+
 // Shared checks and set-up of the two packed entry points.
 static gqa_status varlen_common(const void* q, void* o, float* lse, const int32_t* cu_q, int B, int total_q,
                                 int Hq, int Hkv, int D, int causal, float scale, const gqa_options* opts,
@@ -624,9 +642,19 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
     // keeping the share of the persistent CTAs the plan kernel computes (ws[2])
     SideStream* side = route ? side_stream(s) : nullptr;
     if (side) a.g_eff = ws + 2;
+    if (fp8) {
+        // few row blocks over long caches: cut along the keys, given the room
+        const size_t w = attn_paged_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
+        const size_t p_off = (w + 255) / 256 * 256;
+        if (fp8_may_split(B, total_q, Hq, Hkv) && workspace_bytes >= p_off + fp8_parts_bytes(D) &&
+            (reinterpret_cast<uintptr_t>(wsc) & 255u) == 0) {
+            a.part_o = reinterpret_cast<float*>(wsc + p_off);
+            a.part_lse = a.part_o + (size_t)a.num_sms * 128 * D;
+        }
+    }
     if (gqa::launch_varlen_plan(cu_seqlens_q, cache_seqlens, true, B, a.qpb, a.g, a.causal, total_q,
                                 (long)max_pages * page_size, ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e,
-                                s, route, false, side ? a.num_sms : 0, fp8) != cudaSuccess)
+                                s, route, false, side ? a.num_sms : 0, fp8, a.part_o ? a.num_sms : 0, Hkv) != cudaSuccess)
         return GQA_ERR_CUDA;
     const long items = (long)max_e * Hkv;
     auto launch_chunks = [&](cudaStream_t on) {

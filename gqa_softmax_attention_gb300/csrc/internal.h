@@ -50,6 +50,10 @@ struct PrefillArgs {
     const float* k_scale;
     const float* v_scale;
     const void* q;            // [total_q, Hq, D]: its rows are read by plain loads there
+    // key splits of each (row block, KV head): n_entries[3] parts when these are
+    // set (at most num_sms parts in all), one otherwise
+    float* part_o;            // [parts, 128, D], divided by the part's row sums
+    float* part_lse;          // [parts, 128], base 2
     uint32_t ps_mul, ps_shift;   // n / page_size = (umulhi(n, ps_mul) + n) >> ps_shift for 0 <= n < 2^31
 };
 
@@ -86,11 +90,13 @@ int prefill_d256_take_device_error();
 // two-Q-tile kernel.  With skip_single, n_entries[2] receives how many of
 // `grid` persistent CTAs the listed blocks should keep so that they and the
 // left-out decode steps, run at the same time, end together (grid when there
-// is no decode step); fp8: the caches are e4m3 bytes.
+// is no decode step); fp8: the caches are e4m3 bytes.  With split_grid (the
+// chunk kernel's CTAs) n_entries[3] receives in how many parts each block's
+// keys are cut so that few blocks over long caches still fill those CTAs.
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single = false, bool pairs = false,
-                               int grid = 0, bool fp8 = false);
+                               int grid = 0, bool fp8 = false, int split_grid = 0, int Hkv = 1);
 // tm_q / tm_o: {D, Hq, total_q} with a {64, g, qpb} box.  Packed: tm_k / tm_v
 // {D, Hkv, total_kv} with {64, 1, 128} and {64, 1, 128 or 64 (D = 256)} boxes.
 // Paged: the caches as {64, 8, D / 64, pages * page_size / 8, Hkv} with
@@ -102,6 +108,7 @@ cudaError_t launch_varlen_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_k
                                 const CUtensorMap& tm_o, const PrefillArgs& a, long max_items, cudaStream_t stream);
 // Paged over float8_e4m3fn caches (varlen_paged_fp8.cu): the caches are read
 // through a.k_cache / a.v_cache; tm_o as above; D is 128 or 256.
+// With a.part_o set, a second kernel joins the parts.
 cudaError_t launch_varlen_paged_fp8(const CUtensorMap& tm_o, const PrefillArgs& a, long max_items,
                                     cudaStream_t stream);
 int varlen_packed_take_device_error();

@@ -442,7 +442,9 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     // requests ordered by estimated cost, heaviest first; items are claimed
     // in that order from a counter in the workspace (the plan kernel zeroes
     // it), so that a CTA whose items ran long takes fewer of them.
-    const int n_items = PACKED ? n_e * a.Hkv : n_qtiles * a.B * a.Hq;
+    // kPaged8: each such item may be cut into parts along the keys
+    const int parts = KV8 && a.part_o != nullptr ? a.n_entries[3] : 1;
+    const int n_items = PACKED ? n_e * a.Hkv * parts : n_qtiles * a.B * a.Hq;
     const int G = gridDim.x;
     const int cta = blockIdx.x;
     auto item_of = [&](int r) -> int {
@@ -459,6 +461,8 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
     auto describe = [&](int w) {
         Item it;
+        const int part = KV8 ? w % parts : 0;
+        if constexpr (KV8) w /= parts;
         if constexpr (PACKED) {
             const int4* e = reinterpret_cast<const int4*>(a.entries + (size_t)(w / a.Hkv) * ENTRY_INTS);
             const int4 e0 = e[0], e1 = e[1];
@@ -485,6 +489,11 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             it.mrow = a.mask ? a.mask + (size_t)it.b * a.Skv : nullptr;
         }
         it.first = it.t.kv_begin / BN;
+        if constexpr (KV8) {
+            const int per = (it.t.n_tiles - it.first + parts - 1) / parts;
+            it.first = min(it.first + part * per, it.t.n_tiles);
+            it.t.n_tiles = min(it.first + per, it.t.n_tiles);
+        }
         return it;
     };
     // Visited key tiles of an item (non-empty, in [first, n_tiles)).  Warp-collective.
@@ -1186,7 +1195,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                                        : ((size_t)itm.b * a.Sq + ti.q0 + rq) * a.Hq + head;
             float inv = l_run > 0.f ? 1.f / l_run : 0.f;
             float lse2 = l_run > 0.f ? m_ref + log2f(l_run) : -INFINITY;
-            if (sinks && l_run > 0.f) {
+            if (sinks && l_run > 0.f && parts == 1) {
                 const float s2 = sinks[head] * 1.4426950408889634f;
                 if (s2 == INFINITY) {
                     inv = 0.f;
@@ -1201,6 +1210,36 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             if constexpr (KV8)
                 if (a.v_scale) inv *= a.v_scale[itm.b * a.Hkv + itm.hkv];
+            if (KV8 && parts > 1) {
+                // a part of the keys: FP32 rows for the joining kernel
+                const size_t prow = (size_t)w * BM + r;
+                if (cnt > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < D / 32; ++c) {
+                        float f[32];
+                        __syncwarp();
+                        tmem_ld32(tmem + lane_addr + COL_O + 32 * c, f);
+                        if (c == D / 32 - 1) {
+                            tc_fence_before();
+                            mbar_arrive(stats_empty);
+                            mbar_arrive(o_empty);
+                        }
+                        if (row_ok) {
+                            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                dst[e] = make_float4(f[4 * e] * inv, f[4 * e + 1] * inv, f[4 * e + 2] * inv,
+                                                     f[4 * e + 3] * inv);
+                        }
+                    }
+                } else {
+                    mbar_arrive(stats_empty);
+                    mbar_arrive(o_empty);
+                }
+                if (row_ok) a.part_lse[prow] = lse2;
+                ++n;
+                continue;
+            }
             // Whole blocks go out with TMA; a packed block cut by its request's
             // end is written row by row (its box would reach the next request).
             // The choice is the same for every thread of the item.

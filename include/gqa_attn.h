@@ -343,7 +343,12 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
  *   other arguments   as attn_fwd_paged, q and o 16-bit; the same workspaces
  *                     and streams (with attn_paged_workspace_size bytes the
  *                     one-query requests run on the split decode kernel of
- *                     attn_decode_paged_fp8kv, beside the chunks)
+ *                     attn_decode_paged_fp8kv, beside the chunks).  With
+ *                     attn_paged_fp8kv_workspace_size(...) bytes, 256-byte
+ *                     aligned, calls with few rows over long caches (drafted
+ *                     tokens, a chunk of one request) also cut the keys of
+ *                     each row block into parts for the idle SMs and join
+ *                     them; results agree within the usual tolerance.
  *
  * Keys and values are widened exactly to float16 and the products run in
  * float16 with FP32 accumulation: Q is rounded to float16 once, so a bfloat16
@@ -357,6 +362,11 @@ gqa_status attn_fwd_paged_fp8kv(const void* q, const void* k_cache, const void* 
                                 int B, int total_q, int Hq, int Hkv, int D, int num_pages,
                                 int max_pages, int causal, float scale, const gqa_options* opts,
                                 void* workspace, size_t workspace_bytes, gqa_stream_t stream);
+
+/* Workspace bytes of attn_fwd_paged_fp8kv with everything split that may be
+ * (attn_paged_workspace_size, and a partial row block for every SM where the
+ * sizes allow so few blocks); 0 for invalid sizes. */
+size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int page_size, int max_pages);
 
 /*
  * Metadata of one serving step, built on the device from the requests'

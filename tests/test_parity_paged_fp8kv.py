@@ -110,6 +110,52 @@ def test_matches_oracle(g, case, split_decode):
     check(p, *run(g, p, split_decode=split_decode))
 
 
+SPLIT = [
+    # few rows over long caches: the keys are cut into parts for the idle SMs
+    ([3], [5000], 8, 2, 128, 16), ([2, 5], [9000, 300], 4, 1, 128, 64), ([7], [6001], 24, 2, 256, 16),
+    ([4, 1, 2, 1], [4097, 3000, 513, 7], 8, 2, 128, 24), ([33], [1025], 16, 1, 256, 5), ([5], [2], 8, 2, 128, 16),
+    ([9, 2], [8200, 8191], 32, 8, 128, 128), ([2], [513], 4, 4, 256, 8),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("case", SPLIT, ids=[str(c[:2]) + "/%d/%d/D%d/ps%d" % c[2:] for c in SPLIT])
+def test_keys_in_parts(g, case, dtype):
+    p = inputs(*case, seed=sum(case[1]) % 89, dtype=dtype)
+    Hq, L = case[2], max(case[1])
+    sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(2))
+    sinks[0], sinks[-1] = INF, -INF
+    for kw in (dict(), dict(sinks=sinks), dict(window_left=L // 3), dict(window_left=200, softcap=9.0, sinks=sinks),
+               dict(causal=False, window_left=L // 2, window_right=3)):
+        check(p, *run(g, p, **kw), label=str(kw), **kw)
+
+
+def test_keys_in_parts_of_a_replayed_call(g):
+    """The number of parts follows the lengths on the device; each call fills the same workspace."""
+    p = inputs([6, 3], [7000, 900], 8, 2, 128, 64, seed=2)
+    for n in ("k_cache", "v_cache"):
+        c = p[n].view(torch.uint8)
+        p[n] = torch.where(c == 0x7F, torch.zeros_like(c), c).view(torch.float8_e4m3fn)
+    dev = {n: p[n].cuda() for n in NAMES}
+    size = g.attn_paged_fp8kv_workspace_size(2, 9, 8, 2, 128, 64, p["block_table"].shape[1])
+    assert size > g.attn_paged_workspace_size(2, 9, 8, 2, 128, 64, p["block_table"].shape[1])
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(dev["q"]), torch.empty((9, 8), device="cuda")
+    call = lambda: g.attn_fwd_paged_fp8kv(*[dev[n] for n in NAMES], out=out, lse=lse, workspace=ws)  # noqa: E731
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens, cu in (([7000, 900], [0, 6, 9]), ([130, 40], [0, 6, 9]), ([3000, 899], [0, 8, 9]), ([2, 0], [0, 6, 9])):
+        p["cache_seqlens"], p["cu_seqlens_q"] = (torch.tensor(x, dtype=torch.int32) for x in (lens, cu))
+        dev["cache_seqlens"].copy_(p["cache_seqlens"])
+        dev["cu_seqlens_q"].copy_(p["cu_seqlens_q"])
+        graph.replay()
+        torch.cuda.synchronize()
+        check(p, out.cpu(), lse.cpu(), "replay %s" % lens)
+
+
 @pytest.mark.parametrize("split_decode", [True, False], ids=["split_decode", "packed_only"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "fp16"])
 @pytest.mark.parametrize("geometry", [(24, 2, 256, 32), (32, 8, 128, 64)], ids=str)
