@@ -396,7 +396,7 @@ def attn_fwd_paged(q, k_cache, v_cache, cu_seqlens_q, cache_seqlens, block_table
 
 def _on(device, fn, *args):
     """fn(*args) with `device` current (the library works on the current device)."""
-    if device.index == torch.cuda.current_device():
+    if device.index == torch._C._cuda_getDevice():
         return fn(*args)
     with torch.cuda.device(device):
         return fn(*args)
@@ -412,7 +412,7 @@ def _data(name, t, dtype, shape, device):
     The test that every good argument passes comes first: these calls are
     launched for a few microseconds of work."""
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass

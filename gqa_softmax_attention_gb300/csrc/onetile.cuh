@@ -257,12 +257,14 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     constexpr int NL = (32 + TEAM - 1) / TEAM;    // a warp's loads of a slot
     constexpr int STEP = TEAM * (32 / LPR);       // rows between a warp's loads
     constexpr int GROUP = V ? C::V_GROUP : C::K_GROUP;
-    const int row0 = wid * (32 / LPR) + lane / LPR;      // this lane's row of the first load
-    const int col = lane % LPR;                          // its 16-byte column
+    // This lane's row and 16-byte column of the first load: eight lanes take half
+    // a 128-byte slice of two neighbouring rows, so that their even (or odd)
+    // chunks lie in eight different bank groups of the swizzled tile.
+    const int row0 = wid * (32 / LPR) + (WIDE ? 0 : 2 * (lane >> 4)) + ((lane >> 2) & 1);
+    const int col = (lane & 3) + 4 * (WIDE ? lane >> 3 : (lane >> 3) & 1);
     // where the first of its two chunks of row r goes (the second: bit 4 flipped)
-    const int sw = (lane >> 2) & 1;
     auto place = [&](int r) -> uint32_t {
-        return (r / 8) * GROUP + (col >> 2) * 1024 + (r % 8) * 128 + ((((2 * col) & 7) + sw) ^ (r % 8)) * 16;
+        return (r / 8) * GROUP + (col >> 2) * 1024 + (r % 8) * 128 + (((2 * col) & 7) ^ (r % 8)) * 16;
     };
     constexpr int PER = STEP % 8 == 0 ? 1 : (STEP % 4 == 0 ? 2 : 4);      // loads after which r % 8 repeats
     uint32_t to[PER];
@@ -336,10 +338,9 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
             uint32_t h[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) e4m3x4_to_f16x4(buf[j][e], h[2 * e], h[2 * e + 1]);
-            const uint4 even = make_uint4(h[0], h[1], h[2], h[3]), odd = make_uint4(h[4], h[5], h[6], h[7]);
             const uint32_t p = to[j % PER] + (j / PER) * (PER * STEP / 8) * GROUP;
-            *reinterpret_cast<uint4*>(dst + p) = sw ? odd : even;
-            *reinterpret_cast<uint4*>(dst + (p ^ 16)) = sw ? even : odd;
+            *reinterpret_cast<uint4*>(dst + p) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(dst + (p ^ 16)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
     };
 
