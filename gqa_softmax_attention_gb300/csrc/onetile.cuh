@@ -89,13 +89,15 @@ constexpr int kRegsSoftmax = 208;
 constexpr int kRegsEpi = 152;
 constexpr int kRegsOther = 144;
 static_assert((kRegsSoftmax + kRegsEpi + kRegsOther) * 128 <= kRegsLaunch * NUM_THREADS, "register split");
-// kPaged8: warps 8-11 widen keys, 12-14 values, 15 issues the MMAs.  128
+// kPaged8: warps 8-10 widen keys, 12-15 values, 11 issues the MMAs.  128
 // registers per thread at launch (four warps on each SM sub-partition); softmax
-// 208, epilogue 96, the other two warpgroups 104 each.
+// 208, epilogue 96, the other two warpgroups 104 each.  The values get the
+// fourth warp: P V comes last in a tile, and with three warps the MMAs waited
+// 1600 cycles a tile for values and 380 for keys (D = 256).
 constexpr int NUM_THREADS8 = 512;
 constexpr int WARP_V8 = 12;
-constexpr int WARP_MMA8 = 15;
-constexpr int TEAM_K8 = 4, TEAM_V8 = 3;        // warps of a widening team
+constexpr int WARP_MMA8 = 11;
+constexpr int TEAM_K8 = 3, TEAM_V8 = 4;        // warps of a widening team
 constexpr int kRegsEpi8 = 96;
 constexpr int kRegsOther8 = 104;
 static_assert((kRegsSoftmax + kRegsEpi8 + 2 * kRegsOther8) * 128 <= 128 * NUM_THREADS8, "register split");
@@ -125,7 +127,7 @@ struct Cfg {
     // through L1, which share its 128 bytes a clock), and a sixth slot
     static constexpr bool TQ = MODE == kPaged8 && D == 128;
     // threads at the barrier before TMEM is freed: softmax, epilogue, MMA and Q-writing warps
-    static constexpr int TMEM_USERS = 8 * 32 + 32 + (TQ ? TEAM_K8 * 32 : 0);
+    static constexpr int TMEM_USERS = 8 * 32 + 32 + (TQ ? TEAM_V8 * 32 : 0);
     static constexpr int NS = TQ ? 6 : (D == 256 ? 4 : 5);         // ring slots
     // kPaged8: two rings, slots [0, NK8) for keys and [NK8, NS) for values, each
     // filled by one team: with one ring, a team could come to a slot whose use
@@ -231,7 +233,7 @@ __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float ca
     return sum;
 }
 
-// kPaged8: one item's e4m3 key (V: value) rows, by a team of four (three)
+// kPaged8: one item's e4m3 key (V: value) rows, by a team of three (four)
 // warps, as float16 tiles in the ring slots that hold its keys (values).  A
 // 128-byte stretch of a cache row goes to eight lanes, 16 bytes each, so a
 // warp's load covers 512 bytes, and a slot takes 32 of them.  The loads of the
@@ -242,8 +244,9 @@ __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float ca
 // may spill: the streaming loads evict local memory from the small L1 beside
 // 227 KB of shared memory, and every reload then goes to L2 (10.6 ms instead of
 // RESULT on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128).
-// The key team also writes the Q block (rows q_row0 .. of the packed batch,
-// packed r = query * g + head, bfloat16 rounded to float16), zeros past it.
+// The value team (without TQ both) also writes the Q block (rows q_row0 .. of the
+// packed batch, packed r = query * g + head, bfloat16 rounded to float16), zeros
+// past it.
 template <int D, bool F16, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t full0, uint32_t empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
@@ -348,39 +351,58 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     int4 rows = find_rows(find_pages(first));
     load(0, rows);
     Pages pages = find_pages(first + 1);          // a tile ahead of their use
-    if constexpr (!V) {
-        if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
+    if constexpr (V || !C::TQ) {
         const int n_rows = nq_rows * g;
-        auto q_piece = [&](int r, int c8, uint32_t* w) {          // 8 dims of row r as float16
+        auto q_piece = [&](int r, int c8, uint32_t* w) {          // 8 dims of row r
             const int rr = min(r, n_rows - 1);
             ldg16_or_zero(w, static_cast<const uint16_t*>(a.q) +
                                  (((size_t)q_row0 + rr / g) * a.Hq + hkv * g + rr % g) * D + 8 * c8, r < n_rows);
+        };
+        auto to_f16 = [&](uint32_t* w, int n) {
             if constexpr (!F16) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
+                for (int e = 0; e < n; ++e)
                     w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
             }
         };
         if constexpr (C::TQ) {
-            // TMEM lane = row: warp wid of the team holds rows 32 wid .. + 31
+            // TMEM lane = row: warp wid of the team (warp 12 + wid) holds rows 32 wid .. + 31
+            if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
             tc_fence_after();                     // the S MMAs that read the last Q are complete
 #pragma unroll 1
             for (int half = 0; half < D / 64; ++half) {
                 uint32_t w[32];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) q_piece(wid * 32 + lane, 8 * half + e, w + 4 * e);
+                to_f16(w, 32);
                 __syncwarp();
                 tmem_st32(tmem + ((uint32_t)(wid * 32) << 16) + COL_Q8 + 32 * half, w);
             }
             tc_fence_before();
         } else {
-#pragma unroll 2
-            for (int idx = wid * 32 + lane; idx < BM * (D / 8); idx += TEAM * 32) {
-                const int r = idx / (D / 8), c8 = idx % (D / 8);
-                uint32_t w[4];
-                q_piece(r, c8, w);
-                *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 + (((c8 & 7) ^ (r & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+            // both teams, QB pieces a thread in flight (by one team, two at a time,
+            // the block took 16000 cycles, an eighth of an item of
+            // 6000 keys at D = 256)
+            constexpr int QB = 4, QT = 32 * (TEAM_K8 + TEAM_V8);
+            const int t = (V ? TEAM_K8 + wid : wid) * 32 + lane;
+#pragma unroll 1
+            for (int base = 0; base < BM * (D / 8); base += QB * QT) {
+                uint32_t w[QB][4];
+#pragma unroll
+                for (int u = 0; u < QB; ++u) {
+                    const int idx = base + u * QT + t;
+                    q_piece(idx / (D / 8), idx % (D / 8), w[u]);
+                }
+                if (base == 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
+#pragma unroll
+                for (int u = 0; u < QB; ++u) {
+                    const int idx = base + u * QT + t, r = idx / (D / 8), c8 = idx % (D / 8);
+                    to_f16(w[u], 4);
+                    if (idx < BM * (D / 8))
+                        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 +
+                                                  (((c8 & 7) ^ (r & 7)) << 4)) =
+                            make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
+                }
             }
             fence_proxy_async_smem();
         }
@@ -557,7 +579,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, KV8 ? TEAM_K8 : 1);
+        mbar_init(q_full, !KV8 ? 1 : TEAM_V8 + (C::TQ ? 0 : TEAM_K8));      // TMA, or the warps that write Q
         mbar_init(q_empty, 1);
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(r_full(s), !KV8 ? 1 : (s < C::NK8 ? TEAM_K8 : TEAM_V8));     // TMA, or the widening team
@@ -621,7 +643,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 }
                 __syncwarp();
                 tc_fence_before();
-                if (C::TQ && !team_v) named_bar_arrive(2, C::TMEM_USERS);
+                if (C::TQ && team_v) named_bar_arrive(2, C::TMEM_USERS);
             }
         } else if (!KV8 && warp == WARP_LOAD) {
             // ------------------------------------------------------------ producer
@@ -837,8 +859,11 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 tc_fence_after();
                 return true;
             };
+            // lane 0; kPaged8: the first of two chunks is released as soon as its
+            // MMAs are issued (so that the wideners refill it meanwhile)
+            auto release_half = [&](bool v) { mma_commit(r_empty(slot_of(v, 0))); };
             auto release = [&](bool v, int n) {             // lane 0
-                for (int k = 0; k < n; ++k) mma_commit(r_empty(slot_of(v, k)));
+                for (int k = KV8 ? n - 1 : 0; k < n; ++k) mma_commit(r_empty(slot_of(v, k)));
                 if (KV8 && v) nv += n;
                 else nc += n;
             };
@@ -864,6 +889,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     else
                         mma_bf16_ss(d, qdesc + (qoff >> 4), kdesc[kk / PER] + (koff >> 4), IDESC_QK,
                                     kk > 0 ? 1u : 0u);
+                    if (KV8 && C::CK == 2 && kk == PER - 1) release_half(false);
                 }
                 mma_commit(s_full(gi & 1));
                 release(false, C::CK);
@@ -881,6 +907,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const int kc = (kk % PER) * 16;
                     mma_bf16_ts(tmem + COL_O, p + kk * 8, vdesc[kk / PER] + (((kc / 8) * C::V_GROUP) >> 4), IDESC_PV,
                                 (!fresh || kk > 0) ? 1u : 0u);
+                    if (KV8 && C::CV == 2 && kk == PER - 1) release_half(true);
                 }
                 release(true, C::CV);
                 mma_commit(o_ready);
