@@ -727,6 +727,16 @@ gqa_status attn_fwd_paged_fp8kv(const void* q, const void* k_cache, const void* 
                      workspace_bytes, stream);
 }
 
+// A stretch of memory (none: a null pointer or no bytes).
+struct Span {
+    const void* p;
+    long bytes;
+};
+static bool overlap(const Span& x, const Span& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
+}
+
 // ---------------------------------------------------------------- step metadata
 gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
                             const int32_t* free_pages, const int32_t* free_start, int B, int max_pages,
@@ -745,11 +755,16 @@ gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, i
                           (const void*)cache_seqlens, (const void*)slots, (const void*)positions,
                           (const void*)requests, (const void*)counts})
         if (!aligned4(p)) return GQA_ERR_MISALIGNED;
-    // every block reads the lengths and free_start while block 0 writes its results
-    for (const void* r : {(const void*)past_lens, (const void*)new_lens, (const void*)free_start})
-        for (const void* w : {(const void*)cu_seqlens_q, (const void*)cache_seqlens, (const void*)counts})
-            if (r && r == w) return GQA_ERR_INVALID_ARG;
-    if (free_start && free_start > counts && free_start < counts + 3) return GQA_ERR_INVALID_ARG;
+    // every block reads its inputs while others write results: no overlap
+    const Span reads[] = {{past_lens, B * 4L}, {new_lens, B * 4L}, {free_start, 4}, {free_pages, num_free * 4L},
+                          {block_table, (long)B * max_pages * 4}};
+    const Span writes[] = {{cu_seqlens_q, (B + 1) * 4L}, {cache_seqlens, B * 4L}, {counts, 12},
+                           {slots, max_tokens * 4L}, {positions, max_tokens * 4L}, {requests, max_tokens * 4L}};
+    for (const Span& w : writes)
+        for (const Span& r : reads)
+            if (overlap(w, r)) return GQA_ERR_INVALID_ARG;
+    for (int i = 0; i < 4; ++i)
+        if (overlap(reads[i], reads[4])) return GQA_ERR_INVALID_ARG;        // the table is written too
     gqa::SlotArgs a{};
     a.past_lens = past_lens; a.new_lens = new_lens;
     a.block_table = block_table; a.free_pages = free_pages; a.free_start = free_start;
@@ -812,6 +827,18 @@ static gqa_status rope_common(const gqa_head_rows* q, const gqa_head_rows* k, co
     return GQA_OK;
 }
 
+// Bytes from the first to the last value of T rows of H heads.
+static Span span_of(const gqa_head_rows* r, int T, int H, int D) {
+    return {r->data, ((T - 1L) * r->token_stride + (H - 1L) * r->head_stride + D) * 2};
+}
+// Whether `out` [T, H, D] may be written while `in` of the same shape is read:
+// apart, or the very rows (each warp reads a row before it writes it).
+static bool may_write(const void* out, const gqa_head_rows* in, int T, int H, int D) {
+    const bool same = out == in->data && (T == 1 || in->token_stride == (long)H * D) &&
+                      (H == 1 || in->head_stride == D);
+    return same || !overlap({out, (long)T * H * D * 2}, span_of(in, T, H, D));
+}
+
 gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, const void* q_weight,
                              const void* k_weight, int weight_f32, float eps, const gqa_rope* rope, void* q_out,
                              void* k_out, int T, int Hq, int Hkv, int D, int dtype, gqa_stream_t stream) {
@@ -821,6 +848,10 @@ gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, con
     if (st != GQA_OK || T == 0) return st;
     if (!k_out) return GQA_ERR_INVALID_ARG;
     if (!aligned16(k_out)) return GQA_ERR_MISALIGNED;
+    const Span qo{q_out, (long)T * Hq * D * 2}, ko{k_out, (long)T * Hkv * D * 2};
+    if (!may_write(q_out, q, T, Hq, D) || !may_write(k_out, k, T, Hkv, D) || overlap(qo, ko) ||
+        overlap(qo, span_of(k, T, Hkv, D)) || overlap(ko, span_of(q, T, Hq, D)))
+        return GQA_ERR_INVALID_ARG;
     a.k_out = k_out;
     return gqa::launch_qk_norm_rope(a, D, dtype == GQA_FP16, false, sm_count(),
                                     reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
@@ -848,6 +879,13 @@ gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* 
     if (!aligned4(slots) || !aligned4(requests) || !aligned4(k_scale) || !aligned4(v_scale)) return GQA_ERR_MISALIGNED;
     if (v->token_stride < 0 || v->head_stride < 0) return GQA_ERR_INVALID_ARG;
     if (v->token_stride % 8 || v->head_stride % 8) return GQA_ERR_MISALIGNED;
+    const Span qo{q_out, (long)T * Hq * D * 2}, sq = span_of(q, T, Hq, D), sk = span_of(k, T, Hkv, D),
+               sv = span_of(v, T, Hkv, D);
+    const long pool = (long)num_pages * page_size * Hkv * D * (e4m3 ? 1 : 2);
+    const Span kc{k_cache, pool}, vc{v_cache, pool};
+    if (!may_write(q_out, q, T, Hq, D) || overlap(qo, sk) || overlap(qo, sv) || overlap(kc, vc)) return GQA_ERR_INVALID_ARG;
+    for (const Span& c : {kc, vc})
+        if (overlap(c, qo) || overlap(c, sq) || overlap(c, sk) || overlap(c, sv)) return GQA_ERR_INVALID_ARG;
     a.v = v->data; a.v_ts = v->token_stride; a.v_hs = v->head_stride;
     a.slots = slots;
     a.requests = requests;

@@ -243,15 +243,15 @@ __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float ca
 // the eight lanes of a store cover eight different bank groups.  Nothing here
 // may spill: the streaming loads evict local memory from the small L1 beside
 // 227 KB of shared memory, and every reload then goes to L2 (10.6 ms instead of
-// RESULT on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128).
+// 3.8 on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128).
 // The value team (without TQ both) also writes the Q block (rows q_row0 .. of the
 // packed batch, packed r = query * g + head, bfloat16 rounded to float16), zeros
 // past it.
 template <int D, bool F16, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t full0, uint32_t empty0,
                                          uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
-                                         int q_row0, int nq_rows, int skv, int first, int n_tiles, int g, int wid,
-                                         int lane, uint32_t tmem, int& nc, int& nq) {
+                                         int q_row0, int nq_rows, int skv, int kv_begin, int first, int n_tiles, int g,
+                                         int wid, int lane, uint32_t tmem, int& nc, int& nq) {
     constexpr int NCH = V ? C::CV : C::CK;        // slots per tile
     constexpr int NR = V ? C::NV8 : C::NK8;       // slots of this team's ring
     constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
@@ -279,7 +279,8 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     // Keys of a tile, lane l holding l, l + 32, l + 64 and l + 96: their pages
     // and places in them; and, once the pages have arrived, their cache rows.  A
     // key past the request's end takes the last key's row (its score is masked
-    // and its weight 0), one of a page outside the pool row 0, marked to be
+    // and its weight 0); one of a page outside the pool, or left of every window
+    // of the block (its page may hold anything by now), row 0, marked to be
     // zeroed.  No load stands in a branch: what a branch loads may be moved to
     // its register at the branch's end, which waits out the load's latency.
     struct Pages {
@@ -297,11 +298,11 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
         return p;
     };
     uint32_t bad[4];                               // keys of the tile (32 a word) to be zeroed
-    auto find_rows = [&](const Pages& p) -> int4 {
+    auto find_rows = [&](int tile, const Pages& p) -> int4 {
         int r[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const bool in = (uint32_t)p.page[x] < (uint32_t)a.num_pages;
+            const bool in = (uint32_t)p.page[x] < (uint32_t)a.num_pages && tile * BN + 32 * x + lane >= kv_begin;
             bad[x] = __ballot_sync(0xffffffffu, !in);
             r[x] = in ? p.page[x] * a.page_size + p.off[x] : 0;
         }
@@ -348,7 +349,7 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     };
 
     const int c = n_tiles - first;
-    int4 rows = find_rows(find_pages(first));
+    int4 rows = find_rows(first, find_pages(first));
     load(0, rows);
     Pages pages = find_pages(first + 1);          // a tile ahead of their use
     if constexpr (V || !C::TQ) {
@@ -419,7 +420,7 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
             fence_proxy_async_smem();             // the tensor core reads what the warp wrote
             __syncwarp();
             if (lane == 0) mbar_arrive(full0 + 8u * s);
-            if (ch + 1 == NCH) rows = find_rows(pages);
+            if (ch + 1 == NCH) rows = find_rows(first + i + 1, pages);
             load(ch + 1 < NCH ? ch + 1 : 0, rows);           // past the last tile: the last key's row again
         }
         pages = find_pages(first + i + 2);
@@ -635,10 +636,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     const bool done =
                         team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(C::NK8), r_empty(C::NK8), q_full, q_empty,
                                                            abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                           it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq)
+                                                           it.t.kv_begin, it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq)
                                : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
                                                             abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                            it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq);
+                                                            it.t.kv_begin, it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq);
                     if (!done) break;
                 }
                 __syncwarp();

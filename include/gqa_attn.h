@@ -379,7 +379,7 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
  *                entered behind (no other entry is written)
  *   free_pages   [num_free] int32 page ids, handed out in request order from
  *                index *free_start on (free_start: one device int32, or NULL
- *                for 0; it must not be part of counts)
+ *                for 0)
  *   max_tokens   rows of the packed batch, padding included
  *   cu_seqlens_q [B + 1] (written): min(sum of new_lens before b, max_tokens)
  *   cache_seqlens [B] (written): min(past + new, max_pages * page_size)
@@ -395,8 +395,8 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
  * is exhausted (the table entry is then -1 too) or the page id lies outside
  * [0, num_pages).  Tokens past max_tokens are counted, but get no row and no
  * page: counts[0] > max_tokens asks for another call with more rows.  The call
- * changes nothing it reads, so it may be repeated or replayed.  One launch, no
- * workspace, no host read-back.
+ * changes nothing it reads (an output that overlaps an input is refused), so it
+ * may be repeated or replayed.  One launch, no workspace, no host read-back.
  */
 gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
                             const int32_t* free_pages, const int32_t* free_start, int B, int max_pages,
@@ -449,7 +449,7 @@ typedef struct {
  *   rope                NULL for no rotation
  *   q_out [T, Hq, D], k_out [T, Hkv, D]   contiguous, of the same type
  *                       (written); q_out may be q and k_out k where those are
- *                       contiguous, any other overlap is a caller error
+ *                       contiguous, any other overlap is refused
  *
  * D = 64, 128 or 256.  T = 0 does nothing.
  */

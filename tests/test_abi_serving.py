@@ -20,8 +20,12 @@ def lib():
     return _lib.load()
 
 
-def slots(lib, past=A16, new=A16, table=A16b, free=A16, start=None, B=2, max_pages=4, ps=16, pages=10, n_free=3, T=8,
-          cu=A16b, lens=A16b, slot=A16b, pos=A16b, req=A16b, counts=A16c):
+def at(k):
+    return P((4 << 20) + (k << 12))                     # stand-in buffers of 4 KB
+
+
+def slots(lib, past=at(0), new=at(1), table=at(2), free=at(3), start=None, B=2, max_pages=4, ps=16, pages=10, n_free=3,
+          T=8, cu=at(4), lens=at(5), slot=at(6), pos=at(7), req=at(8), counts=at(9)):
     return lib.attn_paged_slots(past, new, table, free, start, B, max_pages, ps, pages, n_free, T, cu, lens, slot, pos,
                                 req, counts, None)
 
@@ -30,8 +34,8 @@ def test_paged_slots_argument_checks(lib):
     for bad in (dict(B=0), dict(B=-1), dict(max_pages=0), dict(ps=0), dict(pages=-1), dict(n_free=-1), dict(T=-1),
                 dict(past=None), dict(new=None), dict(table=None), dict(free=None), dict(cu=None), dict(lens=None),
                 dict(slot=None), dict(pos=None), dict(req=None), dict(counts=None), dict(max_pages=1 << 26),
-                dict(T=1 << 30), dict(start=A16c), dict(start=P((3 << 20) + 4)), dict(start=P((3 << 20) + 8)),
-                dict(lens=A16), dict(counts=A16)):
+                dict(T=1 << 30), dict(start=at(9)), dict(start=P(at(9).value + 8)), dict(lens=at(0)), dict(counts=at(1)),
+                dict(cu=P(at(1).value + 4)), dict(slot=at(3)), dict(req=P(at(2).value + 28)), dict(past=at(2))):
         assert slots(lib, **bad) == INVALID, bad
     assert slots(lib, pages=1 << 27) == UNSUPPORTED
     for name in ("past", "new", "table", "free", "start", "cu", "lens", "slot", "pos", "req", "counts"):
@@ -74,6 +78,17 @@ def test_qk_norm_rope_argument_checks(lib, call):
                 dict(r=rope(cos=MIS)), dict(r=rope(pos=MIS))):
         assert call(lib, **bad) == MISALIGNED, bad
     assert call(lib, T=0, q=rows(data=None), k=rows(data=None), qo=None) == OK
+
+
+def test_qk_norm_rope_refuses_overlaps(lib):
+    """Outputs may be the very input rows; nothing else may overlap (T = 4: 8 KB of q, 2 KB of k)."""
+    q, k, v = rows(at(0)), rows(at(8), 256), rows(at(16), 256)
+    far, far2 = at(64), at(128)
+    for bad in (dict(q=q, k=k, qo=P(at(0).value + 16)), dict(q=q, k=k, qo=at(8)), dict(q=q, k=k, ko=at(0)),
+                dict(q=q, k=k, qo=far, ko=far), dict(q=rows(at(0), 1280), k=k, qo=at(0))):
+        assert dense(lib, **{**dict(ko=far2), **bad}) == INVALID, bad
+    for bad in (dict(qo=at(16)), dict(kc=at(16)), dict(vc=at(0)), dict(kc=at(200), vc=at(200)), dict(kc=at(64))):
+        assert paged(lib, **{**dict(q=q, k=k, v=v, qo=far, kc=at(200), vc=at(400)), **bad}) == INVALID, bad
 
 
 def test_qk_norm_rope_own_checks(lib):

@@ -181,7 +181,7 @@ def test_refusals(g):
     for bad in (dict(past_lens=i32(past).long()), dict(new_lens=i32(new[:3])), dict(block_table=i32(table)[:, ::2]),
                 dict(block_table=i32(table).cpu()), dict(free_pages=i32([free])), dict(page_size=0),
                 dict(max_tokens=-1), dict(num_pages=-1), dict(free_start=i32([0, 0])), dict(out=counts[:5]),
-                dict(out=counts, free_start=counts[5][1:2]), dict(max_tokens=13, out=counts),
+                dict(out=counts, free_start=counts[5][1:2]), dict(out=counts, past_lens=counts[1]), dict(max_tokens=13, out=counts),
                 dict(past_lens=i32([]), new_lens=i32([]), block_table=torch.empty(0, 4, dtype=torch.int32,
                                                                                   device="cuda"))):
         with pytest.raises(ValueError):

@@ -165,7 +165,8 @@ def test_options(g, geometry, dtype, split_decode):
     sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(9)) * 2
     sinks[0], sinks[-1] = -INF, INF
     for kw in (dict(window_left=300, softcap=20.0, sinks=sinks), dict(window_left=0), dict(softcap=5.0),
-               dict(window_left=129, window_right=0, scale=0.03), dict(scale=-0.1), dict(scale=0.0)):
+               dict(window_left=129, window_right=0, scale=0.03), dict(scale=-0.1), dict(scale=0.0),
+               dict(scale=-0.1, softcap=4.0), dict(scale=0.0, softcap=4.0), dict(scale=2.0, softcap=1.5)):
         check(p, *run(g, p, split_decode=split_decode, **kw), label=str(kw), **kw)
 
 
@@ -236,6 +237,27 @@ def test_bad_page_ids_read_as_zeros_and_stay_in_the_pool(g):
         z[n] = z[n].view(torch.float8_e4m3fn)
     o2, lse2 = run(g, z)
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("D", [128, 256])
+def test_pages_left_of_every_window_may_hold_anything(g, D):
+    """Slots that no query's window reaches any more: freed pages (NaN codes here, or no page at all)."""
+    p = inputs([40, 3, 200], [1000, 700, 900], 8, 2, D, 16, seed=14)
+    wl = 100
+    want = run(g, p, window_left=wl)
+    check(p, *want, window_left=wl)
+    z = dict(p, block_table=p["block_table"].clone())
+    kc, vc = (p[n].view(torch.uint8).clone() for n in ("k_cache", "v_cache"))
+    for b, (n, L) in enumerate(zip([40, 3, 200], [1000, 700, 900])):
+        dead = L - n - wl                                  # keys below it are left of the first query's window
+        for t in range(dead):
+            kc[p["block_table"][b, t // 16], t % 16] = 0x7F
+            vc[p["block_table"][b, t // 16], t % 16] = 0x7F
+        z["block_table"][b, :dead // 16] = -1
+    z["k_cache"], z["v_cache"] = kc.view(torch.float8_e4m3fn), vc.view(torch.float8_e4m3fn)
+    for case in (z, dict(z, block_table=p["block_table"])):
+        got = run(g, case, window_left=wl, split_decode=False)
+        check(p, *got, window_left=wl)
 
 
 def test_rows_outside_the_requests_stay(g):

@@ -333,6 +333,11 @@ def test_refusals(g):
                 dict(out=(torch.empty(T, 8, 2 * D, dtype=q.dtype, device="cuda")[..., :D], torch.empty_like(k)))):
         with pytest.raises(ValueError):
             g.attn_qk_norm_rope(**{**dict(q=q, k=k, cos_sin=table, positions=pos, q_weight=qw, k_weight=kw), **bad})
+    qc, kk = q.contiguous(), k.contiguous()
+    for bad in (dict(q=qc, out=(qc[:1].expand(T, 8, D), torch.empty_like(kk))), dict(k=kk, out=(torch.empty_like(qc), qc[:, :2])),
+                dict(q=kk, k=kk, out=(kk, torch.empty_like(kk)))):
+        with pytest.raises(ValueError):
+            g.attn_qk_norm_rope(**{**dict(q=q, k=k, cos_sin=table, positions=pos, q_weight=qw, k_weight=kw), **bad})
     for bad in (dict(v=v[:3]), dict(v=v[:, :1]), dict(slots=slots.long()), dict(slots=slots[:3]),
                 dict(k_cache=kc.half()), dict(k_cache=kc[:, ::2]), dict(v_cache=vc[:1]), dict(k_scale=s),
                 dict(requests=slots), dict(k_cache=kc.cpu()),
