@@ -765,6 +765,9 @@ gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, i
             if (overlap(w, r)) return GQA_ERR_INVALID_ARG;
     for (int i = 0; i < 4; ++i)
         if (overlap(reads[i], reads[4])) return GQA_ERR_INVALID_ARG;        // the table is written too
+    for (int i = 0; i < 6; ++i)
+        for (int j = 0; j < i; ++j)
+            if (overlap(writes[i], writes[j])) return GQA_ERR_INVALID_ARG;
     gqa::SlotArgs a{};
     a.past_lens = past_lens; a.new_lens = new_lens;
     a.block_table = block_table; a.free_pages = free_pages; a.free_start = free_start;

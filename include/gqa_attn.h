@@ -395,8 +395,8 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
  * is exhausted (the table entry is then -1 too) or the page id lies outside
  * [0, num_pages).  Tokens past max_tokens are counted, but get no row and no
  * page: counts[0] > max_tokens asks for another call with more rows.  The call
- * changes nothing it reads (an output that overlaps an input is refused), so it
- * may be repeated or replayed.  One launch, no workspace, no host read-back.
+ * changes nothing it reads (an output that overlaps an input or another output
+ * is refused), so it may be repeated or replayed.  One launch, no workspace, no host read-back.
  */
 gqa_status attn_paged_slots(const int32_t* past_lens, const int32_t* new_lens, int32_t* block_table,
                             const int32_t* free_pages, const int32_t* free_start, int B, int max_pages,

@@ -42,6 +42,16 @@ def test_paged_slots_argument_checks(lib):
         assert slots(lib, **{name: MIS}) == MISALIGNED, name
 
 
+def test_paged_slots_refuses_outputs_over_each_other(lib):
+    outs = dict(cu=at(4), lens=at(5), slot=at(6), pos=at(7), req=at(8), counts=at(9))      # B = 2, T = 8
+    for a in outs:
+        for b in outs:
+            if a != b:
+                assert slots(lib, **{a: outs[b]}) == INVALID, (a, b)
+    assert slots(lib, pos=P(at(6).value + 28)) == INVALID          # the last of the eight slots
+    assert slots(lib, lens=P(at(4).value + 8)) == INVALID          # the last of the three offsets
+
+
 def rows(data=A16, token=1024, head=128):
     return _lib.HeadRows(data, token, head)
 
