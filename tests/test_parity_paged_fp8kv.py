@@ -260,6 +260,23 @@ def test_pages_left_of_every_window_may_hold_anything(g, D):
         check(p, *got, window_left=wl)
 
 
+@pytest.mark.parametrize("D,Hkv,ps", [(128, 8, 64), (256, 2, 24)])
+def test_pages_past_4_gib_of_a_cache(g, D, Hkv, ps):
+    """Chunks, drafted tokens and decode steps whose pages lie behind byte 2^32."""
+    p = inputs([1, 200, 4], [500, 700, 3000], 4 * Hkv, Hkv, D, ps, seed=31)
+    first = (1 << 32) // (ps * Hkv * D) + 1                    # first page wholly past it
+    far = dict(p, block_table=torch.where(p["block_table"] >= 0, p["block_table"] + first, p["block_table"]))
+    dev = {n: far[n].cuda() for n in NAMES if n not in ("k_cache", "v_cache")}
+    for n in ("k_cache", "v_cache"):
+        pool = torch.full((first + p["num_pages"], ps, Hkv, D), 0x7F, dtype=torch.uint8, device="cuda")
+        pool[first:] = p[n].view(torch.uint8).cuda()
+        dev[n] = pool.view(torch.float8_e4m3fn)
+    for split in (True, False):
+        o, lse = g.attn_fwd_paged_fp8kv(*[dev[n] for n in NAMES], split_decode=split)
+        torch.cuda.synchronize()
+        check(p, o.cpu(), lse.cpu(), "split_decode %s" % split)
+
+
 def test_rows_outside_the_requests_stay(g):
     p = inputs([3, 140, 1], [50, 300, 70], 8, 2, 128, 16, seed=4)
     q = torch.cat([p["q"], torch.full((9, 8, 128), float("nan"), dtype=p["q"].dtype)])

@@ -245,6 +245,24 @@ def test_paged_e4m3(g, shape, as_bytes):
     assert torch.equal(vc.view(-1, Hkv, D)[at].cpu(), v.float().cpu().to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_rows_past_4_gib_of_a_cache(g, e4m3):
+    """Slots whose rows lie behind byte 2^32 of the caches; the same results as in a small pool."""
+    T, Hq, Hkv, D, ps, pages = 37, 8, 8, 128, 16, 5
+    q, k, v, table, pos, qw, kw = inputs(T, Hq, Hkv, D)
+    dt = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    first = (1 << 32) // (ps * Hkv * D * dt.itemsize) + 1      # first page wholly past it
+    slots = slot_map(T, pages, ps)
+    small = [torch.zeros(pages, ps, Hkv, D, dtype=dt, device="cuda") for _ in range(2)]
+    large = [torch.zeros(first + pages, ps, Hkv, D, dtype=dt, device="cuda") for _ in range(2)]
+    a = g.attn_qk_norm_rope_paged(q, k, v, table, pos, slots, *small, qw, kw)
+    b = g.attn_qk_norm_rope_paged(q, k, v, table, pos, slots + first * ps, *large, qw, kw)
+    assert torch.equal(a, b)
+    for s, l in zip(small, large):
+        assert torch.equal(l[first:].view(torch.uint8), s.view(torch.uint8))
+        assert not bool(l[:first].view(torch.int32).any())
+
+
 def test_every_e4m3_rounding(g):
     """All float16 values: nearest even, saturation, subnormals, NaN."""
     bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.float16)
