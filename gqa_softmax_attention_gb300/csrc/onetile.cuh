@@ -43,6 +43,17 @@
 //               stale cache slots, and 0 * NaN would not vanish);
 //   warps 10-11 complete the third warpgroup (register limits are per
 //               warpgroup).
+// kPaged8 has 512 threads and no TMA loads: warps 8-10 widen keys and warps
+// 12-15 values (fp8_item), each team filling a ring of its own and writing the Q
+// block; warp 11 issues QK(i + 1) before PV(i).  e4m3 halves what a key costs in
+// HBM, but the tensor core takes A and B of one type and P needs more than e4m3's
+// four bits, so every key is widened once per row block; that and the softmax,
+// not the MMAs, set the pace.  Measured: a 2048-query chunk over 32768 keys, 64/8
+// heads, D = 128: 1.87-1.90 ms, 1.13 PFLOP/s (the 16-bit call: 2.10 ms); about 2100
+// cycles a tile, 1400 of them softmax and 1445 the issue of its MMAs (QK 681, PV
+// 764), which overlap as far as two S buffers allow.  Five ragged chunks at 24/2,
+// D = 256: 0.50 ms with softcap, 0.45 without (16-bit: 0.56 without); 4800 cycles
+// a tile, of which the MMAs wait 1450 for keys.
 // The MMA shapes stay M128 x N128 (QK) and M128 x N(D) (PV); at D = 256 K is
 // split into two 128-column halves and V into two 64-key halves so that each
 // half fills one ring slot.  Shared-memory operand layouts:
@@ -239,11 +250,14 @@ __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float ca
 // warp's load covers 512 bytes, and a slot takes 32 of them.  The loads of the
 // next slot are issued when this one's are widened and stored: their latency
 // runs beside the wait for the slot.  The lane's 16 codes become two 16-byte chunks
-// of the swizzled tile; lanes 4-7 of eight write the odd chunk first, so that
-// the eight lanes of a store cover eight different bank groups.  Nothing here
+// of the swizzled tile; which row and column a lane takes is chosen so that the
+// eight lanes of a store cover eight different bank groups.  (One row to eight
+// lanes, half of them storing their odd chunk first, needs selects instead: 2.50
+// against 1.90 ms on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128.)
+// Nothing here
 // may spill: the streaming loads evict local memory from the small L1 beside
 // 227 KB of shared memory, and every reload then goes to L2 (10.6 ms instead of
-// 3.8 on a 2048-query chunk over 32768 keys, 64/8 heads, D = 128).
+// 3.8 on that chunk when it was found).
 // The value team (without TQ both) also writes the Q block (rows q_row0 .. of the
 // packed batch, packed r = query * g + head, bfloat16 rounded to float16), zeros
 // past it.

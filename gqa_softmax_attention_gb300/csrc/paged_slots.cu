@@ -15,7 +15,8 @@
 // search among the round's 512 first tokens in shared memory.  A fresh page is
 // entered in the table by the token at its first position, which is always a
 // new token.  Bound by latency: a round is two dependent loads, a block scan
-// and the search.
+// and the search.  Measured: 3.1 us on the GPU for 64 requests of one token (10 us
+// a call from Python, 11 for 768 requests of up to 331 tokens, which write 3 MB).
 #include <climits>
 
 #include "internal.h"

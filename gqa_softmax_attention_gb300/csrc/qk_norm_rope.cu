@@ -19,7 +19,9 @@
 // covers whole 64-byte stretches.  A warp holds 32 / (D / 8) rows at a time
 // and loads U of those before it works on them; its rows are of one kind
 // (queries, keys or values), so nothing diverges.  Arithmetic goes in pairs
-// (f32x2).
+// (f32x2).  Measured, 16384 tokens at D = 128: 32/8 heads dense 57-59 us (86-89 %
+// of the copy rate), 64/8 heads into e4m3 caches 107-109 us (88-89 %); a few tokens
+// 3-4 us on the GPU.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
