@@ -471,10 +471,14 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
     q = q.contiguous()
     if out is None:
         out = torch.empty_like(q)
+        po = out.data_ptr()
+    else:
+        po = _data("out", out, q.dtype, q.shape, dev)
     if lse is None:
         lse = torch.empty((total_q, Hq), dtype=f32, device=dev)
-    po = _data("out", out, q.dtype, q.shape, dev)
-    pl = _data("lse", lse, f32, (total_q, Hq), dev)
+        pl = lse.data_ptr()
+    else:
+        pl = _data("lse", lse, f32, (total_q, Hq), dev)
     lib = _lib.load()
     if workspace is None:
         if split_decode:
@@ -527,19 +531,22 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
     fs = _data("free_start", free_start, i32, (1,), dev) if free_start is not None else None
     if T < 0:
         raise ValueError("max_tokens must be >= 0, got %d" % T)
+    sizes = (B + 1, B, T, T, T, 3)
     if out is None:
-        out = torch.empty(2 * B + 3 * T + 4, dtype=i32, device=dev).split((B + 1, B, T, T, T, 3))
+        buf = torch.empty(2 * B + 3 * T + 4, dtype=i32, device=dev)
+        out, p = buf.split(sizes), buf.data_ptr()
+        at = p, p + 4 * (B + 1), p + 4 * (2 * B + 1), p + 4 * (2 * B + T + 1), p + 4 * (2 * B + 2 * T + 1), \
+            p + 4 * (2 * B + 3 * T + 1)
     elif len(out) != 6:
         raise ValueError("out must hold six tensors")
-    cu, lens, slots, positions, requests, counts = out
+    else:
+        names = "cu_seqlens_q", "cache_seqlens", "slots", "positions", "requests", "counts"
+        at = [_data("out " + n, t, i32, (m,), dev) for n, t, m in zip(names, out, sizes)]
     st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, max_pages, int(page_size), int(num_pages),
-             n_free, T, _data("out cu_seqlens_q", cu, i32, (B + 1,), dev), _data("out cache_seqlens", lens, i32, (B,), dev),
-             _data("out slots", slots, i32, (T,), dev), _data("out positions", positions, i32, (T,), dev),
-             _data("out requests", requests, i32, (T,), dev), _data("out counts", counts, i32, (3,), dev),
-             _raw_stream(dev))
+             n_free, T, *at, _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_paged_slots")
-    return cu, lens, slots, positions, requests, counts
+    return tuple(out)
 
 
 def _head_rows(t, T):
@@ -570,13 +577,13 @@ def _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axe
     dev, dt, lead, D = q.device, q.dtype, q.shape[:-2], q.shape[-1]
     T = lead.numel()
     shape = k.shape
-    for n, t in (("k", k), ("v", v)):
-        if t is not None and (t.dtype is not dt or t.device != dev or t.shape != shape or t.dim() != nd or
-                              shape[:-2] != lead or shape[-1] != D):
-            raise ValueError("q, k and v must have one dtype, device, leading shape and head dim, k and v as many "
-                             "heads: q %s %s, %s %s %s" % (tuple(q.shape), dt, n, tuple(t.shape), t.dtype))
+    if not (len(shape) == nd and shape[:-2] == lead and shape[-1] == D and k.dtype is dt and k.device == dev and
+            (v is None or v.shape == shape and v.dtype is dt and v.device == dev)):
+        raise ValueError("q, k and v must have one dtype, device, leading shape and head dim, k and v as many heads: "
+                         + ", ".join("%s %s" % (tuple(t.shape), t.dtype) for t in (q, k, v) if t is not None))
     f32 = torch.float32
-    wt = f32 if any(w is not None and w.dtype == f32 for w in (q_weight, k_weight)) else dt
+    wt = f32 if (q_weight is not None and q_weight.dtype is f32 or
+                 k_weight is not None and k_weight.dtype is f32) else dt
     pqw = _data("q_weight", q_weight, wt, (D,), dev) if q_weight is not None else None
     pkw = _data("k_weight", k_weight, wt, (D,), dev) if k_weight is not None else None
     rope = None
@@ -607,6 +614,7 @@ def _rope_out(name, out, like):
     """`out` (checked) or a new contiguous tensor like `like`, and its address."""
     if out is None:
         out = torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return out, out.data_ptr()
     return out, _data(name, out, like.dtype, like.shape, like.device)
 
 

@@ -78,6 +78,10 @@ cudaError_t launch_prefill_d256(const CUtensorMap& tm_q, const CUtensorMap& tm_k
                                 const CUtensorMap& tm_o, const PrefillArgs& a, cudaStream_t stream);
 int prefill_d256_take_device_error();
 
+// Key tiles a part of a split block keeps at least: below that the partial
+// results and their joining cost more than the shorter loop saves.
+constexpr int kPartTiles = 4;
+
 // Packed calls (varlen_packed.cu, varlen_paged.cu; onetile.cuh).  The plan
 // kernel lists the (request, row block) entries of a call into `tmp`, then
 // into `entries` ([max_entries, 8] int32 each) ordered by estimated cost,

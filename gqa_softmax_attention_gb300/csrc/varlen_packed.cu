@@ -32,10 +32,6 @@ constexpr double kDecPerKey = 0.011;
 // steps 0.30, 0.30, 0.33, 0.39 and 0.43.
 constexpr double kDecPerKey8 = 0.005;
 
-// Key tiles a part of a split block keeps at least: below that the partial
-// results and their joining cost more than the shorter loop saves.
-constexpr int kPartTiles = 4;
-
 __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb, int g, int causal) {
     const int q0 = e0.y, sq = e0.w, L = e1.y;
     const int nq = min(qpb, sq - q0);
