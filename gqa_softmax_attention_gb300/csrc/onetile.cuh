@@ -44,8 +44,8 @@
 //   warps 10-11 complete the third warpgroup (register limits are per
 //               warpgroup).
 // kPaged8 has 512 threads and no TMA loads: warps 8-10 widen keys and warps
-// 12-15 values (fp8_item), each team filling a ring of its own and writing the Q
-// block; warp 11 issues QK(i + 1) before PV(i).  e4m3 halves what a key costs in
+// 12-15 values (fp8_item), each team filling a ring of its own; the epilogue warps
+// write the next item's Q block (fill_q8); warp 11 issues QK(i + 1) before PV(i).  e4m3 halves what a key costs in
 // HBM, but the tensor core takes A and B of one type and P needs more than e4m3's
 // four bits, so every key is widened once per row block; that and the softmax,
 // not the MMAs, set the pace.  Measured: a 2048-query chunk over 32768 keys, 64/8
@@ -137,8 +137,8 @@ struct Cfg {
     // 192 (K and V written by the wideners and read by the MMAs, and the loads
     // through L1, which share its 128 bytes a clock), and a sixth slot
     static constexpr bool TQ = MODE == kPaged8 && D == 128;
-    // threads at the barrier before TMEM is freed: softmax, epilogue, MMA and Q-writing warps
-    static constexpr int TMEM_USERS = 8 * 32 + 32 + (TQ ? TEAM_V8 * 32 : 0);
+    // threads at the barrier before TMEM is freed: softmax, epilogue and MMA warps
+    static constexpr int TMEM_USERS = 8 * 32 + 32;
     static constexpr int NS = TQ ? 6 : (D == 256 ? 4 : 5);         // ring slots
     // kPaged8: two rings, slots [0, NK8) for keys and [NK8, NS) for values, each
     // filled by one team: with one ring, a team could come to a slot whose use
@@ -258,14 +258,10 @@ __device__ __forceinline__ float capped_exp(uint32_t taddr, float to_y, float ca
 // may spill: the streaming loads evict local memory from the small L1 beside
 // 227 KB of shared memory, and every reload then goes to L2 (10.6 ms instead of
 // 3.8 on that chunk when it was found).
-// The value team (without TQ both) also writes the Q block (rows q_row0 .. of the
-// packed batch, packed r = query * g + head, bfloat16 rounded to float16), zeros
-// past it.
-template <int D, bool F16, class C, bool V>
+template <int D, class C, bool V>
 __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, uint32_t full0, uint32_t empty0,
-                                         uint32_t q_full, uint32_t q_empty, volatile int* abort_flag, int b, int hkv,
-                                         int q_row0, int nq_rows, int skv, int kv_begin, int first, int n_tiles, int g,
-                                         int wid, int lane, uint32_t tmem, int& nc, int& nq) {
+                                         volatile int* abort_flag, int b, int hkv, int skv, int kv_begin, int first,
+                                         int n_tiles, int wid, int lane, int& nc) {
     constexpr int NCH = V ? C::CV : C::CK;        // slots per tile
     constexpr int NR = V ? C::NV8 : C::NK8;       // slots of this team's ring
     constexpr bool WIDE = D == 256 && V;          // a load covers two 256-byte rows, else four 128-byte stretches
@@ -366,65 +362,6 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
     int4 rows = find_rows(first, find_pages(first));
     load(0, rows);
     Pages pages = find_pages(first + 1);          // a tile ahead of their use
-    if constexpr (V || !C::TQ) {
-        const int n_rows = nq_rows * g;
-        auto q_piece = [&](int r, int c8, uint32_t* w) {          // 8 dims of row r
-            const int rr = min(r, n_rows - 1);
-            ldg16_or_zero(w, static_cast<const uint16_t*>(a.q) +
-                                 (((size_t)q_row0 + rr / g) * a.Hq + hkv * g + rr % g) * D + 8 * c8, r < n_rows);
-        };
-        auto to_f16 = [&](uint32_t* w, int n) {
-            if constexpr (!F16) {
-#pragma unroll
-                for (int e = 0; e < n; ++e)
-                    w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
-            }
-        };
-        if constexpr (C::TQ) {
-            // TMEM lane = row: warp wid of the team (warp 12 + wid) holds rows 32 wid .. + 31
-            if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
-            tc_fence_after();                     // the S MMAs that read the last Q are complete
-#pragma unroll 1
-            for (int half = 0; half < D / 64; ++half) {
-                uint32_t w[32];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) q_piece(wid * 32 + lane, 8 * half + e, w + 4 * e);
-                to_f16(w, 32);
-                __syncwarp();
-                tmem_st32(tmem + ((uint32_t)(wid * 32) << 16) + COL_Q8 + 32 * half, w);
-            }
-            tc_fence_before();
-        } else {
-            // both teams, QB pieces a thread in flight (by one team, two at a time,
-            // the block took 16000 cycles, an eighth of an item of
-            // 6000 keys at D = 256)
-            constexpr int QB = 4, QT = 32 * (TEAM_K8 + TEAM_V8);
-            const int t = (V ? TEAM_K8 + wid : wid) * 32 + lane;
-#pragma unroll 1
-            for (int base = 0; base < BM * (D / 8); base += QB * QT) {
-                uint32_t w[QB][4];
-#pragma unroll
-                for (int u = 0; u < QB; ++u) {
-                    const int idx = base + u * QT + t;
-                    q_piece(idx / (D / 8), idx % (D / 8), w[u]);
-                }
-                if (base == 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
-#pragma unroll
-                for (int u = 0; u < QB; ++u) {
-                    const int idx = base + u * QT + t, r = idx / (D / 8), c8 = idx % (D / 8);
-                    to_f16(w[u], 4);
-                    if (idx < BM * (D / 8))
-                        *reinterpret_cast<uint4*>(smem + C::OFF_Q + (c8 >> 3) * BOX + r * 128 +
-                                                  (((c8 & 7) ^ (r & 7)) << 4)) =
-                            make_uint4(w[u][0], w[u][1], w[u][2], w[u][3]);
-                }
-            }
-            fence_proxy_async_smem();
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(q_full);
-        ++nq;
-    }
     for (int i = 0; i < c; ++i) {
 #pragma unroll 1
         for (int ch = 0; ch < NCH; ++ch, ++nc) {
@@ -439,6 +376,70 @@ __device__ __forceinline__ bool fp8_item(const PrefillArgs& a, uint8_t* smem, ui
         }
         pages = find_pages(first + i + 2);
     }
+    return true;
+}
+
+// kPaged8: an item's Q block, by the four epilogue warps: n_rows rows (packed r =
+// query * g + head, the block's first query in row q_row0 of the batch) as
+// float16 (bfloat16 rounded), zeros past them, once the S MMAs that read the last
+// block are complete.  The epilogue warps do it while they would wait for the
+// item before to end, so that no widening team interrupts its stream of keys or
+// values.  D / 4 registers of loads are in flight a thread.
+template <int D, bool F16, class C>
+__device__ __forceinline__ bool fill_q8(const PrefillArgs& a, uint8_t* smem, uint32_t q_full, uint32_t q_empty,
+                                        volatile int* abort_flag, int q_row0, int n_rows, int hkv, int g, int wid,
+                                        int lane, uint32_t tmem, int& nq) {
+    constexpr int N = 16;                         // 16-byte pieces in flight
+    const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((size_t)q_row0 * a.Hq + hkv * g) * D;
+    const uint32_t inv_g = (65535u + g) / g;      // r / g = r * inv_g >> 16 for r < 128, g <= 128
+    auto piece = [&](int r, int c8, uint32_t* w) {          // dims 8 c8 .. of row r
+        const bool ok = r < n_rows;
+        const int rr = ok ? r : 0;
+        // row rr / g of the batch, head rr % g of the group
+        ldg16_or_zero(w, q + ((size_t)((rr * inv_g) >> 16) * (a.Hq - g) + rr) * D + 8 * c8, ok);
+    };
+    auto to_f16 = [&](uint32_t* w) {
+        if constexpr (!F16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+        }
+    };
+#pragma unroll 1
+    for (int k = 0; k < D / 8 / N; ++k) {
+        uint32_t w[4 * N];
+        // TMEM lane = row; shared memory: a warp's load covers a row (D = 256)
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            if constexpr (C::TQ) piece(wid * 32 + lane, u, w + 4 * u);
+            else piece(4 * (k * N + u) + wid, lane, w + 4 * u);
+        }
+        if (k == 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag))) return false;
+            tc_fence_after();
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) to_f16(w + 4 * u);
+        if constexpr (C::TQ) {
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                tmem_st32(tmem + ((uint32_t)(wid * 32) << 16) + COL_Q8 + 32 * h, w + 32 * h);
+        } else {
+#pragma unroll
+            for (int u = 0; u < N; ++u) {
+                const int r = 4 * (k * N + u) + wid;
+                *reinterpret_cast<uint4*>(smem + C::OFF_Q + (lane >> 3) * BOX + r * 128 +
+                                          (((lane & 7) ^ (r & 7)) << 4)) = make_uint4(w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                                                                                     w[4 * u + 3]);
+            }
+        }
+    }
+    if constexpr (C::TQ) tc_fence_before();
+    else fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
+    ++nq;
     return true;
 }
 
@@ -594,7 +595,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
     };
 
     if (threadIdx.x == 0) {
-        mbar_init(q_full, !KV8 ? 1 : TEAM_V8 + (C::TQ ? 0 : TEAM_K8));      // TMA, or the warps that write Q
+        mbar_init(q_full, !KV8 ? 1 : 4);             // TMA, or the epilogue warps
         mbar_init(q_empty, 1);
         for (int s = 0; s < C::NS; ++s) {
             mbar_init(r_full(s), !KV8 ? 1 : (s < C::NK8 ? TEAM_K8 : TEAM_V8));     // TMA, or the widening team
@@ -640,25 +641,19 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             if constexpr (KV8) {
                 const bool team_v = warp >= WARP_V8;
                 const int wid = warp % 4;
-                int nc = 0, nq = 0;                 // slots of the team's ring and Q blocks filled
+                int nc = 0;                         // slots of the team's ring filled
                 for (int r = 0;; ++r) {
                     const int w = warp == WARP_LOAD ? claim_item(r) : next_item(r);
                     if (w < 0) break;
                     const Item it = describe(w);
                     if (it.t.n_tiles == it.first) continue;
-                    const int q_row = it.qs + it.t.q0;
                     const bool done =
-                        team_v ? fp8_item<D, F16, C, true>(a, smem, r_full(C::NK8), r_empty(C::NK8), q_full, q_empty,
-                                                           abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                           it.t.kv_begin, it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq)
-                               : fp8_item<D, F16, C, false>(a, smem, r_full(0), r_empty(0), q_full, q_empty,
-                                                            abort_flag, it.b, it.hkv, q_row, it.t.rows_valid, it.skv,
-                                                            it.t.kv_begin, it.first, it.t.n_tiles, g, wid, lane, tmem, nc, nq);
+                        team_v ? fp8_item<D, C, true>(a, smem, r_full(C::NK8), r_empty(C::NK8), abort_flag, it.b, it.hkv,
+                                                      it.skv, it.t.kv_begin, it.first, it.t.n_tiles, wid, lane, nc)
+                               : fp8_item<D, C, false>(a, smem, r_full(0), r_empty(0), abort_flag, it.b, it.hkv,
+                                                       it.skv, it.t.kv_begin, it.first, it.t.n_tiles, wid, lane, nc);
                     if (!done) break;
                 }
-                __syncwarp();
-                tc_fence_before();
-                if (C::TQ && team_v) named_bar_arrive(2, C::TMEM_USERS);
             }
         } else if (!KV8 && warp == WARP_LOAD) {
             // ------------------------------------------------------------ producer
@@ -939,7 +934,39 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                     if (!mbar_wait(o_empty, oe & 1, abort_flag)) return false;
                 return true;
             };
-            for (int r = 0, n_item = 0; ok; ++r, ++n_item) {
+            if constexpr (KV8) {
+                // the same order from two copies of each step (small code); the
+                // next item is looked up while the last P is awaited
+                auto tiles_of = [&](int w) { const Item it = describe(w); return it.t.n_tiles - it.first; };
+                int w = next_item(0);
+                int c = w >= 0 ? tiles_of(w) : 0;
+                for (int r = 0; ok && w >= 0; ++r) {
+                    if (lane == 0 && c > 0) {
+                        ok = mbar_wait(q_full, nq++ & 1, abort_flag);
+                        if (ok) ok = issue_qk(g_t);
+                        for (int i = 0; i + 1 < c && ok; ++i) {
+                            ok = issue_qk(g_t + i + 1) && wait_o_empty(r);
+                            if (ok) ok = issue_pv(g_t + i, i == 0);
+                        }
+                        if (ok) mma_commit(q_empty);               // every S of the item is issued
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    const int wn = next_item(r + 1);
+                    const int cn = wn >= 0 ? tiles_of(wn) : 0;
+                    if (lane == 0) {
+                        ok = wait_o_empty(r);
+                        if (ok && c > 0) ok = issue_pv(g_t + c - 1, c == 1);
+                        // one phase per item: every MMA of the item has completed
+                        if (ok) mma_commit(o_final);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    g_t += c;
+                    w = wn;
+                    c = cn;
+                }
+            }
+            for (int r = 0, n_item = 0; !KV8 && ok; ++r, ++n_item) {
                 const int w = next_item(r);
                 if (w < 0) break;
                 const Item it = describe(w);
@@ -947,17 +974,6 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 if (lane == 0) {
                     if (c > 0) {
                         ok = mbar_wait(q_full, nq++ & 1, abort_flag);
-                        if constexpr (KV8) {
-                            // the same order from two copies of each step (small code)
-                            if (ok) ok = issue_qk(g_t);
-                            for (int i = 0; i + 1 < c && ok; ++i) {
-                                ok = issue_qk(g_t + i + 1) && wait_o_empty(n_item);
-                                if (ok) ok = issue_pv(g_t + i, i == 0);
-                            }
-                            if (ok) mma_commit(q_empty);
-                            if (ok) ok = wait_o_empty(n_item);
-                            if (ok) ok = issue_pv(g_t + c - 1, c == 1);
-                        } else {
                         if (ok) ok = issue_qk(g_t);
                         if (ok && c > 1) ok = issue_qk(g_t + 1);
                         if (ok) ok = wait_o_empty(n_item);
@@ -969,7 +985,6 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         if (ok) mma_commit(q_empty);               // every S of the item is issued
                         // BSHD: no value row to zero, lane 0 issues the last P V too
                         if (!PACKED && ok) ok = issue_pv(g_t + c - 1, c == 1);
-                        }
                     } else {
                         ok = wait_o_empty(n_item);
                     }
@@ -978,7 +993,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 nc = __shfl_sync(0xffffffffu, nc, 0);
                 nq = __shfl_sync(0xffffffffu, nq, 0);
                 oe = __shfl_sync(0xffffffffu, oe, 0);
-                if (PACKED && !KV8 && ok && c > 0) {
+                if (PACKED && ok && c > 0) {
                     // the item's last P V, by the whole warp
                     const int gi = g_t + c - 1;
                     ok = __all_sync(0xffffffffu, mbar_wait(p_full(gi & 1), (gi >> 1) & 1, abort_flag));
@@ -1015,7 +1030,7 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 mbar_drain(drain, 0);
             }
             __syncwarp();
-            named_bar_sync(2, C::TMEM_USERS);        // softmax and epilogue (and Q-writing) warps are done with TMEM
+            named_bar_sync(2, C::TMEM_USERS);        // softmax and epilogue warps are done with TMEM
             tc_fence_after();
             tmem_dealloc(tmem, TMEM_COLS);
         }
@@ -1217,14 +1232,32 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         int n = 0;                   // items finished
         int nb = 0;                  // output boxes stored (staging buffer alternation)
         bool ok = true;
+        // kPaged8: the Q block of item w (fill_q8), an item ahead
+        int nq = 0, w = -1, w_after = -1;
+        auto fill_q = [&]() -> bool {
+            if (w_after < 0) return true;
+            const Item it = describe(w_after);
+            if (it.t.n_tiles == it.first) return true;
+            return fill_q8<D, F16, C>(a, smem, q_full, q_empty, abort_flag, it.qs + it.t.q0, it.t.rows_valid * g, it.hkv,
+                                      g, warp % 4, lane, tmem, nq);
+        };
+        if constexpr (KV8) {
+            w_after = next_item(0);
+            ok = fill_q();
+        }
         for (int rr = 0;; ++rr) {
-            const int w = next_item(rr);
+            w = KV8 ? w_after : next_item(rr);
             if (w < 0) break;
+            bool q_ok = ok;
+            if constexpr (KV8) {
+                w_after = next_item(rr + 1);
+                q_ok = q_ok && fill_q();
+            }
             const Item itm = describe(w);
             const TileInfo ti = itm.t;
             // warp-collective waits: the warp must be converged at the
             // .aligned barrier below and at every tcgen05.ld
-            ok = __all_sync(0xffffffffu, mbar_wait(stats_full, n & 1, abort_flag));
+            ok = q_ok && __all_sync(0xffffffffu, mbar_wait(stats_full, n & 1, abort_flag));
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_final, n & 1, abort_flag));
             if (!named_bar_and(3, BM, ok)) break;     // the whole warpgroup stops together
             tc_fence_after();
