@@ -531,17 +531,18 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
     fs = _data("free_start", free_start, i32, (1,), dev) if free_start is not None else None
     if T < 0:
         raise ValueError("max_tokens must be >= 0, got %d" % T)
-    sizes = (B + 1, B, T, T, T, 3)
     if out is None:
         buf = torch.empty(2 * B + 3 * T + 4, dtype=i32, device=dev)
-        out, p = buf.split(sizes), buf.data_ptr()
+        out, p = buf.split((B + 1, B, T, T, T, 3)), buf.data_ptr()
         at = p, p + 4 * (B + 1), p + 4 * (2 * B + 1), p + 4 * (2 * B + T + 1), p + 4 * (2 * B + 2 * T + 1), \
             p + 4 * (2 * B + 3 * T + 1)
     elif len(out) != 6:
         raise ValueError("out must hold six tensors")
     else:
-        names = "cu_seqlens_q", "cache_seqlens", "slots", "positions", "requests", "counts"
-        at = [_data("out " + n, t, i32, (m,), dev) for n, t, m in zip(names, out, sizes)]
+        cu, lens, slots, positions, requests, counts = out
+        at = (_data("out cu_seqlens_q", cu, i32, (B + 1,), dev), _data("out cache_seqlens", lens, i32, (B,), dev),
+              _data("out slots", slots, i32, (T,), dev), _data("out positions", positions, i32, (T,), dev),
+              _data("out requests", requests, i32, (T,), dev), _data("out counts", counts, i32, (3,), dev))
     st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, max_pages, int(page_size), int(num_pages),
              n_free, T, *at, _raw_stream(dev))
     if st != 0:
