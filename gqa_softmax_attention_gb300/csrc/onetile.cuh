@@ -51,9 +51,11 @@
 // not the MMAs, set the pace.  Measured: a 2048-query chunk over 32768 keys, 64/8
 // heads, D = 128: 1.87-1.90 ms, 1.13 PFLOP/s (the 16-bit call: 2.10 ms); about 2100
 // cycles a tile, 1400 of them softmax and 1445 the issue of its MMAs (QK 681, PV
-// 764), which overlap as far as two S buffers allow.  Five ragged chunks at 24/2,
-// D = 256: 0.50 ms with softcap, 0.45 without (16-bit: 0.56 without); 4800 cycles
-// a tile, of which the MMAs wait 1450 for keys.
+// 764), which overlap as far as two S buffers allow.  Between two items
+// the MMA warp loses about 9000 cycles (the last P, the new Q, O's hand-over).
+// Five ragged chunks at 24/2, D = 256: 0.45 ms with softcap, 0.43 without (16-bit:
+// 0.56 without); 4200 cycles a tile, of which the MMAs wait 1250 for keys (a ring
+// of one tile: a slot is refilled only after the S before has read it).
 // The MMA shapes stay M128 x N128 (QK) and M128 x N(D) (PV); at D = 256 K is
 // split into two 128-column halves and V into two 64-key halves so that each
 // half fills one ring slot.  Shared-memory operand layouts:
@@ -103,8 +105,8 @@ static_assert((kRegsSoftmax + kRegsEpi + kRegsOther) * 128 <= kRegsLaunch * NUM_
 // kPaged8: warps 8-10 widen keys, 12-15 values, 11 issues the MMAs.  128
 // registers per thread at launch (four warps on each SM sub-partition); softmax
 // 208, epilogue 96, the other two warpgroups 104 each.  The values get the
-// fourth warp: P V comes last in a tile, and with three warps the MMAs waited
-// 1600 cycles a tile for values and 380 for keys (D = 256).
+// fourth warp: P V comes last in a tile (four warps on the keys instead: 0.46
+// against 0.45 ms on five ragged chunks at 24/2, D = 256).
 constexpr int NUM_THREADS8 = 512;
 constexpr int WARP_V8 = 12;
 constexpr int WARP_MMA8 = 11;

@@ -10,7 +10,10 @@ namespace {
 // 2^(lse_p - max) over the parts' base-2 LSEs (MATE "QSA", Core Attention,
 // SplitKV), the sink joining the denominator once.  A few hundred rows of D
 // FP32 values a part: bound by the launch.  Ends at once when the plan cut
-// nothing.
+// nothing.  The whole call with its keys in parts, and in one: 4 queries over
+// 32004 keys 37 and 273 us, over 2000 keys 22 and 30; 256 queries over 32256 keys
+// 157 and 280, over 4096 keys 41 and 48 (32/8 heads, D = 128); 4 queries over 32004
+// keys at 24/2, D = 256: 53 and 653.
 constexpr int JOIN_WARPS = 8;
 
 template <int D, bool F16>
