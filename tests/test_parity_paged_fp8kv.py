@@ -354,6 +354,53 @@ def test_other_stream_and_repeat(g):
         assert torch.equal(o, copies[0][0]) and torch.equal(lse, copies[0][1])
 
 
+def test_two_calls_at_once(g):
+    """Two streams, neither waiting for the other, each with its own tensors."""
+    ps = [inputs([1, 400, 1, 5], [2500, 900, 40, 3000], 32, 8, 128, 64, seed=21),
+          inputs([3, 1, 250], [2000, 700, 600], 24, 2, 256, 16, seed=22)]
+    streams = [torch.cuda.Stream() for _ in ps]
+    devs = [[p[n].cuda() for n in NAMES] for p in ps]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append(g.attn_fwd_paged_fp8kv(*devs[i]))
+    torch.cuda.synchronize()
+    for p, runs in zip(ps, got):
+        check(p, runs[0][0].cpu(), runs[0][1].cpu())
+        for o, lse in runs[1:]:
+            assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
+def test_two_graphs_share_a_workspace(g):
+    """Captured calls of other sizes (one with its keys in parts) replayed in
+    turn over one workspace: nothing in it is taken over from a call."""
+    ps = [inputs([4, 2], [3000, 2500], 32, 8, 128, 64, seed=23),
+          inputs([1, 300, 1], [900, 800, 1200], 32, 8, 128, 16, seed=24)]
+    size = max(g.attn_paged_fp8kv_workspace_size(len(p["cache_seqlens"]), p["q"].shape[0], 32, 8, 128, pg,
+                                                 p["block_table"].shape[1]) for p, pg in zip(ps, (64, 16)))
+    ws = torch.full((size,), 0xFF, dtype=torch.uint8, device="cuda")
+    graphs, outs = [], []
+    for p in ps:
+        dev = [p[n].cuda() for n in NAMES]
+        out, lse = torch.empty_like(dev[0]), torch.empty(p["q"].shape[0], 32, device="cuda")
+        call = lambda: g.attn_fwd_paged_fp8kv(*dev, out=out, lse=lse, workspace=ws)  # noqa: E731
+        call()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            call()
+        graphs.append((graph, dev))
+        outs.append((out, lse))
+    for i in (0, 1, 0, 0, 1, 1, 0):
+        for t in outs[i]:
+            t.fill_(float("nan"))
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        check(ps[i], outs[i][0].cpu(), outs[i][1].cpu(), "graph %d" % i)
+
+
 def test_refusals(g):
     p = inputs([2, 3], [20, 30], 8, 2, 128, 16)
     d = {n: p[n].cuda() for n in NAMES}
