@@ -27,9 +27,9 @@ constexpr int NBUCKET = 2048;
 // 0.606 and 0.683 ms at 0.009, 0.0126 and 0.016).
 constexpr double kDecPerKey = 0.011;
 // Over e4m3 caches a cached key is half the bytes and the split kernel is bound by
-// its instructions: the mixed batch (60 steps, 4 chunks) took 0.57, 0.55, 0.55,
-// 0.59 and 0.67 ms at 0.002, 0.004, 0.006, 0.008 and 0.011, one chunk beside the
-// steps 0.30, 0.30, 0.33, 0.39 and 0.43.
+// its instructions: the mixed batch (60 steps, 4 chunks) took 0.53, 0.51, 0.50,
+// 0.52 and 0.58 ms at 0.002, 0.004, 0.006, 0.008 and 0.011, one chunk beside the
+// steps 0.28, 0.28, 0.29, 0.36 and 0.39.
 constexpr double kDecPerKey8 = 0.005;
 
 __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb, int g, int causal) {
