@@ -1271,11 +1271,14 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             // output row: [B, Sq, Hq] (kBSHD) or [total_q, Hq] (packed)
             const size_t orow = PACKED ? ((size_t)itm.qs + ti.q0 + rq) * a.Hq + head
                                        : ((size_t)itm.b * a.Sq + ti.q0 + rq) * a.Hq + head;
-            float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-            float lse2 = l_run > 0.f ? m_ref + log2f(l_run) : -INFINITY;
-            if (sinks && l_run > 0.f && parts == 1) {
+            // kPaged8: only a sum of exactly 0 means a row without a key; a NaN sum (a
+            // query that is no number) goes on as it is, to the joining kernel too
+            const bool some = KV8 ? l_run != 0.f : l_run > 0.f;
+            float inv = some ? 1.f / l_run : 0.f;
+            float lse2 = some ? m_ref + log2f(l_run) : -INFINITY;
+            if (sinks && some && parts == 1) {
                 const float s2 = sinks[head] * 1.4426950408889634f;
-                if (s2 == INFINITY) {
+                if (s2 == INFINITY && !(KV8 && isnan(l_run))) {
                     inv = 0.f;
                     lse2 = INFINITY;
                 } else {

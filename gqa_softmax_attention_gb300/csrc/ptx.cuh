@@ -402,6 +402,13 @@ __device__ __forceinline__ float softcap_log2(float s, float cap_in, float cap_o
     return cap_out - 2.f * cap_out * rcp_approx(e + 1.f);
 }
 
+// Maximum that is NaN where either is (fmaxf drops a NaN).
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
 // Three-input maximum.
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
     float d;

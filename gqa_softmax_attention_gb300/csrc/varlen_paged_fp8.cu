@@ -8,7 +8,9 @@ namespace {
 
 // Joins the parts of every (row block, KV head): one warp per tile row, weights
 // 2^(lse_p - max) over the parts' base-2 LSEs (MATE "QSA", Core Attention,
-// SplitKV), the sink joining the denominator once.  A few hundred rows of D
+// SplitKV), the sink joining the denominator once.  A part's LSE of -inf means
+// that it saw no key of the row; a NaN one (a query that is no number) makes the
+// row NaN, as it is with its keys in one part.  A few hundred rows of D
 // FP32 values a part: bound by the launch.  Ends at once when the plan cut
 // nothing.  The whole call with its keys in parts, and in one: 4 queries over
 // 32004 keys 37 and 273 us, over 2000 keys 22 and 30; 256 queries over 32256 keys
@@ -32,17 +34,17 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) join_parts_kernel(const Prefi
     const size_t orow = ((size_t)qs + q0 + rq) * a.Hq + head;
     const size_t p0 = (size_t)block * parts * pf::BM + r;     // row of part 0; parts are BM rows apart
     float top = -INFINITY;
-    for (int p = lane; p < parts; p += 32) top = fmaxf(top, a.part_lse[p0 + (size_t)p * pf::BM]);
+    for (int p = lane; p < parts; p += 32) top = max_or_nan(top, a.part_lse[p0 + (size_t)p * pf::BM]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 16; o > 0; o >>= 1) top = max_or_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     constexpr int PER = D / 128;                              // float4 groups per lane
     uint16_t* out = static_cast<uint16_t*>(a.o) + orow * D;
     const float sink = a.x.sinks && top != -INFINITY ? a.x.sinks[head] * 1.4426950408889634f : -INFINITY;
     float acc[PER][4] = {}, den = 0.f, lse = -INFINITY;
-    if (sink == INFINITY) {
+    if (sink == INFINITY && !isnan(top)) {
         lse = INFINITY;
     } else if (top != -INFINITY) {
-        const float M = fmaxf(top, sink);
+        const float M = max_or_nan(top, sink);
         den = sink == -INFINITY ? 0.f : exp2f(sink - M);
 #pragma unroll 4
         for (int p = 0; p < parts; ++p) {

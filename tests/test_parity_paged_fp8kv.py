@@ -419,3 +419,44 @@ def test_refusals(g):
     d64["q"], d64["k_cache"], d64["v_cache"] = (d64[n][..., :64].contiguous() for n in ("q", "k_cache", "v_cache"))
     with pytest.raises(ValueError):
         g.attn_fwd_paged_fp8kv(**d64)                                     # D = 64
+
+
+def one_part(g, p):
+    """A workspace without room for key parts: the same call with the keys of every block in one part."""
+    (T, Hq, D), (_, ps, Hkv, _) = p["q"].shape, p["k_cache"].shape
+    size = g.attn_paged_workspace_size(len(p["cache_seqlens"]), T, Hq, Hkv, D, ps, p["block_table"].shape[1])
+    return torch.empty(size, dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("value", [float("nan"), INF, -INF, 1e5], ids=str)
+@pytest.mark.parametrize("geometry", [(8, 2, 128, 64), (24, 2, 256, 16)], ids=str)
+def test_queries_that_are_no_numbers_show(g, geometry, value):
+    """A NaN or infinite value in one head of one query (in bfloat16 also one past
+    float16's range, which becomes infinite): that row is NaN, O and LSE, with its keys
+    in one part and in several, with a sink and without; every other row is as it was.
+    Infinite scores of both signs among 5000 keys make every such row inf - inf."""
+    p = inputs([4], [5000], *geometry, seed=41)
+    Hq, D = geometry[0], geometry[2]
+    bad = dict(p, q=p["q"].clone())
+    bad["q"][1, 2, 5] = value
+    bad["q"][3, Hq - 1, D - 1] = value
+    hit = torch.zeros(4, Hq, dtype=torch.bool)
+    hit[1, 2] = hit[3, Hq - 1] = True
+    sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(3))
+    sinks[-1] = INF
+    for kw in (dict(), dict(sinks=sinks), dict(window_left=3000)):
+        for ws in (None, one_part(g, p)):
+            o, lse = run(g, bad, workspace=ws, **kw)
+            assert bool(o[hit].isnan().all()) and bool(lse[hit].isnan().all()), str(kw)
+            clean, cl = run(g, p, workspace=ws, **kw)
+            o[hit], lse[hit] = clean[hit], cl[hit]
+            check(p, o, lse, label=str(kw), **kw)
+
+
+def test_a_query_without_a_key_is_empty_whatever_it_holds(g):
+    """NaN in a row whose mask leaves nothing: zeros and -inf, as for any row without a key."""
+    p = inputs([600, 3], [40, 5000], 8, 2, 128, 64, seed=43)
+    p["q"][:560] = float("nan")
+    o, lse = run(g, p)
+    assert bool(torch.isneginf(lse[:560]).all()) and bool((o[:560].float() == 0).all())
+    check(p, o, lse)
