@@ -859,14 +859,14 @@ __device__ __forceinline__ void fp8_swap_consumer(const DecodeArgs& a, const Wor
             wgt[u] = fast_exp2(mg[(u * C::RW + rr) * C::MROW + D] - M_use);
             L += wgt[u] * mg[(u * C::RW + rr) * C::MROW + D + 1];
         }
-        const float inv = L > 0.f ? vs / L : 0.f;
+        const float inv = L != 0.f ? vs / L : 0.f;      // a NaN sum is no empty row
         for (int d = wk * DW + lane; d < (wk + 1) * DW; d += 32) {
             float o = 0.f;
 #pragma unroll
             for (int u = 0; u < C::KSPLIT; ++u) o += wgt[u] * mg[(u * C::RW + rr) * C::MROW + d];
             a.part_o[(part_row0 + rr) * D + d] = o * inv;
         }
-        if (wk == 0 && lane == 0) a.part_lse[part_row0 + rr] = L > 0.f ? M + log2f(L) : -INFINITY;
+        if (wk == 0 && lane == 0) a.part_lse[part_row0 + rr] = L != 0.f ? M + log2f(L) : -INFINITY;
     }
 }
 
@@ -1193,7 +1193,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                 const int rl = mf * 16 + (lane >> 2) + 8 * h;
                 if (rl >= w.rows_here) continue;
                 const float l = l_run[h];
-                const float inv = l > 0.f ? vs / l : 0.f;
+                const float inv = l != 0.f ? vs / l : 0.f;      // a NaN sum is no empty row
                 float* dst = a.part_o + (part_row0 + rl) * D + 4 * t4;
 #pragma unroll
                 for (int q = 0; q < D / 32; ++q)
@@ -1204,7 +1204,7 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                         *reinterpret_cast<float4*>(dst + 32 * q + 16 * i) =
                             make_float4(ev[2 * h] * inv, od[2 * h] * inv, ev[2 * h + 1] * inv, od[2 * h + 1] * inv);
                     }
-                if (t4 == 0) a.part_lse[part_row0 + rl] = l > 0.f ? m_run[h] + log2f(l) : -INFINITY;
+                if (t4 == 0) a.part_lse[part_row0 + rl] = l != 0.f ? m_run[h] + log2f(l) : -INFINITY;
             }
         } else {
             named_bar_sync(1, C::NCT);                  // every consumer warp is done with the ring
@@ -1245,14 +1245,14 @@ decode_fp8_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constan
                     wgt[u] = fast_exp2(frag[(u * 16 + rr) * C::MROW + D] - M_use);
                     L += wgt[u] * frag[(u * 16 + rr) * C::MROW + D + 1];
                 }
-                const float inv = L > 0.f ? vs / L : 0.f;
+                const float inv = L != 0.f ? vs / L : 0.f;      // a NaN sum is no empty row
                 for (int d = wk * DW + lane; d < (wk + 1) * DW; d += 32) {
                     float o = 0.f;
 #pragma unroll
                     for (int u = 0; u < C::KSPLIT; ++u) o += wgt[u] * frag[(u * 16 + rr) * C::MROW + d];
                     a.part_o[(part_row0 + rl) * D + d] = o * inv;
                 }
-                if (wk == 0 && lane == 0) a.part_lse[part_row0 + rl] = L > 0.f ? M + log2f(L) : -INFINITY;
+                if (wk == 0 && lane == 0) a.part_lse[part_row0 + rl] = L != 0.f ? M + log2f(L) : -INFINITY;
             }
         }
     }
@@ -1307,17 +1307,17 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeArgs a,
     }
 
     float M = -INFINITY;
-    for (int s = lane; s < n; s += 32) M = fmaxf(M, a.part_lse[base + (size_t)s * R]);
+    for (int s = lane; s < n; s += 32) M = max_or_nan(M, a.part_lse[base + (size_t)s * R]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    for (int o = 16; o > 0; o >>= 1) M = max_or_nan(M, __shfl_xor_sync(0xffffffffu, M, o));
 
     __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(a.o) + (size_t)orow * D;
     constexpr int PER = D / 128 > 0 ? D / 128 : 1;     // float4 groups per lane
     // A sink joins the denominator once per row (GQAPagedFwdOp sinks): the
     // weights are taken against max(M, s); +inf zeroes the row.  A row no
-    // split saw stays zero with LSE -inf.
+    // split saw stays zero with LSE -inf; one with a NaN LSE among its splits is NaN.
     const float s2 = (a.x.sinks && M != -INFINITY) ? a.x.sinks[h] * 1.4426950408889634f : -INFINITY;
-    if (s2 == INFINITY) {
+    if (s2 == INFINITY && !isnan(M)) {
 #pragma unroll
         for (int q = 0; q < PER; ++q) {
             const int d = (q * 32 + lane) * 4;
@@ -1326,7 +1326,7 @@ __global__ void __launch_bounds__(128) decode_combine_kernel(const DecodeArgs a,
         if (lane == 0 && a.lse) a.lse[orow] = INFINITY;
         return;
     }
-    M = fmaxf(M, s2);
+    M = max_or_nan(M, s2);
     if (M == -INFINITY) {
 #pragma unroll
         for (int q = 0; q < PER; ++q) {

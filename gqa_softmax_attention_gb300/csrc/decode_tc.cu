@@ -812,7 +812,9 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 tc_fence_after();
                 const int id = c.s + cta;                  // partial id of this piece
                 const size_t part_row = (size_t)id * R + r;
-                const float inv = l_run > 0.f ? o_scale / l_run : 0.f;
+                // e4m3: only a sum of exactly 0 means no key; a NaN one goes on to the combine
+                const bool some = KV8 ? l_run != 0.f : l_run > 0.f;
+                const float inv = some ? o_scale / l_run : 0.f;
 #pragma unroll 1
                 for (int cc = 0; cc < D / 32; cc += 2) {
                     float o[64];
@@ -827,7 +829,7 @@ decode_tc_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                                                  o[4 * e + 3] * inv);
                     }
                 }
-                if (row_ok) a.part_lse[part_row] = l_run > 0.f ? m_ref + log2f(l_run) : -INFINITY;
+                if (row_ok) a.part_lse[part_row] = some ? m_ref + log2f(l_run) : -INFINITY;
                 if (piece_lt0 == 0 && r == 0) {
                     // this CTA holds the segment's first tile: record its pieces
                     const long seg_start = (long)rg.g0 + it - c.lt;

@@ -460,3 +460,26 @@ def test_a_query_without_a_key_is_empty_whatever_it_holds(g):
     o, lse = run(g, p)
     assert bool(torch.isneginf(lse[:560]).all()) and bool((o[:560].float() == 0).all())
     check(p, o, lse)
+
+
+@pytest.mark.parametrize("value", [float("nan"), INF, -INF, 1e5], ids=str)
+@pytest.mark.parametrize("geometry", [(32, 8, 128, 64), (24, 2, 256, 16), (12, 1, 128, 24), (36, 2, 128, 64),
+                                      (64, 2, 256, 64), (64, 2, 128, 5)], ids=str)
+def test_single_queries_that_are_no_numbers_show(g, geometry, value):
+    """The same in single-token requests, on the split decode kernels (rows of up to 8, 16
+    and 32 per KV head, the tensor-core form, pages that do not fit its boxes)."""
+    p = inputs([1, 1, 1], [3000, 200, 1], *geometry, seed=47)
+    Hq, D = geometry[0], geometry[2]
+    bad = dict(p, q=p["q"].clone())
+    bad["q"][0, Hq - 1, 5] = value
+    bad["q"][1, 0, D - 1] = value
+    hit = torch.zeros(3, Hq, dtype=torch.bool)
+    hit[0, Hq - 1] = hit[1, 0] = True
+    sinks = torch.randn(Hq, generator=torch.Generator().manual_seed(3))
+    sinks[0] = INF
+    for kw in (dict(), dict(sinks=sinks), dict(window_left=150)):
+        o, lse = run(g, bad, **kw)
+        assert bool(o[hit].isnan().all()) and bool(lse[hit].isnan().all()), str(kw)
+        clean, cl = run(g, p, **kw)
+        o[hit], lse[hit] = clean[hit], cl[hit]
+        check(p, o, lse, label=str(kw), **kw)
