@@ -597,13 +597,17 @@ def _rope_args(q, k, v, cos_sin, positions, q_weight, k_weight, interleaved, axe
         if axes is None:
             n_axes, pa, pshape = 1, None, lead
         else:
-            if len(axes) != rot // 2 or not isinstance(positions, torch.Tensor) or positions.dim() < 2:
+            try:                       # value by value: bytes(array) would take an array's memory
+                pa = bytes(list(axes))
+            except (TypeError, ValueError) as e:
+                raise ValueError("axes must be integers in [0, 4)") from e
+            if len(pa) != rot // 2 or not isinstance(positions, torch.Tensor) or positions.dim() < 2:
                 raise ValueError("axes must name the axis of each of the rot / 2 = %d pairs, positions be "
                                  "[n_axes, ...]" % (rot // 2))
             n_axes = positions.shape[0]
-            if n_axes > 4 or (rot > 0 and not 0 <= min(axes) <= max(axes) < n_axes):
+            if n_axes > 4 or (rot > 0 and max(pa) >= n_axes):
                 raise ValueError("axes must lie in [0, n_axes = %d), at most four axes" % n_axes)
-            pa, pshape = bytes(axes), (n_axes, *lead)
+            pshape = (n_axes, *lead)
         pp = _data("positions", positions, torch.int32, pshape, dev)
         rope = _lib.Rope(pc, pp, max_pos, rot, 1 if interleaved else 0, n_axes, pa)
     elif positions is not None or axes is not None:
@@ -629,7 +633,7 @@ def attn_qk_norm_rope(q, k, cos_sin, positions, q_weight=None, k_weight=None, ep
     cos_sin [max_pos, rot] float32: cosines of the rot / 2 pairs, then their
     sines (rope_table), or None for no rotation; positions int32 of q's leading
     shape.  A pair is dims (j, j + rot / 2), or (2j, 2j + 1) with interleaved; dims
-    past rot pass through.  axes: the position axis of each pair (rot / 2 ints),
+    past rot pass through.  axes: the position axis of each pair (rot / 2 integers),
     positions then [n_axes, *leading] with up to four axes.
     q_weight / k_weight [D] (q's dtype, or both float32) or None for no norm of
     that side.  FP32 throughout, rounded once.

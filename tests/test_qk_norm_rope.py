@@ -384,3 +384,23 @@ def test_extreme_scales(g):
     g.attn_qk_norm_rope_paged(z, z, v, None, None, slots, kc, vc, v_scale=vs, requests=slots)
     want = (v.float().cpu() / vs.cpu()[..., None]).clamp(-448, 448).to(torch.float8_e4m3fn)
     assert torch.equal(vc.view(T, Hkv, D).cpu().float(), want.float())
+
+
+@pytest.mark.parametrize("n_axes", [2, 3])
+def test_axes_of_every_integer_type(g, n_axes):
+    """axes as a list, a tuple, bytes, a NumPy array of any integer type, a tensor: the same result."""
+    np = pytest.importorskip("numpy")
+    q, k, v, table, pos, qw, kw = inputs(9, 6, 2, 128, n_axes=n_axes)
+    axes = [(j * j + 1) % n_axes for j in range(64)]
+    want = g.attn_qk_norm_rope(q, k, table, pos, qw, kw, axes=axes)
+    close16(want[0], *reference(q, qw, table, pos, axes=axes))
+    forms = [tuple(axes), bytes(axes), torch.tensor(axes), torch.tensor(axes, dtype=torch.int32).cuda()]
+    forms += [np.array(axes, dtype=t) for t in ("int8", "uint8", "int16", "int32", "uint32", "int64", ">i4")]
+    forms += [np.array([axes, axes], dtype="int64").T[:, 0], [np.int64(a) for a in axes]]
+    for form in forms:
+        for o, w in zip(g.attn_qk_norm_rope(q, k, table, pos, qw, kw, axes=form), want):
+            assert torch.equal(o, w), type(form)
+    for bad in ([0.0] * 64, np.zeros(64), np.zeros((64, 2), dtype="int64"), torch.zeros(64), ["0"] * 64, [-1] * 64,
+                [n_axes] * 64, [256] * 64, np.full(64, 256), [0] * 63, 7):
+        with pytest.raises(ValueError):
+            g.attn_qk_norm_rope(q, k, table, pos, qw, kw, axes=bad)
