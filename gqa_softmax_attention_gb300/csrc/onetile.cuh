@@ -66,7 +66,8 @@
 // Both are described by a slice stride and an 8-key-group stride, which is
 // all the MMA descriptors need.
 //
-// The lazy rescale is that of prefill.cu.  Rescaling O before PV of tile i
+// The lazy rescale is that of prefill.cu (kPaged8: from a reference below the max,
+// kLead8).  Rescaling O before PV of tile i
 // needs PV of tile i-1 complete (o_ready, waited for only by a warp that
 // rescales): S of tile i having landed implies PV of tile i-2, so the phase
 // waited for is never more than one behind.  Every wait is bounded; on a
@@ -161,7 +162,15 @@ struct Cfg {
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 constexpr uint32_t COL_S0 = 0, COL_O = 256, COL_Q8 = 384, TMEM_COLS = 512;
-constexpr float kSumLimit8 = 32768.f;          // kPaged8: P is float16
+// kPaged8: P is float16.  The reference stands kLead8 binades below the row's max,
+// so that P = 2^kLead8 for the strongest key and weights down to 2^-20 of its keep
+// float16's eleven bits; below that a weight is off by at most half a subnormal
+// step, 2^-25 in P, 2^-31 of the strongest.  (With the reference at the max, weights
+// below 2^-25 of it vanished from P V but not from the row sum: one strong key before
+// 131071 equal ones took 3.8e-3 from a mean of 3.8e-3.)  Up to 2^(kLead8 + 8) between
+// rescales and up to kSumLimit8 on a plain tile, P stays a finite float16.
+constexpr float kLead8 = 6.f;
+constexpr float kSumLimit8 = 65504.f;
 
 // tanh of two values of magnitude at most 0.6: y times a polynomial of degree 4
 // in y^2, the minimax one for the relative error there (Remez exchange in 40
@@ -1111,11 +1120,12 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 uint32_t sr[BN];
                 tmem_ld128(tmem + lane_addr + col_s, sr);
                 float* s = reinterpret_cast<float*>(sr);
+                float most_lead = kLead8 + kRescaleThreshold;        // kPaged8: of the max over the reference
                 if constexpr (KV8) {
                     // Once every row of the warp has a reference max, a plain tile
                     // is exponentiated against it without taking its own; a row
-                    // sum past kSumLimit8 (no P of the row can be larger, and
-                    // float16 holds it) sends the warp to the full step, the scores
+                    // sum past kSumLimit8 (no P of the row is larger than the sum, and
+                    // float16 holds that) sends the warp to the full step, the scores
                     // being still in TMEM.
                     if (has_ref && !prepare && !capped) {
                         uint32_t pk[BN / 2];
@@ -1131,6 +1141,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                             continue;
                         }
                         tmem_ld128(tmem + lane_addr + col_s, sr);
+                        // a row with such a sum has a score 9 binades or more above
+                        // its reference: it takes a new one, so that the tiles after
+                        // this one are plain again
+                        most_lead = kLead8 + 2.f;
                     }
                 }
 
@@ -1173,9 +1187,11 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 const float mx_raw = fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3]));
                 const float mx = !fast ? mx_raw : (late_cap ? tanh_mufu(mx_raw * to_y) * mul : mx_raw * mul);
                 float alpha = 1.f;
-                if (mx > m_ref + kRescaleThreshold) {
-                    alpha = fast_exp2(m_ref - mx);
-                    m_ref = mx;
+                // (the difference of two near values is exact: no large score rounds past the threshold)
+                if (KV8 ? mx - m_ref > most_lead : mx > m_ref + kRescaleThreshold) {
+                    const float ref = KV8 ? mx - kLead8 : mx;
+                    alpha = fast_exp2(m_ref - ref);
+                    m_ref = ref;
                 }
                 const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                 const float fa = fast ? mul : 1.f;

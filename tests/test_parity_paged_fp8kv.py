@@ -11,6 +11,8 @@ parity.compare does not fit here: a row that sees one key returns its value, up
 to 5.5 x 2 with scales up to 2, and half a bfloat16 step between 8 and 16 is
 2^-5 = 3.1e-2.  The LSE limit (1e-3) and the empty rows are those of compare.
 """
+import math
+
 import pytest
 import torch
 
@@ -483,3 +485,40 @@ def test_single_queries_that_are_no_numbers_show(g, geometry, value):
         clean, cl = run(g, p, **kw)
         o[hit], lse[hit] = clean[hit], cl[hit]
         check(p, o, lse, label=str(kw), **kw)
+
+
+@pytest.mark.parametrize("parts", [False, True], ids=["one_part", "in_parts"])
+@pytest.mark.parametrize("cap", [None, 20.0], ids=["plain", "softcap"])
+@pytest.mark.parametrize("geometry", [(4, 1, 128, 64), (12, 1, 256, 16)], ids=str)
+@pytest.mark.parametrize("bits", [12.0, 20.6, 25.05, 27.5])
+def test_one_strong_key_and_a_long_flat_tail(g, bits, geometry, cap, parts):
+    """Key 0 leads every other of 131072 keys by `bits` binades and has the value
+    zero, so the result is what the tail's small weights carry:
+    n w / (1 + n w), w = 2^-bits, n keys behind the first.
+
+    Tolerance: half a step of the output; a weight above float16's normal range keeps
+    2^-11 of itself, one below it is off by half a float16 subnormal step, 2^-25, in
+    units of 2^-6 of the leading weight: n 2^-31 in all; scores of at most 20 log2
+    units carry 2^-13 of each weight (2^-23 relative of 38, and the softcap's 1e-7 of
+    20 / ln 2 log2 units)."""
+    Hq, Hkv, D, ps = geometry
+    L, nq = 131072, 3
+    lead = bits * math.log(2.0)                              # the leading score in nats
+    z = lead if cap is None else cap * math.atanh(lead / cap)
+    kc = torch.zeros(L // ps, ps, Hkv, D, dtype=torch.uint8)
+    kc[0, 0] = 0x38                                          # 1.0
+    vc = torch.full_like(kc, 0x38)
+    vc[0, 0] = 0
+    p = dict(q=torch.ones(nq, Hq, D, dtype=torch.float16), k_cache=kc.view(torch.float8_e4m3fn),
+             v_cache=vc.view(torch.float8_e4m3fn), k_scale=torch.ones(1, Hkv), v_scale=torch.ones(1, Hkv),
+             cu_seqlens_q=torch.tensor([0, nq], dtype=torch.int32), cache_seqlens=torch.tensor([L], dtype=torch.int32),
+             block_table=torch.arange(L // ps, dtype=torch.int32)[None].contiguous())
+    o, lse = run(g, p, scale=z / D, softcap=cap, workspace=None if parts else one_part(g, p))
+    n = (L - nq + torch.arange(nq, dtype=torch.float64))[:, None, None]
+    nw = n * 2.0 ** -bits
+    want = (nw / (1 + nw)).expand(nq, Hq, D)
+    tol = torch.finfo(o.dtype).eps / 2 * want + (2.0 ** -11 + 2.0 ** -13) * want + n * 2.0 ** -31
+    off = (o.double() - want).abs()
+    assert bool((off <= tol).all()), "%.3g of its tolerance" % float((off / tol).max())
+    ref = lead + torch.log1p(nw[..., 0])
+    assert bool(((lse.double() - ref).abs() <= 2.0 ** -13).all())
