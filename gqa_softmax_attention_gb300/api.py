@@ -520,6 +520,12 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
     out: the six tensors of an earlier call, written again (the buffers of a
     captured graph).  Nothing is read back: counts[0] > max_tokens, or
     counts[2] > n, tells the caller later that rows or pages ran out.
+    The attention calls place query i of a request at cache_seqlens - nq + i, so a
+    request whose tokens were cut (by max_tokens, or past the table's capacity of
+    max_pages * page_size tokens: cache_seqlens < past + new, which counts does not
+    show) has its queries, the valid ones too, at wrong positions: do not use their
+    attention; repeat the step with new_lens cut to what fits.  Cache rows and
+    other requests are not affected.
     """
     B = _size("past_lens", past_lens, 1, 0)
     dev, i32, T = past_lens.device, torch.int32, int(max_tokens)

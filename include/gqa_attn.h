@@ -394,7 +394,17 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
  * A token has slot -1 where its request runs past the capacity, the free list
  * is exhausted (the table entry is then -1 too) or the page id lies outside
  * [0, num_pages).  Tokens past max_tokens are counted, but get no row and no
- * page: counts[0] > max_tokens asks for another call with more rows.  The call
+ * page: counts[0] > max_tokens asks for another call with more rows.
+ *
+ * The attention calls place the i-th of a request's nq queries at position
+ * cache_seqlens - nq + i.  That is past + i unless the request was cut: one that
+ * runs past the table's capacity (cache_seqlens < past + new; counts does NOT
+ * show it), or one whose tokens max_tokens cut off (counts[0] > max_tokens).  The
+ * queries of such a request, those with a valid slot too, are attended at the wrong
+ * positions and must not be used; its cache rows and the other requests are right.
+ * Keep past + new within the capacity, or repeat the step with new_lens cut to it.
+ *
+ * The call
  * changes nothing it reads (an output that overlaps an input or another output
  * is refused), so it may be repeated or replayed.  One launch, no workspace, no host read-back.
  */

@@ -136,3 +136,88 @@ def test_chunks_then_decode(g, e4m3, graph):
         got, gl = torch.cat(hist[b]["o"]).double(), torch.cat(hist[b]["lse"]).double()
         assert float((got - ref).abs().max()) <= 2e-2 and float((got - ref).abs().mean()) <= 2e-3
         assert float((gl - torch.logsumexp(z, -1).t()).abs().max()) <= 1e-3
+
+
+@pytest.mark.parametrize("over", ["capacity", "rows"])
+@pytest.mark.parametrize("e4m3", [False, True], ids=["bf16", "e4m3"])
+def test_a_request_that_does_not_fit(g, e4m3, over):
+    """One request past the table's capacity, or a batch cut by its rows: the other
+    requests are as ever, the tokens with a slot are stored, the cut shows where the
+    documentation says, and the step repeated with the lengths cut is right throughout."""
+    dev, Hq, Hkv, D, ps, max_pages = "cuda", 8, 2, 128, 16, 6
+    cap, B = ps * max_pages, 3
+    gen = torch.Generator().manual_seed(5)
+    held = [40, cap - 2, 20] if over == "capacity" else [40, 30, 20]
+    asked = [3, 5, 2] if over == "capacity" else [3, 2, 6]
+    fits = [3, 2, 2]
+    T = 12 if over == "capacity" else 7
+    num_pages = B * max_pages + 4
+    cdtype = torch.float8_e4m3fn if e4m3 else torch.bfloat16
+    raw = torch.uint8 if e4m3 else torch.bfloat16
+    kc, vc = (torch.randn(num_pages, ps, Hkv, D, generator=gen).to(cdtype).to(dev) for _ in range(2))
+    sc = torch.full((B, Hkv), 0.02, device=dev) if e4m3 else None
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    ids = torch.randperm(num_pages, generator=gen).int()
+    table, at = torch.full((B, max_pages), -1, dtype=torch.int32), 0
+    for b, n in enumerate(held):
+        m = -(-n // ps)
+        table[b, :m] = ids[at:at + m]
+        at += m
+    table, free = table.to(dev), ids[at:].contiguous().to(dev)
+    qkv = torch.randn(T, Hq + 2 * Hkv, D, generator=gen).bfloat16().to(dev)
+    q, k, v = qkv[:, :Hq], qkv[:, Hq:Hq + Hkv], qkv[:, Hq + Hkv:]
+    cos_sin, w = g.rope_table(cap + 8, D, device=dev), torch.ones(D, dtype=torch.bfloat16, device=dev)
+
+    def step(new, x):
+        m = g.attn_paged_slots(i32(held), i32(new), table, free, ps, num_pages, T)
+        a = (x[0], x[1], x[2], cos_sin, m[3], m[2], kc, vc, w, w)
+        qo = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        if e4m3:
+            g.attn_qk_norm_rope_paged(*a, k_scale=sc, v_scale=sc, requests=m[4], out=qo)
+            o, lse = g.attn_fwd_paged_fp8kv(qo, kc, vc, sc, sc, m[0], m[1], table)
+        else:
+            g.attn_qk_norm_rope_paged(*a, out=qo)
+            o, lse = g.attn_fwd_paged(qo, kc, vc, m[0], m[1], table)
+        torch.cuda.synchronize()
+        return m, qo, o, lse
+
+    def right(b, m, qo, o, lse, n):
+        """Request b's n queries, at positions held + i, against 64 bits."""
+        a, L = int(m[0][b]), held[b] + n
+        t = torch.arange(L, device=dev)
+        rows = table[b].long()[t // ps] * ps + t % ps
+        f = 0.02 if e4m3 else 1.0
+        k64, v64 = ((c.view(raw).view(-1, Hkv, D)[rows].view(cdtype).float().cpu().double() * f)
+                    .repeat_interleave(Hq // Hkv, 1) for c in (kc, vc))
+        z = torch.einsum("ihd,jhd->hij", qo[a:a + n].cpu().double(), k64) / math.sqrt(D)
+        z.masked_fill_(torch.arange(L)[None] > (held[b] + torch.arange(n))[:, None], -math.inf)
+        ref = torch.einsum("hij,jhd->ihd", torch.softmax(z, -1), v64)
+        assert float((o[a:a + n].cpu().double() - ref).abs().max()) <= 2e-2
+        assert float((lse[a:a + n].cpu().double() - torch.logsumexp(z, -1).t()).abs().max()) <= 1e-3
+
+    m, qo, o, lse = step(asked, (q, k, v))
+    cut = 1 if over == "capacity" else 2
+    for b in range(B):
+        if b != cut:
+            right(b, m, qo, o, lse, asked[b])
+    slots, pos, req, counts = (x.tolist() for x in m[2:])
+    a = int(m[0][cut])
+    for i in range(min(asked[cut], T - a)):
+        p = held[cut] + i
+        assert req[a + i] == cut and pos[a + i] == p
+        assert slots[a + i] == (int(table[cut, p // ps]) * ps + p % ps if p < cap else -1)
+    stored = g.attn_qk_norm_rope(q, k, cos_sin, m[3], w, w)[1]
+    if not e4m3:
+        for i in range(fits[cut]):
+            assert torch.equal(kc.view(-1, Hkv, D)[slots[a + i]], stored[a + i])
+            assert torch.equal(vc.view(-1, Hkv, D)[slots[a + i]], v[a + i])
+    short = [L < h + n for L, h, n in zip(m[1].tolist(), held, asked)]
+    assert short == [False, over == "capacity", False]
+    assert (counts[0] > T) == (over == "rows") and counts[0] == sum(asked)
+    # the step again, with what fits (the tokens that are left out closed up)
+    keep = [int(m[0][b]) + i for b in range(B) for i in range(fits[b])]
+    keep += [t for t in range(T) if t not in keep]
+    m, qo, o, lse = step(fits, (q[keep], k[keep], v[keep]))
+    assert m[5].tolist()[0] == sum(fits)
+    for b in range(B):
+        right(b, m, qo, o, lse, fits[b])
