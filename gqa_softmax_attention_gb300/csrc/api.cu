@@ -448,6 +448,10 @@ static bool fp8_may_split(int B, int total_q, int Hq, int Hkv, long capacity) {
 }
 
 size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int page_size, int max_pages) {
+    // sizes the call itself refuses
+    if ((D != 128 && D != 256) || page_size <= 0 || max_pages <= 0 || total_q >= kMaxSeq ||
+        (long)max_pages * page_size >= kMaxSeq)
+        return 0;
     const size_t w = attn_paged_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
     if (w == 0 || !fp8_may_split(B, total_q, Hq, Hkv, (long)max_pages * page_size)) return w;
     return (w + 255) / 256 * 256 + fp8_parts_bytes(D);

@@ -169,3 +169,15 @@ def test_rope_table_matches_its_formula():
     assert t.shape == (1000, 48)
     with pytest.raises(ValueError):
         rope_table(10, 7)
+
+
+def test_fp8kv_workspace_size_of_invalid_sizes(lib):
+    size = lambda **k: lib.attn_paged_fp8kv_workspace_size(*{**dict(B=2, total_q=8, Hq=8, Hkv=2, D=128, page_size=16,  # noqa: E731
+                                                                    max_pages=400), **k}.values())
+    assert size() >= lib.attn_paged_workspace_size(2, 8, 8, 2, 128, 16, 400) > 0      # and room for key parts, on a GPU
+    assert size(D=256) > 0 and size(max_pages=2) > 0
+    for bad in (dict(D=64), dict(D=96), dict(D=0), dict(D=-1), dict(D=-1000), dict(D=512), dict(page_size=0),
+                dict(page_size=-16), dict(max_pages=0), dict(max_pages=-3), dict(page_size=-16, max_pages=-400),
+                dict(max_pages=1 << 26), dict(total_q=-1), dict(total_q=1 << 30), dict(B=0), dict(Hq=0), dict(Hkv=0),
+                dict(Hq=6, Hkv=4), dict(Hq=258, Hkv=2)):
+        assert size(**bad) == 0, bad
