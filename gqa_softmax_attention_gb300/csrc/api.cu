@@ -457,8 +457,8 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
     return (w + 255) / 256 * 256 + fp8_parts_bytes(D);
 }
 
-// Shared checks and set-up of the packed entry points (tq: nullptr where no map
-// of q is wanted).
+// Shared checks and set-up of the packed entry points (tq, to: nullptr where no
+// map of q or o is wanted, or not yet).
 static gqa_status varlen_common(const void* q, void* o, float* lse, const int32_t* cu_q, int B, int total_q,
                                 int Hq, int Hkv, int D, int causal, float scale, const gqa_options* opts,
                                 void* workspace, size_t workspace_bytes, PrefillArgs* a, CUtensorMap* tq,
@@ -479,7 +479,7 @@ static gqa_status varlen_common(const void* q, void* o, float* lse, const int32_
     const bool f16 = opts && opts->dtype == GQA_FP16;
     const int g = Hq / Hkv, qpb = 128 / g;
     if (total_q > 0 && ((tq && !make_thd_map(tq, q, total_q, Hq, D, g, qpb, f16)) ||
-                        !make_thd_map(to, o, total_q, Hq, D, g, qpb, f16)))
+                        (to && !make_thd_map(to, o, total_q, Hq, D, g, qpb, f16))))
         return GQA_ERR_CUDA;
     a->mask = nullptr;
     a->o = o;
@@ -577,6 +577,16 @@ static SideStream* side_stream(cudaStream_t caller) {
     return &ss;
 }
 
+// A stretch of memory (none: a null pointer or no bytes).
+struct Span {
+    const void* p;
+    long bytes;
+};
+static bool overlap(const Span& x, const Span& y) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return x.p && y.p && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
+}
+
 // Packed queries over a paged cache: 16-bit, or (fp8) e4m3fn bytes with scales.
 static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_cache, bool fp8, const float* k_scale,
                             const float* v_scale, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
@@ -596,12 +606,31 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
         if (D == 64) return GQA_ERR_UNSUPPORTED;
     }
     gqa_status st = varlen_common(q, o, lse, cu_seqlens_q, B, total_q, Hq, Hkv, D, causal, scale, opts, workspace,
-                                  workspace_bytes, &a, fp8 ? nullptr : &tq, &to);
+                                  workspace_bytes, &a, fp8 ? nullptr : &tq, fp8 ? nullptr : &to);
     if (st != GQA_OK) return st;
     if (!k_cache || !v_cache || !cache_seqlens || !block_table) return GQA_ERR_INVALID_ARG;
     if (!aligned16(k_cache) || !aligned16(v_cache)) return GQA_ERR_MISALIGNED;
     if (!aligned4(cache_seqlens) || !aligned4(block_table)) return GQA_ERR_MISALIGNED;
     if (total_q == 0) return GQA_OK;
+    if (fp8) {
+        // Chunks, decode steps and parts run side by side, and a Q block is read while
+        // the one before is written out: nothing written may overlap anything read.
+        const size_t uses = attn_paged_fp8kv_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
+        const long rows_q = (long)total_q * Hq, cache = (long)num_pages * page_size * Hkv * D;
+        const Span writes[] = {{o, rows_q * D * 2}, {lse, rows_q * 4},
+                               {workspace, (long)(uses < workspace_bytes ? uses : workspace_bytes)}};
+        const Span reads[] = {{q, rows_q * D * 2}, {k_cache, cache}, {v_cache, cache},
+                              {k_scale, (long)B * Hkv * 4}, {v_scale, (long)B * Hkv * 4},
+                              {cu_seqlens_q, (B + 1L) * 4}, {cache_seqlens, B * 4L},
+                              {block_table, (long)B * max_pages * 4}, {opts ? opts->sinks : nullptr, Hq * 4L}};
+        for (int i = 0; i < 3; ++i) {
+            for (const Span& r : reads)
+                if (overlap(writes[i], r)) return GQA_ERR_INVALID_ARG;
+            for (int j = 0; j < i; ++j)
+                if (overlap(writes[i], writes[j])) return GQA_ERR_INVALID_ARG;
+        }
+        if (!make_thd_map(&to, o, total_q, Hq, D, a.g, a.qpb, a.f16)) return GQA_ERR_CUDA;
+    }
     a.table = block_table;
     a.page_size = page_size;
     a.max_pages = max_pages;
@@ -733,16 +762,6 @@ gqa_status attn_fwd_paged_fp8kv(const void* q, const void* k_cache, const void* 
     return fwd_paged(q, k_cache, v_cache, true, k_scale, v_scale, cu_seqlens_q, cache_seqlens, block_table, page_size,
                      o, lse, B, total_q, Hq, Hkv, D, num_pages, max_pages, causal, scale, opts, workspace,
                      workspace_bytes, stream);
-}
-
-// A stretch of memory (none: a null pointer or no bytes).
-struct Span {
-    const void* p;
-    long bytes;
-};
-static bool overlap(const Span& x, const Span& y) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
-    return x.p && y.p && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
 }
 
 // ---------------------------------------------------------------- step metadata

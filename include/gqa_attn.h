@@ -350,6 +350,9 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
  *                     each row block into parts for the idle SMs and join
  *                     them; results agree within the usual tolerance.
  *
+ * o, lse and the workspace may overlap neither one another nor anything that is read
+ * (GQA_ERR_INVALID_ARG): chunks, decode steps and parts run side by side.
+ *
  * Keys and values are widened exactly to float16 and the products run in
  * float16 with FP32 accumulation: Q is rounded to float16 once, so a bfloat16
  * Q must stay below 65504 (attn_decode_paged_fp8kv).  D = 128 or 256

@@ -181,3 +181,32 @@ def test_fp8kv_workspace_size_of_invalid_sizes(lib):
                 dict(max_pages=1 << 26), dict(total_q=-1), dict(total_q=1 << 30), dict(B=0), dict(Hq=0), dict(Hkv=0),
                 dict(Hq=6, Hkv=4), dict(Hq=258, Hkv=2)):
         assert size(**bad) == 0, bad
+
+
+def test_fwd_paged_fp8kv_refuses_overlaps(lib):
+    """Nothing written (o, lse, the workspace) may overlap what is read or another of them."""
+    MB = 1 << 20
+    place = {n: (16 + 16 * i) * MB for i, n in enumerate(("q", "kc", "vc", "ks", "vs", "cu", "lens", "table", "o", "lse",
+                                                          "ws", "sinks"))}
+    B, T, Hq, Hkv, D, ps, pages, max_pages = 3, 40, 8, 2, 128, 16, 50, 20
+    size = lib.attn_paged_fp8kv_workspace_size(B, T, Hq, Hkv, D, ps, max_pages)
+    bytes_of = dict(q=T * Hq * D * 2, kc=pages * ps * Hkv * D, vc=pages * ps * Hkv * D, ks=B * Hkv * 4, vs=B * Hkv * 4,
+                    cu=(B + 1) * 4, lens=B * 4, table=B * max_pages * 4, sinks=Hq * 4, o=T * Hq * D * 2, lse=T * Hq * 4,
+                    ws=size)
+
+    def call(**moved):
+        p = {n: P(a) for n, a in {**place, **moved}.items()}
+        opt = _lib.Options(-1, -1, 0.0, p["sinks"], 0)
+        return lib.attn_fwd_paged_fp8kv(p["q"], p["kc"], p["vc"], p["ks"], p["vs"], p["cu"], p["lens"], p["table"], ps,
+                                        p["o"], p["lse"], B, T, Hq, Hkv, D, pages, max_pages, 1, 0.125,
+                                        ctypes.byref(opt), p["ws"], size + (1 << 30), None)
+
+    for w in ("o", "lse", "ws"):
+        for r in bytes_of:
+            if r == w:
+                continue
+            up = 256 * ((bytes_of[r] - 1) // 256)                      # the last 256 bytes of the other
+            assert call(**{w: place[r]}) == INVALID, (w, r)
+            assert call(**{w: place[r] + up}) == INVALID, (w, r)
+            down = 256 * ((bytes_of[w] - 1) // 256)
+            assert call(**{w: place[r] - down}) == INVALID, (w, r)

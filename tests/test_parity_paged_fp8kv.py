@@ -522,3 +522,27 @@ def test_one_strong_key_and_a_long_flat_tail(g, bits, geometry, cap, parts):
     assert bool((off <= tol).all()), "%.3g of its tolerance" % float((off / tol).max())
     ref = lead + torch.log1p(nw[..., 0])
     assert bool(((lse.double() - ref).abs() <= 2.0 ** -13).all())
+
+
+def test_outputs_over_inputs_are_refused_and_next_to_them_are_not(g):
+    p = inputs([3, 40], [700, 90], 8, 2, 128, 16, seed=51)
+    d = {n: p[n].cuda() for n in NAMES}
+    T, n = 43, 43 * 8 * 128
+    size = g.attn_paged_fp8kv_workspace_size(2, T, 8, 2, 128, 16, p["block_table"].shape[1])
+    # q, o, lse and the workspace one behind the other in one buffer
+    buf = torch.zeros(4 * n + T * 8 * 4 + 256 + size, dtype=torch.uint8, device="cuda")
+    q, o = (buf[i * 2 * n:(i + 1) * 2 * n].view(torch.bfloat16).view(T, 8, 128) for i in range(2))
+    lse = buf[4 * n:4 * n + T * 8 * 4].view(torch.float32).view(T, 8)
+    at = (4 * n + T * 8 * 4 + 255) // 256 * 256
+    ws = buf[at:at + size]
+    q.copy_(d["q"])
+    d["q"] = q
+    g.attn_fwd_paged_fp8kv(**d, out=o, lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    check(p, o.cpu(), lse.cpu())
+    kb = d["k_cache"].view(torch.uint8).flatten()
+    for bad in (dict(out=q), dict(lse=buf[:T * 8 * 4].view(torch.float32).view(T, 8)),
+                dict(out=kb[:2 * n].view(torch.bfloat16).view(T, 8, 128)), dict(workspace=buf),
+                dict(workspace=kb), dict(out=o, lse=o.view(torch.float32).flatten()[:T * 8].view(T, 8))):
+        with pytest.raises(ValueError):
+            g.attn_fwd_paged_fp8kv(**d, **bad)
