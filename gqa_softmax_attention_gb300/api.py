@@ -486,7 +486,7 @@ def attn_fwd_paged_fp8kv(q, k_cache, v_cache, k_scale, v_scale, cu_seqlens_q, ca
         else:
             need = lib.attn_varlen_workspace_size(B, total_q, Hq, Hkv)
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif not workspace.is_contiguous() or workspace.device != dev:
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     opt, _keep = _options(window_left, window_right, softcap, sinks, Hq, dev, _DTYPES[q.dtype])
     st = _on(dev, lib.attn_fwd_paged_fp8kv, q.data_ptr(), kc, vc, ks, vs, cq, sl, bt, page_size, po, pl, B, total_q,

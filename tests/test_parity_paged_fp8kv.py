@@ -546,3 +546,12 @@ def test_outputs_over_inputs_are_refused_and_next_to_them_are_not(g):
                 dict(workspace=kb), dict(out=o, lse=o.view(torch.float32).flatten()[:T * 8].view(T, 8))):
         with pytest.raises(ValueError):
             g.attn_fwd_paged_fp8kv(**d, **bad)
+
+
+def test_a_workspace_that_is_no_tensor_is_refused(g):
+    p = inputs([2, 3], [20, 30], 8, 2, 128, 16)
+    d = {n: p[n].cuda() for n in NAMES}
+    for bad in (1 << 20, b"0" * 4096, [0] * 4096, torch.empty(1 << 20, dtype=torch.uint8),
+                torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
+        with pytest.raises(ValueError):
+            g.attn_fwd_paged_fp8kv(**d, workspace=bad)
