@@ -535,8 +535,11 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
     pt = _data("block_table", block_table, i32, (B, max_pages), dev)
     pf = _data("free_pages", free_pages, i32, (n_free,), dev)
     fs = _data("free_start", free_start, i32, (1,), dev) if free_start is not None else None
-    if T < 0:
-        raise ValueError("max_tokens must be >= 0, got %d" % T)
+    ps, pool = int(page_size), int(num_pages)
+    if not 0 <= T < 1 << 30:
+        raise ValueError("max_tokens must lie in [0, 2^30), got %d" % T)
+    if not (0 < ps < 1 << 30 and 0 <= pool < 1 << 31):           # a C int would take their low 32 bits
+        raise ValueError("page_size must lie in [1, 2^30), num_pages in [0, 2^31), got %d, %d" % (ps, pool))
     if out is None:
         buf = torch.empty(2 * B + 3 * T + 4, dtype=i32, device=dev)
         out, p = buf.split((B + 1, B, T, T, T, 3)), buf.data_ptr()
@@ -549,8 +552,8 @@ def attn_paged_slots(past_lens, new_lens, block_table, free_pages, page_size, nu
         at = (_data("out cu_seqlens_q", cu, i32, (B + 1,), dev), _data("out cache_seqlens", lens, i32, (B,), dev),
               _data("out slots", slots, i32, (T,), dev), _data("out positions", positions, i32, (T,), dev),
               _data("out requests", requests, i32, (T,), dev), _data("out counts", counts, i32, (3,), dev))
-    st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, max_pages, int(page_size), int(num_pages),
-             n_free, T, *at, _raw_stream(dev))
+    st = _on(dev, _lib.load().attn_paged_slots, pp, pn, pt, pf, fs, B, max_pages, ps, pool, n_free, T, *at,
+             _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_paged_slots")
     return tuple(out)

@@ -186,3 +186,14 @@ def test_refusals(g):
                                                                                   device="cuda"))):
         with pytest.raises(ValueError):
             g.attn_paged_slots(**args(**bad))
+
+
+def test_sizes_past_32_bits_are_refused(g):
+    """A size whose low 32 bits would pass for a good one."""
+    past, new, table, free, ps, num_pages = draw(9, 4, 1, 3, 10, 8)
+    for bad in (dict(page_size=(1 << 32) + ps), dict(num_pages=(1 << 32) + num_pages), dict(max_tokens=(1 << 32) + 12),
+                dict(max_tokens=1 << 30), dict(page_size=1 << 31), dict(page_size=ps - (1 << 32)),
+                dict(num_pages=num_pages - (1 << 32)), dict(max_tokens=12 - (1 << 32))):
+        with pytest.raises(ValueError):
+            g.attn_paged_slots(**{**dict(past_lens=i32(past), new_lens=i32(new), block_table=i32(table),
+                                         free_pages=i32(free), page_size=ps, num_pages=num_pages, max_tokens=12), **bad})
