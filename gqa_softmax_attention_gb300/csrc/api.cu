@@ -3,6 +3,7 @@
 // allocated and no device data is read back on the attention paths.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -436,15 +437,15 @@ size_t attn_paged_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int
 static size_t fp8_parts_bytes(int D) { return (size_t)sm_count() * 128 * (D + 1) * sizeof(float); }
 
 // Whether some split of these sizes into requests leaves so few row blocks that
-// their keys would be cut (at most half as many as SMs): a lower bound of the
-// blocks, those of total_q - B queries, which no B single queries can be.  Never
-// where a whole table row holds too few keys for two parts: the joining launch
-// would be for nothing (1.4 us of 20 on the GPU for 4 queries over 700 keys).
-static bool fp8_may_split(int B, int total_q, int Hq, int Hkv, long capacity) {
-    if ((capacity + 127) / 128 < 2 * gqa::kPartTiles) return false;
+// their keys would be cut (at most half as many as SMs, and tiles enough for the
+// plan kernel's rule): from a lower bound of the blocks, those of total_q - B queries,
+// which no B single queries can be, and the most key tiles that a block can visit.
+// Where none does, the joining launch would be for nothing (1.4 us of 20 on the GPU
+// for 4 queries over 700 keys).
+static bool fp8_may_split(int B, int total_q, int Hq, int Hkv, long tiles) {
     const int qpb = 128 / (Hq / Hkv);
-    const long least = ((long)(total_q > B ? total_q - B : 0) + qpb - 1) / qpb;
-    return least * Hkv * 2 <= sm_count();
+    const long least = ((long)(total_q > B ? total_q - B : 0) + qpb - 1) / qpb * Hkv;
+    return least * 2 <= sm_count() && gqa::cut_pays(tiles, least);
 }
 
 size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int D, int page_size, int max_pages) {
@@ -453,7 +454,7 @@ size_t attn_paged_fp8kv_workspace_size(int B, int total_q, int Hq, int Hkv, int 
         (long)max_pages * page_size >= kMaxSeq)
         return 0;
     const size_t w = attn_paged_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
-    if (w == 0 || !fp8_may_split(B, total_q, Hq, Hkv, (long)max_pages * page_size)) return w;
+    if (w == 0 || !fp8_may_split(B, total_q, Hq, Hkv, ((long)max_pages * page_size + 127) / 128)) return w;
     return (w + 255) / 256 * 256 + fp8_parts_bytes(D);
 }
 
@@ -683,7 +684,13 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
         // few row blocks over long caches: cut along the keys, given the room
         const size_t w = attn_paged_workspace_size(B, total_q, Hq, Hkv, D, page_size, max_pages);
         const size_t p_off = (w + 255) / 256 * 256;
-        if (fp8_may_split(B, total_q, Hq, Hkv, (long)max_pages * page_size) && workspace_bytes >= p_off + fp8_parts_bytes(D) &&
+        long tiles = ((long)max_pages * page_size + 127) / 128;
+        if (a.x.wl >= 0 && (a.causal || a.x.wr >= 0)) {
+            // the keys of a block's windows, and a tile more where they begin inside one
+            const long seen = (long)a.x.wl + a.qpb + (a.causal ? 0 : a.x.wr);
+            tiles = std::min(tiles, (seen + 126) / 128 + 1);
+        }
+        if (fp8_may_split(B, total_q, Hq, Hkv, tiles) && workspace_bytes >= p_off + fp8_parts_bytes(D) &&
             (reinterpret_cast<uintptr_t>(wsc) & 255u) == 0) {
             a.part_o = reinterpret_cast<float*>(wsc + p_off);
             a.part_lse = a.part_o + (size_t)a.num_sms * 128 * D;
@@ -691,7 +698,8 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
     }
     if (gqa::launch_varlen_plan(cu_seqlens_q, cache_seqlens, true, B, a.qpb, a.g, a.causal, total_q,
                                 (long)max_pages * page_size, ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e,
-                                s, route, false, side ? a.num_sms : 0, fp8, a.part_o ? a.num_sms : 0, Hkv) != cudaSuccess)
+                                s, route, false, side ? a.num_sms : 0, fp8, a.part_o ? a.num_sms : 0, Hkv, a.x.wl,
+                                a.x.wr) != cudaSuccess)
         return GQA_ERR_CUDA;
     const long items = (long)max_e * Hkv;
     auto launch_chunks = [&](cudaStream_t on) {

@@ -78,9 +78,16 @@ cudaError_t launch_prefill_d256(const CUtensorMap& tm_q, const CUtensorMap& tm_k
                                 const CUtensorMap& tm_o, const PrefillArgs& a, cudaStream_t stream);
 int prefill_d256_take_device_error();
 
-// Key tiles a part of a split block keeps at least: below that the partial
-// results and their joining cost more than the shorter loop saves.
+// Key tiles a part of a split block takes at least (its last part the rest): below that
+// the partial results and their joining cost more than the shorter loop saves.
 constexpr int kPartTiles = 4;
+// Whether cutting pays: `tiles` the most that a block visits, `blocks` those of all KV
+// heads.  Two parts at least, and the more rows there are to join, the longer they have to
+// be.  At 32/8 heads, D = 128, in parts (this rule left out) and in one: 8 blocks of 9 tiles
+// 24.1 and 24.0 us, of 12 23.8 and 26.4; 32 blocks of 9 27.3 and 24.0, of 12 27.0 and 27.4; 64 of 9 30.0 and
+// 24.3, of 16 32.1 and 31.3, of 24 37.5 and 39.7.  At 24/2, D = 256: 30 of 9 34.9 and 32.4, of 12
+// 34.7 and 38.4; 70 of 12 43.3 and 39.9, of 16 46.8 and 46.6, of 24 54.3 and 61.3.
+__host__ __device__ constexpr bool cut_pays(long tiles, long blocks) { return tiles >= 2 * kPartTiles + blocks / 8; }
 
 // Packed calls (varlen_packed.cu, varlen_paged.cu; onetile.cuh).  The plan
 // kernel lists the (request, row block) entries of a call into `tmp`, then
@@ -96,11 +103,13 @@ constexpr int kPartTiles = 4;
 // left-out decode steps, run at the same time, end together (grid when there
 // is no decode step); fp8: the caches are e4m3 bytes.  With split_grid (the
 // chunk kernel's CTAs) n_entries[3] receives in how many parts each block's
-// keys are cut so that few blocks over long caches still fill those CTAs.
+// keys are cut so that few blocks over long caches still fill those CTAs; wl and
+// wr, the window, bound the key tiles that a block visits.
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single = false, bool pairs = false,
-                               int grid = 0, bool fp8 = false, int split_grid = 0, int Hkv = 1);
+                               int grid = 0, bool fp8 = false, int split_grid = 0, int Hkv = 1, int wl = -1,
+                               int wr = -1);
 // tm_q / tm_o: {D, Hq, total_q} with a {64, g, qpb} box.  Packed: tm_k / tm_v
 // {D, Hkv, total_kv} with {64, 1, 128} and {64, 1, 128 or 64 (D = 256)} boxes.
 // Paged: the caches as {64, 8, D / 64, pages * page_size / 8, Hkv} with

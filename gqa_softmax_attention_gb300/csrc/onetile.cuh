@@ -540,7 +540,10 @@ onetile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         }
         it.first = it.t.kv_begin / BN;
         if constexpr (KV8) {
-            const int per = (it.t.n_tiles - it.first + parts - 1) / parts;
+            // equal parts, of kPartTiles tiles at least: a block with fewer tiles than
+            // the longest fills only its first parts
+            int per = (it.t.n_tiles - it.first + parts - 1) / parts;
+            if (parts > 1) per = max(per, kPartTiles);
             it.first = min(it.first + part * per, it.t.n_tiles);
             it.t.n_tiles = min(it.first + per, it.t.n_tiles);
         }

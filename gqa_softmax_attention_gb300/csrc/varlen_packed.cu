@@ -46,10 +46,10 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
                                                           int B, int qpb, int g, int causal, int total_q,
                                                           long kv_cap, int32_t* tmp, int32_t* entries,
                                                           int32_t* n_entries, int max_entries, int grid,
-                                                          double dec_per_key, int split_grid, int Hkv) {
+                                                          double dec_per_key, int split_grid, int Hkv, int wl, int wr) {
     __shared__ int warp_sum[32];
     __shared__ unsigned long long pre_cost, dec_keys;   // listed blocks' cost; decode steps' cached keys
-    __shared__ int base, most_tiles;
+    __shared__ int base, most_tiles;                    // most key tiles that a block visits
     __shared__ int bucket[NBUCKET];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     // pairs (flag bit 2): an entry covers two consecutive row blocks
@@ -107,7 +107,14 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         int total = 0;
         for (int k = 0; k < nrb; ++k) total += cost_of(b, k * span, qs, sq, ks, L);
         if (total > 0) atomicAdd(&pre_cost, (unsigned long long)total);
-        if (split_grid > 0 && nrb > 0) atomicMax(&most_tiles, (L + 127) / 128);
+        if (split_grid > 0) {
+            int most = 0;
+            for (int k = 0; k < nrb; ++k) {
+                const pf::TileInfo t = pf::tile_info_n(k * span, span, sq, L, causal, wl, wr);
+                most = max(most, t.n_tiles - t.kv_begin / pf::BN);
+            }
+            if (most > 0) atomicMax(&most_tiles, most);
+        }
         if ((paged & 2) && sq == 1 && b < B && L > 0) atomicAdd(&dec_keys, (unsigned long long)L);
         const int key = min(NBUCKET - 1, total / 16);
         for (int k = 0; k < nrb; ++k) {
@@ -202,10 +209,14 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         }
         n_entries[2] = ge;
         if (split_grid > 0) {
-            // as many parts as leave every one a CTA, but none under kPartTiles tiles
+            // as many parts as leave every one a CTA, but no more than give the block
+            // with the most visited tiles kPartTiles each (shorter blocks fill fewer
+            // parts: onetile_kernel); none where cutting does not pay
             const int ctas = grid > 0 ? ge : split_grid;
             const long blocks = (long)n * Hkv;
-            n_entries[3] = blocks > 0 ? (int)max(1L, min(ctas / blocks, (long)(most_tiles / kPartTiles))) : 1;
+            n_entries[3] = blocks > 0 && cut_pays(most_tiles, blocks)
+                               ? (int)max(1L, min(ctas / blocks, (long)(most_tiles / kPartTiles)))
+                               : 1;
         }
     }
 }
@@ -215,13 +226,13 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single, bool pairs, int grid,
-                               bool fp8, int split_grid, int Hkv) {
+                               bool fp8, int split_grid, int Hkv, int wl, int wr) {
     // flags: bit 0 paged (kv holds cache lengths), bit 1 skip single-query
     // requests, bit 2 pairs of row blocks
     const int flags = (paged ? 1 : 0) | (skip_single ? 2 : 0) | (pairs ? 4 : 0);
     varlen_plan_kernel<<<1, 1024, 0, stream>>>(cu_q, kv, flags, B, qpb, g, causal, total_q, kv_cap, tmp,
                                                entries, n_entries, max_entries, grid,
-                                               fp8 ? kDecPerKey8 : kDecPerKey, split_grid, Hkv);
+                                               fp8 ? kDecPerKey8 : kDecPerKey, split_grid, Hkv, wl, wr);
     return cudaGetLastError();
 }
 

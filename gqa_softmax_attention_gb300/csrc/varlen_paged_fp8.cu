@@ -13,9 +13,9 @@ namespace {
 // row NaN, as it is with its keys in one part.  A few hundred rows of D
 // FP32 values a part: bound by the launch.  Ends at once when the plan cut
 // nothing.  The whole call with its keys in parts, and in one: 4 queries over
-// 32004 keys 37 and 273 us, over 2000 keys 22 and 30; 256 queries over 32256 keys
-// 157 and 280, over 4096 keys 41 and 48 (32/8 heads, D = 128); 4 queries over 32004
-// keys at 24/2, D = 256: 53 and 653.
+// 32004 keys 37 and 270 us, over 2048 keys 23 and 29; 256 queries over 32256 keys
+// 155 and 277, over 4096 keys 41 and 48 (32/8 heads, D = 128); 4 queries over 32004
+// keys at 24/2, D = 256: 50 and 569 (cut_pays has the borders).
 constexpr int JOIN_WARPS = 8;
 
 template <int D, bool F16>

@@ -348,7 +348,10 @@ gqa_status attn_fwd_paged(const void* q, const void* k_cache, const void* v_cach
  *                     aligned, calls with few rows over long caches (drafted
  *                     tokens, a chunk of one request) also cut the keys of
  *                     each row block into parts for the idle SMs and join
- *                     them; results agree within the usual tolerance.
+ *                     them; results agree within the usual tolerance.  Whether
+ *                     the rows are few is judged from total_q, padding rows
+ *                     included: a batch padded far past its real rows keeps
+ *                     each block's keys in one part.
  *
  * o, lse and the workspace may overlap neither one another nor anything that is read
  * (GQA_ERR_INVALID_ARG): chunks, decode steps and parts run side by side.

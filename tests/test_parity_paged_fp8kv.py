@@ -555,3 +555,24 @@ def test_a_workspace_that_is_no_tensor_is_refused(g):
                 torch.empty(1 << 20, 2, dtype=torch.uint8, device="cuda")[:, 0]):
         with pytest.raises(ValueError):
             g.attn_fwd_paged_fp8kv(**d, workspace=bad)
+
+
+@pytest.mark.parametrize("lens,kw,parts", [
+    # 8 KV heads, one block each: the tiles visited by the longest block decide, four of them to a part
+    ([100000], dict(window_left=200), (1, 1)), ([9000, 300], dict(window_left=400), (1, 1)),
+    ([100000], dict(window_left=4095), (2, 9)), ([1100], dict(window_left=300), (1, 1)), ([1100], dict(), (2, 2)),
+    ([1100] * 9, dict(), (1, 1)),
+    ([8192, 300, 3], dict(), (2, 6)), ([20000], dict(causal=False, window_left=300, window_right=10), (1, 1)),
+], ids=str)
+def test_parts_follow_the_visited_tiles(g, lens, kw, parts):
+    """The plan leaves the number of parts in the fourth word of the workspace (where the
+    window alone already rules parts out, it is not asked)."""
+    p = inputs([4] + [2] * (len(lens) - 1), lens, 16, 8, 128, 64, seed=53)
+    T, B = p["q"].shape[0], len(lens)
+    size = g.attn_paged_fp8kv_workspace_size(B, T, 16, 8, 128, 64, p["block_table"].shape[1])
+    ws = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    ws[:16].view(torch.int32)[3] = 1
+    o, lse = run(g, p, workspace=ws, **kw)
+    check(p, o, lse, label=str(kw), **kw)
+    got = int(ws[:16].view(torch.int32)[3])
+    assert parts[0] <= got <= parts[1], got
