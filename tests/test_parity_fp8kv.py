@@ -181,3 +181,23 @@ def test_full_size_workload(g, name):
     sel = torch.tensor(reqs)
     compare(o[sel], lse[sel], ro[sel], rl[sel], name)
     assert not torch.isnan(o.float()).any() and bool(torch.isfinite(lse).all())
+
+
+@pytest.mark.parametrize("geometry", [(32, 8, 1, 128, 64), (8, 2, 3, 128, 16), (24, 2, 4, 256, 64)], ids=str)
+def test_queries_that_are_no_numbers_show(g, geometry):
+    """NaN and infinite queries give NaN rows (O and LSE), every other row the bits that it had:
+    rows of up to 8 and 16 per KV head, and the tensor-core form (48)."""
+    Hq, Hkv, Sq, D, ps = geometry
+    p = W.paged_fp8_inputs(3, Sq, Hq, Hkv, D, ps, lengths=[2500, 300, Sq], seed=7)
+    names = ("q", "k_cache", "v_cache", "k_scale", "v_scale", "real_seqlen_kv", "block_table")
+    dev = {n: p[n].cuda() for n in names}
+    o, lse = g.attn_decode_paged_fp8kv(*[dev[n] for n in names], causal=True)
+    q = dev["q"].clone()
+    hit = torch.zeros(3, Sq, Hq, dtype=torch.bool, device="cuda")
+    for b, i, h, d, v in ((0, Sq - 1, 1, 5, float("nan")), (1, 0, Hq - 1, D - 1, float("inf")), (0, 0, Hq // 2, 9, 1e6)):
+        q[b, i, h, d] = v
+        hit[b, i, h] = True
+    bo, bl = g.attn_decode_paged_fp8kv(q, *[dev[n] for n in names[1:]], causal=True)
+    torch.cuda.synchronize()
+    assert bool(bo[hit].isnan().all()) and bool(bl[hit].isnan().all())
+    assert torch.equal(bo[~hit], o[~hit]) and torch.equal(bl[~hit], lse[~hit])
