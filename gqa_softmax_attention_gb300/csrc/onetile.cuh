@@ -49,13 +49,16 @@
 // HBM, but the tensor core takes A and B of one type and P needs more than e4m3's
 // four bits, so every key is widened once per row block; that and the softmax,
 // not the MMAs, set the pace.  Measured: a 2048-query chunk over 32768 keys, 64/8
-// heads, D = 128: 1.87-1.90 ms, 1.13 PFLOP/s (the 16-bit call: 2.10 ms); about 2100
+// heads, D = 128: 1.86-1.88 ms, 1.14 PFLOP/s (the 16-bit call: 2.10 ms); about 2100
 // cycles a tile, 1400 of them softmax and 1445 the issue of its MMAs (QK 681, PV
 // 764), which overlap as far as two S buffers allow.  Between two items
 // the MMA warp loses about 9000 cycles (the last P, the new Q, O's hand-over).
-// Five ragged chunks at 24/2, D = 256: 0.45 ms with softcap, 0.43 without (16-bit:
-// 0.56 without); 4200 cycles a tile, of which the MMAs wait 1250 for keys (a ring
-// of one tile: a slot is refilled only after the S before has read it).
+// Five ragged chunks at 24/2, D = 256: 0.33-0.41 ms with softcap over three draws, 0.31-0.38
+// without (a draw that takes 0.43: the 16-bit call 0.56); 4200-4400 cycles a tile, in which the
+// data pipe of shared memory and L1 carries 1536 wavefronts of MMA operands, 1366 of
+// stores and 1435 of loads (ncu): 4337, if they share it, so the port is full.  The MMAs
+// wait 1250 cycles a tile for keys (a ring of one tile: a slot is refilled only after
+// the S before has read it).
 // The MMA shapes stay M128 x N128 (QK) and M128 x N(D) (PV); at D = 256 K is
 // split into two 128-column halves and V into two 64-key halves so that each
 // half fills one ring slot.  Shared-memory operand layouts:

@@ -27,9 +27,13 @@ constexpr int NBUCKET = 2048;
 // 0.606 and 0.683 ms at 0.009, 0.0126 and 0.016).
 constexpr double kDecPerKey = 0.011;
 // Over e4m3 caches a cached key is half the bytes and the split kernel is bound by
-// its instructions: the mixed batch (60 steps, 4 chunks) took 0.53, 0.51, 0.50,
-// 0.52 and 0.58 ms at 0.002, 0.004, 0.006, 0.008 and 0.011, one chunk beside the
-// steps 0.28, 0.28, 0.29, 0.36 and 0.39.
+// its instructions.  60 steps and 4 chunks (1 chunk), mean of three draws of lengths:
+//   0.002  0.0035  0.005  0.007  0.009  0.012
+//    574     573    576    574    608    660   us at 32/8 heads, D = 128
+//   (292)   (285)  (288)  (304)  (345)  (386)
+//    747     746    752    749    749    762   at 24/2, D = 256, pages of 64
+//   (332)   (333)  (333)  (332)  (330)  (359)
+// so one constant does for both.
 constexpr double kDecPerKey8 = 0.005;
 
 __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb, int g, int causal) {

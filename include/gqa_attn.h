@@ -489,7 +489,8 @@ gqa_status attn_qk_norm_rope(const gqa_head_rows* q, const gqa_head_rows* k, con
  *   k_scale, v_scale  [B, Hkv] float, or NULL for ones; e4m3 only: the stored
  *                code is x / scale rounded to nearest even, +-448 beyond the
  *                range (x from FP32, not through 16 bits); finite and positive
- *                scales are a caller obligation
+ *                scales are a caller obligation.  At D = 64 e4m3 caches are
+ *                filled too, but no attention call here reads them
  *   requests     [T] int32: the token's row of the scales (not read without
  *                scales); a token whose row lies outside [0, B) is padding
  */
