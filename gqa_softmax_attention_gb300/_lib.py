@@ -67,6 +67,18 @@ def load() -> ctypes.CDLL:
     lib.attn_qk_norm_rope.restype = i
     lib.attn_qk_norm_rope_paged.argtypes = [vp] * 5 + [i, f] + [vp] * 5 + [i] + [vp] * 3 + [i] * 8 + [vp]
     lib.attn_qk_norm_rope_paged.restype = i
+    lib.attn_latent_norm_rope_paged.argtypes = [vp] * 3 + [i, f] + [vp] * 5 + [i] * 5 + [vp]
+    lib.attn_latent_norm_rope_paged.restype = i
+    lib.attn_latent_gather.argtypes = [vp] * 3 + [i, vp] + [i] * 4 + [vp]
+    lib.attn_latent_gather.restype = i
+    lib.attn_fwd_latent_varlen.argtypes = [vp] * 8 + [i] * 5 + [f, i, vp, sz, vp]
+    lib.attn_fwd_latent_varlen.restype = i
+    lib.attn_fwd_latent_paged.argtypes = [vp] * 5 + [i, vp, vp] + [i] * 6 + [f, i, vp, sz, vp]
+    lib.attn_fwd_latent_paged.restype = i
+    lib.attn_latent_varlen_workspace_size.argtypes = [i] * 3
+    lib.attn_latent_varlen_workspace_size.restype = sz
+    lib.attn_latent_paged_workspace_size.argtypes = [i] * 3
+    lib.attn_latent_paged_workspace_size.restype = sz
     lib.attn_varlen_workspace_size.argtypes = [i] * 4
     lib.attn_varlen_workspace_size.restype = sz
     lib.attn_paged_workspace_size.argtypes = [i] * 7

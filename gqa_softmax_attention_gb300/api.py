@@ -712,6 +712,215 @@ def attn_qk_norm_rope_paged(q, k, v, cos_sin, positions, slots, k_cache, v_cache
     return oq
 
 
+LATENT_DIM, LATENT_ROPE = 512, 64               # a latent cache row: latent, shared rotated dims
+LATENT_ROW = LATENT_DIM + LATENT_ROPE
+LATENT_NOPE, LATENT_V = 128, 128                # expanded, per head: key dims beside the shared ones, value dims
+
+
+def _rows(name, t, T, H, width, dtype, device):
+    """gqa_head_rows of t [T, H, width] (t [T, width] counts as one head), read in
+    place where the kernels take its strides, else from a copy (returned to keep it
+    alive)."""
+    shape = (T, width) if H is None else (T, H, width)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
+        raise ValueError("%s must be a %s CUDA tensor" % (name, dtype))
+    if t.shape != shape or t.device != device:
+        raise ValueError("%s must have shape %s on %s, got %s on %s" % (name, shape, device, tuple(t.shape), t.device))
+    if H is None:
+        t = t.unsqueeze(1)
+    if (T > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
+        t = t.contiguous()                           # broadcast rows
+    return _head_rows(t, T)
+
+
+def attn_latent_norm_rope_paged(q_pe, kv, cos_sin, positions, slots, kv_cache, kv_weight=None, eps=1e-6,
+                                interleaved=False, out=None, kv_out=None):
+    """New rows into a paged latent cache: the latents normed, the shared key dims
+    and the queries' own rotated dims turned by position, in one pass.
+
+    q_pe [T, H, 64] and kv [T, 576] (a latent of 512, then the shared key dims):
+    bfloat16 or float16 CUDA tensors, slices of a projection read in place (strides
+    of multiples of 8).  cos_sin [max_pos, 64] float32 (rope_table), positions and
+    slots [T] int32 (attn_paged_slots); a pair is dims (j, j + 32), or (2j, 2j + 1)
+    with interleaved.  kv_cache [num_pages, page_size, 576], contiguous, is
+    written in place.  kv_weight [512] (kv's dtype or float32), or None for no norm.
+    A token with a slot outside the pool is padding: its rows of every result stay as
+    they were.  FP32 throughout, rounded once.
+    out: the turned q_pe go into this [T, H, 64] tensor, a slice too (the last 64
+    dims of absorbed queries), or q_pe itself.  kv_out [T, 576], contiguous: the
+    cache rows, packed, for the projection of a prompt; it may be kv.
+    Returns out.
+    """
+    _check_16_cuda("q_pe", q_pe, 3)
+    dev, dt, f32 = q_pe.device, q_pe.dtype, torch.float32
+    T, H, R = q_pe.shape
+    if R != LATENT_ROPE:
+        raise ValueError("q_pe must be [T, H, %d], got %s" % (LATENT_ROPE, tuple(q_pe.shape)))
+    num_pages, page_size = _size("kv_cache", kv_cache, 3, 0), kv_cache.shape[1]
+    pc = _data("kv_cache", kv_cache, dt, (num_pages, page_size, LATENT_ROW), dev)
+    max_pos = _size("cos_sin", cos_sin, 2, 0)
+    pt = _data("cos_sin", cos_sin, f32, (max_pos, LATENT_ROPE), dev)
+    pp = _data("positions", positions, torch.int32, (T,), dev)
+    ps = _data("slots", slots, torch.int32, (T,), dev)
+    wf = kv_weight is not None and kv_weight.dtype is f32
+    pw = _data("kv_weight", kv_weight, f32 if wf else dt, (LATENT_DIM,), dev) if kv_weight is not None else None
+    if out is None:
+        out = torch.empty((T, H, R), dtype=dt, device=dev)
+    ro, ko = _rows("out", out, T, H, R, dt, dev)
+    if ko.data_ptr() != out.data_ptr():
+        raise ValueError("out must have strides of multiples of 8 and a 16-byte aligned start, got %s" % (out.stride(),))
+    po = _data("kv_out", kv_out, dt, (T, LATENT_ROW), dev) if kv_out is not None else None
+    rq, _kq = _rows("q_pe", q_pe, T, H, R, dt, dev)
+    rk, _kk = _rows("kv", kv, T, None, LATENT_ROW, dt, dev)
+    rope = _lib.Rope(pt, pp, max_pos, LATENT_ROPE, 1 if interleaved else 0, 1, None)
+    st = _on(dev, _lib.load().attn_latent_norm_rope_paged, ctypes.byref(rq), ctypes.byref(rk), pw, 1 if wf else 0, eps,
+             ctypes.byref(rope), ctypes.byref(ro), po, ps, pc, T, H, num_pages, page_size, _DTYPES[dt],
+             _raw_stream(dev))
+    if st != 0:
+        _raise(st, "attn_latent_norm_rope_paged")
+    return out
+
+
+def attn_latent_gather(kv_cache, cu_seqlens_kv, block_table, total_kv, out=None):
+    """Cached rows of requests, packed, for the projection that expands them.
+
+    kv_cache [num_pages, page_size, 576] bfloat16 or float16, cu_seqlens_kv [B + 1]
+    and block_table [B, max_pages] int32 CUDA tensors; total_kv: rows of the result,
+    at least cu_seqlens_kv[B] (which stays on the GPU).  Row cu_seqlens_kv[b] + t is
+    token t of request b; rows of no request are left as they are, tokens without a
+    page read as zeros.  Returns out [total_kv, 576].
+    """
+    _check_16_cuda("kv_cache", kv_cache, 3)
+    dev, i32 = kv_cache.device, torch.int32
+    num_pages, page_size, row = kv_cache.shape
+    pc = _data("kv_cache", kv_cache, kv_cache.dtype, (num_pages, page_size, LATENT_ROW), dev)
+    B = _size("block_table", block_table, 2, 0)
+    max_pages, total = block_table.shape[1], int(total_kv)
+    if not 0 <= total < 1 << 30:
+        raise ValueError("total_kv must lie in [0, 2^30), got %d" % total)
+    cu = _data("cu_seqlens_kv", cu_seqlens_kv, i32, (B + 1,), dev)
+    bt = _data("block_table", block_table, i32, (B, max_pages), dev)
+    if out is None:
+        out = torch.empty((total, LATENT_ROW), dtype=kv_cache.dtype, device=dev)
+        po = out.data_ptr()
+    else:
+        po = _data("out", out, kv_cache.dtype, (total, LATENT_ROW), dev)
+    st = _on(dev, _lib.load().attn_latent_gather, pc, cu, bt, page_size, po, B, total, num_pages, max_pages,
+             _raw_stream(dev))
+    if st != 0:
+        _raise(st, "attn_latent_gather")
+    return out
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != device:
+        raise ValueError("workspace must be a contiguous tensor on %s" % device)
+    return workspace
+
+
+def attn_fwd_latent_varlen(q, k, v, k_pe, cu_seqlens_q, cu_seqlens_kv, causal=True, scale=None, out=None, lse=None,
+                           workspace=None):
+    """Latent attention in its expanded form: packed prompts and chunks over keys
+    and values projected from the latents, and the key dims that all heads share.
+
+    q [total_q, H, 192] (128 dims for k, then 64 for k_pe); k and v [total_kv, H,
+    128], k_pe [total_kv, 64]: all bfloat16 or all float16; k, v and k_pe may be
+    slices (halves of one projection, the end of latent rows: strides of multiples of
+    8, other layouts are copied first).  cu_seqlens_q / cu_seqlens_kv and the mask as
+    attn_fwd_varlen; scale None: 1/sqrt(192).
+    workspace: optional, attn_latent_varlen_workspace_size bytes.
+    Returns (o [total_q, H, 128], lse [total_q, H] float32).
+    """
+    _check_16_cuda("q", q, 3)
+    dev, dt, i32, f32 = q.device, q.dtype, torch.int32, torch.float32
+    total_q, H, dq = q.shape
+    if dq != LATENT_NOPE + LATENT_ROPE:
+        raise ValueError("q must be [total_q, H, %d], got %s" % (LATENT_NOPE + LATENT_ROPE, tuple(q.shape)))
+    total_kv = _size("k", k, 3, 0)
+    rk, _kk = _rows("k", k, total_kv, H, LATENT_NOPE, dt, dev)
+    rv, _kv = _rows("v", v, total_kv, H, LATENT_V, dt, dev)
+    rp, _kp = _rows("k_pe", k_pe, total_kv, None, LATENT_ROPE, dt, dev)
+    B = _size("cu_seqlens_q", cu_seqlens_q, 1, 0) - 1
+    if B < 1:
+        raise ValueError("cu_seqlens_q must hold B + 1 >= 2 offsets")
+    cq = _data("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev)
+    ck = _data("cu_seqlens_kv", cu_seqlens_kv, i32, (B + 1,), dev)
+    q = q.contiguous()
+    if out is None:
+        out = torch.empty((total_q, H, LATENT_V), dtype=dt, device=dev)
+    po = _data("out", out, dt, (total_q, H, LATENT_V), dev)
+    if lse is None:
+        lse = torch.empty((total_q, H), dtype=f32, device=dev)
+    pl = _data("lse", lse, f32, (total_q, H), dev)
+    lib = _lib.load()
+    workspace = _workspace(workspace, lib.attn_latent_varlen_workspace_size(B, total_q, H), dev)
+    st = _on(dev, lib.attn_fwd_latent_varlen, q.data_ptr(), ctypes.byref(rk), ctypes.byref(rv), ctypes.byref(rp), cq, ck,
+             po, pl, B, total_q, total_kv, H, 1 if causal else 0, resolve_scale(scale, dq), _DTYPES[dt],
+             workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
+    if st != 0:
+        _raise(st, "attn_fwd_latent_varlen")
+    return out, lse
+
+
+def attn_fwd_latent_paged(q, kv_cache, cu_seqlens_q, cache_seqlens, block_table, scale, causal=True, out=None, lse=None,
+                          workspace=None):
+    """Latent attention in its absorbed form: packed queries, already projected into
+    the latent space, over a paged latent cache.
+
+    q [total_q, H, 576] and kv_cache [num_pages, page_size, 576], both bfloat16 or
+    both float16, the cache contiguous; cu_seqlens_q [B + 1], cache_seqlens [B]
+    (query tokens included) and block_table [B, max_pages] int32 CUDA tensors, as
+    attn_fwd_paged; any page size (multiples of 8 move by TMA, others are gathered row
+    by row).  scale: the multiplier of the scores, 1 / sqrt of the expanded head's
+    key dims by custom.
+    workspace: optional, attn_latent_paged_workspace_size bytes.
+    Returns (o [total_q, H, 512], the weighted sums of the latents, lse [total_q, H]
+    float32).
+    """
+    _check_16_cuda("q", q, 3)
+    dev, dt, i32, f32 = q.device, q.dtype, torch.int32, torch.float32
+    total_q, H, row = q.shape
+    if row != LATENT_ROW:
+        raise ValueError("q must be [total_q, H, %d], got %s" % (LATENT_ROW, tuple(q.shape)))
+    num_pages, page_size = _size("kv_cache", kv_cache, 3, 0), kv_cache.shape[1]
+    pc = _data("kv_cache", kv_cache, dt, (num_pages, page_size, LATENT_ROW), dev)
+    B = _size("cache_seqlens", cache_seqlens, 1, 0)
+    max_pages = _size("block_table", block_table, 2, 1)
+    cq = _data("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev)
+    sl = _data("cache_seqlens", cache_seqlens, i32, (B,), dev)
+    bt = _data("block_table", block_table, i32, (B, max_pages), dev)
+    q = q.contiguous()
+    if out is None:
+        out = torch.empty((total_q, H, LATENT_DIM), dtype=dt, device=dev)
+    po = _data("out", out, dt, (total_q, H, LATENT_DIM), dev)
+    if lse is None:
+        lse = torch.empty((total_q, H), dtype=f32, device=dev)
+    pl = _data("lse", lse, f32, (total_q, H), dev)
+    lib = _lib.load()
+    if workspace is None:
+        workspace = _workspace(None, _on(dev, lib.attn_latent_paged_workspace_size, B, total_q, H), dev)
+    else:
+        _workspace(workspace, 0, dev)
+    st = _on(dev, lib.attn_fwd_latent_paged, q.data_ptr(), pc, cq, sl, bt, page_size, po, pl, B, total_q, H, num_pages,
+             max_pages, 1 if causal else 0, float(scale), _DTYPES[dt], workspace.data_ptr(),
+             workspace.numel() * workspace.element_size(), _raw_stream(dev))
+    if st != 0:
+        _raise(st, "attn_fwd_latent_paged")
+    return out, lse
+
+
+def attn_latent_varlen_workspace_size(B, total_q, H):
+    """Workspace bytes of attn_fwd_latent_varlen."""
+    return int(_lib.load().attn_latent_varlen_workspace_size(B, total_q, H))
+
+
+def attn_latent_paged_workspace_size(B, total_q, H):
+    """Workspace bytes of attn_fwd_latent_paged on the current device."""
+    return int(_lib.load().attn_latent_paged_workspace_size(B, total_q, H))
+
+
 def rope_table(max_pos, rot, base=10000.0, device="cuda"):
     """cos_sin [max_pos, rot] float32 of attn_qk_norm_rope with the angles
     p * base^(-2j / rot), formed in 64 bits."""

@@ -588,6 +588,15 @@ static bool overlap(const Span& x, const Span& y) {
     return x.p && y.p && x.bytes > 0 && y.bytes > 0 && a < b + y.bytes && b < a + x.bytes;
 }
 
+// n / page_size = (umulhi(n, mul) + n) >> shift for 0 <= n < 2^31: division by a
+// constant as a multiplication (Granlund and Montgomery, "Division by Invariant
+// Integers using Multiplication", 1994).
+static void page_divisor(int page_size, uint32_t* mul, uint32_t* shift) {
+    *shift = 0;
+    while ((1L << *shift) < page_size) ++*shift;
+    *mul = (uint32_t)(((1ull << 32) * ((1ull << *shift) - page_size)) / page_size + 1);
+}
+
 // Packed queries over a paged cache: 16-bit, or (fp8) e4m3fn bytes with scales.
 static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_cache, bool fp8, const float* k_scale,
                             const float* v_scale, const int32_t* cu_seqlens_q, const int32_t* cache_seqlens,
@@ -645,10 +654,7 @@ static gqa_status fwd_paged(const void* q, const void* k_cache, const void* v_ca
         a.q = q;
         a.k_scale = k_scale;
         a.v_scale = v_scale;
-        // division by a constant as a multiplication (Granlund and Montgomery,
-        // "Division by Invariant Integers using Multiplication", 1994)
-        while ((1L << a.ps_shift) < page_size) ++a.ps_shift;
-        a.ps_mul = (uint32_t)(((1ull << 32) * ((1ull << a.ps_shift) - page_size)) / page_size + 1);
+        page_divisor(page_size, &a.ps_mul, &a.ps_shift);
     } else if (page_size % 8 == 0) {
         // pages move as 8-row TMA blocks
         a.bt_k = gcd_int(page_size, 128);
@@ -938,6 +944,310 @@ gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* 
                : GQA_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------- latent attention
+// Strided rows [T, H, width] of 16-bit values that may be written while others are
+// read: apart as a whole, or, with one token stride, side by side within it (slices
+// of one projection).
+struct Rows {
+    const void* p;
+    long ts, hs;            // elements
+    int T, H, width;
+    long row() const { return ((H - 1L) * hs + width) * 2; }     // bytes of a token
+    Span span() const { return {p, p ? (T - 1L) * ts * 2 + row() : 0}; }
+};
+static bool rows_overlap(const Rows& x, const Rows& y) {
+    if (!overlap(x.span(), y.span())) return false;
+    const long stride = x.ts * 2;
+    if (x.ts != y.ts || stride <= 0) return true;
+    const long off = (long)(reinterpret_cast<intptr_t>(y.p) - reinterpret_cast<intptr_t>(x.p));
+    const long d = ((off % stride) + stride) % stride;
+    return !(d >= x.row() && d + y.row() <= stride);
+}
+static bool strides_ok(long ts, long hs) { return ts >= 0 && hs >= 0; }
+
+gqa_status attn_latent_norm_rope_paged(const gqa_head_rows* q_pe, const gqa_head_rows* kv, const void* kv_weight,
+                                       int weight_f32, float eps, const gqa_rope* rope, const gqa_head_rows* q_out,
+                                       void* kv_out, const int32_t* slots, void* kv_cache, int T, int H, int num_pages,
+                                       int page_size, int dtype, gqa_stream_t stream) {
+    if (T < 0 || T >= kMaxSeq || H <= 0 || !q_pe || !kv || !q_out || !rope) return GQA_ERR_INVALID_ARG;
+    if (num_pages < 0 || page_size <= 0) return GQA_ERR_INVALID_ARG;
+    if (dtype != GQA_BF16 && dtype != GQA_FP16) return GQA_ERR_INVALID_ARG;
+    if (!std::isfinite(eps) || eps < 0.f) return GQA_ERR_INVALID_ARG;
+    if (rope->max_pos <= 0 || rope->n_axes != 1) return GQA_ERR_INVALID_ARG;
+    if (rope->rot != gqa::kLatentRope) return GQA_ERR_UNSUPPORTED;
+    if ((long)num_pages * page_size >= (1L << 31) || (long)T * ((long)H + 1) >= (1L << 32)) return GQA_ERR_UNSUPPORTED;
+    if (T == 0) return GQA_OK;
+    if (!q_pe->data || !kv->data || !q_out->data || !slots || !rope->cos_sin || !rope->positions ||
+        (num_pages > 0 && !kv_cache))
+        return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q_pe->data) || !aligned16(kv->data) || !aligned16(q_out->data) || !aligned16(kv_weight) ||
+        !aligned16(kv_out) || !aligned16(kv_cache) || !aligned16(rope->cos_sin) || !aligned4(rope->positions) ||
+        !aligned4(slots))
+        return GQA_ERR_MISALIGNED;
+    for (const gqa_head_rows* r : {q_pe, kv, q_out}) {
+        if (!strides_ok(r->token_stride, r->head_stride)) return GQA_ERR_INVALID_ARG;
+        if (r->token_stride % 8 || r->head_stride % 8) return GQA_ERR_MISALIGNED;
+    }
+    const Rows qi{q_pe->data, (long)q_pe->token_stride, (long)q_pe->head_stride, T, H, gqa::kLatentRope};
+    const Rows qo{q_out->data, (long)q_out->token_stride, (long)q_out->head_stride, T, H, gqa::kLatentRope};
+    const Rows ki{kv->data, (long)kv->token_stride, 0, T, 1, gqa::kLatentRow};
+    const Rows ko{kv_out, gqa::kLatentRow, 0, T, 1, gqa::kLatentRow};
+    // written rows lie apart from one another
+    if ((T > 1 && qo.ts < qo.row() / 2 && !(H > 1 && qo.ts >= gqa::kLatentRope && qo.hs >= (T - 1) * qo.ts + gqa::kLatentRope)) ||
+        (H > 1 && qo.hs < gqa::kLatentRope))
+        return GQA_ERR_INVALID_ARG;
+    // every warp reads its rows before it writes them: the very rows may be written
+    const bool q_same = qo.p == qi.p && (T == 1 || qo.ts == qi.ts) && (H == 1 || qo.hs == qi.hs);
+    const bool k_same = ko.p == ki.p && (T == 1 || ko.ts == ki.ts);
+    if ((!q_same && rows_overlap(qo, qi)) || rows_overlap(qo, ki) ||
+        (kv_out && ((!k_same && rows_overlap(ko, ki)) || rows_overlap(ko, qi) || rows_overlap(ko, qo))))
+        return GQA_ERR_INVALID_ARG;
+    const Span cache{kv_cache, (long)num_pages * page_size * gqa::kLatentRow * 2};
+    const Span small[] = {{slots, T * 4L}, {rope->positions, T * 4L},
+                          {rope->cos_sin, (long)rope->max_pos * gqa::kLatentRope * 4},
+                          {kv_weight, gqa::kLatentDim * (weight_f32 ? 4L : 2L)}};
+    for (const Rows* r : {&qi, &qo, &ki, &ko})
+        if (overlap(cache, r->span())) return GQA_ERR_INVALID_ARG;
+    for (const Span& x : small)
+        if (overlap(x, cache) || overlap(x, qo.span()) || (kv_out && overlap(x, ko.span()))) return GQA_ERR_INVALID_ARG;
+    gqa::LatentAppendArgs a{};
+    a.q = qi.p; a.q_ts = qi.ts; a.q_hs = qi.hs;
+    a.q_out = const_cast<void*>(qo.p); a.qo_ts = qo.ts; a.qo_hs = qo.hs;
+    a.kv = ki.p; a.kv_ts = ki.ts;
+    a.kv_out = kv_out; a.kvo_ts = ko.ts;
+    a.cache = kv_cache;
+    a.weight = kv_weight;
+    a.weight_f32 = weight_f32 ? 1 : 0;
+    a.eps = eps;
+    a.cos_sin = rope->cos_sin;
+    a.positions = rope->positions;
+    a.slots = slots;
+    a.max_pos = rope->max_pos;
+    a.interleaved = rope->interleaved ? 1 : 0;
+    a.T = T; a.H = H;
+    a.num_slots = (long)num_pages * page_size;
+    return gqa::launch_latent_append(a, dtype == GQA_FP16, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
+gqa_status attn_latent_gather(const void* kv_cache, const int32_t* cu_seqlens_kv, const int32_t* block_table,
+                              int page_size, void* out, int B, int total_kv, int num_pages, int max_pages,
+                              gqa_stream_t stream) {
+    if (B <= 0 || total_kv < 0 || total_kv >= kMaxSeq || page_size <= 0 || num_pages < 0 || max_pages <= 0)
+        return GQA_ERR_INVALID_ARG;
+    if ((long)max_pages * page_size >= kMaxSeq) return GQA_ERR_INVALID_ARG;
+    if ((long)num_pages * page_size >= (1L << 31)) return GQA_ERR_UNSUPPORTED;
+    if (!cu_seqlens_kv || !block_table || (num_pages > 0 && !kv_cache) || (total_kv > 0 && !out)) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(kv_cache) || !aligned16(out) || !aligned4(cu_seqlens_kv) || !aligned4(block_table))
+        return GQA_ERR_MISALIGNED;
+    if (total_kv == 0) return GQA_OK;
+    const Span w{out, (long)total_kv * gqa::kLatentRow * 2};
+    for (const Span& r : {Span{kv_cache, (long)num_pages * page_size * gqa::kLatentRow * 2},
+                          Span{cu_seqlens_kv, (B + 1L) * 4}, Span{block_table, (long)B * max_pages * 4}})
+        if (overlap(w, r)) return GQA_ERR_INVALID_ARG;
+    gqa::LatentGatherArgs a{};
+    a.cache = kv_cache;
+    a.cu = cu_seqlens_kv;
+    a.table = block_table;
+    a.out = out;
+    a.B = B; a.total = total_kv; a.page_size = page_size; a.num_pages = num_pages; a.max_pages = max_pages;
+    return gqa::launch_latent_gather(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+// Rows [T, H, width] with a token and a head stride as a 3-D map {width, H, T}
+// with a {64, 1, box_t} box and 128-byte swizzle.
+static bool make_rows_map(CUtensorMap* map, const Rows& r, int box_t, bool f16) {
+    auto fn = encode_fn();
+    if (!fn || r.T <= 0) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)r.width, (cuuint64_t)r.H, (cuuint64_t)r.T};
+    // the stride of an axis of one element is not used, but is checked
+    const cuuint64_t strides[2] = {(cuuint64_t)(r.H > 1 ? r.hs : r.width) * 2, (cuuint64_t)(r.T > 1 ? r.ts : r.width) * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)box_t};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, elem_type(f16), 3, const_cast<void*>(r.p), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+size_t attn_latent_varlen_workspace_size(int B, int total_q, int H) {
+    return total_q < kMaxSeq ? varlen_ws_bytes(B, total_q, H, H) : 0;
+}
+
+gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const gqa_head_rows* v,
+                                  const gqa_head_rows* k_pe, const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_kv,
+                                  void* o, float* lse, int B, int total_q, int total_kv, int H, int causal, float scale,
+                                  int dtype, void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    if (total_kv < 0 || total_kv >= kMaxSeq || !k || !v || !k_pe) return GQA_ERR_INVALID_ARG;
+    if (dtype != GQA_BF16 && dtype != GQA_FP16) return GQA_ERR_INVALID_ARG;
+    gqa_options opt{-1, -1, 0.f, nullptr, dtype};
+    PrefillArgs a{};
+    const gqa_status st = varlen_common(q, o, lse, cu_seqlens_q, B, total_q, H, H, gqa::kLatentV, causal, scale, &opt,
+                                        workspace, workspace_bytes, &a, nullptr, nullptr);
+    if (st != GQA_OK) return st;
+    if (!cu_seqlens_kv || (total_kv > 0 && (!k->data || !v->data || !k_pe->data))) return GQA_ERR_INVALID_ARG;
+    if (!aligned4(cu_seqlens_kv)) return GQA_ERR_MISALIGNED;
+    for (const gqa_head_rows* r : {k, v, k_pe}) {
+        if (!strides_ok(r->token_stride, r->head_stride)) return GQA_ERR_INVALID_ARG;
+        if (!aligned16(r->data) || r->token_stride % 8 || r->head_stride % 8) return GQA_ERR_MISALIGNED;
+        // a tensor map takes no stride of zero (a broadcast axis)
+        if ((total_kv > 1 && r->token_stride == 0) || (H > 1 && r != k_pe && r->head_stride == 0)) return GQA_ERR_INVALID_ARG;
+    }
+    const int max_e = varlen_max_entries(B, total_q, 128);
+    if ((long)max_e * H >= (1L << 31) - 512) return GQA_ERR_UNSUPPORTED;     // the items are counted in an int
+    if (total_q == 0) return GQA_OK;
+    const Rows rk{k->data, (long)k->token_stride, (long)k->head_stride, total_kv, H, gqa::kLatentNope},
+        rv{v->data, (long)v->token_stride, (long)v->head_stride, total_kv, H, gqa::kLatentV},
+        rp{k_pe->data, (long)k_pe->token_stride, 0, total_kv, 1, gqa::kLatentRope};
+    const long rows = (long)total_q * H;
+    constexpr int dq = gqa::kLatentNope + gqa::kLatentRope;
+    const Span writes[] = {{o, rows * gqa::kLatentV * 2}, {lse, rows * 4},
+                           {workspace, (long)varlen_ws_bytes(B, total_q, H, H)}};
+    const Span reads[] = {{q, rows * dq * 2}, rk.span(), rv.span(), rp.span(), {cu_seqlens_q, (B + 1L) * 4},
+                          {cu_seqlens_kv, (B + 1L) * 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& r : reads)
+            if (overlap(writes[i], r)) return GQA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(writes[i], writes[j])) return GQA_ERR_INVALID_ARG;
+    }
+    const Rows rq{q, (long)H * dq, dq, total_q, H, dq};
+    CUtensorMap tq, tk, tv, tp;
+    // with no key at all the maps are never read; they then describe q
+    const bool some = total_kv > 0;
+    if (!make_rows_map(&tq, rq, 128, a.f16) || !make_rows_map(&tk, some ? rk : rq, 128, a.f16) ||
+        !make_rows_map(&tv, some ? rv : rq, 64, a.f16) || !make_rows_map(&tp, some ? rp : rq, 128, a.f16))
+        return GQA_ERR_CUDA;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    int32_t* ws = static_cast<int32_t*>(workspace);
+    if (gqa::launch_varlen_plan(cu_seqlens_q, cu_seqlens_kv, false, B, 128, 1, a.causal, total_q, total_kv,
+                                ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e, s, false, true) != cudaSuccess)
+        return GQA_ERR_CUDA;
+    return gqa::launch_latent_varlen(tq, tk, tv, tp, a, (long)max_e * H, s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+}
+
+// Rows and offsets into them are ints on the device, with room for a team's rows past the last.
+static bool latent_rows_ok(int total_q, int H) { return (long)total_q * H < (1L << 31) - 1024; }
+
+// CTAs that take neighbouring rows of a request and read the same keys side by
+// side (so that L2 serves the second): two once a request brings more than
+// one CTA's rows, on average.
+static int latent_team(int B, int total_q, int H) {
+    return (long)total_q * H > (long)B * gqa::kLatentRows ? 2 : 1;
+}
+struct LatentParts {
+    int team, teams;
+    size_t join, ml, o;     // bytes
+};
+static LatentParts latent_parts(int B, int total_q, int H) {
+    LatentParts p;
+    const int n = sm_count(), sms = n <= 0 ? 148 : (n < 256 ? n : 256);   // 256: the joining kernel's table
+    p.team = latent_team(B, total_q, H);
+    p.teams = sms / p.team > 0 ? sms / p.team : 1;
+    const size_t slots = 2 * (size_t)p.team * p.teams;
+    p.join = ((size_t)p.teams * 16 + 255) / 256 * 256;
+    p.ml = slots * gqa::kLatentRows * sizeof(float2);
+    p.o = slots * gqa::kLatentRows * gqa::kLatentDim * sizeof(float);
+    return p;
+}
+constexpr int kLatentMaxB = 16384;      // their tile counts are summed in shared memory
+
+size_t attn_latent_paged_workspace_size(int B, int total_q, int H) {
+    if (B <= 0 || B > kLatentMaxB || total_q < 0 || total_q >= kMaxSeq || H <= 0 || !latent_rows_ok(total_q, H)) return 0;
+    const LatentParts p = latent_parts(B, total_q, H);
+    return p.join + p.ml + p.o;
+}
+
+// The latent cache as {64, 8, 9, rows / 8} (8-row groups of 64-dim slices) with a
+// {64, 8, slices, box_tokens / 8} box.
+static bool make_latent_map(CUtensorMap* map, const void* cache, long rows, int slices, int box_tokens, bool f16) {
+    auto fn = encode_fn();
+    if (!fn || rows % 8 != 0 || rows <= 0) return false;
+    constexpr cuuint64_t row = gqa::kLatentRow * 2;
+    const cuuint64_t dims[4] = {64, 8, gqa::kLatentRow / 64, (cuuint64_t)(rows / 8)};
+    const cuuint64_t strides[3] = {row, 128, 8 * row};
+    const cuuint32_t box[4] = {64, 8, (cuuint32_t)slices, (cuuint32_t)(box_tokens / 8)};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, elem_type(f16), 4, const_cast<void*>(cache), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// [total_q * H, 576] as {64, rows, 9} with a {64, kLatentRows, 9} box: a CTA's Q rows at once.
+static bool make_latent_q_map(CUtensorMap* map, const void* q, long rows, bool f16) {
+    auto fn = encode_fn();
+    if (!fn || rows <= 0) return false;
+    const cuuint64_t dims[3] = {64, (cuuint64_t)rows, gqa::kLatentRow / 64};
+    const cuuint64_t strides[2] = {gqa::kLatentRow * 2, 128};
+    const cuuint32_t box[3] = {64, gqa::kLatentRows, gqa::kLatentRow / 64};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, elem_type(f16), 3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int32_t* cu_seqlens_q,
+                                 const int32_t* cache_seqlens, const int32_t* block_table, int page_size, void* o,
+                                 float* lse, int B, int total_q, int H, int num_pages, int max_pages, int causal,
+                                 float scale, int dtype, void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
+    if (B <= 0 || total_q < 0 || H <= 0 || page_size <= 0 || num_pages <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
+    if (total_q >= kMaxSeq || (long)max_pages * page_size >= kMaxSeq) return GQA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || (dtype != GQA_BF16 && dtype != GQA_FP16)) return GQA_ERR_INVALID_ARG;
+    if (B > kLatentMaxB || !latent_rows_ok(total_q, H) || (long)num_pages * page_size >= (1L << 31))
+        return GQA_ERR_UNSUPPORTED;
+    if (!q || !kv_cache || !cu_seqlens_q || !cache_seqlens || !block_table || !o) return GQA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o)) return GQA_ERR_MISALIGNED;
+    for (const void* p : {(const void*)cu_seqlens_q, (const void*)cache_seqlens, (const void*)block_table, (const void*)lse})
+        if (!aligned4(p)) return GQA_ERR_MISALIGNED;
+    const LatentParts parts = latent_parts(B, total_q, H);
+    const size_t need = parts.join + parts.ml + parts.o;
+    if (!workspace || workspace_bytes < need) return GQA_ERR_WORKSPACE;
+    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GQA_ERR_MISALIGNED;
+    if (total_q == 0) return GQA_OK;
+    const long rows = (long)total_q * H, slots = (long)num_pages * page_size;
+    const Span writes[] = {{o, rows * gqa::kLatentDim * 2}, {lse, rows * 4}, {workspace, (long)need}};
+    const Span reads[] = {{q, rows * gqa::kLatentRow * 2}, {kv_cache, slots * gqa::kLatentRow * 2},
+                          {cu_seqlens_q, (B + 1L) * 4}, {cache_seqlens, B * 4L}, {block_table, (long)B * max_pages * 4}};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& r : reads)
+            if (overlap(writes[i], r)) return GQA_ERR_INVALID_ARG;
+        for (int j = 0; j < i; ++j)
+            if (overlap(writes[i], writes[j])) return GQA_ERR_INVALID_ARG;
+    }
+    gqa::LatentArgs a{};
+    a.cu_q = cu_seqlens_q;
+    a.lens = cache_seqlens;
+    a.table = block_table;
+    a.cache = kv_cache;
+    a.o = o;
+    a.lse = lse;
+    char* ws = static_cast<char*>(workspace);
+    a.join = reinterpret_cast<int32_t*>(ws);
+    a.part_ml = reinterpret_cast<float2*>(ws + parts.join);
+    a.part_o = reinterpret_cast<float*>(ws + parts.join + parts.ml);
+    a.B = B; a.total_q = total_q; a.H = H;
+    a.page_size = page_size; a.num_pages = num_pages; a.max_pages = max_pages;
+    a.causal = causal ? 1 : 0;
+    a.f16 = dtype == GQA_FP16 ? 1 : 0;
+    a.team = parts.team; a.teams = parts.teams;
+    a.min_tiles = 2;
+    a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
+    page_divisor(page_size, &a.ps_mul, &a.ps_shift);
+    CUtensorMap tq, tkv, tpe;
+    if (!make_latent_q_map(&tq, q, rows, a.f16)) return GQA_ERR_CUDA;
+    tkv = tpe = tq;                     // gathered rows: the maps go unused
+    if (page_size % 8 == 0) {
+        // pages move as 8-row TMA blocks
+        a.box_tokens = gcd_int(page_size, 128);
+        if (!make_latent_map(&tkv, kv_cache, slots, 2, a.box_tokens, a.f16) ||
+            !make_latent_map(&tpe, kv_cache, slots, 1, a.box_tokens, a.f16))
+            return GQA_ERR_CUDA;
+    }
+    return gqa::launch_latent_paged(tq, tkv, tpe, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GQA_OK
+               : GQA_ERR_CUDA;
+}
+
 gqa_status attn_validate_paged(const int32_t* real_seqlen_kv, const int32_t* block_table, int B, int Sq,
                                int page_size, int num_pages, int max_pages, int causal, gqa_stream_t stream) {
     (void)causal;
@@ -984,8 +1294,10 @@ gqa_status gqa_device_error(void) {
     const int v3 = gqa::varlen_paged_fp8_take_device_error();
     const int d = gqa::decode_take_device_error();
     const int t = gqa::decode_tc_take_device_error();
-    if (e < 0 || e2 < 0 || v1 < 0 || v2 < 0 || v3 < 0 || d < 0 || t < 0) return GQA_ERR_CUDA;
-    return (e || e2 || v1 || v2 || v3 || d || t) ? GQA_ERR_TIMEOUT : GQA_OK;
+    const int l1 = gqa::latent_paged_take_device_error();
+    const int l2 = gqa::latent_varlen_take_device_error();
+    if (e < 0 || e2 < 0 || v1 < 0 || v2 < 0 || v3 < 0 || d < 0 || t < 0 || l1 < 0 || l2 < 0) return GQA_ERR_CUDA;
+    return (e || e2 || v1 || v2 || v3 || d || t || l1 || l2) ? GQA_ERR_TIMEOUT : GQA_OK;
 }
 
 const char* gqa_version(void) { return "gqa_attn 0.1 sm_103a"; }

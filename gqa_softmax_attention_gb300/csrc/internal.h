@@ -254,4 +254,72 @@ struct RopeArgs {
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int D, bool f16, bool paged, int num_sms, cudaStream_t stream);
 
+// Latent attention: a cache row is kLatentDim latent and kLatentRope shared
+// rotated values; expanded, a head has kLatentNope + kLatentRope key dims and
+// kLatentV value dims.
+constexpr int kLatentDim = 512, kLatentRope = 64, kLatentNope = 128, kLatentV = 128;
+constexpr int kLatentRow = kLatentDim + kLatentRope;
+
+// Norm, rotation and append of latent rows (latent_rows.cu; see
+// attn_latent_norm_rope_paged).  Strides in elements.
+struct LatentAppendArgs {
+    const void* q;                  // [T, H, kLatentRope]
+    void* q_out;
+    const void* kv;                 // [T, kLatentRow]
+    void* kv_out;                   // [T, kLatentRow] or nullptr
+    void* cache;                    // [num_slots, kLatentRow]
+    long q_ts, q_hs, qo_ts, qo_hs, kv_ts, kvo_ts;
+    const void* weight;             // [kLatentDim] or nullptr
+    int weight_f32;
+    float eps;
+    const float* cos_sin;           // [max_pos, kLatentRope]
+    const int32_t* positions;       // [T]
+    const int32_t* slots;           // [T]
+    int max_pos, interleaved, T, H;
+    long num_slots;
+};
+cudaError_t launch_latent_append(const LatentAppendArgs& a, bool f16, int num_sms, cudaStream_t stream);
+struct LatentGatherArgs {
+    const void* cache;              // [num_pages, page_size, kLatentRow]
+    const int32_t* cu;              // [B + 1]
+    const int32_t* table;           // [B, max_pages]
+    void* out;                      // [total, kLatentRow]
+    int B, total, page_size, num_pages, max_pages;
+};
+cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t stream);
+
+// Packed queries [total_q, H, kLatentRow] over a paged latent cache
+// (latent_paged.cu; see attn_fwd_latent_paged).
+constexpr int kLatentRows = 64;     // (query, head) rows of a CTA
+struct LatentArgs {
+    const int32_t* cu_q;            // [B + 1]
+    const int32_t* lens;            // [B]
+    const int32_t* table;           // [B, max_pages]
+    const void* cache;
+    void* o;                        // [total_q, H, kLatentDim]
+    float* lse;                     // [total_q, H] or nullptr
+    float* part_o;                  // [CTAs, 2, kLatentDim / 128, rows / 4, 128, 4]: O of a cut row group's pieces
+    float2* part_ml;                // [CTAs, 2, rows]: reference maximum (base 2) and sum
+    int32_t* join;                  // [teams, 4]: pieces, first row, rows, slot of the first piece
+    int B, total_q, H, page_size, num_pages, max_pages, causal, f16;
+    int team, teams;                // CTAs that read the same keys for further rows; teams of the grid
+    int min_tiles;                  // least tiles of a team
+    int box_tokens;                 // tokens of a TMA box; 0: rows gathered with cp.async
+    float scale_log2;
+    uint32_t ps_mul, ps_shift;      // n / page_size as in PrefillArgs
+};
+// tm_q: [total_q * H, 576] as {64, rows, 9} with a {64, kLatentRows, 9} box;
+// tm_kv / tm_pe: the cache as {64, 8, 9, rows / 8} with {64, 8, 2 / 1, box_tokens / 8} boxes.
+cudaError_t launch_latent_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
+                                const LatentArgs& a, cudaStream_t stream);
+int latent_paged_take_device_error();
+
+// Packed queries over expanded keys and values (latent_varlen.cu; see
+// attn_fwd_latent_varlen): PrefillArgs with D = kLatentV, g = 1, qpb = 128.
+// tm_q {192, H, total_q}, tm_k / tm_v {128, H, total_kv} with {64, 1, 128}
+// boxes (tm_v: 64 rows), tm_pe {64, total_kv} with a {64, 128} box.
+cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 const CUtensorMap& tm_pe, const PrefillArgs& a, long max_items, cudaStream_t stream);
+int latent_varlen_take_device_error();
+
 }  // namespace gqa

@@ -1,0 +1,523 @@
+// Latent attention in its expanded form, for prompts and chunks: packed queries
+// over the keys and values that a projection of the latents gives each head.
+//
+//   s_ij = scale * (q_i[0:128] . k_j + q_i[128:192] . k_pe_j),  j <= i + Skv - Sq
+//   o_i = sum_j softmax(s_i)_j v_j                              (FP32, base 2)
+//
+// per head; k and v are strided slices of the projection's output and the 64
+// rotated dims k_pe are one row for all heads, so no [total_kv, H, 192] key tensor
+// is ever written.  640 FLOP a (query, key, head): tensor bound.
+//
+// As prefill.cu, one CTA holds two 128-row query tiles of consecutive row blocks of
+// one request and head, S and O of both in TMEM (S0 | S1 | O0 | O1), and the tensor
+// core works on one while the other is softmaxed (TileOPs "Attention Operators",
+// GQAVarlenFwdOp, mask and statistics).  What differs is the memory: a query
+// tile is 48 KB, a key tile 48 KB and a value tile 32 KB, which no ring of whole
+// tiles holds twice.  Keys and values go through one ring of eight 16 KB slots
+// instead, in the order K0 V0 K1 V1 ...: a key tile is three slots of 64 dims, a
+// value tile two of 64 keys, each of which the MMAs use and release by itself.
+//   warp 8      producer: claims items (entry of the plan, head), loads
+//   warp 9      MMA issuer
+//   warps 0-7   softmax of the two tiles, one row per thread, and the output
+//   warps 10-11 zero the value rows past a request's end in its last tile
+// Items of one head follow one another, so that the row blocks of a request read
+// its keys from L2.
+#include <cmath>
+
+#include "internal.h"
+#include "prefill_tiles.cuh"
+#include "ptx.cuh"
+
+namespace gqa {
+namespace {
+
+__device__ int g_latent_varlen_error;
+
+using namespace pf;
+constexpr int NQ = 2;
+constexpr int DQ = kLatentNope + kLatentRope;   // 192
+constexpr int DV = kLatentV;                    // 128
+constexpr int NUM_THREADS = 384;
+constexpr int WARP_LOAD = 8;
+constexpr int WARP_MMA = 9;
+// registers as in prefill.cu: 192 * 256 + 120 * 128 = 168 * 384, the launch total
+constexpr int kRegsSoftmax = 192;
+constexpr int kRegsOther = 120;
+
+constexpr int SLOT = BN * 128;                  // bytes: 128 keys x 64 dims, or 64 keys x 128 dims
+constexpr int NS = 8;                           // ring slots
+constexpr int KU = DQ / 64, VU = 2;             // slots of a key and a value tile
+constexpr int UNITS = KU + VU;
+constexpr int Q_TILE = KU * SLOT;
+constexpr int OFF_Q = 0;
+constexpr int OFF_RING = OFF_Q + NQ * Q_TILE;
+constexpr int OFF_BAR = OFF_RING + NS * SLOT;
+// q_full[2], q_empty[2], full[NS], empty[NS], s_full[2], p_full[2], o_final[2],
+// drain, info_full[2], info_empty[2], v_landed, v_fixed
+constexpr int NBAR = 4 + 2 * NS + 6 + 1 + 4 + 2;
+constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int OFF_INFO = OFF_MISC + 16;         // two item records: claimed item, tiles of Q0 and of Q1
+constexpr int REC = 4;
+constexpr int SMEM_BYTES = OFF_INFO + 2 * REC * 4 + 1024;
+constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + DV, TMEM_COLS = 512;
+static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+template <bool F16>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_pe,
+                     const PrefillArgs a) {
+    constexpr uint32_t IDESC_QK = make_idesc_16<F16>(BM, BN, false, false);
+    constexpr uint32_t IDESC_PV = make_idesc_16<F16>(BM, DV, false, true);
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_u32(smem_raw);
+    uint8_t* smem = smem_raw + ((1024 - (raw_base & 1023)) & 1023);
+    const uint32_t sb = smem_u32(smem);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+
+    const int n_entries = *a.n_entries;
+    const long n_items = (long)n_entries * a.Hq;
+    struct Item {
+        int h, q0, qs, sq, ks, skv;     // head; first query of the item; first query / key row of the request and its counts
+        TileInfo t0, t1;
+    };
+    auto describe = [&](int w) {
+        Item it;
+        const int4* e = reinterpret_cast<const int4*>(a.entries + (size_t)(w % n_entries) * 8);
+        const int4 e0 = e[0], e1 = e[1];
+        it.h = w / n_entries;
+        it.q0 = e0.y;
+        it.qs = e0.z;
+        it.sq = e0.w;
+        it.ks = e1.x;
+        it.skv = e1.y;
+        it.t0 = tile_info_n(it.q0, BM, it.sq, it.skv, a.causal, -1, -1);
+        it.t1 = tile_info_n(it.q0 + BM, BM, it.sq, it.skv, a.causal, -1, -1);
+        return it;
+    };
+
+    const uint32_t bar0 = sb + OFF_BAR;
+    auto q_full = [&](int k) { return bar0 + 8u * k; };
+    auto q_empty = [&](int k) { return bar0 + 8u * (2 + k); };
+    auto full = [&](int i) { return bar0 + 8u * (4 + i); };
+    auto empty = [&](int i) { return bar0 + 8u * (4 + NS + i); };
+    auto s_full = [&](int k) { return bar0 + 8u * (4 + 2 * NS + k); };
+    auto p_full = [&](int k) { return bar0 + 8u * (6 + 2 * NS + k); };
+    auto o_final = [&](int k) { return bar0 + 8u * (8 + 2 * NS + k); };
+    const uint32_t drain = bar0 + 8u * (10 + 2 * NS);
+    auto info_full = [&](int i) { return bar0 + 8u * (11 + 2 * NS + i); };
+    auto info_empty = [&](int i) { return bar0 + 8u * (13 + 2 * NS + i); };
+    const uint32_t v_landed = bar0 + 8u * (15 + 2 * NS), v_fixed = bar0 + 8u * (16 + 2 * NS);
+    int* info = reinterpret_cast<int*>(smem + OFF_INFO);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+    // Unit u of the loads (KU key slots, then VU value slots, per tile) is use u / NS of slot u % NS.
+    auto slot_addr = [&](long u) { return sb + OFF_RING + (uint32_t)(u % NS) * SLOT; };
+
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < NQ; ++k) {
+            mbar_init(q_full(k), 1);
+            mbar_init(q_empty(k), 1);
+            mbar_init(s_full(k), 1);
+            mbar_init(p_full(k), BM);
+            mbar_init(o_final(k), 1);
+            mbar_init(info_full(k), 1);
+            mbar_init(info_empty(k), 1 + 8 + 2);   // the MMA thread, the softmax warps, warps 10-11
+        }
+        for (int i = 0; i < NS; ++i) { mbar_init(full(i), 1); mbar_init(empty(i), 1); }
+        mbar_init(drain, 1);
+        mbar_init(v_landed, 1);
+        mbar_init(v_fixed, 2);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == WARP_MMA) {
+        tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    // As in prefill.cu each role ends by itself; the MMA warp frees TMEM once the
+    // softmax warps have arrived on barrier 2.
+    if (warp >= 8) {
+        regs_dec<kRegsOther>();
+        if (warp == WARP_LOAD) {
+            // ------------------------------------------------------------ producer (lane 0)
+            long nu = 0;                           // units loaded
+            int nq[2] = {0, 0};
+            if (lane == 0) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_k);
+                tma_prefetch_desc(&tm_v);
+                tma_prefetch_desc(&tm_pe);
+                bool ok = true;
+                for (int r = 0; ok; ++r) {
+                    const int w = atomicAdd(a.work, 1);
+                    const bool none = w >= n_items;
+                    int c[2] = {0, 0};
+                    Item it;
+                    if (!none) {
+                        it = describe(w);
+                        c[0] = it.t0.n_tiles;
+                        c[1] = it.t1.n_tiles;
+                    }
+                    ok = mbar_wait(info_empty(r & 1), ((r >> 1) & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    int* rec = info + REC * (r & 1);
+                    rec[0] = none ? -1 : w;
+                    rec[1] = c[0];
+                    rec[2] = c[1];
+                    mbar_arrive(info_full(r & 1));
+                    if (none) break;
+                    auto load_q = [&](int k) {
+                        if (!mbar_wait(q_empty(k), (nq[k] & 1) ^ 1, abort_flag)) return false;
+                        mbar_arrive_expect_tx(q_full(k), Q_TILE);
+#pragma unroll
+                        for (int s = 0; s < KU; ++s)
+                            tma_load_3d(sb + OFF_Q + k * Q_TILE + s * SLOT, &tm_q, q_full(k), s * 64, it.h,
+                                        it.qs + it.q0 + k * BM);
+                        ++nq[k];
+                        return true;
+                    };
+                    if (c[0] > 0) ok = load_q(0);
+                    const int n = max(c[0], c[1]);
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int key = it.ks + j * BN;
+                        for (int x = 0; x < UNITS && ok; ++x, ++nu) {
+                            const uint32_t f = full((int)(nu % NS));
+                            ok = mbar_wait(empty((int)(nu % NS)), (uint32_t)((nu / NS) & 1) ^ 1u, abort_flag);
+                            if (!ok) break;
+                            const uint32_t dst = slot_addr(nu);
+                            mbar_arrive_expect_tx(f, SLOT);
+                            if (x < KU - 1) {
+                                tma_load_3d(dst, &tm_k, f, x * 64, it.h, key);
+                            } else if (x == KU - 1) {
+                                tma_load_3d(dst, &tm_pe, f, 0, 0, key);
+                            } else {
+                                const int k0 = key + (x - KU) * 64;
+                                tma_load_3d(dst, &tm_v, f, 0, it.h, k0);
+                                tma_load_3d(dst + SLOT / 2, &tm_v, f, 64, it.h, k0);
+                            }
+                            // Q1 behind the first key tile, so that S0 starts early
+                            if (j == 0 && x == KU - 1 && c[1] > 0) ok = load_q(1);
+                        }
+                    }
+                }
+                if (*abort_flag) {
+                    // let the copies in flight land: the last load of each slot
+                    for (long u = max(0L, nu - NS); u < nu; ++u) mbar_drain(full((int)(u % NS)), (uint32_t)((u / NS) & 1));
+                    for (int k = 0; k < 2; ++k)
+                        if (nq[k] > 0) mbar_drain(q_full(k), (nq[k] - 1) & 1);
+                }
+            }
+            __syncwarp();
+        } else if (warp == WARP_MMA) {
+            // ------------------------------------------------------------ MMA issuer (lane 0)
+            if (lane == 0) {
+                long u0 = 0;                       // first unit of the item
+                int nq[2] = {0, 0}, np[2] = {0, 0}, nfix = 0;
+                bool ok = true;
+                for (int r = 0; ok; ++r) {
+                    ok = mbar_wait(info_full(r & 1), (r >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    const int* rec = info + REC * (r & 1);
+                    const int w = rec[0], c0 = rec[1], c1 = rec[2];
+                    mbar_arrive(info_empty(r & 1));
+                    if (w < 0) break;
+                    const int n = max(c0, c1);
+                    auto unit_ready = [&](long u) {
+                        if (!mbar_wait(full((int)(u % NS)), (uint32_t)((u / NS) & 1), abort_flag)) return false;
+                        tc_fence_after();
+                        return true;
+                    };
+                    // S_k of tile i; `last`: no other query tile needs these keys
+                    auto issue_s = [&](int k, int i, bool last) {
+                        const uint32_t d = tmem + (k == 0 ? COL_S0 : COL_S1);
+                        const uint32_t qb = sb + OFF_Q + k * Q_TILE;
+#pragma unroll
+                        for (int x = 0; x < KU; ++x) {
+                            const long u = u0 + (long)i * UNITS + x;
+                            if (!unit_ready(u)) return false;
+                            const uint64_t qd = make_sdesc_sw128(qb + x * SLOT, 16, 1024);
+                            const uint64_t kd = make_sdesc_sw128(slot_addr(u), 16, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, IDESC_QK, (x > 0 || kk > 0) ? 1u : 0u);
+                            if (last) mma_commit(empty((int)(u % NS)));
+                        }
+                        mma_commit(s_full(k));
+                        return true;
+                    };
+                    auto issue_pv = [&](int k, int i, bool last) {
+                        if (!mbar_wait(p_full(k), np[k]++ & 1, abort_flag)) return false;
+                        tc_fence_after();
+                        const uint32_t d = tmem + (k == 0 ? COL_O0 : COL_O1), p = tmem + (k == 0 ? COL_S0 : COL_S1);
+#pragma unroll
+                        for (int x = 0; x < VU; ++x) {
+                            const long u = u0 + (long)i * UNITS + KU + x;
+                            // dims-major B: 64-dim halves 8 KB apart, 8-key groups 1 KB apart
+                            const uint64_t vd = make_sdesc_sw128(slot_addr(u), SLOT / 2, 1024);
+#pragma unroll
+                            for (int kk = 0; kk < 4; ++kk)
+                                mma_bf16_ts(d, p + (4 * x + kk) * 8, vd + (uint64_t)((kk * 2048) >> 4), IDESC_PV,
+                                            (i > 0 || x > 0 || kk > 0) ? 1u : 0u);
+                            if (last) mma_commit(empty((int)(u % NS)));
+                        }
+                        return true;
+                    };
+                    auto values_ready = [&](int i) {
+                        for (int x = 0; x < VU; ++x)
+                            if (!unit_ready(u0 + (long)i * UNITS + KU + x)) return false;
+                        if (i == n - 1) {
+                            // the item's last tile: rows past the request's end are zeroed first
+                            mbar_arrive(v_landed);
+                            if (!mbar_wait(v_fixed, nfix++ & 1, abort_flag)) return false;
+                            tc_fence_after();
+                        }
+                        return true;
+                    };
+                    if (c0 == 0) mma_commit(o_final(0));
+                    if (c1 == 0) mma_commit(o_final(1));
+                    if (c0 > 0) {
+                        ok = mbar_wait(q_full(0), nq[0]++ & 1, abort_flag) && issue_s(0, 0, c1 == 0);
+                        if (ok && c0 == 1) mma_commit(q_empty(0));
+                    }
+                    if (ok && c1 > 0) {
+                        ok = mbar_wait(q_full(1), nq[1]++ & 1, abort_flag) && issue_s(1, 0, true);
+                        if (ok && c1 == 1) mma_commit(q_empty(1));
+                    }
+                    for (int i = 0; i < n && ok; ++i) {
+                        ok = values_ready(i);
+                        if (ok && i < c0) {
+                            ok = issue_pv(0, i, i >= c1);
+                            if (ok && i + 1 == c0) mma_commit(o_final(0));
+                            if (ok && i + 1 < c0) {
+                                ok = issue_s(0, i + 1, i + 1 >= c1);
+                                if (ok && i + 2 == c0) mma_commit(q_empty(0));
+                            }
+                        }
+                        if (ok && i < c1) {
+                            ok = issue_pv(1, i, true);
+                            if (ok && i + 1 == c1) mma_commit(o_final(1));
+                            if (ok && i + 1 < c1) {
+                                ok = issue_s(1, i + 1, true);
+                                if (ok && i + 2 == c1) mma_commit(q_empty(1));
+                            }
+                        }
+                    }
+                    u0 += (long)n * UNITS;
+                }
+                mma_commit(drain);                // every MMA issued above has completed once this arrives
+                mbar_drain(drain, 0);
+            }
+            __syncwarp();
+            named_bar_sync(2, 8 * 32 + 32);       // softmax warps are done with TMEM
+            tc_fence_after();
+            tmem_dealloc(tmem, TMEM_COLS);
+        } else {
+            // ------------------------------------------------------------ warps 10-11
+            // Value rows past the request's end hold the next request's rows, where
+            // 0 * NaN would not vanish: zero them before the last tile's P V.
+            const int t = (warp - 10) * 32 + lane;
+            long u0 = 0;
+            int nl = 0;
+            for (int r = 0;; ++r) {
+                const bool got = __all_sync(0xffffffffu, mbar_wait(info_full(r & 1), (r >> 1) & 1, abort_flag));
+                const int* rec = info + REC * (r & 1);
+                const int w = got ? rec[0] : -1, n = got ? max(rec[1], rec[2]) : 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(info_empty(r & 1));
+                if (w < 0) break;
+                if (n == 0) continue;
+                const Item it = describe(w);
+                const long uv = u0 + (long)(n - 1) * UNITS + KU;
+                u0 += (long)n * UNITS;
+                if (!__all_sync(0xffffffffu, mbar_wait(v_landed, nl & 1, abort_flag))) break;
+                ++nl;
+                for (int x = 0; x < VU; ++x) {
+                    // the MMA thread has seen the slot full; so does the writer here
+                    if (!__all_sync(0xffffffffu, mbar_wait(full((int)((uv + x) % NS)), (uint32_t)(((uv + x) / NS) & 1),
+                                                           abort_flag)))
+                        break;
+                    const int r0 = it.skv - (n - 1) * BN - x * 64;   // first row of the half past the end
+                    uint8_t* base = smem + (slot_addr(uv + x) - sb);
+                    for (int y = max(r0, 0) * 16 + t; y < 64 * 16; y += 64) {
+                        const int row = y / 16, sl = (y / 8) % 2, q = y % 8;
+                        *reinterpret_cast<uint4*>(base + sl * (SLOT / 2) + row * 128 + q * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                fence_proxy_async_smem();           // generic writes, read by the tensor core
+                __syncwarp();
+                if (lane == 0) mbar_arrive(v_fixed);
+            }
+        }
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // ------------------------------------------------------------ softmax warps 0-7
+        const int k = warp / 4;
+        const int r = (warp % 4) * 32 + lane;                  // row of the tile == TMEM lane
+        const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
+        const uint32_t col_s = k == 0 ? COL_S0 : COL_S1, col_o = k == 0 ? COL_O0 : COL_O1;
+        const float sl = a.scale_log2;
+        int sf = 0;                  // S tiles taken so far (s_full parity)
+        int n_done = 0;              // items finished (o_final parity)
+        bool ok = true;
+        for (int rr = 0;; ++rr) {
+            ok = __all_sync(0xffffffffu, mbar_wait(info_full(rr & 1), (rr >> 1) & 1, abort_flag));
+            const int w = ok ? info[REC * (rr & 1)] : -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(info_empty(rr & 1));
+            __syncwarp();
+            if (!named_bar_and(3 + k, BM, ok) || w < 0) break;
+            const Item itm = describe(w);
+            const TileInfo ti = k == 0 ? itm.t0 : itm.t1;
+            const int lim = (int)key_hi((long)ti.q0 + r + itm.skv - itm.sq, itm.skv, a.causal, -1);   // keys this row sees
+            float m_ref = -INFINITY;     // reference max (log2 units, scaled)
+            float l_run = 0.f;
+            for (int j = 0; j < ti.n_tiles; ++j) {
+                const int kbase = j * BN;
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full(k), sf & 1, abort_flag));
+                ++sf;
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t sr[BN];
+                tmem_ld128(tmem + lane_addr + col_s, sr);
+                float* s = reinterpret_cast<float*>(sr);
+                // raw scores where the whole tile is visible and the scale positive
+                // (the scale goes into the exponent's FMA), logits with -inf for
+                // hidden keys otherwise
+                const bool fast = kbase + BN <= ti.lim_first && sl > 0.f;
+                auto to_logits = [&]() {
+                    if (fast) return;
+#pragma unroll
+                    for (int c = 0; c < BN; ++c) s[c] = kbase + c < lim ? s[c] * sl : -INFINITY;
+                };
+                to_logits();
+                const float fa = fast ? sl : 1.f;
+                float alpha = 1.f, rs = 0.f;
+                // as in prefill.cu: against the standing reference while the row
+                // sums stay below the limit, else with the tile's row maximum
+                bool done = false;
+                if (__all_sync(0xffffffffu, m_ref != -INFINITY)) {
+                    uint32_t pk[BN / 2];
+                    rs = exp_row<F16>(s, fa, m_ref, pk);
+                    if (!__any_sync(0xffffffffu, !(rs <= (F16 ? 65504.f : kSumLimit)))) {
+                        tmem_st64(tmem + lane_addr + col_s, pk);
+                        done = true;
+                    }
+                }
+                if (!done) {
+                    tmem_ld128(tmem + lane_addr + col_s, sr);
+                    to_logits();
+                    float mx8[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) mx8[e] = -INFINITY;
+#pragma unroll
+                    for (int c = 0; c < BN; c += 2) mx8[(c >> 1) & 7] = fmax3(mx8[(c >> 1) & 7], s[c], s[c + 1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) mx8[e] = fmaxf(mx8[e], mx8[e + 4]);
+                    const float mx_raw = fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3]));
+                    const float mx = fast ? mx_raw * sl : mx_raw;
+                    if (mx > m_ref + kRescaleThreshold) {
+                        alpha = fast_exp2(m_ref - mx);
+                        m_ref = mx;
+                    }
+                    const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+                    uint32_t pk[BN / 2];
+                    rs = exp_row<F16>(s, fa, m_use, pk);
+                    tmem_st64(tmem + lane_addr + col_s, pk);
+                }
+                l_run = l_run * alpha + rs;
+                // P V of the tile before is complete (this S landed after it)
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 32) {
+                        float o[32];
+                        tmem_ld32(tmem + lane_addr + col_o + c, o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= alpha;
+                        tmem_st32(tmem + lane_addr + col_o + c, reinterpret_cast<uint32_t*>(o));
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(p_full(k));
+            }
+            // ---- the tile's end (also after a wait gave up: all four warps pass the barrier below)
+            if (ok) {
+                ok = __all_sync(0xffffffffu, mbar_wait(o_final(k), n_done & 1, abort_flag));
+                if (ok) tc_fence_after();
+            }
+            ++n_done;
+            const bool row_ok = r < ti.rows_valid;
+            const size_t orow = (size_t)(itm.qs + ti.q0 + r) * a.Hq + itm.h;
+            const bool some = l_run != 0.f && ti.n_tiles > 0;    // 0: no key; NaN goes on
+            const float inv = some ? 1.f / l_run : 0.f;
+            if (row_ok && a.lse && ok) a.lse[orow] = some ? (m_ref + log2f(l_run)) * kLn2 : -INFINITY;
+            uint16_t* dst = static_cast<uint16_t*>(a.o) + orow * DV;
+            if (ti.rows_valid > 0 && ok) {
+#pragma unroll 1
+                for (int c = 0; c < DV; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    if (ti.n_tiles > 0) {
+                        tmem_ld32(tmem + lane_addr + col_o + c, o);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                    }
+                    if (row_ok) {
+                        uint32_t wd[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            wd[e] = pack2<F16>(some ? o[2 * e] * inv : 0.f, some ? o[2 * e + 1] * inv : 0.f);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            *reinterpret_cast<uint4*>(dst + c + 8 * e) =
+                                make_uint4(wd[4 * e], wd[4 * e + 1], wd[4 * e + 2], wd[4 * e + 3]);
+                    }
+                }
+            }
+            tc_fence_before();
+            if (!named_bar_and(3 + k, BM, ok)) break;     // the whole warpgroup stops together
+        }
+        __syncwarp();
+        named_bar_arrive(2, 8 * 32 + 32);
+        if (threadIdx.x == 0 && *abort_flag) atomicExch(&g_latent_varlen_error, (int)kErrPrefillWait);
+    }
+}
+
+template <bool F16>
+cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_pe,
+                     const PrefillArgs& a, long max_items, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(latent_varlen_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    const long sms = a.num_sms > 0 ? a.num_sms : 148;
+    const long grid = max_items < sms ? max_items : sms;    // persistent: one CTA per SM
+    if (grid <= 0) return cudaSuccess;
+    latent_varlen_kernel<F16><<<(unsigned)grid, NUM_THREADS, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, tm_pe, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
+                                 const CUtensorMap& tm_pe, const PrefillArgs& a, long max_items, cudaStream_t stream) {
+    return a.f16 ? launch_t<true>(tm_q, tm_k, tm_v, tm_pe, a, max_items, stream)
+                 : launch_t<false>(tm_q, tm_k, tm_v, tm_pe, a, max_items, stream);
+}
+
+int latent_varlen_take_device_error() {
+    int v = 0;
+    if (cudaMemcpyFromSymbol(&v, g_latent_varlen_error, sizeof(int)) != cudaSuccess) return -1;
+    if (v != 0) {
+        const int zero = 0;
+        cudaMemcpyToSymbol(g_latent_varlen_error, &zero, sizeof(int));
+    }
+    return v;
+}
+
+}  // namespace gqa

@@ -501,6 +501,98 @@ gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* 
                                    const int32_t* requests, int B, int T, int Hq, int Hkv, int D,
                                    int num_pages, int page_size, int dtype, gqa_stream_t stream);
 
+/*
+ * Latent attention (TileOPs "Attention Operators", the decode with q, q_pe, k,
+ * k_pe): every token has ONE row for all heads, a normed latent c of 512 values, from
+ * which a projection gives each head its 128 key and 128 value dims, and 64 rotated
+ * key dims k_pe that the heads share.  A latent cache is [num_pages, page_size, 576]
+ * 16-bit, contiguous.  Two forms of one attention:
+ *   expanded  attn_fwd_latent_varlen over the projected keys and values (prompts,
+ *             chunks; attn_latent_gather brings the cached rows to the projection)
+ *   absorbed  attn_fwd_latent_paged over the cache itself: with the key projection W_k
+ *             [128, 512] of a head, q = [W_k^T q_nope, q_pe], and the value
+ *             projection applied to its output (decode steps, drafted tokens)
+ * dtype (gqa_dtype) names the type of every 16-bit tensor of a call.  A key value
+ * that is infinite or no number makes every query of a request that shares a row
+ * block with one that sees it undefined, as in the other attention calls.
+ */
+
+/*
+ * New rows into a latent cache, with the queries' rotated dims turned beside it:
+ *     row = [c / sqrt(mean(c^2) + eps) * kv_weight, R(p) k_pe],  q_out = R(p) q_pe
+ * in FP32, rounded once; R(p) is gqa_rope's rotation of all 64 dims.
+ *
+ *   q_pe     [T, H, 64] (a slice of the query projection)
+ *   kv       [T, 576] (head_stride is not used): c, then k_pe
+ *   kv_weight  [512], of dtype or float with weight_f32; NULL: c is stored as it is
+ *   rope     rot = 64, n_axes = 1
+ *   q_out    [T, H, 64], strided as well (the last 64 dims of absorbed queries);
+ *            may be q_pe
+ *   kv_out   [T, 576] contiguous, or NULL: the same rows, packed; may be kv where that
+ *            is contiguous
+ *   slots    [T] int32: cache row page * page_size + offset (attn_paged_slots).  A
+ *            token whose slot lies outside the cache is padding: its rows of every
+ *            output stay as they were.  Two tokens with one slot are a caller
+ *            error (either may win, value by value)
+ * Data 16-byte aligned, strides multiples of 8 elements.  Outputs may overlap no
+ * input but the very rows named, and not one another.  T = 0 does nothing.
+ */
+gqa_status attn_latent_norm_rope_paged(const gqa_head_rows* q_pe, const gqa_head_rows* kv, const void* kv_weight,
+                                       int weight_f32, float eps, const gqa_rope* rope, const gqa_head_rows* q_out,
+                                       void* kv_out, const int32_t* slots, void* kv_cache, int T, int H,
+                                       int num_pages, int page_size, int dtype, gqa_stream_t stream);
+
+/*
+ * Cached rows of B requests, packed: row cu_seqlens_kv[b] + t of out [total_kv, 576]
+ * is the row of token t of request b.  Rows of no request (before
+ * cu_seqlens_kv[0] or from cu_seqlens_kv[B] on) stay as they were; a token past
+ * max_pages * page_size or with a page id outside [0, num_pages) reads as zeros.
+ */
+gqa_status attn_latent_gather(const void* kv_cache, const int32_t* cu_seqlens_kv, const int32_t* block_table,
+                              int page_size, void* out, int B, int total_kv, int num_pages, int max_pages,
+                              gqa_stream_t stream);
+
+/*
+ * The expanded form, packed variable-length (attn_fwd_varlen's offsets and mask):
+ *   q     [total_q, H, 192]: 128 dims for k, then 64 for k_pe
+ *   k, v  [total_kv, H, 128], strided (halves of one projection)
+ *   k_pe  [total_kv, 64], strided (the end of latent rows; head_stride is not used)
+ *   o     [total_q, H, 128], lse [total_q, H] or NULL
+ *   workspace  attn_latent_varlen_workspace_size bytes, 16-byte aligned
+ * Data 16-byte aligned, strides multiples of 8 elements.  o, lse and the workspace
+ * may overlap nothing that is read, nor one another.
+ */
+gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const gqa_head_rows* v,
+                                  const gqa_head_rows* k_pe, const int32_t* cu_seqlens_q,
+                                  const int32_t* cu_seqlens_kv, void* o, float* lse, int B, int total_q,
+                                  int total_kv, int H, int causal, float scale, int dtype, void* workspace,
+                                  size_t workspace_bytes, gqa_stream_t stream);
+
+/*
+ * The absorbed form: packed queries over a paged latent cache.
+ *   q     [total_q, H, 576]
+ *   cu_seqlens_q, cache_seqlens, block_table, mask, lengths and page ids as for
+ *         attn_fwd_paged (any page_size >= 1; sizes that are no multiple of 8 are
+ *         gathered row by row)
+ *   o     [total_q, H, 512]: the softmax-weighted sum of the latents
+ *   lse   [total_q, H] or NULL
+ *   scale that of the full head, 1 / sqrt(192) by custom, as given
+ *   workspace  attn_latent_paged_workspace_size bytes, 256-byte aligned; calls
+ *         sharing one must not overlap on the GPU
+ * B up to 16384.  o, lse and the workspace may overlap nothing that is read, nor one
+ * another.
+ */
+gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int32_t* cu_seqlens_q,
+                                 const int32_t* cache_seqlens, const int32_t* block_table, int page_size, void* o,
+                                 float* lse, int B, int total_q, int H, int num_pages, int max_pages, int causal,
+                                 float scale, int dtype, void* workspace, size_t workspace_bytes,
+                                 gqa_stream_t stream);
+
+/* Workspace bytes of the two attention calls (0 for sizes that they refuse); the
+ * absorbed form's depends on the current device. */
+size_t attn_latent_varlen_workspace_size(int B, int total_q, int H);
+size_t attn_latent_paged_workspace_size(int B, int total_q, int H);
+
 /* Workspace bytes of attn_fwd_varlen / attn_fwd_paged (0 for invalid sizes). */
 size_t attn_varlen_workspace_size(int B, int total_q, int Hq, int Hkv);
 
