@@ -1130,20 +1130,19 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
 // Rows and offsets into them are ints on the device, with room for a team's rows past the last.
 static bool latent_rows_ok(int total_q, int H) { return (long)total_q * H < (1L << 31) - 1024; }
 
-// CTAs that take neighbouring rows of a request and read the same keys side by
-// side (so that L2 serves the second): two once a request brings more than
-// one CTA's rows, on average.
-static int latent_team(int B, int total_q, int H) {
-    return (long)total_q * H > (long)B * gqa::kLatentRows ? 2 : 1;
-}
+// Rows of a CTA, and CTAs that take neighbouring rows of a request and read the
+// same keys side by side (so that L2 serves the second): as many rows as a request
+// brings, on average, up to two CTAs of 64.
 struct LatentParts {
-    int team, teams;
+    int nr, team, teams;
     size_t join, ml, o;     // bytes
 };
 static LatentParts latent_parts(int B, int total_q, int H) {
     LatentParts p;
     const int n = sm_count(), sms = n <= 0 ? 148 : (n < 256 ? n : 256);   // 256: the joining kernel's table
-    p.team = latent_team(B, total_q, H);
+    const long mean = (long)total_q * H / B;       // rows of a request, on average
+    p.nr = mean <= 16 ? 16 : (mean <= 32 ? 32 : gqa::kLatentRows);
+    p.team = mean > gqa::kLatentRows ? 2 : 1;
     p.teams = sms / p.team > 0 ? sms / p.team : 1;
     const size_t slots = 2 * (size_t)p.team * p.teams;
     p.join = ((size_t)p.teams * 16 + 255) / 256 * 256;
@@ -1173,13 +1172,13 @@ static bool make_latent_map(CUtensorMap* map, const void* cache, long rows, int 
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// [total_q * H, 576] as {64, rows, 9} with a {64, kLatentRows, 9} box: a CTA's Q rows at once.
-static bool make_latent_q_map(CUtensorMap* map, const void* q, long rows, bool f16) {
+// [total_q * H, 576] as {64, rows, 9} with a {64, nr, 9} box: a CTA's Q rows at once.
+static bool make_latent_q_map(CUtensorMap* map, const void* q, long rows, int nr, bool f16) {
     auto fn = encode_fn();
     if (!fn || rows <= 0) return false;
     const cuuint64_t dims[3] = {64, (cuuint64_t)rows, gqa::kLatentRow / 64};
     const cuuint64_t strides[2] = {gqa::kLatentRow * 2, 128};
-    const cuuint32_t box[3] = {64, gqa::kLatentRows, gqa::kLatentRow / 64};
+    const cuuint32_t box[3] = {64, (cuuint32_t)nr, gqa::kLatentRow / 64};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, elem_type(f16), 3, const_cast<void*>(q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1230,15 +1229,16 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     a.causal = causal ? 1 : 0;
     a.f16 = dtype == GQA_FP16 ? 1 : 0;
     a.team = parts.team; a.teams = parts.teams;
-    a.min_tiles = 2;
+    a.min_tiles = 4;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     page_divisor(page_size, &a.ps_mul, &a.ps_shift);
     CUtensorMap tq, tkv, tpe;
-    if (!make_latent_q_map(&tq, q, rows, a.f16)) return GQA_ERR_CUDA;
+    a.nr = page_size % 8 == 0 ? parts.nr : gqa::kLatentRows;
+    if (!make_latent_q_map(&tq, q, rows, a.nr, a.f16)) return GQA_ERR_CUDA;
     tkv = tpe = tq;                     // gathered rows: the maps go unused
     if (page_size % 8 == 0) {
         // pages move as 8-row TMA blocks
-        a.box_tokens = gcd_int(page_size, 128);
+        a.box_tokens = gcd_int(page_size, 64);
         if (!make_latent_map(&tkv, kv_cache, slots, 2, a.box_tokens, a.f16) ||
             !make_latent_map(&tpe, kv_cache, slots, 1, a.box_tokens, a.f16))
             return GQA_ERR_CUDA;

@@ -290,7 +290,7 @@ cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t stream)
 
 // Packed queries [total_q, H, kLatentRow] over a paged latent cache
 // (latent_paged.cu; see attn_fwd_latent_paged).
-constexpr int kLatentRows = 64;     // (query, head) rows of a CTA
+constexpr int kLatentRows = 64;     // most (query, head) rows of a CTA
 struct LatentArgs {
     const int32_t* cu_q;            // [B + 1]
     const int32_t* lens;            // [B]
@@ -302,13 +302,14 @@ struct LatentArgs {
     float2* part_ml;                // [CTAs, 2, rows]: reference maximum (base 2) and sum
     int32_t* join;                  // [teams, 4]: pieces, first row, rows, slot of the first piece
     int B, total_q, H, page_size, num_pages, max_pages, causal, f16;
+    int nr;                         // rows of a CTA: 16, 32 or 64 (64 with gathered rows)
     int team, teams;                // CTAs that read the same keys for further rows; teams of the grid
     int min_tiles;                  // least tiles of a team
     int box_tokens;                 // tokens of a TMA box; 0: rows gathered with cp.async
     float scale_log2;
     uint32_t ps_mul, ps_shift;      // n / page_size as in PrefillArgs
 };
-// tm_q: [total_q * H, 576] as {64, rows, 9} with a {64, kLatentRows, 9} box;
+// tm_q: [total_q * H, 576] as {64, rows, 9} with a {64, nr, 9} box;
 // tm_kv / tm_pe: the cache as {64, 8, 9, rows / 8} with {64, 8, 2 / 1, box_tokens / 8} boxes.
 cudaError_t launch_latent_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
                                 const LatentArgs& a, cudaStream_t stream);

@@ -10,29 +10,38 @@
 //
 // Packed queries: request b owns queries [cu_q[b], cu_q[b + 1]), its rows are
 // r = i * H + h (query i, head h), and query i sees the keys
-// j <= i + L_b - Sq_b.  NR rows go to one CTA; a team of one or two CTAs takes
-// the rows [seg * team * NR, ...) of a request and reads the same keys at the
-// same time, so that the second reading comes from L2.
+// j <= i + L_b - Sq_b.  NR rows (16, 32 or 64) go to one CTA; a team of one or two
+// CTAs takes the rows [seg * team * NR, ...) of a request and reads the same keys
+// at the same time, so that the second reading comes from L2.
 //
 // The products are formed transposed, keys and dims on the MMAs' M side and the
 // rows on N, because O of 512 dims by 64 rows then takes half of TMEM (as O
 // itself it would take all of it, whatever the row count):
-//   S^T [128 keys, NR]  = K [128, 576] Q^T            36 MMAs of K = 16
-//   O^T [512 dims, NR] += V^T [512, 128 keys] P^T     4 x 8 MMAs
+//   S^T [64 keys, NR]   = K [64, 576] Q^T            36 MMAs of K = 16
+//   O^T [512 dims, NR] += V^T [512, 64 keys] P^T     4 x 4 MMAs
 // A cache tile lies in shared memory once and is both operands: K-major for
-// S^T, dims-major (transposed) for O^T.  Shared memory holds Q (72 KB at 64
-// rows) and one tile (144 KB); so that loads keep running, the tile is four
-// slots of 128 dims and one of the 64 shared dims, each released by itself as
-// O^T has taken it, and P^T is written over the shared dims, which only S^T needs.
+// S^T, dims-major (transposed) for O^T.  MMAs with so few columns are bound by
+// reading their A operand from shared memory (128 bytes a cycle: 33 and 49 cycles
+// a step at 64 rows, 24 and 40 at 16; measured), 2000 or 1500 cycles a tile where
+// HBM brings one every 3200.
 //
-// A softmax thread owns a key: its S^T row holds the key's score with every
-// row of queries.  The reference maximum of a row (column) is kept in shared
-// memory and moves only when a score exceeds it by more than 2^8, which the
-// threads vote on; the row sums are kept as per-thread parts and joined across
-// the keys once per piece.
+// Shared memory holds Q (72 KB at 64 rows) and two to nearly three tiles of 72 KB: a
+// ring of slots of 128 dims, four a tile, and one of the 64 shared dims.  P^T is
+// written over the shared dims, which only S^T needs.  With one tile of 128 keys at a
+// time the loads of a tile could not run while the tile before was worked on, and
+// all CTAs loaded and all computed at the same time (64 requests of 1K to 16K
+// keys, 16 heads: 188 us).
+//   warps 0-3  softmax; the output
+//   warp 4     MMA issuer: takes whichever is ready, P V of a tile or S^T of a slot of
+//              the next, through one elected lane
+//   warp 5     producer (TMA), or warps 5-6 (rows gathered)
+// A softmax thread owns a key and half of the rows.  The reference maximum of a row
+// (column) is kept in shared memory and moves only when a score exceeds it by more
+// than 2^8, which the threads vote on; the row sums are kept as per-thread parts
+// and joined across the keys once per piece.
 //
 // Work is balanced: the row groups of all requests, laid end to end, form one
-// sequence of 128-key tiles, and each team takes an equal range.  A row group
+// sequence of 64-key tiles, and each team takes an equal range.  A row group
 // that lies in one range is written out directly; of one that is cut, each
 // piece leaves O, maximum and sum in FP32, at most two pieces a team, and
 // latent_join_kernel adds them up.
@@ -49,7 +58,7 @@ namespace {
 
 __device__ int g_latent_paged_error;
 
-constexpr int BN = 128;                    // keys per tile
+constexpr int BN = 64;                     // keys per tile
 constexpr int DC = kLatentDim;             // 512: latent
 constexpr int DR = kLatentRope;            // 64: shared rotated dims
 constexpr int DK = DC + DR;
@@ -63,24 +72,27 @@ constexpr int kSmBar = 1;                  // named barrier of the softmax warps
 
 template <int NR, bool GATHER>
 struct LCfg {
-    static constexpr int NP = 4;                                   // slots of 128 dims
-    static constexpr int PAIR = BN * 256;                          // bytes of a slot: [16 groups][2 slices][8 keys][128]
-    static constexpr int ROPE = BN * 128;                          // shared dims, later P^T: [128 keys][128]
+    static constexpr int NP = NR == 64 ? 8 : (NR == 32 ? 10 : 11); // slots of 128 dims, NJ a tile
+    static constexpr int NT = NR == 64 ? 2 : 3;                    // slots of the shared dims, one a tile
+    static constexpr int PAIR = BN * 256;                          // [8 groups][2 slices][8 keys][128 bytes]
+    static constexpr int ROPE = BN * 128;                          // shared dims, later P^T: [64 keys][128 bytes]
     static constexpr int Q_SLICE = NR * 128;                       // 64 dims of Q
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (DK / 64) * Q_SLICE;
-    static constexpr int OFF_KV = OFF_P + ROPE;
-    static constexpr int OFF_COL = OFF_KV + NP * PAIR;             // per row: -reference, rescale, limit, sums [4]
+    static constexpr int OFF_KV = OFF_P + NT * ROPE;
+    static constexpr int OFF_COL = OFF_KV + NP * PAIR;             // per row: -reference, factor, limit, reference, [4] per warp
     static constexpr int OFF_BAR = OFF_COL + 8 * NR * 4;
-    // kv_full[NP], kv_empty[NP], pe_full, q_full, q_empty, s_full, p_full, o_done, drain
-    static constexpr int NBAR = 2 * NP + 7;
+    // kv_full[NP], kv_empty[NP], pe_full[NT], pe_empty[NT], q_full, q_empty,
+    // s_full[2], p_full[2], o_done, drain
+    static constexpr int NBAR = 2 * NP + 2 * NT + 8;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
-    static constexpr int LOAD_WARPS = GATHER ? 2 : 1;      // 8 warps at most: 255 registers a thread
+    static constexpr int LOAD_WARPS = GATHER ? 2 : 1;
     static constexpr int THREADS = 32 * (5 + LOAD_WARPS);
-    static constexpr uint32_t COL_S = NJ * NR;                     // TMEM: O^T blocks | S^T
+    static constexpr uint32_t COL_S = NJ * NR;                     // TMEM: O^T blocks | S^T of even, of odd tiles
     static constexpr uint32_t TMEM_COLS = 512;
-    static_assert(COL_S + NR <= TMEM_COLS, "TMEM budget");
+    static_assert(COL_S + 2 * NR <= TMEM_COLS, "TMEM budget");
+    static_assert(NP >= 2 * NJ, "two tiles");
     static_assert(OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
@@ -148,31 +160,70 @@ struct Piece {
     }
 };
 
-// Order-preserving integers of floats, for the warp-wide maximum (NaN ends up
-// above +inf or below -inf; the row's weights are NaN either way).
-__device__ __forceinline__ int ordered(float x) {
-    const int i = __float_as_int(x);
-    return i ^ ((i >> 31) & 0x7fffffff);
-}
-__device__ __forceinline__ float unordered(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
-
-// Sums of v[0 .. N) over the warp's lanes: lane l returns columns
-// l * N / 32 .. of them in v[0 .. max(1, N / 32)).  Each step exchanges the
-// half of the columns that the other half of the lanes keeps.
-template <int N>
-__device__ __forceinline__ void warp_column_sums(float* v, int lane) {
-    static_assert(N == 64 || N == 32, "columns");
+// Sums or maxima of v[0 .. N) over the 16 lanes of a half-warp: lane l returns the
+// columns l * N / 16 .. of them in v[0 .. max(1, N / 16)) (N = 8: lanes 2c and 2c + 1
+// column c).  Each step exchanges the half of the columns that the other lanes keep.
+template <int N, bool MAX>
+__device__ __forceinline__ void half_warp_columns(float* v, int lane) {
+    static_assert(N == 32 || N == 16 || N == 8, "columns");
+    auto both = [](float x, float y) { return MAX ? fmaxf(x, y) : x + y; };
 #pragma unroll
-    for (int o = 16, w = N / 2; o >= 1; o >>= 1, w >>= 1) {
+    for (int o = 8, w = N / 2; o >= 1; o >>= 1, w >>= 1) {
         const bool up = (lane & o) != 0;
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
             if (i < w) {
                 const float mine = up ? v[i + w] : v[i], other = up ? v[i] : v[i + w];
-                v[i] = mine + __shfl_xor_sync(0xffffffffu, other, o);
+                v[i] = both(mine, __shfl_xor_sync(0xffffffffu, other, o));
             }
         }
+        if (w == 0) v[0] = both(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
     }
+}
+
+// 16 lanes x 2 N columns of TMEM -> N registers per thread, lanes l and l + 16 of
+// the warp reading columns 0 .. N - 1 and N .. 2 N - 1 of TMEM lane l (the rows
+// of an M = 64 accumulator lie in the first 16 lanes of each warp's quarter).
+// The caller waits.
+template <int N>
+__device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float* v) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    if constexpr (N == 32) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x32bx2.x32.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+            "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32], 32;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+              "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+              "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+              "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+            : "r"(taddr)
+            : "memory");
+    } else if constexpr (N == 16) {
+        asm volatile(
+            "tcgen05.ld.sync.aligned.16x32bx2.x16.b32 "
+            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16], 16;"
+            : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+              "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+              "=r"(r[14]), "=r"(r[15])
+            : "r"(taddr)
+            : "memory");
+    } else {
+        asm volatile("tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8], 8;"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                     : "r"(taddr)
+                     : "memory");
+    }
+}
+
+// One lane of the (converged) warp.  Of a lane chosen like this, unlike lane 0 by
+// comparison, the compiler knows that it runs alone: MMAs then go out at 24 to 49
+// cycles a step, the shared-memory limit, instead of one every 50 to 54.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // n / page_size for 0 <= n < 2^31
@@ -193,15 +244,25 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint32_t raw = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // through a shuffle, so that the compiler knows the roles' branches to be uniform
+    // and keeps descriptors and addresses in uniform registers
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
     const int team = blockIdx.x / a.team, rank = blockIdx.x % a.team;
     const int group = a.team * NR;               // rows of a team
 
     const uint32_t bar0 = sb + C::OFF_BAR;
     auto kv_full = [&](int i) { return bar0 + 8u * i; };
     auto kv_empty = [&](int i) { return bar0 + 8u * (C::NP + i); };
-    const uint32_t pe_full = bar0 + 8u * (2 * C::NP), q_full = pe_full + 8, q_empty = pe_full + 16,
-                   s_full = pe_full + 24, p_full = pe_full + 32, o_done = pe_full + 40, drain = pe_full + 48;
+    auto pe_full = [&](int i) { return bar0 + 8u * (2 * C::NP + i); };
+    auto pe_empty = [&](int i) { return bar0 + 8u * (2 * C::NP + C::NT + i); };
+    const uint32_t bar1 = bar0 + 8u * (2 * C::NP + 2 * C::NT);
+    const uint32_t q_full = bar1, q_empty = bar1 + 8, o_done = bar1 + 16, drain = bar1 + 24;
+    auto s_full = [&](int i) { return bar1 + 32 + 8u * i; };
+    auto p_full = [&](int i) { return bar1 + 48 + 8u * i; };
+    // Tile it's slots: dims 128 j .. are use u / NP of slot u % NP with u = NJ it + j, its
+    // shared dims and P^T use it / NT of slot it % NT; a fill's parity is that use's.
+    auto pair_addr = [&](int i) { return sb + C::OFF_KV + (uint32_t)i * C::PAIR; };
+    auto rope_addr = [&](int i) { return sb + C::OFF_P + (uint32_t)i * C::ROPE; };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     LRange* range = reinterpret_cast<LRange*>(smem + C::OFF_MISC + 16);
@@ -209,11 +270,10 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (threadIdx.x == 0) {
         const int fills = GATHER ? 32 * C::LOAD_WARPS : 1;
         for (int i = 0; i < C::NP; ++i) { mbar_init(kv_full(i), fills); mbar_init(kv_empty(i), 1); }
-        mbar_init(pe_full, fills);
+        for (int i = 0; i < C::NT; ++i) { mbar_init(pe_full(i), fills); mbar_init(pe_empty(i), 1); }
+        for (int i = 0; i < 2; ++i) { mbar_init(s_full(i), 1); mbar_init(p_full(i), 128); }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        mbar_init(s_full, 1);
-        mbar_init(p_full, 128);
         mbar_init(o_done, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -282,6 +342,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ------------------------------------------------------------ producer
         const int pw = warp - WARP_LOAD;
         int it = 0, nq = 0;                      // tiles and Q blocks loaded
+        int ps = 0, ts = 0;                      // next slots, and the parities of their uses
+        uint32_t pp = 0, tp = 0;
         bool ok = true;
         if (lane == 0) {
             tma_prefetch_desc(&tm_q);
@@ -292,14 +354,21 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         Piece p;
         p.first(a, rg, group, NR, rank);
-        bool more = true;
         // Page id that holds token t of the piece's request, as the table has it
         // (-1 past the request's end).
         auto page_at = [&](const Piece& c, int t) {
             const int lp = page_of(a, (uint32_t)t);
             return t < c.L ? ldg_int(a.table + (size_t)c.b * a.max_pages + lp) : -1;
         };
-        for (; more && ok; more = p.next(a, group, NR, rank)) {
+        auto step = [&](int j) {                 // past slot j of a tile (j = NJ: the shared dims)
+            if (j < NJ) {
+                if (++ps == C::NP) { ps = 0; pp ^= 1; }
+            } else if (++ts == C::NT) {
+                ts = 0;
+                tp ^= 1;
+            }
+        };
+        for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
             if (p.n == 0) continue;
             if (pw == 0) {
                 // the piece's Q rows, once the last S^T of the piece before is done
@@ -329,27 +398,24 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                         ? (int)(((long)page * a.page_size + in_page) >> 3)
                                         : outside;
                     if (k + 1 < p.n) page = lane < nbox ? page_at(p, token(k + 1)) : -1;
-                    for (int j = 0; j <= NJ && ok; ++j) {
-                        const uint32_t full = j < NJ ? kv_full(j) : pe_full;
-                        if (lane == 0) {
-                            // P^T of the tile before lies where the shared dims go
-                            ok = j < NJ ? mbar_wait(kv_empty(j), (it & 1) ^ 1, abort_flag)
-                                        : mbar_wait(o_done, (it & 1) ^ 1, abort_flag);
-                            if (ok) mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
-                        }
-                        ok = __shfl_sync(0xffffffffu, ok, 0);
+                    for (int j = 0; j <= NJ; ++j) {
+                        const uint32_t full = j < NJ ? kv_full(ps) : pe_full(ts);
+                        ok = __all_sync(0xffffffffu, j < NJ ? mbar_wait(kv_empty(ps), pp ^ 1, abort_flag)
+                                                            : mbar_wait(pe_empty(ts), tp ^ 1, abort_flag));
                         if (!ok) break;
+                        if (lane == 0) mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
                         __syncwarp();            // the expect-tx precedes every lane's copy
                         if (lane < nbox) {
                             if (j < NJ)
-                                tma_load_4d(sb + C::OFF_KV + j * C::PAIR + lane * bt * 256, &tm_kv, full, 0, 0, 2 * j, grp);
+                                tma_load_4d(pair_addr(ps) + lane * bt * 256, &tm_kv, full, 0, 0, 2 * j, grp);
                             else
-                                tma_load_4d(sb + C::OFF_P + lane * bt * 128, &tm_pe, full, 0, 0, 2 * NJ, grp);
+                                tma_load_4d(rope_addr(ts) + lane * bt * 128, &tm_pe, full, 0, 0, 2 * NJ, grp);
                         }
+                        step(j);
                     }
                 }
             } else {
-                // Rows one by one: a warp copies 64 of them, eight lanes a row's 128
+                // Rows one by one: a warp copies 32 of them, eight lanes a row's 128
                 // bytes; a slot is announced once the copies of the next one are under
                 // way, or at once where the next slot is not free yet.
                 uint32_t pending = 0;
@@ -360,46 +426,44 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         pending = 0;
                     }
                 };
-                auto row_of = [&](int k, int half) {   // cache row of one of this lane's keys of tile k, -1 for zeros
-                    const int t = (p.lt0 + k) * BN + pw * 64 + half * 32 + lane;
+                auto row_of = [&](int k) {       // cache row of this lane's key of tile k, -1 for zeros
+                    const int t = (p.lt0 + k) * BN + pw * 32 + lane;
                     const int page = page_at(p, t);
                     return page >= 0 && page < a.num_pages
                                ? page * a.page_size + (t - page_of(a, (uint32_t)t) * a.page_size)
                                : -1;
                 };
-                int row0 = row_of(0, 0), row1 = row_of(0, 1);
+                int row = row_of(0);
                 for (int k = 0; k < p.n && ok; ++k, ++it) {
-                    const int now0 = row0, now1 = row1;
-                    if (k + 1 < p.n) {
-                        row0 = row_of(k + 1, 0);
-                        row1 = row_of(k + 1, 1);
-                    }
-                    for (int j = 0; j <= NJ && ok; ++j) {
-                        const uint32_t empty = j < NJ ? kv_empty(j) : o_done;
-                        if (!__all_sync(0xffffffffu, mbar_test_wait(empty, (it & 1) ^ 1))) {
+                    const int now = row;
+                    if (k + 1 < p.n) row = row_of(k + 1);
+                    for (int j = 0; j <= NJ; ++j) {
+                        const uint32_t empty = j < NJ ? kv_empty(ps) : pe_empty(ts), parity = (j < NJ ? pp : tp) ^ 1;
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) {
                             cp_async_wait<0>();
                             announce();
-                            ok = __all_sync(0xffffffffu, mbar_wait(empty, (it & 1) ^ 1, abort_flag));
+                            ok = __all_sync(0xffffffffu, mbar_wait(empty, parity, abort_flag));
                             if (!ok) break;
                         }
-                        const uint32_t dst = sb + (j < NJ ? C::OFF_KV + j * C::PAIR : C::OFF_P);
+                        const uint32_t dst = j < NJ ? pair_addr(ps) : rope_addr(ts);
                         const int stride = j < NJ ? 2048 : 1024, slices = j < NJ ? 2 : 1;
 #pragma unroll 4
-                        for (int e = 0; e < 16; ++e) {
-                            const int key = pw * 64 + 4 * e + lane / 8, c = lane % 8;
-                            const int r = __shfl_sync(0xffffffffu, e < 8 ? now0 : now1, (4 * e + lane / 8) & 31);
+                        for (int e = 0; e < 8; ++e) {
+                            const int key = pw * 32 + 4 * e + lane / 8, c = lane % 8;
+                            const int r = __shfl_sync(0xffffffffu, now, 4 * e + lane / 8);
                             const char* src = static_cast<const char*>(a.cache) + (size_t)max(r, 0) * ROW_BYTES +
                                               j * 256 + c * 16;
-                            for (int s = 0; s < slices; ++s)
-                                cp_async16(dst + (key >> 3) * stride + s * 1024 + (key & 7) * 128 + ((c ^ (key & 7)) << 4),
-                                           src + s * 128, r >= 0 ? 16 : 0);
+                            for (int x = 0; x < slices; ++x)
+                                cp_async16(dst + (key >> 3) * stride + x * 1024 + (key & 7) * 128 + ((c ^ (key & 7)) << 4),
+                                           src + x * 128, r >= 0 ? 16 : 0);
                         }
                         cp_async_commit();
                         if (pending) {
                             cp_async_wait<1>();
                             announce();
                         }
-                        pending = j < NJ ? kv_full(j) : pe_full;
+                        pending = j < NJ ? kv_full(ps) : pe_full(ts);
+                        step(j);
                     }
                 }
                 cp_async_wait<0>();
@@ -407,89 +471,136 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
         }
         if (*abort_flag && pw == 0 && lane == 0) {
-            // let the copies in flight land: the last load of each slot
-            if (!GATHER && it > 0) {
-                for (int j = 0; j < C::NP; ++j) mbar_drain(kv_full(j), (it - 1) & 1);
-                mbar_drain(pe_full, (it - 1) & 1);
+            // let the copies in flight land: the last fill of each slot
+            if (!GATHER) {
+                for (int i = 0; i < C::NP; ++i)
+                    if (it > 0 || i < ps) mbar_drain(kv_full(i), i < ps ? pp : pp ^ 1);
+                for (int i = 0; i < C::NT; ++i)
+                    if (it > 0 || i < ts) mbar_drain(pe_full(i), i < ts ? tp : tp ^ 1);
             }
             if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
         }
     } else if (warp == WARP_MMA) {
-        // ------------------------------------------------------------ MMA issuer (lane 0 issues)
-        Piece p;
-        p.first(a, rg, group, NR, rank);
-        bool more = true, ok = true;
-        int it = 0, nq = 0;
-        const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
-        const uint64_t pdesc = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
-        for (; more && ok; more = p.next(a, group, NR, rank)) {
-            for (int k = 0; k < p.n && ok; ++k, ++it) {
-                // S^T of the tile: the slots as they land, the shared dims last
-                if (k == 0) ok = __all_sync(0xffffffffu, mbar_wait(q_full, nq & 1, abort_flag));
-                for (int j = 0; j <= NJ && ok; ++j) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(j < NJ ? kv_full(j) : pe_full, it & 1, abort_flag));
-                    if (!ok) break;
+        // ------------------------------------------------------------ MMA issuer
+        // One elected lane.  S^T runs up to one tile ahead of O^T; whatever is ready
+        // goes first, O^T before S^T, because it frees slots.
+        if (elect_one()) {
+            Piece pq, pv;                        // pieces of the next S^T and the next O^T
+            pq.first(a, rg, group, NR, rank);
+            pv = pq;
+            bool q_more = true, v_more = true;
+            int kq = 0, kv = 0;                  // their tiles within the pieces
+            int itq = 0, itv = 0, nq = 0;        // tiles of S^T and O^T issued, Q blocks taken
+            int j = 0;                           // next slot of the S^T under way
+            int sq = 0, tq = 0, sv = 0, tv = 0;  // their slots and the parities of the uses of sq, tq
+            uint32_t pq_par = 0, tq_par = 0;
+            auto skip = [&](Piece& p, int& k, bool& more) {     // to a piece with a tile
+                while (more && k >= p.n) {
+                    k = 0;
+                    more = p.next(a, group, NR, rank);
+                }
+            };
+            skip(pq, kq, q_more);
+            skip(pv, kv, v_more);
+            const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
+            // K-major A: 8-key groups 2 KB apart (1 KB in the shared dims' slot)
+            const uint64_t kdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 16, 2048), edesc0 = make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
+            // dims-major A: 64-dim slices 1 KB apart, 8-key groups 2 KB apart
+            const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 2048), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
+            unsigned long long idle = 0;
+            while (v_more) {
+                if (itv < itq && mbar_test_wait(p_full(itv & 1), (itv >> 1) & 1)) {
+                    idle = 0;
                     tc_fence_after();
-                    if (lane == 0) {
-                        // K-major A: 8-key groups 2 KB apart (1 KB in the shared dims' slot)
-                        const uint64_t kdesc = j < NJ ? make_sdesc_sw128(sb + C::OFF_KV + j * C::PAIR, 16, 2048)
-                                                      : make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
-                        const uint64_t qd = qdesc + (uint64_t)((2 * j * C::Q_SLICE) >> 4);
+                    const uint64_t pdesc = pdesc0 + (uint64_t)((tv * C::ROPE) >> 4);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            if (kk < 4 || j < NJ)
-                                mma_bf16_ss(tmem + C::COL_S, kdesc + (uint64_t)(((kk / 4) * 1024 + (kk % 4) * 32) >> 4),
-                                            qd + (uint64_t)(((kk / 4) * C::Q_SLICE + (kk % 4) * 32) >> 4), IDESC_S,
-                                            (j > 0 || kk > 0) ? 1u : 0u);
-                    }
-                    __syncwarp();
-                }
-                if (!ok) break;
-                if (lane == 0) {
-                    mma_commit(s_full);
-                    if (k == p.n - 1) mma_commit(q_empty);
-                }
-                if (k == p.n - 1) ++nq;
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, mbar_wait(p_full, it & 1, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        // dims-major A: 64-dim slices 1 KB apart, 8-key groups 2 KB apart
-                        const uint64_t vdesc = make_sdesc_sw128(sb + C::OFF_KV + j * C::PAIR, 1024, 2048);
+                    for (int jj = 0; jj < NJ; ++jj) {
+                        const uint64_t vdesc = vdesc0 + (uint64_t)((sv * C::PAIR) >> 4);
 #pragma unroll
                         for (int kk = 0; kk < BN / 16; ++kk)
-                            mma_bf16_ss(tmem + j * NR, vdesc + (uint64_t)((kk * 4096) >> 4),
-                                        pdesc + (uint64_t)((kk * 2048) >> 4), IDESC_O, (k > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(kv_empty(j));
+                            mma_bf16_ss(tmem + jj * NR, vdesc + (uint64_t)((kk * 4096) >> 4),
+                                        pdesc + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kv > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(kv_empty(sv));
+                        if (++sv == C::NP) sv = 0;
                     }
+                    mma_commit(pe_empty(tv));
                     mma_commit(o_done);
+                    if (++tv == C::NT) tv = 0;
+                    ++itv;
+                    ++kv;
+                    skip(pv, kv, v_more);
+                    continue;
                 }
-                __syncwarp();
+                const bool s_may = q_more && itq <= itv + 1 && (j > 0 || kq > 0 || mbar_test_wait(q_full, nq & 1));
+                const uint32_t d = tmem + C::COL_S + (itq & 1) * NR;
+                bool did = false;
+                while (s_may && j < NJ && mbar_test_wait(kv_full(sq), pq_par)) {
+                    tc_fence_after();
+                    const uint64_t kdesc = kdesc0 + (uint64_t)((sq * C::PAIR) >> 4);
+                    const uint64_t qd = qdesc + (uint64_t)((2 * j * C::Q_SLICE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        mma_bf16_ss(d, kdesc + (uint64_t)(((kk / 4) * 1024 + (kk % 4) * 32) >> 4),
+                                    qd + (uint64_t)(((kk / 4) * C::Q_SLICE + (kk % 4) * 32) >> 4), IDESC_S,
+                                    (j > 0 || kk > 0) ? 1u : 0u);
+                    ++j;
+                    if (++sq == C::NP) { sq = 0; pq_par ^= 1; }
+                    did = true;
+                }
+                if (s_may && j == NJ && mbar_test_wait(pe_full(tq), tq_par)) {
+                    tc_fence_after();
+                    const uint64_t edesc = edesc0 + (uint64_t)((tq * C::ROPE) >> 4);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_bf16_ss(d, edesc + 2 * kk, qdesc + (uint64_t)((2 * NJ * C::Q_SLICE + kk * 32) >> 4), IDESC_S, 1u);
+                    mma_commit(s_full(itq & 1));
+                    j = 0;
+                    if (++tq == C::NT) { tq = 0; tq_par ^= 1; }
+                    ++itq;
+                    if (++kq == pq.n) {
+                        mma_commit(q_empty);
+                        ++nq;
+                        skip(pq, kq, q_more);
+                    }
+                    did = true;
+                }
+                if (did) {
+                    idle = 0;
+                    continue;
+                }
+                // nothing ready: within the wait limit
+                const unsigned long long now = globaltimer_ns();
+                if (idle == 0) idle = now;
+                if (*abort_flag) break;
+                if (now - idle > kWaitTimeoutNs) {
+                    *abort_flag = 1;
+                    break;
+                }
             }
-        }
-        if (lane == 0) {
             mma_commit(drain);                   // every MMA issued above has completed once this arrives
             mbar_drain(drain, 0);
         }
         __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax warps 0-3
-        const int kk = threadIdx.x;              // this thread's key of a tile (TMEM lane), or its row where rows are meant
+        constexpr int HC = NR / 2;               // rows (columns of S^T) of a thread
+        const int row = threadIdx.x;             // this thread's row, where rows are meant
+        const int key = warp * 16 + lane % 16, c0 = (lane / 16) * HC;   // its key of a tile and first column
         const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
         float* neg_ref = reinterpret_cast<float*>(smem + C::OFF_COL);   // -reference maximum (0 while there is none)
         float* factor = neg_ref + NR;                                   // rescale factor of the last move; 1 / sum
         int* limit = reinterpret_cast<int*>(neg_ref + 2 * NR);          // keys that the row sees
-        float* cross = neg_ref + 4 * NR;                                // [4][NR]: per warp
         float* ref = neg_ref + 3 * NR;                                  // reference maximum, -inf while there is none
+        float* cross = neg_ref + 4 * NR;                                // [4][NR]: per warp
         const float sl = a.scale_log2;
         Piece p;
         p.first(a, rg, group, NR, rank);
         bool more = true, ok = true, at_start = true;
-        int it = 0;
+        int it = 0, sv = 0, tv = 0;              // tile; its slots
         long at = rg.g0;                         // the piece's first tile in the sequence
+        // Columns of a half-warp's result (half_warp_columns): this lane's first one, and how many.
+        constexpr int OWN = HC >= 16 ? HC / 16 : 1;
+        const int own = c0 + (HC >= 16 ? (lane % 16) * OWN : (lane % 16) / 2);
         // A wait that gave up (ok false) ends the work but not the walk: all four
         // warps pass the same named barriers to the end.
         for (; more; more = p.next(a, group, NR, rank), at_start = false) {
@@ -502,28 +613,28 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     return a.causal ? max(0, min(p.L, p.L - p.sq + i + 1)) : p.L;
                 };
                 lim_all = lim_of(0);             // every row sees the keys below
-                if (kk < NR) {
-                    limit[kk] = lim_of(kk);
-                    neg_ref[kk] = 0.f;
-                    ref[kk] = -INFINITY;
+                if (row < NR) {
+                    limit[row] = lim_of(row);
+                    neg_ref[row] = 0.f;
+                    ref[row] = -INFINITY;
                 }
             }
             named_bar_sync(kSmBar, 128);
-            float sums[NR];
+            float sums[HC];
 #pragma unroll
-            for (int c = 0; c < NR; ++c) sums[c] = 0.f;
+            for (int c = 0; c < HC; ++c) sums[c] = 0.f;
             for (int k = 0; k < p.n; ++k, ++it) {
-                const int t = (p.lt0 + k) * BN + kk;
+                const int t = (p.lt0 + k) * BN + key;
                 const bool all_seen = (p.lt0 + k + 1) * BN <= lim_all;
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full, it & 1, abort_flag));
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(s_full(it & 1), (it >> 1) & 1, abort_flag));
                 tc_fence_after();
-                float s[NR];
+                float s[HC];
                 auto load = [&]() {              // scores in log2 units against the rows' references; hidden ones -inf
+                    tmem_ld_half<HC>(tmem + lane_addr + C::COL_S + (it & 1) * NR, s);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                    for (int c = 0; c < NR; c += 32) tmem_ld32(tmem + lane_addr + C::COL_S + c, s + c);
-#pragma unroll
-                    for (int c = 0; c < NR; c += 4) {
-                        const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c);
+                    for (int c = 0; c < HC; c += 4) {
+                        const float4 nr = *reinterpret_cast<const float4*>(neg_ref + c0 + c);
                         s[c] = fmaf(s[c], sl, nr.x);
                         s[c + 1] = fmaf(s[c + 1], sl, nr.y);
                         s[c + 2] = fmaf(s[c + 2], sl, nr.z);
@@ -531,8 +642,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                     if (!all_seen) {
 #pragma unroll
-                        for (int c = 0; c < NR; c += 4) {
-                            const int4 li = *reinterpret_cast<const int4*>(limit + c);
+                        for (int c = 0; c < HC; c += 4) {
+                            const int4 li = *reinterpret_cast<const int4*>(limit + c0 + c);
                             s[c] = t < li.x ? s[c] : -INFINITY;
                             s[c + 1] = t < li.y ? s[c + 1] : -INFINITY;
                             s[c + 2] = t < li.z ? s[c + 2] : -INFINITY;
@@ -540,61 +651,56 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         }
                     }
                 };
-                if (ok) {
-                    load();
-                } else {
-#pragma unroll
-                    for (int c = 0; c < NR; ++c) s[c] = -INFINITY;
-                }
+                load();
                 float top = -INFINITY;
-                {
 #pragma unroll
-                    for (int c = 0; c < NR; c += 2) top = fmax3(top, s[c], s[c + 1]);
-                }
+                for (int c = 0; c < HC; c += 2) top = fmax3(top, s[c], s[c + 1]);
                 // The first tile gives every row that sees a key its reference;
                 // a row that sees none there sees none in later tiles either.
                 const bool keep = named_bar_and(kSmBar, 128, ok && k > 0 && !(top > kRescaleThreshold));
                 if (!keep) {
-                    // column maxima over the 128 keys
+                    // column maxima over the tile's keys
+                    half_warp_columns<HC, true>(s, lane);
 #pragma unroll
-                    for (int c = 0; c < NR; ++c) {
-                        const int m = __reduce_max_sync(0xffffffffu, ordered(s[c]));
-                        if (lane == c % 32) cross[warp * NR + c] = unordered(m);
-                    }
+                    for (int e = 0; e < OWN; ++e) cross[warp * NR + own + e] = s[e];
                     named_bar_sync(kSmBar, 128);
-                    if (kk < NR) {
-                        const float d = fmaxf(fmaxf(cross[kk], cross[NR + kk]), fmaxf(cross[2 * NR + kk], cross[3 * NR + kk]));
-                        const float old = ref[kk];
+                    if (row < NR) {
+                        const float d = fmaxf(fmaxf(cross[row], cross[NR + row]), fmaxf(cross[2 * NR + row], cross[3 * NR + row]));
+                        const float old = ref[row];
                         float f = 1.f;
                         if (old == -INFINITY || d > kRescaleThreshold) {
-                            const float m = d - neg_ref[kk];          // neg_ref is 0 while there is no reference
+                            const float m = d - neg_ref[row];         // neg_ref is 0 while there is no reference
                             f = old == -INFINITY ? 0.f : fast_exp2(old - m);
-                            ref[kk] = m;
-                            neg_ref[kk] = m == -INFINITY ? 0.f : -m;
+                            ref[row] = m;
+                            neg_ref[row] = m == -INFINITY ? 0.f : -m;
                         }
-                        factor[kk] = f;
+                        factor[row] = f;
                     }
                     named_bar_sync(kSmBar, 128);
-                    if (ok) load();
+                    load();
                     if (k > 0 && ok) {
-                        // O^T of the tiles before is complete (this S^T came after it)
+                        // O^T has to hold the tile before (and, as this S^T was issued behind it,
+                        // holds the one before that)
+                        ok = __all_sync(0xffffffffu, mbar_wait(o_done, (it - 1) & 1, abort_flag));
+                        tc_fence_after();
 #pragma unroll
-                        for (int c = 0; c < NR; ++c) sums[c] *= factor[c];
+                        for (int c = 0; c < HC; ++c) sums[c] *= factor[c0 + c];
+                        if (ok) {
 #pragma unroll 1
-                        for (int c = 0; c < NJ * NR; c += 32) {
-                            float o[32];
-                            tmem_ld32(tmem + lane_addr + c, o);
+                            for (int c = 0; c < NJ * NR; c += 32) {
+                                float o[32];
+                                tmem_ld32(tmem + lane_addr + c, o);
 #pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= factor[(c + e) % NR];
-                            tmem_st32(tmem + lane_addr + c, reinterpret_cast<uint32_t*>(o));
+                                for (int e = 0; e < 32; ++e) o[e] *= factor[(c + e) % NR];
+                                tmem_st32(tmem + lane_addr + c, reinterpret_cast<uint32_t*>(o));
+                            }
                         }
                     }
                 }
-                if (!ok) continue;
                 // P^T: row = key, 128 bytes with the 128-byte swizzle
-                const uint32_t prow = sb + C::OFF_P + kk * 128;
+                const uint32_t prow = rope_addr(tv) + key * 128;
 #pragma unroll
-                for (int c = 0; c < NR; c += 8) {
+                for (int c = 0; c < HC; c += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -603,41 +709,47 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         sums[c + 2 * e + 1] += p1;
                         w[e] = pack2<F16>(p0, p1);
                     }
-                    st_shared_v4(prow + (((c / 8) ^ (kk & 7)) << 4), w[0], w[1], w[2], w[3]);
+                    if (ok) st_shared_v4(prow + ((((c0 + c) / 8) ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
                 }
-                if (t >= p.L) {
-                    // a row past the request's end: whatever the page holds there must not reach O^T
-                    for (int j = 0; j < NJ; ++j)
-                        for (int c = 0; c < 16; ++c)
-                            st_shared_v4(sb + C::OFF_KV + j * C::PAIR + (kk >> 3) * 2048 + (c >> 3) * 1024 + (kk & 7) * 128 +
-                                             (c & 7) * 16, 0u, 0u, 0u, 0u);
+                if (++tv == C::NT) tv = 0;
+                for (int j = 0; j < NJ; ++j) {
+                    if (t >= p.L && ok) {
+                        // a row past the request's end: whatever the page holds there must not
+                        // reach O^T (a slice for each of the key's two threads)
+                        const uint32_t v = pair_addr(sv) + (key >> 3) * 2048 + (lane / 16) * 1024 + (key & 7) * 128;
+                        for (int c = 0; c < 128; c += 16) st_shared_v4(v + c, 0u, 0u, 0u, 0u);
+                    }
+                    if (++sv == C::NP) sv = 0;
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
-                mbar_arrive(p_full);
+                if (ok) mbar_arrive(p_full(it & 1));
             }
             // ---- the piece's end
             __syncwarp();
             if (ok && p.n > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(o_done, (it - 1) & 1, abort_flag));
+                // S^T of the last tile only says that O^T holds the tiles up to the last but
+                // two: one phase after the other, so that a parity names the right one
+                if (it > 1) ok = __all_sync(0xffffffffu, mbar_wait(o_done, it & 1, abort_flag));
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_done, (it - 1) & 1, abort_flag));
                 tc_fence_after();
             }
-            warp_column_sums<NR>(sums, lane);
+            half_warp_columns<HC, false>(sums, lane);
 #pragma unroll
-            for (int e = 0; e < NR / 32; ++e) cross[warp * NR + lane * (NR / 32) + e] = sums[e];
+            for (int e = 0; e < OWN; ++e) cross[warp * NR + own + e] = sums[e];
             ok = named_bar_and(kSmBar, 128, ok);
             if (p.rows > 0) {
                 const long orow = (long)p.qs * a.H + p.row0;       // first row of the block in [total_q * H]
-                if (kk < NR) {
-                    const float m = ref[kk];
-                    const float l = (cross[kk] + cross[NR + kk]) + (cross[2 * NR + kk] + cross[3 * NR + kk]);
+                if (row < NR) {
+                    const float m = ref[row];
+                    const float l = (cross[row] + cross[NR + row]) + (cross[2 * NR + row] + cross[3 * NR + row]);
                     const bool some = p.n > 0 && l != 0.f;         // 0: no key; NaN goes on
                     if (whole) {
-                        factor[kk] = some ? 1.f / l : 0.f;
-                        if (kk < p.rows && a.lse) a.lse[orow + kk] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
+                        factor[row] = some ? 1.f / l : 0.f;
+                        if (row < p.rows && a.lse) a.lse[orow + row] = some ? (m + log2f(l)) * kLn2 : -INFINITY;
                     } else {
-                        const int id = 2 * blockIdx.x + (at_start ? 0 : 1);
-                        a.part_ml[(size_t)id * NR + kk] = some ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+                        const size_t id = 2 * (size_t)blockIdx.x + (at_start ? 0 : 1);
+                        a.part_ml[id * NR + row] = some ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
                     }
                 }
                 named_bar_sync(kSmBar, 128);
@@ -647,30 +759,30 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     uint32_t* out = reinterpret_cast<uint32_t*>(a.o);
                     const bool odd = lane & 1;
 #pragma unroll 1
-                    for (int j = 0; j < NJ; ++j) {
-#pragma unroll 1
-                        for (int c = 0; c < NR; c += 32) {
-                            float o[32];
-                            if (p.n > 0) {
-                                __syncwarp();
-                                tmem_ld32(tmem + lane_addr + j * NR + c, o);
-                            }
+                    for (int c = 0; c < NJ * NR; c += 32) {
+                        float o[32];
+                        __syncwarp();
+                        if (p.n > 0) {
+                            tmem_ld32(tmem + lane_addr + c, o);
+                        } else {
 #pragma unroll
-                            for (int e = 0; e < 32; e += 2) {
-                                const float o0 = p.n > 0 ? o[e] * factor[c + e] : 0.f;
-                                const float o1 = p.n > 0 ? o[e + 1] * factor[c + e + 1] : 0.f;
-                                const float got = __shfl_xor_sync(0xffffffffu, odd ? o0 : o1, 1);
-                                const int r = c + e + (odd ? 1 : 0);
-                                if (r < p.rows)
-                                    out[((orow + r) * DC + j * 128 + warp * 32 + (lane & ~1)) / 2] =
-                                        odd ? pack2<F16>(got, o1) : pack2<F16>(o0, got);
-                            }
+                            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; e += 2) {
+                            const int j = (c + e) / NR, r0 = (c + e) % NR;
+                            const float o0 = p.n > 0 ? o[e] * factor[r0] : 0.f, o1 = p.n > 0 ? o[e + 1] * factor[r0 + 1] : 0.f;
+                            const float got = __shfl_xor_sync(0xffffffffu, odd ? o0 : o1, 1);
+                            const int r = r0 + (odd ? 1 : 0);
+                            if (r < p.rows)
+                                out[((orow + r) * DC + j * 128 + warp * 32 + (lane & ~1)) / 2] =
+                                    odd ? pack2<F16>(got, o1) : pack2<F16>(o0, got);
                         }
                     }
                 } else if (p.n > 0) {
                     // as it lies, [block][four rows][dim][4], for the joining kernel
                     const size_t id = 2 * (size_t)blockIdx.x + (at_start ? 0 : 1);
-                    float4* dst = reinterpret_cast<float4*>(a.part_o) + id * (NJ * NR / 4) * 128 + kk;
+                    float4* dst = reinterpret_cast<float4*>(a.part_o) + id * (NJ * NR / 4) * 128 + row;
 #pragma unroll 1
                     for (int c = 0; c < NJ * NR; c += 32) {
                         float o[32];
@@ -682,7 +794,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     }
                 }
             }
-            if (!whole && p.lt0 == 0 && kk == 0 && rank == 0) {
+            if (!whole && p.lt0 == 0 && row == 0 && rank == 0) {
                 // this team holds the row group's first tile: where its pieces lie
                 const long last = (at + p.nt - 1) / rg.per;
                 *reinterpret_cast<int4*>(a.join + 4 * team) =
@@ -787,10 +899,17 @@ cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CU
 cudaError_t launch_latent_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
                                 const LatentArgs& a, cudaStream_t stream) {
     const bool gather = a.box_tokens == 0;
-    if (a.f16) return gather ? launch_t<kLatentRows, true, true>(tm_q, tm_kv, tm_pe, a, stream)
-                             : launch_t<kLatentRows, true, false>(tm_q, tm_kv, tm_pe, a, stream);
-    return gather ? launch_t<kLatentRows, false, true>(tm_q, tm_kv, tm_pe, a, stream)
-                  : launch_t<kLatentRows, false, false>(tm_q, tm_kv, tm_pe, a, stream);
+    switch ((gather ? 64 : a.nr) * 4 + (a.f16 ? 2 : 0) + (gather ? 1 : 0)) {
+        case 16 * 4: return launch_t<16, false, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 16 * 4 + 2: return launch_t<16, true, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 32 * 4: return launch_t<32, false, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 32 * 4 + 2: return launch_t<32, true, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 64 * 4: return launch_t<64, false, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 64 * 4 + 2: return launch_t<64, true, false>(tm_q, tm_kv, tm_pe, a, stream);
+        case 64 * 4 + 1: return launch_t<64, false, true>(tm_q, tm_kv, tm_pe, a, stream);
+        case 64 * 4 + 3: return launch_t<64, true, true>(tm_q, tm_kv, tm_pe, a, stream);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 int latent_paged_take_device_error() {
