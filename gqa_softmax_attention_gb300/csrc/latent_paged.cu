@@ -32,9 +32,9 @@
 // all CTAs loaded and all computed at the same time (64 requests of 1K to 16K
 // keys, 16 heads: 188 us).
 //   warps 0-3  softmax; the output
-//   warp 4     MMA issuer: takes whichever is ready, P V of a tile or S^T of a slot of
-//              the next, through one elected lane
-//   warp 5     producer (TMA), or warps 5-6 (rows gathered)
+//   warps 4, 5 MMA issuers of S^T, which runs up to a tile ahead, and of O^T, an elected
+//              lane each: the tensor core takes whichever is ready
+//   warp 6     producer (TMA), or warps 6-7 (rows gathered)
 // A softmax thread owns a key and half of the rows.  The reference maximum of a row
 // (column) is kept in shared memory and moves only when a score exceeds it by more
 // than 2^8, which the threads vote on; the row sums are kept as per-thread parts
@@ -66,8 +66,8 @@ constexpr int ROW_BYTES = DK * 2;
 constexpr int NJ = DC / 128;               // 128-dim blocks of O^T (pairs of 64-dim slices)
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleThreshold = 8.f;
-constexpr int WARP_MMA = 4;
-constexpr int WARP_LOAD = 5;
+constexpr int WARP_S = 4, WARP_O = 5;      // MMA issuers of S^T and of O^T
+constexpr int WARP_LOAD = 6;
 constexpr int kSmBar = 1;                  // named barrier of the softmax warps
 
 template <int NR, bool GATHER>
@@ -83,12 +83,12 @@ struct LCfg {
     static constexpr int OFF_COL = OFF_KV + NP * PAIR;             // per row: -reference, factor, limit, reference, [4] per warp
     static constexpr int OFF_BAR = OFF_COL + 8 * NR * 4;
     // kv_full[NP], kv_empty[NP], pe_full[NT], pe_empty[NT], q_full, q_empty,
-    // s_full[2], p_full[2], o_done, drain
+    // drain[2], s_full[2], p_full[2]
     static constexpr int NBAR = 2 * NP + 2 * NT + 8;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
     static constexpr int LOAD_WARPS = GATHER ? 2 : 1;
-    static constexpr int THREADS = 32 * (5 + LOAD_WARPS);
+    static constexpr int THREADS = 32 * (WARP_LOAD + LOAD_WARPS);
     static constexpr uint32_t COL_S = NJ * NR;                     // TMEM: O^T blocks | S^T of even, of odd tiles
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(COL_S + 2 * NR <= TMEM_COLS, "TMEM budget");
@@ -226,6 +226,14 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// A shared-memory descriptor moved by `bytes`: only the address field of its low
+// word changes, so one 32-bit addition does.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"((uint32_t)d + (bytes >> 4)), "r"((uint32_t)(d >> 32)));
+    return r;
+}
+
 // n / page_size for 0 <= n < 2^31
 __device__ __forceinline__ int page_of(const LatentArgs& a, uint32_t n) {
     return (int)((__umulhi(n, a.ps_mul) + n) >> a.ps_shift);
@@ -256,7 +264,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     auto pe_full = [&](int i) { return bar0 + 8u * (2 * C::NP + i); };
     auto pe_empty = [&](int i) { return bar0 + 8u * (2 * C::NP + C::NT + i); };
     const uint32_t bar1 = bar0 + 8u * (2 * C::NP + 2 * C::NT);
-    const uint32_t q_full = bar1, q_empty = bar1 + 8, o_done = bar1 + 16, drain = bar1 + 24;
+    const uint32_t q_full = bar1, q_empty = bar1 + 8;
+    auto drain = [&](int i) { return bar1 + 16 + 8u * i; };
     auto s_full = [&](int i) { return bar1 + 32 + 8u * i; };
     auto p_full = [&](int i) { return bar1 + 48 + 8u * i; };
     // Tile it's slots: dims 128 j .. are use u / NP of slot u % NP with u = NJ it + j, its
@@ -271,11 +280,9 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int fills = GATHER ? 32 * C::LOAD_WARPS : 1;
         for (int i = 0; i < C::NP; ++i) { mbar_init(kv_full(i), fills); mbar_init(kv_empty(i), 1); }
         for (int i = 0; i < C::NT; ++i) { mbar_init(pe_full(i), fills); mbar_init(pe_empty(i), 1); }
-        for (int i = 0; i < 2; ++i) { mbar_init(s_full(i), 1); mbar_init(p_full(i), 128); }
+        for (int i = 0; i < 2; ++i) { mbar_init(s_full(i), 1); mbar_init(p_full(i), 128); mbar_init(drain(i), 1); }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
-        mbar_init(o_done, 1);
-        mbar_init(drain, 1);
         *abort_flag = 0;
         *range = LRange{0, 0, 0, 0, 0, 0, 0};
         fence_mbar_init();
@@ -326,7 +333,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
         }
     }
-    if (warp == WARP_MMA) {
+    if (warp == WARP_S) {
         tmem_alloc(smem_u32(tmem_slot), C::TMEM_COLS);
         tmem_relinquish();
     }
@@ -403,13 +410,23 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         ok = __all_sync(0xffffffffu, j < NJ ? mbar_wait(kv_empty(ps), pp ^ 1, abort_flag)
                                                             : mbar_wait(pe_empty(ts), tp ^ 1, abort_flag));
                         if (!ok) break;
-                        if (lane == 0) mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
-                        __syncwarp();            // the expect-tx precedes every lane's copy
-                        if (lane < nbox) {
-                            if (j < NJ)
-                                tma_load_4d(pair_addr(ps) + lane * bt * 256, &tm_kv, full, 0, 0, 2 * j, grp);
-                            else
-                                tma_load_4d(rope_addr(ts) + lane * bt * 128, &tm_pe, full, 0, 0, 2 * NJ, grp);
+                        if (nbox == 1) {
+                            const int g0 = __shfl_sync(0xffffffffu, grp, 0);
+                            if (elect_one()) {
+                                mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
+                                if (j < NJ) tma_load_4d(pair_addr(ps), &tm_kv, full, 0, 0, 2 * j, g0);
+                                else tma_load_4d(rope_addr(ts), &tm_pe, full, 0, 0, 2 * NJ, g0);
+                            }
+                            __syncwarp();
+                        } else {
+                            if (lane == 0) mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
+                            __syncwarp();        // the expect-tx precedes every lane's copy
+                            if (lane < nbox) {
+                                if (j < NJ)
+                                    tma_load_4d(pair_addr(ps) + lane * bt * 256, &tm_kv, full, 0, 0, 2 * j, grp);
+                                else
+                                    tma_load_4d(rope_addr(ts) + lane * bt * 128, &tm_pe, full, 0, 0, 2 * NJ, grp);
+                            }
                         }
                         step(j);
                     }
@@ -480,105 +497,86 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
         }
-    } else if (warp == WARP_MMA) {
-        // ------------------------------------------------------------ MMA issuer
-        // One elected lane.  S^T runs up to one tile ahead of O^T; whatever is ready
-        // goes first, O^T before S^T, because it frees slots.
+    } else if (warp == WARP_S) {
+        // ------------------------------------------------------------ S^T issuer (one elected lane)
         if (elect_one()) {
-            Piece pq, pv;                        // pieces of the next S^T and the next O^T
-            pq.first(a, rg, group, NR, rank);
-            pv = pq;
-            bool q_more = true, v_more = true;
-            int kq = 0, kv = 0;                  // their tiles within the pieces
-            int itq = 0, itv = 0, nq = 0;        // tiles of S^T and O^T issued, Q blocks taken
-            int j = 0;                           // next slot of the S^T under way
-            int sq = 0, tq = 0, sv = 0, tv = 0;  // their slots and the parities of the uses of sq, tq
-            uint32_t pq_par = 0, tq_par = 0;
-            auto skip = [&](Piece& p, int& k, bool& more) {     // to a piece with a tile
-                while (more && k >= p.n) {
-                    k = 0;
-                    more = p.next(a, group, NR, rank);
-                }
-            };
-            skip(pq, kq, q_more);
-            skip(pv, kv, v_more);
+            Piece p;
+            p.first(a, rg, group, NR, rank);
+            int it = 0, nq = 0, ps = 0, ts = 0;  // tile, Q blocks taken, slots and the parities of their uses
+            uint32_t pp = 0, tp = 0;
+            bool ok = true;
             const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
             // K-major A: 8-key groups 2 KB apart (1 KB in the shared dims' slot)
             const uint64_t kdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 16, 2048), edesc0 = make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
-            // dims-major A: 64-dim slices 1 KB apart, 8-key groups 2 KB apart
-            const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 2048), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
-            unsigned long long idle = 0;
-            while (v_more) {
-                if (itv < itq && mbar_test_wait(p_full(itv & 1), (itv >> 1) & 1)) {
-                    idle = 0;
+            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+                for (int k = 0; k < p.n && ok; ++k, ++it) {
+                    if (k == 0) ok = mbar_wait(q_full, nq & 1, abort_flag);
+                    // at most one tile ahead of O^T, so that no barrier runs two phases ahead
+                    // of who waits on it: the tile before the last is done, and its S^T read
+                    if (ok && it > 1) ok = mbar_wait(pe_empty((it - 2) % C::NT), ((it - 2) / C::NT) & 1, abort_flag);
+                    const uint32_t d = tmem + C::COL_S + (it & 1) * NR;
                     tc_fence_after();
-                    const uint64_t pdesc = pdesc0 + (uint64_t)((tv * C::ROPE) >> 4);
 #pragma unroll
-                    for (int jj = 0; jj < NJ; ++jj) {
-                        const uint64_t vdesc = vdesc0 + (uint64_t)((sv * C::PAIR) >> 4);
+                    for (int j = 0; j < NJ; ++j) {
+                        if (ok) ok = mbar_wait(kv_full(ps), pp, abort_flag);
+                        if (!ok) break;
+                        const uint64_t kdesc = desc_at(kdesc0, ps * C::PAIR);
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            mma_bf16_ss(tmem + jj * NR, vdesc + (uint64_t)((kk * 4096) >> 4),
-                                        pdesc + (uint64_t)((kk * 2048) >> 4), IDESC_O, (kv > 0 || kk > 0) ? 1u : 0u);
-                        mma_commit(kv_empty(sv));
-                        if (++sv == C::NP) sv = 0;
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_bf16_ss(d, desc_at(kdesc, (kk / 4) * 1024 + (kk % 4) * 32),
+                                        desc_at(qdesc, (2 * j + kk / 4) * C::Q_SLICE + (kk % 4) * 32), IDESC_S,
+                                        (j > 0 || kk > 0) ? 1u : 0u);
+                        if (++ps == C::NP) { ps = 0; pp ^= 1; }
                     }
-                    mma_commit(pe_empty(tv));
-                    mma_commit(o_done);
-                    if (++tv == C::NT) tv = 0;
-                    ++itv;
-                    ++kv;
-                    skip(pv, kv, v_more);
-                    continue;
-                }
-                const bool s_may = q_more && itq <= itv + 1 && (j > 0 || kq > 0 || mbar_test_wait(q_full, nq & 1));
-                const uint32_t d = tmem + C::COL_S + (itq & 1) * NR;
-                bool did = false;
-                while (s_may && j < NJ && mbar_test_wait(kv_full(sq), pq_par)) {
-                    tc_fence_after();
-                    const uint64_t kdesc = kdesc0 + (uint64_t)((sq * C::PAIR) >> 4);
-                    const uint64_t qd = qdesc + (uint64_t)((2 * j * C::Q_SLICE) >> 4);
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_bf16_ss(d, kdesc + (uint64_t)(((kk / 4) * 1024 + (kk % 4) * 32) >> 4),
-                                    qd + (uint64_t)(((kk / 4) * C::Q_SLICE + (kk % 4) * 32) >> 4), IDESC_S,
-                                    (j > 0 || kk > 0) ? 1u : 0u);
-                    ++j;
-                    if (++sq == C::NP) { sq = 0; pq_par ^= 1; }
-                    did = true;
-                }
-                if (s_may && j == NJ && mbar_test_wait(pe_full(tq), tq_par)) {
-                    tc_fence_after();
-                    const uint64_t edesc = edesc0 + (uint64_t)((tq * C::ROPE) >> 4);
+                    if (ok) ok = mbar_wait(pe_full(ts), tp, abort_flag);
+                    if (!ok) break;
+                    const uint64_t edesc = desc_at(edesc0, ts * C::ROPE);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss(d, edesc + 2 * kk, qdesc + (uint64_t)((2 * NJ * C::Q_SLICE + kk * 32) >> 4), IDESC_S, 1u);
-                    mma_commit(s_full(itq & 1));
-                    j = 0;
-                    if (++tq == C::NT) { tq = 0; tq_par ^= 1; }
-                    ++itq;
-                    if (++kq == pq.n) {
+                        mma_bf16_ss(d, desc_at(edesc, kk * 32), desc_at(qdesc, 2 * NJ * C::Q_SLICE + kk * 32), IDESC_S, 1u);
+                    mma_commit(s_full(it & 1));
+                    if (k == p.n - 1) {
                         mma_commit(q_empty);
                         ++nq;
-                        skip(pq, kq, q_more);
                     }
-                    did = true;
-                }
-                if (did) {
-                    idle = 0;
-                    continue;
-                }
-                // nothing ready: within the wait limit
-                const unsigned long long now = globaltimer_ns();
-                if (idle == 0) idle = now;
-                if (*abort_flag) break;
-                if (now - idle > kWaitTimeoutNs) {
-                    *abort_flag = 1;
-                    break;
+                    if (++ts == C::NT) { ts = 0; tp ^= 1; }
                 }
             }
-            mma_commit(drain);                   // every MMA issued above has completed once this arrives
-            mbar_drain(drain, 0);
+            mma_commit(drain(0));                // every MMA issued above has completed once this arrives
+            mbar_drain(drain(0), 0);
+        }
+        __syncwarp();
+    } else if (warp == WARP_O) {
+        // ------------------------------------------------------------ O^T issuer (one elected lane)
+        if (elect_one()) {
+            Piece p;
+            p.first(a, rg, group, NR, rank);
+            int it = 0, ps = 0, ts = 0;
+            bool ok = true;
+            // dims-major A: 64-dim slices 1 KB apart, 8-key groups 2 KB apart
+            const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 2048), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
+            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+                for (int k = 0; k < p.n; ++k, ++it) {
+                    ok = mbar_wait(p_full(it & 1), (it >> 1) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t pdesc = desc_at(pdesc0, ts * C::ROPE);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const uint64_t vdesc = desc_at(vdesc0, ps * C::PAIR);
+#pragma unroll
+                        for (int kk = 0; kk < BN / 16; ++kk)
+                            mma_bf16_ss(tmem + j * NR, desc_at(vdesc, kk * 4096), desc_at(pdesc, kk * 2048), IDESC_O,
+                                        (k > 0 || kk > 0) ? 1u : 0u);
+                        mma_commit(kv_empty(ps));
+                        if (++ps == C::NP) ps = 0;
+                    }
+                    mma_commit(pe_empty(ts));    // the tile's O^T is complete as well
+                    if (++ts == C::NT) ts = 0;
+                }
+            }
+            mma_commit(drain(1));
+            mbar_drain(drain(1), 0);
         }
         __syncwarp();
     } else {
@@ -679,9 +677,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     named_bar_sync(kSmBar, 128);
                     load();
                     if (k > 0 && ok) {
-                        // O^T has to hold the tile before (and, as this S^T was issued behind it,
-                        // holds the one before that)
-                        ok = __all_sync(0xffffffffu, mbar_wait(o_done, (it - 1) & 1, abort_flag));
+                        // O^T has to hold the tile before
+                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pe_empty((it - 1) % C::NT), ((it - 1) / C::NT) & 1, abort_flag));
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < HC; ++c) sums[c] *= factor[c0 + c];
@@ -728,10 +725,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             // ---- the piece's end
             __syncwarp();
             if (ok && p.n > 0) {
-                // S^T of the last tile only says that O^T holds the tiles up to the last but
-                // two: one phase after the other, so that a parity names the right one
-                if (it > 1) ok = __all_sync(0xffffffffu, mbar_wait(o_done, it & 1, abort_flag));
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(o_done, (it - 1) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, mbar_wait(pe_empty((it - 1) % C::NT), ((it - 1) / C::NT) & 1, abort_flag));
                 tc_fence_after();
             }
             half_warp_columns<HC, false>(sums, lane);
@@ -810,7 +804,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
     tc_fence_before();
     __syncthreads();
-    if (warp == WARP_MMA) {
+    if (warp == WARP_S) {
         tc_fence_after();
         tmem_dealloc(tmem, C::TMEM_COLS);
     }
