@@ -217,23 +217,6 @@ __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float* v) {
     }
 }
 
-// One lane of the (converged) warp.  Of a lane chosen like this, unlike lane 0 by
-// comparison, the compiler knows that it runs alone: MMAs then go out at 24 to 49
-// cycles a step, the shared-memory limit, instead of one every 50 to 54.
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
-    return p != 0;
-}
-
-// A shared-memory descriptor moved by `bytes`: only the address field of its low
-// word changes, so one 32-bit addition does.
-__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"((uint32_t)d + (bytes >> 4)), "r"((uint32_t)(d >> 32)));
-    return r;
-}
-
 // n / page_size for 0 <= n < 2^31
 __device__ __forceinline__ int page_of(const LatentArgs& a, uint32_t n) {
     return (int)((__umulhi(n, a.ps_mul) + n) >> a.ps_shift);

@@ -73,7 +73,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw_base & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // through a shuffle, so that the compiler knows the roles' branches to be uniform
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
 
     const int n_entries = *a.n_entries;
     const long n_items = (long)n_entries * a.Hq;
@@ -112,7 +113,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
     // Unit u of the loads (KU key slots, then VU value slots, per tile) is use u / NS of slot u % NS.
-    auto slot_addr = [&](long u) { return sb + OFF_RING + (uint32_t)(u % NS) * SLOT; };
+    auto slot_addr = [&](uint32_t u) { return sb + OFF_RING + u % NS * SLOT; };
+    auto parity_of = [&](uint32_t u) { return u / NS & 1; };
 
     if (threadIdx.x == 0) {
         for (int k = 0; k < NQ; ++k) {
@@ -145,10 +147,10 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     if (warp >= 8) {
         regs_dec<kRegsOther>();
         if (warp == WARP_LOAD) {
-            // ------------------------------------------------------------ producer (lane 0)
-            long nu = 0;                           // units loaded
+            // ------------------------------------------------------------ producer (one elected lane)
+            uint32_t nu = 0;                       // units loaded (modulo 2^32, a multiple of NS)
             int nq[2] = {0, 0};
-            if (lane == 0) {
+            if (elect_one()) {
                 tma_prefetch_desc(&tm_q);
                 tma_prefetch_desc(&tm_k);
                 tma_prefetch_desc(&tm_v);
@@ -187,8 +189,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     for (int j = 0; j < n && ok; ++j) {
                         const int key = it.ks + j * BN;
                         for (int x = 0; x < UNITS && ok; ++x, ++nu) {
-                            const uint32_t f = full((int)(nu % NS));
-                            ok = mbar_wait(empty((int)(nu % NS)), (uint32_t)((nu / NS) & 1) ^ 1u, abort_flag);
+                            const uint32_t f = full(nu % NS);
+                            ok = mbar_wait(empty(nu % NS), parity_of(nu) ^ 1u, abort_flag);
                             if (!ok) break;
                             const uint32_t dst = slot_addr(nu);
                             mbar_arrive_expect_tx(f, SLOT);
@@ -208,16 +210,16 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 }
                 if (*abort_flag) {
                     // let the copies in flight land: the last load of each slot
-                    for (long u = max(0L, nu - NS); u < nu; ++u) mbar_drain(full((int)(u % NS)), (uint32_t)((u / NS) & 1));
+                    for (uint32_t u = nu < NS ? 0 : nu - NS; u != nu; ++u) mbar_drain(full(u % NS), parity_of(u));
                     for (int k = 0; k < 2; ++k)
                         if (nq[k] > 0) mbar_drain(q_full(k), (nq[k] - 1) & 1);
                 }
             }
             __syncwarp();
         } else if (warp == WARP_MMA) {
-            // ------------------------------------------------------------ MMA issuer (lane 0)
-            if (lane == 0) {
-                long u0 = 0;                       // first unit of the item
+            // ------------------------------------------------------------ MMA issuer (one elected lane)
+            if (elect_one()) {
+                uint32_t u0 = 0;                   // first unit of the item
                 int nq[2] = {0, 0}, np[2] = {0, 0}, nfix = 0;
                 bool ok = true;
                 for (int r = 0; ok; ++r) {
@@ -228,25 +230,24 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     mbar_arrive(info_empty(r & 1));
                     if (w < 0) break;
                     const int n = max(c0, c1);
-                    auto unit_ready = [&](long u) {
-                        if (!mbar_wait(full((int)(u % NS)), (uint32_t)((u / NS) & 1), abort_flag)) return false;
-                        tc_fence_after();
-                        return true;
-                    };
+                    // (no tcgen05 fence: the slots come by TMA, and the fence would wait for
+                    // the MMAs under way)
+                    auto unit_ready = [&](uint32_t u) { return mbar_wait(full(u % NS), parity_of(u), abort_flag); };
                     // S_k of tile i; `last`: no other query tile needs these keys
                     auto issue_s = [&](int k, int i, bool last) {
                         const uint32_t d = tmem + (k == 0 ? COL_S0 : COL_S1);
                         const uint32_t qb = sb + OFF_Q + k * Q_TILE;
 #pragma unroll
                         for (int x = 0; x < KU; ++x) {
-                            const long u = u0 + (long)i * UNITS + x;
+                            const uint32_t u = u0 + i * UNITS + x;
                             if (!unit_ready(u)) return false;
                             const uint64_t qd = make_sdesc_sw128(qb + x * SLOT, 16, 1024);
                             const uint64_t kd = make_sdesc_sw128(slot_addr(u), 16, 1024);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_ss(d, qd + 2 * kk, kd + 2 * kk, IDESC_QK, (x > 0 || kk > 0) ? 1u : 0u);
-                            if (last) mma_commit(empty((int)(u % NS)));
+                                mma_bf16_ss(d, desc_at(qd, 32 * kk), desc_at(kd, 32 * kk), IDESC_QK,
+                                            (x > 0 || kk > 0) ? 1u : 0u);
+                            if (last) mma_commit(empty(u % NS));
                         }
                         mma_commit(s_full(k));
                         return true;
@@ -257,20 +258,20 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         const uint32_t d = tmem + (k == 0 ? COL_O0 : COL_O1), p = tmem + (k == 0 ? COL_S0 : COL_S1);
 #pragma unroll
                         for (int x = 0; x < VU; ++x) {
-                            const long u = u0 + (long)i * UNITS + KU + x;
+                            const uint32_t u = u0 + i * UNITS + KU + x;
                             // dims-major B: 64-dim halves 8 KB apart, 8-key groups 1 KB apart
                             const uint64_t vd = make_sdesc_sw128(slot_addr(u), SLOT / 2, 1024);
 #pragma unroll
                             for (int kk = 0; kk < 4; ++kk)
-                                mma_bf16_ts(d, p + (4 * x + kk) * 8, vd + (uint64_t)((kk * 2048) >> 4), IDESC_PV,
+                                mma_bf16_ts(d, p + (4 * x + kk) * 8, desc_at(vd, kk * 2048), IDESC_PV,
                                             (i > 0 || x > 0 || kk > 0) ? 1u : 0u);
-                            if (last) mma_commit(empty((int)(u % NS)));
+                            if (last) mma_commit(empty(u % NS));
                         }
                         return true;
                     };
                     auto values_ready = [&](int i) {
                         for (int x = 0; x < VU; ++x)
-                            if (!unit_ready(u0 + (long)i * UNITS + KU + x)) return false;
+                            if (!unit_ready(u0 + i * UNITS + KU + x)) return false;
                         if (i == n - 1) {
                             // the item's last tile: rows past the request's end are zeroed first
                             mbar_arrive(v_landed);
@@ -279,8 +280,6 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         }
                         return true;
                     };
-                    if (c0 == 0) mma_commit(o_final(0));
-                    if (c1 == 0) mma_commit(o_final(1));
                     if (c0 > 0) {
                         ok = mbar_wait(q_full(0), nq[0]++ & 1, abort_flag) && issue_s(0, 0, c1 == 0);
                         if (ok && c0 == 1) mma_commit(q_empty(0));
@@ -308,7 +307,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             }
                         }
                     }
-                    u0 += (long)n * UNITS;
+                    u0 += n * UNITS;
                 }
                 mma_commit(drain);                // every MMA issued above has completed once this arrives
                 mbar_drain(drain, 0);
@@ -322,7 +321,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // Value rows past the request's end hold the next request's rows, where
             // 0 * NaN would not vanish: zero them before the last tile's P V.
             const int t = (warp - 10) * 32 + lane;
-            long u0 = 0;
+            uint32_t u0 = 0;
             int nl = 0;
             for (int r = 0;; ++r) {
                 const bool got = __all_sync(0xffffffffu, mbar_wait(info_full(r & 1), (r >> 1) & 1, abort_flag));
@@ -333,14 +332,13 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (w < 0) break;
                 if (n == 0) continue;
                 const Item it = describe(w);
-                const long uv = u0 + (long)(n - 1) * UNITS + KU;
-                u0 += (long)n * UNITS;
+                const uint32_t uv = u0 + (n - 1) * UNITS + KU;
+                u0 += n * UNITS;
                 if (!__all_sync(0xffffffffu, mbar_wait(v_landed, nl & 1, abort_flag))) break;
                 ++nl;
                 for (int x = 0; x < VU; ++x) {
                     // the MMA thread has seen the slot full; so does the writer here
-                    if (!__all_sync(0xffffffffu, mbar_wait(full((int)((uv + x) % NS)), (uint32_t)(((uv + x) / NS) & 1),
-                                                           abort_flag)))
+                    if (!__all_sync(0xffffffffu, mbar_wait(full((uv + x) % NS), parity_of(uv + x), abort_flag)))
                         break;
                     const int r0 = it.skv - (n - 1) * BN - x * 64;   // first row of the half past the end
                     uint8_t* base = smem + (slot_addr(uv + x) - sb);
@@ -363,7 +361,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint32_t col_s = k == 0 ? COL_S0 : COL_S1, col_o = k == 0 ? COL_O0 : COL_O1;
         const float sl = a.scale_log2;
         int sf = 0;                  // S tiles taken so far (s_full parity)
-        int n_done = 0;              // items finished (o_final parity)
+        int n_done = 0;              // items with a tile finished (o_final parity)
         bool ok = true;
         for (int rr = 0;; ++rr) {
             ok = __all_sync(0xffffffffu, mbar_wait(info_full(rr & 1), (rr >> 1) & 1, abort_flag));
@@ -446,11 +444,13 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 mbar_arrive(p_full(k));
             }
             // ---- the tile's end (also after a wait gave up: all four warps pass the barrier below)
-            if (ok) {
+            // An item without a tile for this warpgroup has no phase of o_final: the
+            // MMA thread could end it before the phase of the item before has been seen.
+            if (ok && ti.n_tiles > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(o_final(k), n_done & 1, abort_flag));
+                ++n_done;
                 if (ok) tc_fence_after();
             }
-            ++n_done;
             const bool row_ok = r < ti.rows_valid;
             const size_t orow = (size_t)(itm.qs + ti.q0 + r) * a.Hq + itm.h;
             const bool some = l_run != 0.f && ti.n_tiles > 0;    // 0: no key; NaN goes on

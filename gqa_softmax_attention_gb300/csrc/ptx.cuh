@@ -321,6 +321,23 @@ __device__ __forceinline__ uint64_t make_sdesc_sw128(uint32_t saddr, uint32_t lb
     return d;
 }
 
+// One lane of the (converged) warp.  Of a lane chosen like this, unlike lane 0 by
+// comparison, the compiler knows that it runs alone: MMAs then go out at 24 to 49
+// cycles a step, the shared-memory limit, instead of one every 50 to 54.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// A shared-memory descriptor moved by `bytes`: only the address field of its low
+// word changes, so one 32-bit addition does.
+__device__ __forceinline__ uint64_t desc_at(uint64_t d, uint32_t bytes) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"((uint32_t)d + (bytes >> 4)), "r"((uint32_t)(d >> 32)));
+    return r;
+}
+
 // 32 lanes x 32 columns of 32-bit TMEM words -> 32 registers per thread
 // (thread t of the warp reads lane (warp%4)*32 + t).  Waits for completion.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {

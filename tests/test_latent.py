@@ -516,3 +516,23 @@ def test_both_forms_agree(g):
     d = (o1.double() - o2).abs()
     assert d.max().item() <= 16 * unit(dt) * 4 and d.mean().item() <= 16 * unit(dt), (d.max().item(), d.mean().item())
     assert (lse1 - lse2).abs().max().item() <= 32 * unit(dt)
+
+
+def test_expanded_blocks_without_a_partner(g):
+    """Many requests of one row block each, and some without a key: items of which one
+    or both query tiles take no part, among others that do; no wait may give up."""
+    gen = torch.Generator().manual_seed(22)
+    nq = [int(x) for x in torch.randint(1, 129, (150,), generator=gen)]
+    nq[::7] = [300] * len(nq[::7])
+    lens = [n + 5 * (i % 3) for i, n in enumerate(nq)]
+    lens[3::10] = [0] * len(lens[3::10])
+    c = varlen_case(gen, nq, lens, 4, torch.bfloat16)
+    args = (c["q"], c["k"], c["v"], c["pe"], c["cq"], c["ck"])
+    o, lse = g.attn_fwd_latent_varlen(*args)
+    for _ in range(300):
+        o2, lse2 = g.attn_fwd_latent_varlen(*args)
+    torch.cuda.synchronize()
+    g.gqa_device_error()
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b, h, rows, ref in varlen_refs(c):
+        check(o[rows, h], lse[rows, h], ref, "request %d head %d" % (b, h))
