@@ -717,20 +717,27 @@ LATENT_ROW = LATENT_DIM + LATENT_ROPE
 LATENT_NOPE, LATENT_V = 128, 128                # expanded, per head: key dims beside the shared ones, value dims
 
 
-def _rows(name, t, T, H, width, dtype, device):
-    """gqa_head_rows of t [T, H, width] (t [T, width] counts as one head), read in
-    place where the kernels take its strides, else from a copy (returned to keep it
-    alive)."""
-    shape = (T, width) if H is None else (T, H, width)
+def _rows(name, t, shape, dtype, device):
+    """gqa_head_rows of t [T, H, width] (or [T, width], one head), read in place where
+    the kernels take its strides, else from a copy (returned to keep it alive).  As in
+    _data, what every good argument passes comes first."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index:
+            st, p = t.stride(), t.data_ptr()
+            ts, hs = st[0], st[1] if len(st) == 3 else 8
+            if ts and hs and st[-1] == 1 and not (ts | hs) & 7 and not p & 15:
+                return _lib.HeadRows(p, ts, hs), t
+    except AttributeError:
+        pass
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype:
         raise ValueError("%s must be a %s CUDA tensor" % (name, dtype))
     if t.shape != shape or t.device != device:
         raise ValueError("%s must have shape %s on %s, got %s on %s" % (name, shape, device, tuple(t.shape), t.device))
-    if H is None:
+    if len(shape) == 2:
         t = t.unsqueeze(1)
-    if (T > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
+    if (shape[0] > 1 and t.stride(0) == 0) or (t.shape[1] > 1 and t.stride(1) == 0):
         t = t.contiguous()                           # broadcast rows
-    return _head_rows(t, T)
+    return _head_rows(t, shape[0])
 
 
 def attn_latent_norm_rope_paged(q_pe, kv, cos_sin, positions, slots, kv_cache, kv_weight=None, eps=1e-6,
@@ -766,12 +773,12 @@ def attn_latent_norm_rope_paged(q_pe, kv, cos_sin, positions, slots, kv_cache, k
     pw = _data("kv_weight", kv_weight, f32 if wf else dt, (LATENT_DIM,), dev) if kv_weight is not None else None
     if out is None:
         out = torch.empty((T, H, R), dtype=dt, device=dev)
-    ro, ko = _rows("out", out, T, H, R, dt, dev)
-    if ko.data_ptr() != out.data_ptr():
+    ro, ko = _rows("out", out, (T, H, R), dt, dev)
+    if ko is not out and ko.data_ptr() != out.data_ptr():
         raise ValueError("out must have strides of multiples of 8 and a 16-byte aligned start, got %s" % (out.stride(),))
     po = _data("kv_out", kv_out, dt, (T, LATENT_ROW), dev) if kv_out is not None else None
-    rq, _kq = _rows("q_pe", q_pe, T, H, R, dt, dev)
-    rk, _kk = _rows("kv", kv, T, None, LATENT_ROW, dt, dev)
+    rq, _kq = _rows("q_pe", q_pe, (T, H, R), dt, dev)
+    rk, _kk = _rows("kv", kv, (T, LATENT_ROW), dt, dev)
     rope = _lib.Rope(pt, pp, max_pos, LATENT_ROPE, 1 if interleaved else 0, 1, None)
     st = _on(dev, _lib.load().attn_latent_norm_rope_paged, ctypes.byref(rq), ctypes.byref(rk), pw, 1 if wf else 0, eps,
              ctypes.byref(rope), ctypes.byref(ro), po, ps, pc, T, H, num_pages, page_size, _DTYPES[dt],
@@ -800,16 +807,20 @@ def attn_latent_gather(kv_cache, cu_seqlens_kv, block_table, total_kv, out=None)
         raise ValueError("total_kv must lie in [0, 2^30), got %d" % total)
     cu = _data("cu_seqlens_kv", cu_seqlens_kv, i32, (B + 1,), dev)
     bt = _data("block_table", block_table, i32, (B, max_pages), dev)
-    if out is None:
-        out = torch.empty((total, LATENT_ROW), dtype=kv_cache.dtype, device=dev)
-        po = out.data_ptr()
-    else:
-        po = _data("out", out, kv_cache.dtype, (total, LATENT_ROW), dev)
+    out, po = _result("out", out, (total, LATENT_ROW), kv_cache.dtype, dev)
     st = _on(dev, _lib.load().attn_latent_gather, pc, cu, bt, page_size, po, B, total, num_pages, max_pages,
              _raw_stream(dev))
     if st != 0:
         _raise(st, "attn_latent_gather")
     return out
+
+
+def _result(name, out, shape, dtype, device):
+    """`out` (checked) or a new contiguous tensor, and its address."""
+    if out is None:
+        out = torch.empty(shape, dtype=dtype, device=device)
+        return out, out.data_ptr()
+    return out, _data(name, out, dtype, shape, device)
 
 
 def _workspace(workspace, need, device):
@@ -839,21 +850,17 @@ def attn_fwd_latent_varlen(q, k, v, k_pe, cu_seqlens_q, cu_seqlens_kv, causal=Tr
     if dq != LATENT_NOPE + LATENT_ROPE:
         raise ValueError("q must be [total_q, H, %d], got %s" % (LATENT_NOPE + LATENT_ROPE, tuple(q.shape)))
     total_kv = _size("k", k, 3, 0)
-    rk, _kk = _rows("k", k, total_kv, H, LATENT_NOPE, dt, dev)
-    rv, _kv = _rows("v", v, total_kv, H, LATENT_V, dt, dev)
-    rp, _kp = _rows("k_pe", k_pe, total_kv, None, LATENT_ROPE, dt, dev)
+    rk, _kk = _rows("k", k, (total_kv, H, LATENT_NOPE), dt, dev)
+    rv, _kv = _rows("v", v, (total_kv, H, LATENT_V), dt, dev)
+    rp, _kp = _rows("k_pe", k_pe, (total_kv, LATENT_ROPE), dt, dev)
     B = _size("cu_seqlens_q", cu_seqlens_q, 1, 0) - 1
     if B < 1:
         raise ValueError("cu_seqlens_q must hold B + 1 >= 2 offsets")
     cq = _data("cu_seqlens_q", cu_seqlens_q, i32, (B + 1,), dev)
     ck = _data("cu_seqlens_kv", cu_seqlens_kv, i32, (B + 1,), dev)
     q = q.contiguous()
-    if out is None:
-        out = torch.empty((total_q, H, LATENT_V), dtype=dt, device=dev)
-    po = _data("out", out, dt, (total_q, H, LATENT_V), dev)
-    if lse is None:
-        lse = torch.empty((total_q, H), dtype=f32, device=dev)
-    pl = _data("lse", lse, f32, (total_q, H), dev)
+    out, po = _result("out", out, (total_q, H, LATENT_V), dt, dev)
+    lse, pl = _result("lse", lse, (total_q, H), f32, dev)
     lib = _lib.load()
     workspace = _workspace(workspace, lib.attn_latent_varlen_workspace_size(B, total_q, H), dev)
     st = _on(dev, lib.attn_fwd_latent_varlen, q.data_ptr(), ctypes.byref(rk), ctypes.byref(rv), ctypes.byref(rp), cq, ck,
@@ -892,12 +899,8 @@ def attn_fwd_latent_paged(q, kv_cache, cu_seqlens_q, cache_seqlens, block_table,
     sl = _data("cache_seqlens", cache_seqlens, i32, (B,), dev)
     bt = _data("block_table", block_table, i32, (B, max_pages), dev)
     q = q.contiguous()
-    if out is None:
-        out = torch.empty((total_q, H, LATENT_DIM), dtype=dt, device=dev)
-    po = _data("out", out, dt, (total_q, H, LATENT_DIM), dev)
-    if lse is None:
-        lse = torch.empty((total_q, H), dtype=f32, device=dev)
-    pl = _data("lse", lse, f32, (total_q, H), dev)
+    out, po = _result("out", out, (total_q, H, LATENT_DIM), dt, dev)
+    lse, pl = _result("lse", lse, (total_q, H), f32, dev)
     lib = _lib.load()
     if workspace is None:
         workspace = _workspace(None, _on(dev, lib.attn_latent_paged_workspace_size, B, total_q, H), dev)

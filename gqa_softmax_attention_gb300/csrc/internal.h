@@ -2,6 +2,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -253,6 +254,22 @@ struct RopeArgs {
     int e4m3, B;
 };
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, int D, bool f16, bool paged, int num_sms, cudaStream_t stream);
+
+// A kernel's shared-memory limit, raised once per device (the attribute is the
+// device context's, and setting it costs a microsecond a call).
+struct SmemLimit {
+    std::atomic<uint64_t> done{0};      // devices 0 .. 63
+    cudaError_t set(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+        if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 
 // Latent attention: a cache row is kLatentDim latent and kLatentRope shared
 // rotated values; expanded, a head has kLatentNope + kLatentRope key dims and

@@ -852,8 +852,8 @@ template <int NR, bool F16, bool GATHER>
 cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe, const LatentArgs& a,
                      cudaStream_t stream) {
     using C = LCfg<NR, GATHER>;
-    cudaError_t e = cudaFuncSetAttribute(latent_paged_kernel<NR, F16, GATHER>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    static SmemLimit limit;
+    cudaError_t e = limit.set(reinterpret_cast<const void*>(latent_paged_kernel<NR, F16, GATHER>), C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const unsigned ctas = (unsigned)(a.teams * a.team);
     latent_paged_kernel<NR, F16, GATHER><<<ctas, C::THREADS, C::SMEM_BYTES, stream>>>(tm_q, tm_kv, tm_pe, a);

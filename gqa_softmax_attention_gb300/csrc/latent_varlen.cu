@@ -492,8 +492,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 template <bool F16>
 cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_pe,
                      const PrefillArgs& a, long max_items, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(latent_varlen_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               SMEM_BYTES);
+    static SmemLimit limit;
+    const cudaError_t e = limit.set(reinterpret_cast<const void*>(latent_varlen_kernel<F16>), SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const long sms = a.num_sms > 0 ? a.num_sms : 148;
     const long grid = max_items < sms ? max_items : sms;    // persistent: one CTA per SM
