@@ -1229,21 +1229,22 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     a.causal = causal ? 1 : 0;
     a.f16 = dtype == GQA_FP16 ? 1 : 0;
     a.team = parts.team; a.teams = parts.teams;
-    a.min_tiles = 4;
+    a.min_tiles = 2;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     page_divisor(page_size, &a.ps_mul, &a.ps_shift);
-    CUtensorMap tq, tkv, tpe;
+    CUtensorMap tq, tkv, tpe, trow;
     a.nr = page_size % 8 == 0 ? parts.nr : gqa::kLatentRows;
     if (!make_latent_q_map(&tq, q, rows, a.nr, a.f16)) return GQA_ERR_CUDA;
-    tkv = tpe = tq;                     // gathered rows: the maps go unused
+    tkv = tpe = trow = tq;              // gathered rows: the maps go unused
     if (page_size % 8 == 0) {
         // pages move as 8-row TMA blocks
         a.box_tokens = gcd_int(page_size, 64);
-        if (!make_latent_map(&tkv, kv_cache, slots, 2, a.box_tokens, a.f16) ||
-            !make_latent_map(&tpe, kv_cache, slots, 1, a.box_tokens, a.f16))
+        if (!make_latent_map(&tkv, kv_cache, slots, 4, a.box_tokens, a.f16) ||
+            !make_latent_map(&tpe, kv_cache, slots, 1, a.box_tokens, a.f16) ||
+            !make_latent_map(&trow, kv_cache, slots, gqa::kLatentRow / 64, a.box_tokens, a.f16))
             return GQA_ERR_CUDA;
     }
-    return gqa::launch_latent_paged(tq, tkv, tpe, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return gqa::launch_latent_paged(tq, tkv, tpe, trow, a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GQA_OK
                : GQA_ERR_CUDA;
 }

@@ -327,9 +327,10 @@ struct LatentArgs {
     uint32_t ps_mul, ps_shift;      // n / page_size as in PrefillArgs
 };
 // tm_q: [total_q * H, 576] as {64, rows, 9} with a {64, nr, 9} box;
-// tm_kv / tm_pe: the cache as {64, 8, 9, rows / 8} with {64, 8, 2 / 1, box_tokens / 8} boxes.
+// tm_kv / tm_pe / tm_row: the cache as {64, 8, 9, rows / 8} with {64, 8, 4 / 1 / 9,
+// box_tokens / 8} boxes.
 cudaError_t launch_latent_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
-                                const LatentArgs& a, cudaStream_t stream);
+                                const CUtensorMap& tm_row, const LatentArgs& a, cudaStream_t stream);
 int latent_paged_take_device_error();
 
 // Packed queries over expanded keys and values (latent_varlen.cu; see

@@ -25,9 +25,10 @@
 // a step at 64 rows, 24 and 40 at 16; measured), 2000 or 1500 cycles a tile where
 // HBM brings one every 3200.
 //
-// Shared memory holds Q (72 KB at 64 rows) and two to nearly three tiles of 72 KB: a
-// ring of slots of 128 dims, four a tile, and one of the 64 shared dims.  P^T is
-// written over the shared dims, which only S^T needs.  With one tile of 128 keys at a
+// Shared memory holds Q (72 KB at 64 rows) and two to two and a half tiles of 72 KB: a
+// ring of slots of 256 dims, two a tile, and one of the 64 shared dims.  P^T is
+// written over the shared dims, which only S^T needs.  (Slots of 128 dims took the
+// producer five hand-overs of 400 cycles a tile, 700 with pages of 16.)  With one tile of 128 keys at a
 // time the loads of a tile could not run while the tile before was worked on, and
 // all CTAs loaded and all computed at the same time (64 requests of 1K to 16K
 // keys, 16 heads: 188 us).
@@ -49,6 +50,7 @@
 #include <cuda_fp16.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "internal.h"
 #include "ptx.cuh"
@@ -64,6 +66,7 @@ constexpr int DR = kLatentRope;            // 64: shared rotated dims
 constexpr int DK = DC + DR;
 constexpr int ROW_BYTES = DK * 2;
 constexpr int NJ = DC / 128;               // 128-dim blocks of O^T (pairs of 64-dim slices)
+constexpr int NU = 2;                      // slots of latents a tile takes: 256 dims, 4 slices, 2 blocks each
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kRescaleThreshold = 8.f;
 constexpr int WARP_S = 4, WARP_O = 5;      // MMA issuers of S^T and of O^T
@@ -72,19 +75,18 @@ constexpr int kSmBar = 1;                  // named barrier of the softmax warps
 
 template <int NR, bool GATHER>
 struct LCfg {
-    static constexpr int NP = NR == 64 ? 8 : (NR == 32 ? 10 : 11); // slots of 128 dims, NJ a tile
+    static constexpr int NP = NR == 64 ? 4 : 5;                    // slots of 256 dims, NU a tile
     static constexpr int NT = NR == 64 ? 2 : 3;                    // slots of the shared dims, one a tile
-    static constexpr int PAIR = BN * 256;                          // [8 groups][2 slices][8 keys][128 bytes]
+    static constexpr int HALF = BN * 512;                          // [8 groups][4 slices][8 keys][128 bytes]
     static constexpr int ROPE = BN * 128;                          // shared dims, later P^T: [64 keys][128 bytes]
     static constexpr int Q_SLICE = NR * 128;                       // 64 dims of Q
     static constexpr int OFF_Q = 0;
     static constexpr int OFF_P = OFF_Q + (DK / 64) * Q_SLICE;
     static constexpr int OFF_KV = OFF_P + NT * ROPE;
-    static constexpr int OFF_COL = OFF_KV + NP * PAIR;             // per row: -reference, factor, limit, reference, [4] per warp
+    static constexpr int OFF_COL = OFF_KV + NP * HALF;             // per row: -reference, factor, limit, reference, [4] per warp
     static constexpr int OFF_BAR = OFF_COL + 8 * NR * 4;
-    // kv_full[NP], kv_empty[NP], pe_full[NT], pe_empty[NT], q_full, q_empty,
-    // drain[2], s_full[2], p_full[2]
-    static constexpr int NBAR = 2 * NP + 2 * NT + 8;
+    // kv_full[NP], kv_empty[NP], q_full, q_empty, drain[2], s_full[2], p_full[2]
+    static constexpr int NBAR = 2 * NP + 8;
     static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 64 + 1024;
     static constexpr int LOAD_WARPS = GATHER ? 2 : 1;
@@ -92,7 +94,9 @@ struct LCfg {
     static constexpr uint32_t COL_S = NJ * NR;                     // TMEM: O^T blocks | S^T of even, of odd tiles
     static constexpr uint32_t TMEM_COLS = 512;
     static_assert(COL_S + 2 * NR <= TMEM_COLS, "TMEM budget");
-    static_assert(NP >= 2 * NJ, "two tiles");
+    // The shared dims' slot of a tile is free when its second slot of latents is: that one
+    // was last used by a tile that came after the shared dims' last one, or with it.
+    static_assert((NP == 4 && NT == 2) || (NP == 5 && NT == 3), "slots that come free together");
     static_assert(OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
@@ -225,7 +229,7 @@ __device__ __forceinline__ int page_of(const LatentArgs& a, uint32_t n) {
 template <int NR, bool F16, bool GATHER>
 __global__ void __launch_bounds__((LCfg<NR, GATHER>::THREADS), 1)
 latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_kv,
-                    const __grid_constant__ CUtensorMap tm_pe, const LatentArgs a) {
+                    const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ CUtensorMap tm_row, const LatentArgs a) {
     using C = LCfg<NR, GATHER>;
     constexpr uint32_t IDESC_S = make_idesc_16<F16>(BN, NR, false, false);
     constexpr uint32_t IDESC_O = make_idesc_16<F16>(128, NR, true, true);
@@ -244,17 +248,21 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const uint32_t bar0 = sb + C::OFF_BAR;
     auto kv_full = [&](int i) { return bar0 + 8u * i; };
     auto kv_empty = [&](int i) { return bar0 + 8u * (C::NP + i); };
-    auto pe_full = [&](int i) { return bar0 + 8u * (2 * C::NP + i); };
-    auto pe_empty = [&](int i) { return bar0 + 8u * (2 * C::NP + C::NT + i); };
-    const uint32_t bar1 = bar0 + 8u * (2 * C::NP + 2 * C::NT);
+    const uint32_t bar1 = bar0 + 8u * (2 * C::NP);
     const uint32_t q_full = bar1, q_empty = bar1 + 8;
     auto drain = [&](int i) { return bar1 + 16 + 8u * i; };
     auto s_full = [&](int i) { return bar1 + 32 + 8u * i; };
     auto p_full = [&](int i) { return bar1 + 48 + 8u * i; };
-    // Tile it's slots: dims 128 j .. are use u / NP of slot u % NP with u = NJ it + j, its
-    // shared dims and P^T use it / NT of slot it % NT; a fill's parity is that use's.
-    auto pair_addr = [&](int i) { return sb + C::OFF_KV + (uint32_t)i * C::PAIR; };
+    // Tile it's latents are units u = NU it, NU it + 1 of the ring: use u / NP of slot
+    // u % NP; its shared dims, and P^T later, lie in slot it % NT and are loaded with the
+    // second unit.  A fill's parity is its use's.
+    auto slot_addr = [&](int i) { return sb + C::OFF_KV + (uint32_t)i * C::HALF; };
     auto rope_addr = [&](int i) { return sb + C::OFF_P + (uint32_t)i * C::ROPE; };
+    // Whether O^T holds tile it: its second unit's slot has been released.
+    auto tile_done = [&](int it, volatile int* abort) {
+        const uint32_t u = (uint32_t)(NU * it + 1);
+        return mbar_wait(kv_empty((int)(u % C::NP)), u / C::NP & 1, abort);
+    };
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::OFF_MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 4);
     LRange* range = reinterpret_cast<LRange*>(smem + C::OFF_MISC + 16);
@@ -262,7 +270,6 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (threadIdx.x == 0) {
         const int fills = GATHER ? 32 * C::LOAD_WARPS : 1;
         for (int i = 0; i < C::NP; ++i) { mbar_init(kv_full(i), fills); mbar_init(kv_empty(i), 1); }
-        for (int i = 0; i < C::NT; ++i) { mbar_init(pe_full(i), fills); mbar_init(pe_empty(i), 1); }
         for (int i = 0; i < 2; ++i) { mbar_init(s_full(i), 1); mbar_init(p_full(i), 128); mbar_init(drain(i), 1); }
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -331,93 +338,124 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp >= WARP_LOAD) {
         // ------------------------------------------------------------ producer
         const int pw = warp - WARP_LOAD;
-        int it = 0, nq = 0;                      // tiles and Q blocks loaded
-        int ps = 0, ts = 0;                      // next slots, and the parities of their uses
-        uint32_t pp = 0, tp = 0;
+        int nq = 0;                              // Q blocks loaded
+        int ps = 0, ts = 0;                      // next slots, and the parity of the use of ps
+        uint32_t pp = 0, units = 0;
         bool ok = true;
-        if (lane == 0) {
-            tma_prefetch_desc(&tm_q);
-            if (!GATHER) {
-                tma_prefetch_desc(&tm_kv);
-                tma_prefetch_desc(&tm_pe);
-            }
-        }
         Piece p;
         p.first(a, rg, group, NR, rank);
-        // Page id that holds token t of the piece's request, as the table has it
-        // (-1 past the request's end).
-        auto page_at = [&](const Piece& c, int t) {
-            const int lp = page_of(a, (uint32_t)t);
-            return t < c.L ? ldg_int(a.table + (size_t)c.b * a.max_pages + lp) : -1;
+        auto step = [&](int u) {                 // past unit u of a tile
+            ++units;
+            if (++ps == C::NP) { ps = 0; pp ^= 1; }
+            if (u == NU - 1 && ++ts == C::NT) ts = 0;
         };
-        auto step = [&](int j) {                 // past slot j of a tile (j = NJ: the shared dims)
-            if (j < NJ) {
-                if (++ps == C::NP) { ps = 0; pp ^= 1; }
-            } else if (++ts == C::NT) {
-                ts = 0;
-                tp ^= 1;
-            }
+        // The piece's Q rows, once the last S^T of the piece before is done (one lane).
+        auto load_q = [&]() {
+            if (!mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag)) return false;
+            mbar_arrive_expect_tx(q_full, (DK / 64) * C::Q_SLICE);
+            tma_load_3d(sb + C::OFF_Q, &tm_q, q_full, 0, p.qs * a.H + p.row0, 0);
+            return true;
         };
-        for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
-            if (p.n == 0) continue;
-            if (pw == 0) {
-                // the piece's Q rows, once the last S^T of the piece before is done
-                if (lane == 0) {
-                    ok = mbar_wait(q_empty, (nq & 1) ^ 1, abort_flag);
-                    if (ok) {
-                        mbar_arrive_expect_tx(q_full, (DK / 64) * C::Q_SLICE);
-                        tma_load_3d(sb + C::OFF_Q, &tm_q, q_full, 0, p.qs * a.H + p.row0, 0);
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) break;
-                ++nq;
-            }
-            if constexpr (!GATHER) {
-                // Lane i loads page block i of the tile: 8-row groups of the cache as
-                // one box of 128 dims each; a block past the request's end or of a
-                // page outside the pool lies outside the map and comes as zeros.
-                const int bt = a.box_tokens, nbox = BN / bt;
+        if constexpr (!GATHER) {
+            // Page blocks of a tile: 8-row groups of the cache as one box of 256 dims a
+            // unit, and one of the shared dims; a block past the request's end or of a
+            // page outside the pool lies outside the map and comes as zeros.  One elected
+            // lane does it all: as a whole warp, which meets at every wait, it fell into a
+            // slow state at some row groups' starts (800 cycles a copy for 200).
+            // NB: blocks of a tile, or the most there can be.
+            auto run = [&](auto blocks) {
+                constexpr int NB = decltype(blocks)::value;
+                const int bt = a.box_tokens, nbox = NB == 1 ? 1 : BN / bt;
                 const int outside = a.num_pages * (a.page_size / 8);
-                auto token = [&](int k) { return (p.lt0 + k) * BN + lane * bt; };
-                int page = lane < nbox ? page_at(p, token(0)) : -1;
-                for (int k = 0; k < p.n && ok; ++k, ++it) {
-                    const int t = token(k);
-                    const int in_page = t - page_of(a, (uint32_t)t) * a.page_size;
-                    const int grp = page >= 0 && page < a.num_pages
-                                        ? (int)(((long)page * a.page_size + in_page) >> 3)
-                                        : outside;
-                    if (k + 1 < p.n) page = lane < nbox ? page_at(p, token(k + 1)) : -1;
-                    for (int j = 0; j <= NJ; ++j) {
-                        const uint32_t full = j < NJ ? kv_full(ps) : pe_full(ts);
-                        ok = __all_sync(0xffffffffu, j < NJ ? mbar_wait(kv_empty(ps), pp ^ 1, abort_flag)
-                                                            : mbar_wait(pe_empty(ts), tp ^ 1, abort_flag));
-                        if (!ok) break;
-                        if (nbox == 1) {
-                            const int g0 = __shfl_sync(0xffffffffu, grp, 0);
-                            if (elect_one()) {
-                                mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
-                                if (j < NJ) tma_load_4d(pair_addr(ps), &tm_kv, full, 0, 0, 2 * j, g0);
-                                else tma_load_4d(rope_addr(ts), &tm_pe, full, 0, 0, 2 * NJ, g0);
-                            }
-                            __syncwarp();
-                        } else {
-                            if (lane == 0) mbar_arrive_expect_tx(full, j < NJ ? C::PAIR : C::ROPE);
-                            __syncwarp();        // the expect-tx precedes every lane's copy
-                            if (lane < nbox) {
-                                if (j < NJ)
-                                    tma_load_4d(pair_addr(ps) + lane * bt * 256, &tm_kv, full, 0, 0, 2 * j, grp);
-                                else
-                                    tma_load_4d(rope_addr(ts) + lane * bt * 128, &tm_pe, full, 0, 0, 2 * NJ, grp);
-                            }
+                for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+                    if (p.n == 0) continue;
+                    const int32_t* table = a.table + (size_t)p.b * a.max_pages;
+                    // page ids of tile k's blocks as the table has them (-1 past the request's end)
+                    auto pages = [&](int k, int (&pg)[NB]) {
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int t = (p.lt0 + k) * BN + i * bt;
+                            pg[i] = -1;
+                            if (k < p.n && i < nbox && t < p.L) pg[i] = ldg_int(table + page_of(a, (uint32_t)t));
                         }
-                        step(j);
+                    };
+                    auto groups = [&](int k, const int (&pg)[NB], int (&gr)[NB]) {
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int t = (p.lt0 + k) * BN + i * bt;
+                            const int in_page = t - page_of(a, (uint32_t)t) * a.page_size;
+                            gr[i] = pg[i] >= 0 && pg[i] < a.num_pages ? (int)(((long)pg[i] * a.page_size + in_page) >> 3)
+                                                                      : outside;
+                        }
+                    };
+                    // tiles k, k + 1, k + 2; a tile is brought to L2 two tiles before its slots come free
+                    int g0[NB], g1[NB], g2[NB], pg[NB];
+                    pages(0, pg);
+                    pages(1, g1);
+                    pages(2, g2);
+                    if (!(ok = load_q())) break;
+                    ++nq;
+                    groups(0, pg, g0);
+                    groups(1, g1, g1);
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) pg[i] = g2[i];
+                    for (int k = 0; k < p.n && ok; ++k) {
+                        groups(k + 2, pg, g2);
+                        pages(k + 3, pg);
+                        if (rank == 0) {
+#pragma unroll
+                            for (int i = 0; i < NB; ++i)
+                                if (i < nbox && g2[i] != outside) tma_prefetch_4d(&tm_row, 0, 0, 0, g2[i]);
+                        }
+#pragma unroll
+                        for (int u = 0; u < NU; ++u) {
+                            if (!(ok = mbar_wait(kv_empty(ps), pp ^ 1, abort_flag))) break;
+                            const uint32_t full = kv_full(ps), dst = slot_addr(ps), dst_pe = rope_addr(ts);
+                            mbar_arrive_expect_tx(full, C::HALF + (u == NU - 1 ? C::ROPE : 0));
+#pragma unroll
+                            for (int i = 0; i < NB; ++i) {
+                                if (i < nbox) {
+                                    tma_load_4d(dst + i * bt * 512, &tm_kv, full, 0, 0, 4 * u, g0[i]);
+                                    if (u == NU - 1) tma_load_4d(dst_pe + i * bt * 128, &tm_pe, full, 0, 0, 4 * NU, g0[i]);
+                                }
+                            }
+                            step(u);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            g0[i] = g1[i];
+                            g1[i] = g2[i];
+                        }
                     }
                 }
-            } else {
-                // Rows one by one: a warp copies 32 of them, eight lanes a row's 128
-                // bytes; a slot is announced once the copies of the next one are under
-                // way, or at once where the next slot is not free yet.
+                if (*abort_flag) {
+                    // let the copies in flight land: the last fill of each slot
+                    for (uint32_t u = units < C::NP ? 0 : units - C::NP; u != units; ++u)
+                        mbar_drain(kv_full((int)(u % C::NP)), u / C::NP & 1);
+                    if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
+                }
+            };
+            if (elect_one()) {
+                tma_prefetch_desc(&tm_q);
+                tma_prefetch_desc(&tm_kv);
+                tma_prefetch_desc(&tm_pe);
+                tma_prefetch_desc(&tm_row);
+                if (a.box_tokens == BN) run(std::integral_constant<int, 1>{});
+                else run(std::integral_constant<int, BN / 8>{});
+            }
+            __syncwarp();
+        } else {
+            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+                if (p.n == 0) continue;
+                if (pw == 0) {
+                    if (lane == 0) ok = load_q();
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                    ++nq;
+                }
+                // Rows one by one: a warp copies 32 of them, 512 bytes at a time; a slot is
+                // announced once the copies of the next one are under way, or at once where
+                // the next slot is not free yet.
                 uint32_t pending = 0;
                 auto announce = [&]() {
                     if (pending) {
@@ -428,101 +466,96 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 };
                 auto row_of = [&](int k) {       // cache row of this lane's key of tile k, -1 for zeros
                     const int t = (p.lt0 + k) * BN + pw * 32 + lane;
-                    const int page = page_at(p, t);
-                    return page >= 0 && page < a.num_pages
-                               ? page * a.page_size + (t - page_of(a, (uint32_t)t) * a.page_size)
-                               : -1;
+                    const int lp = page_of(a, (uint32_t)t);
+                    const int page = t < p.L ? ldg_int(a.table + (size_t)p.b * a.max_pages + lp) : -1;
+                    return page >= 0 && page < a.num_pages ? page * a.page_size + (t - lp * a.page_size) : -1;
                 };
                 int row = row_of(0);
-                for (int k = 0; k < p.n && ok; ++k, ++it) {
+                for (int k = 0; k < p.n && ok; ++k) {
                     const int now = row;
                     if (k + 1 < p.n) row = row_of(k + 1);
-                    for (int j = 0; j <= NJ; ++j) {
-                        const uint32_t empty = j < NJ ? kv_empty(ps) : pe_empty(ts), parity = (j < NJ ? pp : tp) ^ 1;
-                        if (!__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) {
+#pragma unroll
+                    for (int u = 0; u < NU; ++u) {
+                        if (!__all_sync(0xffffffffu, mbar_test_wait(kv_empty(ps), pp ^ 1))) {
                             cp_async_wait<0>();
                             announce();
-                            ok = __all_sync(0xffffffffu, mbar_wait(empty, parity, abort_flag));
+                            ok = __all_sync(0xffffffffu, mbar_wait(kv_empty(ps), pp ^ 1, abort_flag));
                             if (!ok) break;
                         }
-                        const uint32_t dst = j < NJ ? pair_addr(ps) : rope_addr(ts);
-                        const int stride = j < NJ ? 2048 : 1024, slices = j < NJ ? 2 : 1;
+                        const uint32_t dst = slot_addr(ps), dst_pe = rope_addr(ts);
 #pragma unroll 4
-                        for (int e = 0; e < 8; ++e) {
-                            const int key = pw * 32 + 4 * e + lane / 8, c = lane % 8;
-                            const int r = __shfl_sync(0xffffffffu, now, 4 * e + lane / 8);
-                            const char* src = static_cast<const char*>(a.cache) + (size_t)max(r, 0) * ROW_BYTES +
-                                              j * 256 + c * 16;
-                            for (int x = 0; x < slices; ++x)
-                                cp_async16(dst + (key >> 3) * stride + x * 1024 + (key & 7) * 128 + ((c ^ (key & 7)) << 4),
-                                           src + x * 128, r >= 0 ? 16 : 0);
+                        for (int e = 0; e < 32; ++e) {
+                            const int r = __shfl_sync(0xffffffffu, now, e), key = pw * 32 + e;
+                            const char* src = static_cast<const char*>(a.cache) + (size_t)max(r, 0) * ROW_BYTES + u * 512 +
+                                              lane * 16;
+                            cp_async16(dst + (key >> 3) * 4096 + (lane / 8) * 1024 + (key & 7) * 128 +
+                                           (((lane % 8) ^ (key & 7)) << 4), src, r >= 0 ? 16 : 0);
+                        }
+                        if (u == NU - 1) {
+#pragma unroll 4
+                            for (int e = 0; e < 8; ++e) {
+                                const int r = __shfl_sync(0xffffffffu, now, 4 * e + lane / 8), key = pw * 32 + 4 * e + lane / 8;
+                                const char* src = static_cast<const char*>(a.cache) + (size_t)max(r, 0) * ROW_BYTES +
+                                                  NU * 512 + (lane % 8) * 16;
+                                cp_async16(dst_pe + key * 128 + (((lane % 8) ^ (key & 7)) << 4), src, r >= 0 ? 16 : 0);
+                            }
                         }
                         cp_async_commit();
                         if (pending) {
                             cp_async_wait<1>();
                             announce();
                         }
-                        pending = j < NJ ? kv_full(ps) : pe_full(ts);
-                        step(j);
+                        pending = kv_full(ps);
+                        step(u);
                     }
                 }
                 cp_async_wait<0>();
                 announce();
             }
-        }
-        if (*abort_flag && pw == 0 && lane == 0) {
-            // let the copies in flight land: the last fill of each slot
-            if (!GATHER) {
-                for (int i = 0; i < C::NP; ++i)
-                    if (it > 0 || i < ps) mbar_drain(kv_full(i), i < ps ? pp : pp ^ 1);
-                for (int i = 0; i < C::NT; ++i)
-                    if (it > 0 || i < ts) mbar_drain(pe_full(i), i < ts ? tp : tp ^ 1);
-            }
-            if (nq > 0) mbar_drain(q_full, (nq - 1) & 1);
+            if (*abort_flag && pw == 0 && lane == 0 && nq > 0) mbar_drain(q_full, (nq - 1) & 1);
         }
     } else if (warp == WARP_S) {
         // ------------------------------------------------------------ S^T issuer (one elected lane)
         if (elect_one()) {
             Piece p;
             p.first(a, rg, group, NR, rank);
-            int it = 0, nq = 0, ps = 0, ts = 0;  // tile, Q blocks taken, slots and the parities of their uses
-            uint32_t pp = 0, tp = 0;
+            int it = 0, nq = 0, ps = 0, ts = 0;  // tile, Q blocks taken, slots and the parity of the use of ps
+            uint32_t pp = 0;
             bool ok = true;
             const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
-            // K-major A: 8-key groups 2 KB apart (1 KB in the shared dims' slot)
-            const uint64_t kdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 16, 2048), edesc0 = make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
+            // K-major A: 8-key groups 4 KB apart (1 KB in the shared dims' slot)
+            const uint64_t kdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 16, 4096), edesc0 = make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
             for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
                 for (int k = 0; k < p.n && ok; ++k, ++it) {
                     if (k == 0) ok = mbar_wait(q_full, nq & 1, abort_flag);
                     // at most one tile ahead of O^T, so that no barrier runs two phases ahead
                     // of who waits on it: the tile before the last is done, and its S^T read
-                    if (ok && it > 1) ok = mbar_wait(pe_empty((it - 2) % C::NT), ((it - 2) / C::NT) & 1, abort_flag);
+                    if (ok && it > 1) ok = tile_done(it - 2, abort_flag);
                     const uint32_t d = tmem + C::COL_S + (it & 1) * NR;
                     tc_fence_after();
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
+                    for (int u = 0; u < NU; ++u) {
                         if (ok) ok = mbar_wait(kv_full(ps), pp, abort_flag);
                         if (!ok) break;
-                        const uint64_t kdesc = desc_at(kdesc0, ps * C::PAIR);
+                        const uint64_t kdesc = desc_at(kdesc0, ps * C::HALF);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
+                        for (int kk = 0; kk < 16; ++kk)
                             mma_bf16_ss(d, desc_at(kdesc, (kk / 4) * 1024 + (kk % 4) * 32),
-                                        desc_at(qdesc, (2 * j + kk / 4) * C::Q_SLICE + (kk % 4) * 32), IDESC_S,
-                                        (j > 0 || kk > 0) ? 1u : 0u);
+                                        desc_at(qdesc, (4 * u + kk / 4) * C::Q_SLICE + (kk % 4) * 32), IDESC_S,
+                                        (u > 0 || kk > 0) ? 1u : 0u);
                         if (++ps == C::NP) { ps = 0; pp ^= 1; }
                     }
-                    if (ok) ok = mbar_wait(pe_full(ts), tp, abort_flag);
                     if (!ok) break;
                     const uint64_t edesc = desc_at(edesc0, ts * C::ROPE);
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_bf16_ss(d, desc_at(edesc, kk * 32), desc_at(qdesc, 2 * NJ * C::Q_SLICE + kk * 32), IDESC_S, 1u);
+                        mma_bf16_ss(d, desc_at(edesc, kk * 32), desc_at(qdesc, 4 * NU * C::Q_SLICE + kk * 32), IDESC_S, 1u);
                     mma_commit(s_full(it & 1));
                     if (k == p.n - 1) {
                         mma_commit(q_empty);
                         ++nq;
                     }
-                    if (++ts == C::NT) { ts = 0; tp ^= 1; }
+                    if (++ts == C::NT) ts = 0;
                 }
             }
             mma_commit(drain(0));                // every MMA issued above has completed once this arrives
@@ -536,8 +569,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             p.first(a, rg, group, NR, rank);
             int it = 0, ps = 0, ts = 0;
             bool ok = true;
-            // dims-major A: 64-dim slices 1 KB apart, 8-key groups 2 KB apart
-            const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 2048), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
+            // dims-major A: 64-dim slices 1 KB apart, 8-key groups 4 KB apart
+            const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 4096), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
             for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
                 for (int k = 0; k < p.n; ++k, ++it) {
                     ok = mbar_wait(p_full(it & 1), (it >> 1) & 1, abort_flag);
@@ -545,16 +578,18 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     tc_fence_after();
                     const uint64_t pdesc = desc_at(pdesc0, ts * C::ROPE);
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const uint64_t vdesc = desc_at(vdesc0, ps * C::PAIR);
+                    for (int u = 0; u < NU; ++u) {
+                        const uint64_t vdesc = desc_at(vdesc0, ps * C::HALF);
 #pragma unroll
-                        for (int kk = 0; kk < BN / 16; ++kk)
-                            mma_bf16_ss(tmem + j * NR, desc_at(vdesc, kk * 4096), desc_at(pdesc, kk * 2048), IDESC_O,
-                                        (k > 0 || kk > 0) ? 1u : 0u);
+                        for (int j = 0; j < NJ / NU; ++j) {
+#pragma unroll
+                            for (int kk = 0; kk < BN / 16; ++kk)
+                                mma_bf16_ss(tmem + (u * (NJ / NU) + j) * NR, desc_at(vdesc, j * 2048 + kk * 8192),
+                                            desc_at(pdesc, kk * 2048), IDESC_O, (k > 0 || kk > 0) ? 1u : 0u);
+                        }
                         mma_commit(kv_empty(ps));
                         if (++ps == C::NP) ps = 0;
                     }
-                    mma_commit(pe_empty(ts));    // the tile's O^T is complete as well
                     if (++ts == C::NT) ts = 0;
                 }
             }
@@ -661,7 +696,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     load();
                     if (k > 0 && ok) {
                         // O^T has to hold the tile before
-                        if (ok) ok = __all_sync(0xffffffffu, mbar_wait(pe_empty((it - 1) % C::NT), ((it - 1) / C::NT) & 1, abort_flag));
+                        if (ok) ok = __all_sync(0xffffffffu, tile_done(it - 1, abort_flag));
                         tc_fence_after();
 #pragma unroll
                         for (int c = 0; c < HC; ++c) sums[c] *= factor[c0 + c];
@@ -692,12 +727,12 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     if (ok) st_shared_v4(prow + ((((c0 + c) / 8) ^ (key & 7)) << 4), w[0], w[1], w[2], w[3]);
                 }
                 if (++tv == C::NT) tv = 0;
-                for (int j = 0; j < NJ; ++j) {
+                for (int u = 0; u < NU; ++u) {
                     if (t >= p.L && ok) {
                         // a row past the request's end: whatever the page holds there must not
-                        // reach O^T (a slice for each of the key's two threads)
-                        const uint32_t v = pair_addr(sv) + (key >> 3) * 2048 + (lane / 16) * 1024 + (key & 7) * 128;
-                        for (int c = 0; c < 128; c += 16) st_shared_v4(v + c, 0u, 0u, 0u, 0u);
+                        // reach O^T (two slices for each of the key's two threads)
+                        const uint32_t v = slot_addr(sv) + (key >> 3) * 4096 + (lane / 16) * 2048 + (key & 7) * 128;
+                        for (int c = 0; c < 256; c += 16) st_shared_v4(v + (c >> 7) * 1024 + (c & 127), 0u, 0u, 0u, 0u);
                     }
                     if (++sv == C::NP) sv = 0;
                 }
@@ -708,7 +743,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             // ---- the piece's end
             __syncwarp();
             if (ok && p.n > 0) {
-                ok = __all_sync(0xffffffffu, mbar_wait(pe_empty((it - 1) % C::NT), ((it - 1) / C::NT) & 1, abort_flag));
+                ok = __all_sync(0xffffffffu, tile_done(it - 1, abort_flag));
                 tc_fence_after();
             }
             half_warp_columns<HC, false>(sums, lane);
@@ -807,7 +842,7 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
     if (n <= 0 || r0 >= j.z) return;
     __shared__ float4 m_s[256], l_s[256];          // n <= teams <= 256
     __shared__ float inv[4];
-    const int d = threadIdx.x;
+    const int d = threadIdx.x, lane = d % 32;
     auto slot = [&](int p) { return 2 * ((team + p) * a.team + rank) + (p == 0 ? j.w : 0); };
     for (int p = d; p < n; p += 512) {
         const float2* ml = a.part_ml + (size_t)slot(p) * NR + 4 * c4;
@@ -815,18 +850,25 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
         l_s[p] = make_float4(ml[0].y, ml[1].y, ml[2].y, ml[3].y);
     }
     __syncthreads();
-    if (d < 4) {
-        float* m = reinterpret_cast<float*>(m_s) + d;
-        const float* l = reinterpret_cast<const float*>(l_s) + d;
+    if (d < 4 * 32) {                              // a warp per row
+        float* m = reinterpret_cast<float*>(m_s) + d / 32;
+        const float* l = reinterpret_cast<const float*>(l_s) + d / 32;
         float M = -INFINITY, L = 0.f;
-        for (int p = 0; p < n; ++p) M = fmaxf(M, m[4 * p]);
-        for (int p = 0; p < n; ++p) {
+        for (int p = lane; p < n; p += 32) M = fmaxf(M, m[4 * p]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int p = lane; p < n; p += 32) {
             const float w = l[4 * p] == 0.f ? 0.f : fast_exp2(m[4 * p] - M);
             m[4 * p] = w;
             L += w * l[4 * p];
         }
-        inv[d] = L != 0.f ? 1.f / L : 0.f;
-        if (r0 + d < j.z && a.lse) a.lse[(size_t)j.y + r0 + d] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) {
+            const int e = d / 32;
+            inv[e] = L != 0.f ? 1.f / L : 0.f;
+            if (r0 + e < j.z && a.lse) a.lse[(size_t)j.y + r0 + e] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+        }
     }
     __syncthreads();
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -849,14 +891,14 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
 }
 
 template <int NR, bool F16, bool GATHER>
-cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe, const LatentArgs& a,
-                     cudaStream_t stream) {
+cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
+                     const CUtensorMap& tm_row, const LatentArgs& a, cudaStream_t stream) {
     using C = LCfg<NR, GATHER>;
     static SmemLimit limit;
     cudaError_t e = limit.set(reinterpret_cast<const void*>(latent_paged_kernel<NR, F16, GATHER>), C::SMEM_BYTES);
     if (e != cudaSuccess) return e;
     const unsigned ctas = (unsigned)(a.teams * a.team);
-    latent_paged_kernel<NR, F16, GATHER><<<ctas, C::THREADS, C::SMEM_BYTES, stream>>>(tm_q, tm_kv, tm_pe, a);
+    latent_paged_kernel<NR, F16, GATHER><<<ctas, C::THREADS, C::SMEM_BYTES, stream>>>(tm_q, tm_kv, tm_pe, tm_row, a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -874,17 +916,17 @@ cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CU
 }  // namespace
 
 cudaError_t launch_latent_paged(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CUtensorMap& tm_pe,
-                                const LatentArgs& a, cudaStream_t stream) {
+                                const CUtensorMap& tm_row, const LatentArgs& a, cudaStream_t stream) {
     const bool gather = a.box_tokens == 0;
     switch ((gather ? 64 : a.nr) * 4 + (a.f16 ? 2 : 0) + (gather ? 1 : 0)) {
-        case 16 * 4: return launch_t<16, false, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 16 * 4 + 2: return launch_t<16, true, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 32 * 4: return launch_t<32, false, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 32 * 4 + 2: return launch_t<32, true, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 64 * 4: return launch_t<64, false, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 64 * 4 + 2: return launch_t<64, true, false>(tm_q, tm_kv, tm_pe, a, stream);
-        case 64 * 4 + 1: return launch_t<64, false, true>(tm_q, tm_kv, tm_pe, a, stream);
-        case 64 * 4 + 3: return launch_t<64, true, true>(tm_q, tm_kv, tm_pe, a, stream);
+        case 16 * 4: return launch_t<16, false, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 16 * 4 + 2: return launch_t<16, true, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 32 * 4: return launch_t<32, false, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 32 * 4 + 2: return launch_t<32, true, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 64 * 4: return launch_t<64, false, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 64 * 4 + 2: return launch_t<64, true, false>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 64 * 4 + 1: return launch_t<64, false, true>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
+        case 64 * 4 + 3: return launch_t<64, true, true>(tm_q, tm_kv, tm_pe, tm_row, a, stream);
         default: return cudaErrorInvalidValue;
     }
 }
