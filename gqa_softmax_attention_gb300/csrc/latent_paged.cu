@@ -104,7 +104,7 @@ struct LCfg {
 // Where this team's range of the tile sequence starts.
 struct LRange {
     long g0, n, per;        // first tile, tiles, tiles per team
-    int b, seg, lt, pad;    // request, row group and tile of the first one
+    int b, seg, off, pad;   // request and row group of the first one, and its place in that
 };
 
 __device__ __forceinline__ int request_len(const LatentArgs& a, int b) {
@@ -115,12 +115,19 @@ __device__ __forceinline__ void request_rows(const LatentArgs& a, int b, int& qs
     sq = min(max(a.cu_q[b + 1], qs), a.total_q) - qs;
 }
 
+// A row group counts kStartTiles tiles more than it has: a piece's start and end cost a
+// team about as much, and a range of many short row groups would take longer than
+// one of a single long one (64 requests of 1K to 16K keys, 128 heads: ranges of four
+// pieces ended 24 us after those of one, of 155).
+constexpr int kStartTiles = 2;
+
 // A stretch of one row group's tiles, and the walk over those of a range.
 struct Piece {
     int b, seg, nseg, nt;    // request, row group, its groups, tiles of each
     int qs, sq, L;
     int lt0, lt1;            // tiles [lt0, lt1) of the row group
-    long left;               // tiles of the range from lt0 on
+    long at;                 // place of the row group's first tile in the sequence
+    long pos, left;          // place of the next tile, tiles of the range from there on (start tiles included)
     int row0, rows;          // this CTA's rows (of the request's sq * H)
     int n;                   // tiles from lt0 on with a key that one of its rows sees
     __device__ __forceinline__ void request(const LatentArgs& a, int rb, int group) {
@@ -130,8 +137,15 @@ struct Piece {
         nseg = (sq * a.H + group - 1) / group;
         nt = max(1, (L + BN - 1) / BN);
     }
-    __device__ __forceinline__ void fit(const LatentArgs& a, int group, int nr, int rank) {
-        lt1 = (int)min((long)nt, lt0 + left);
+    __device__ __forceinline__ bool whole() const { return lt0 == 0 && lt1 == nt; }
+    // The stretch from place `off` of the row group on; false: none but start tiles.
+    __device__ __forceinline__ bool fit(const LatentArgs& a, long off, int group, int nr, int rank) {
+        const long end = min((long)nt + kStartTiles, off + left);
+        at = pos - off + kStartTiles;
+        pos += end - off;
+        left -= end - off;
+        lt0 = (int)max(0L, off - kStartTiles);
+        lt1 = (int)max(0L, end - kStartTiles);
         row0 = seg * group + rank * nr;
         rows = min(nr, sq * a.H - row0);
         n = 0;
@@ -140,18 +154,17 @@ struct Piece {
             const int lim = a.causal ? max(0, min(L, L - sq + i_last + 1)) : L;
             n = max(0, min(lt1, (lim + BN - 1) / BN) - lt0);
         }
+        return lt1 > lt0;
     }
-    __device__ __forceinline__ void first(const LatentArgs& a, const LRange& r, int group, int nr, int rank) {
+    __device__ __forceinline__ bool first(const LatentArgs& a, const LRange& r, int group, int nr, int rank) {
         request(a, r.b, group);
         seg = r.seg;
-        lt0 = r.lt;
+        pos = r.g0;
         left = r.n;
-        fit(a, group, nr, rank);
+        return fit(a, r.off, group, nr, rank);
     }
     __device__ __forceinline__ bool next(const LatentArgs& a, int group, int nr, int rank) {
-        left -= lt1 - lt0;
         if (left <= 0) return false;
-        lt0 = 0;
         if (++seg >= nseg) {
             seg = 0;
             do {
@@ -159,8 +172,7 @@ struct Piece {
                 request(a, b + 1, group);
             } while (nseg == 0);
         }
-        fit(a, group, nr, rank);
-        return true;
+        return fit(a, 0, group, nr, rank);
     }
 };
 
@@ -220,6 +232,9 @@ __device__ __forceinline__ void tmem_ld_half(uint32_t taddr, float* v) {
                      : "memory");
     }
 }
+
+// o / sum: exact zeros for a row without a key (whose O^T may hold anything)
+__device__ __forceinline__ float scaled(float o, float factor) { return factor != 0.f ? o * factor : 0.f; }
 
 // n / page_size for 0 <= n < 2^31
 __device__ __forceinline__ int page_of(const LatentArgs& a, uint32_t n) {
@@ -290,7 +305,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (b < a.B) {
                 Piece p;
                 p.request(a, b, group);
-                x = (long)p.nseg * p.nt;
+                x = (long)p.nseg * (p.nt + kStartTiles);
             }
             const long own = x;
 #pragma unroll
@@ -318,7 +333,8 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 if (lo <= g0 && g0 < hi) {
                     Piece p;
                     p.request(a, b, group);
-                    *range = LRange{g0, n, per, b, (int)((g0 - lo) / p.nt), (int)((g0 - lo) % p.nt), 0};
+                    const int each = p.nt + kStartTiles;
+                    *range = LRange{g0, n, per, b, (int)((g0 - lo) / each), (int)((g0 - lo) % each), 0};
                 }
             }
         }
@@ -343,7 +359,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         uint32_t pp = 0, units = 0;
         bool ok = true;
         Piece p;
-        p.first(a, rg, group, NR, rank);
+        bool more = p.first(a, rg, group, NR, rank);
         auto step = [&](int u) {                 // past unit u of a tile
             ++units;
             if (++ps == C::NP) { ps = 0; pp ^= 1; }
@@ -367,7 +383,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 constexpr int NB = decltype(blocks)::value;
                 const int bt = a.box_tokens, nbox = NB == 1 ? 1 : BN / bt;
                 const int outside = a.num_pages * (a.page_size / 8);
-                for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+                for (; more && ok; more = p.next(a, group, NR, rank)) {
                     if (p.n == 0) continue;
                     const int32_t* table = a.table + (size_t)p.b * a.max_pages;
                     // page ids of tile k's blocks as the table has them (-1 past the request's end)
@@ -445,7 +461,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             __syncwarp();
         } else {
-            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+            for (; more && ok; more = p.next(a, group, NR, rank)) {
                 if (p.n == 0) continue;
                 if (pw == 0) {
                     if (lane == 0) ok = load_q();
@@ -518,14 +534,14 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ------------------------------------------------------------ S^T issuer (one elected lane)
         if (elect_one()) {
             Piece p;
-            p.first(a, rg, group, NR, rank);
+            bool more = p.first(a, rg, group, NR, rank);
             int it = 0, nq = 0, ps = 0, ts = 0;  // tile, Q blocks taken, slots and the parity of the use of ps
             uint32_t pp = 0;
             bool ok = true;
             const uint64_t qdesc = make_sdesc_sw128(sb + C::OFF_Q, 16, 1024);
             // K-major A: 8-key groups 4 KB apart (1 KB in the shared dims' slot)
             const uint64_t kdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 16, 4096), edesc0 = make_sdesc_sw128(sb + C::OFF_P, 16, 1024);
-            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+            for (; more && ok; more = p.next(a, group, NR, rank)) {
                 for (int k = 0; k < p.n && ok; ++k, ++it) {
                     if (k == 0) ok = mbar_wait(q_full, nq & 1, abort_flag);
                     // at most one tile ahead of O^T, so that no barrier runs two phases ahead
@@ -566,12 +582,12 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         // ------------------------------------------------------------ O^T issuer (one elected lane)
         if (elect_one()) {
             Piece p;
-            p.first(a, rg, group, NR, rank);
+            bool more = p.first(a, rg, group, NR, rank);
             int it = 0, ps = 0, ts = 0;
             bool ok = true;
             // dims-major A: 64-dim slices 1 KB apart, 8-key groups 4 KB apart
             const uint64_t vdesc0 = make_sdesc_sw128(sb + C::OFF_KV, 1024, 4096), pdesc0 = make_sdesc_sw128(sb + C::OFF_P, 1024, 1024);
-            for (bool more = true; more && ok; more = p.next(a, group, NR, rank)) {
+            for (; more && ok; more = p.next(a, group, NR, rank)) {
                 for (int k = 0; k < p.n; ++k, ++it) {
                     ok = mbar_wait(p_full(it & 1), (it >> 1) & 1, abort_flag);
                     if (!ok) break;
@@ -610,17 +626,15 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         float* cross = neg_ref + 4 * NR;                                // [4][NR]: per warp
         const float sl = a.scale_log2;
         Piece p;
-        p.first(a, rg, group, NR, rank);
-        bool more = true, ok = true, at_start = true;
+        bool more = p.first(a, rg, group, NR, rank), ok = true, at_start = true;
         int it = 0, sv = 0, tv = 0;              // tile; its slots
-        long at = rg.g0;                         // the piece's first tile in the sequence
         // Columns of a half-warp's result (half_warp_columns): this lane's first one, and how many.
         constexpr int OWN = HC >= 16 ? HC / 16 : 1;
         const int own = c0 + (HC >= 16 ? (lane % 16) * OWN : (lane % 16) / 2);
         // A wait that gave up (ok false) ends the work but not the walk: all four
         // warps pass the same named barriers to the end.
-        for (; more; more = p.next(a, group, NR, rank), at_start = false) {
-            const bool whole = p.lt0 == 0 && p.lt1 == p.nt;
+        while (more) {
+            const bool whole = p.whole();
             int lim_all = 0;
             if (p.rows > 0) {
                 // row r of the block is query (row0 + r) / H; blocks cut short see what their last row sees
@@ -740,8 +754,10 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 tc_fence_before();
                 if (ok) mbar_arrive(p_full(it & 1));
             }
-            // ---- the piece's end
+            // ---- the piece's end; the next one is looked up while O^T comes to an end
             __syncwarp();
+            Piece nx = p;
+            more = nx.next(a, group, NR, rank);
             if (ok && p.n > 0) {
                 ok = __all_sync(0xffffffffu, tile_done(it - 1, abort_flag));
                 tc_fence_after();
@@ -766,10 +782,11 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 named_bar_sync(kSmBar, 128);
                 if (whole) {
-                    // O^T [dim, row] / sum -> [row, dim]: two lanes exchange so that each
-                    // holds two neighbouring dims of one row
-                    uint32_t* out = reinterpret_cast<uint32_t*>(a.o);
-                    const bool odd = lane & 1;
+                    // O^T [dim, row] / sum -> [row, dim].  A lane has one dim of 32 rows; in
+                    // three exchanges eight lanes turn 8 dims x 32 rows of 16 bits so that
+                    // each holds 8 dims of 4 rows, which go out 16 bytes at a time (4-byte
+                    // stores after the first exchange took 6.6 us for 64 rows, 24 cycles each).
+                    char* out = static_cast<char*>(a.o) + (orow * DC + warp * 32 + (lane & 24)) * 2;
 #pragma unroll 1
                     for (int c = 0; c < NJ * NR; c += 32) {
                         float o[32];
@@ -780,15 +797,34 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 #pragma unroll
                             for (int e = 0; e < 32; ++e) o[e] = 0.f;
                         }
+                        uint32_t v[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 2) {
-                            const int j = (c + e) / NR, r0 = (c + e) % NR;
-                            const float o0 = p.n > 0 ? o[e] * factor[r0] : 0.f, o1 = p.n > 0 ? o[e + 1] * factor[r0 + 1] : 0.f;
-                            const float got = __shfl_xor_sync(0xffffffffu, odd ? o0 : o1, 1);
-                            const int r = r0 + (odd ? 1 : 0);
+                        for (int e = 0; e < 32; e += 4) {
+                            const float4 f = *reinterpret_cast<const float4*>(factor + (c + e) % NR);
+                            v[e / 2] = pack2<F16>(scaled(o[e], f.x), scaled(o[e + 1], f.y));
+                            v[e / 2 + 1] = pack2<F16>(scaled(o[e + 2], f.z), scaled(o[e + 3], f.w));
+                        }
+                        const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {       // (rows 2e, 2e + 1; dim) -> (row 2e + b0; two dims)
+                            const uint32_t x = __shfl_xor_sync(0xffffffffu, v[e], 1);
+                            v[e] = b0 ? __byte_perm(x, v[e], 0x7632) : __byte_perm(v[e], x, 0x5410);
+                        }
+                        uint2 w[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {        // -> (row 4e + 2 b1 + b0; four dims)
+                            const uint32_t x = __shfl_xor_sync(0xffffffffu, b1 ? v[2 * e] : v[2 * e + 1], 2);
+                            w[e] = b1 ? make_uint2(x, v[2 * e + 1]) : make_uint2(v[2 * e], x);
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {        // -> (row 8e + 4 b2 + 2 b1 + b0; eight dims)
+                            const uint2 mine = b2 ? w[2 * e + 1] : w[2 * e], other = b2 ? w[2 * e] : w[2 * e + 1];
+                            const uint32_t x = __shfl_xor_sync(0xffffffffu, other.x, 4);
+                            const uint32_t y = __shfl_xor_sync(0xffffffffu, other.y, 4);
+                            const int i = c + 8 * e + (lane & 7), r = i % NR;
                             if (r < p.rows)
-                                out[((orow + r) * DC + j * 128 + warp * 32 + (lane & ~1)) / 2] =
-                                    odd ? pack2<F16>(got, o1) : pack2<F16>(o0, got);
+                                *reinterpret_cast<uint4*>(out + (size_t)r * DC * 2 + (i / NR) * 256) =
+                                    b2 ? make_uint4(x, y, mine.x, mine.y) : make_uint4(mine.x, mine.y, x, y);
                         }
                     }
                 } else if (p.n > 0) {
@@ -808,14 +844,15 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             if (!whole && p.lt0 == 0 && row == 0 && rank == 0) {
                 // this team holds the row group's first tile: where its pieces lie
-                const long last = (at + p.nt - 1) / rg.per;
+                const long last = (p.at + p.nt - 1) / rg.per;
                 *reinterpret_cast<int4*>(a.join + 4 * team) =
                     make_int4((int)(last - team) + 1, (int)((long)p.qs * a.H) + p.seg * group,
                               min(group, p.sq * a.H - p.seg * group), at_start ? 0 : 1);
             }
-            at += p.lt1 - p.lt0;
             tc_fence_before();
             named_bar_sync(kSmBar, 128);           // the rows' numbers may be written again
+            p = nx;
+            at_start = false;
         }
     }
     }
@@ -830,64 +867,75 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 }
 
 // Adds up the pieces of the row groups that were cut: o = sum_p w_p O_p / sum_p
-// w_p l_p with w_p = 2^(m_p - M).  Block (CTA of the team's first piece, four
-// rows of it); thread = dim, so a piece is read 512 x 16 bytes at a time.
+// w_p l_p with w_p = 2^(m_p - M).  Block (CTA of the team's first piece, JR rows of
+// it): a warp per row for the weights, then thread = dim, four rows at a time, so that
+// a piece is read 512 x 16 bytes at a time (four rows a block: 16 us where 128 heads
+// of 64 requests leave 36 MB of pieces).
+constexpr int JR = 16;
 template <int NR, bool F16>
 __global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
     griddep_wait();
-    const int team = blockIdx.x / a.team, rank = blockIdx.x % a.team, c4 = blockIdx.y;
+    const int team = blockIdx.x / a.team, rank = blockIdx.x % a.team, r_first = blockIdx.y * JR;
     const int4 j = *reinterpret_cast<const int4*>(a.join + 4 * team);
     const int n = min(j.x, a.teams - team);
-    const int r0 = rank * NR + 4 * c4;             // row of the group
+    const int r0 = rank * NR + r_first;            // row of the group
     if (n <= 0 || r0 >= j.z) return;
-    __shared__ float4 m_s[256], l_s[256];          // n <= teams <= 256
-    __shared__ float inv[4];
-    const int d = threadIdx.x, lane = d % 32;
+    __shared__ float w_s[256][JR];                 // n <= teams <= 256
+    __shared__ float inv[JR];
+    const int d = threadIdx.x, lane = d % 32, warp = d / 32;
     auto slot = [&](int p) { return 2 * ((team + p) * a.team + rank) + (p == 0 ? j.w : 0); };
-    for (int p = d; p < n; p += 512) {
-        const float2* ml = a.part_ml + (size_t)slot(p) * NR + 4 * c4;
-        m_s[p] = make_float4(ml[0].x, ml[1].x, ml[2].x, ml[3].x);
-        l_s[p] = make_float4(ml[0].y, ml[1].y, ml[2].y, ml[3].y);
-    }
-    __syncthreads();
-    if (d < 4 * 32) {                              // a warp per row
-        float* m = reinterpret_cast<float*>(m_s) + d / 32;
-        const float* l = reinterpret_cast<const float*>(l_s) + d / 32;
+    {
+        const float2* ml = a.part_ml + r_first + warp;
         float M = -INFINITY, L = 0.f;
-        for (int p = lane; p < n; p += 32) M = fmaxf(M, m[4 * p]);
+        for (int p = lane; p < n; p += 32) {
+            const float m = ml[(size_t)slot(p) * NR].x;
+            w_s[p][warp] = m;
+            M = fmaxf(M, m);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         for (int p = lane; p < n; p += 32) {
-            const float w = l[4 * p] == 0.f ? 0.f : fast_exp2(m[4 * p] - M);
-            m[4 * p] = w;
-            L += w * l[4 * p];
+            const float l = ml[(size_t)slot(p) * NR].y;
+            const float w = l == 0.f ? 0.f : fast_exp2(w_s[p][warp] - M);
+            w_s[p][warp] = w;
+            L += w * l;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         if (lane == 0) {
-            const int e = d / 32;
-            inv[e] = L != 0.f ? 1.f / L : 0.f;
-            if (r0 + e < j.z && a.lse) a.lse[(size_t)j.y + r0 + e] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            inv[warp] = L != 0.f ? 1.f / L : 0.f;
+            if (r0 + warp < j.z && a.lse) a.lse[(size_t)j.y + r0 + warp] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
         }
     }
     __syncthreads();
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + ((d / 128) * (NR / 4) + c4) * 128 + d % 128;
-#pragma unroll 4
+    float4 acc[JR / 4];
+#pragma unroll
+    for (int g = 0; g < JR / 4; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + ((d / 128) * (NR / 4) + r_first / 4) * 128 + d % 128;
+#pragma unroll 2
     for (int p = 0; p < n; ++p) {
-        const float4 w = m_s[p];
-        const float4 o = src[(size_t)slot(p) * (NJ * NR / 4) * 128];
-        // a piece with no key for a row has not written its O
-        acc.x = w.x != 0.f ? fmaf(w.x, o.x, acc.x) : acc.x;
-        acc.y = w.y != 0.f ? fmaf(w.y, o.y, acc.y) : acc.y;
-        acc.z = w.z != 0.f ? fmaf(w.z, o.z, acc.z) : acc.z;
-        acc.w = w.w != 0.f ? fmaf(w.w, o.w, acc.w) : acc.w;
+        const float4* s = src + (size_t)slot(p) * (NJ * NR / 4) * 128;
+        float4 o[JR / 4];
+#pragma unroll
+        for (int g = 0; g < JR / 4; ++g) o[g] = s[g * 128];
+#pragma unroll
+        for (int g = 0; g < JR / 4; ++g) {
+            const float4 w = *reinterpret_cast<const float4*>(&w_s[p][4 * g]);
+            // a piece with no key for a row has not written its O
+            acc[g].x = w.x != 0.f ? fmaf(w.x, o[g].x, acc[g].x) : acc[g].x;
+            acc[g].y = w.y != 0.f ? fmaf(w.y, o[g].y, acc[g].y) : acc[g].y;
+            acc[g].z = w.z != 0.f ? fmaf(w.z, o[g].z, acc[g].z) : acc[g].z;
+            acc[g].w = w.w != 0.f ? fmaf(w.w, o[g].w, acc[g].w) : acc[g].w;
+        }
     }
     uint16_t* out = static_cast<uint16_t*>(a.o) + ((size_t)j.y + r0) * DC + d;
-    const float v[4] = {acc.x * inv[0], acc.y * inv[1], acc.z * inv[2], acc.w * inv[3]};
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        if (r0 + e < j.z) out[e * DC] = (uint16_t)pack2<F16>(v[e], 0.f);
+    for (int g = 0; g < JR / 4; ++g) {
+        const float v[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (r0 + 4 * g + e < j.z) out[(4 * g + e) * DC] = (uint16_t)pack2<F16>(v[e] * inv[4 * g + e], 0.f);
+    }
 }
 
 template <int NR, bool F16, bool GATHER>
@@ -902,7 +950,7 @@ cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CU
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, NR / 4);
+    cfg.gridDim = dim3(ctas, NR / JR);
     cfg.blockDim = dim3(512);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
