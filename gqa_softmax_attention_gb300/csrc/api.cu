@@ -1039,10 +1039,10 @@ gqa_status attn_latent_gather(const void* kv_cache, const int32_t* cu_seqlens_kv
         return GQA_ERR_INVALID_ARG;
     if ((long)max_pages * page_size >= kMaxSeq) return GQA_ERR_INVALID_ARG;
     if ((long)num_pages * page_size >= (1L << 31)) return GQA_ERR_UNSUPPORTED;
-    if (!cu_seqlens_kv || !block_table || (num_pages > 0 && !kv_cache) || (total_kv > 0 && !out)) return GQA_ERR_INVALID_ARG;
+    if (total_kv == 0) return GQA_OK;
+    if (!cu_seqlens_kv || !block_table || (num_pages > 0 && !kv_cache) || !out) return GQA_ERR_INVALID_ARG;
     if (!aligned16(kv_cache) || !aligned16(out) || !aligned4(cu_seqlens_kv) || !aligned4(block_table))
         return GQA_ERR_MISALIGNED;
-    if (total_kv == 0) return GQA_OK;
     const Span w{out, (long)total_kv * gqa::kLatentRow * 2};
     for (const Span& r : {Span{kv_cache, (long)num_pages * page_size * gqa::kLatentRow * 2},
                           Span{cu_seqlens_kv, (B + 1L) * 4}, Span{block_table, (long)B * max_pages * 4}})
@@ -1081,6 +1081,8 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
                                   int dtype, void* workspace, size_t workspace_bytes, gqa_stream_t stream) {
     if (total_kv < 0 || total_kv >= kMaxSeq || !k || !v || !k_pe) return GQA_ERR_INVALID_ARG;
     if (dtype != GQA_BF16 && dtype != GQA_FP16) return GQA_ERR_INVALID_ARG;
+    if (B <= 0 || total_q < 0 || H <= 0 || !std::isfinite(scale)) return GQA_ERR_INVALID_ARG;
+    if (total_q == 0) return GQA_OK;                 // (empty tensors have no address)
     gqa_options opt{-1, -1, 0.f, nullptr, dtype};
     PrefillArgs a{};
     const gqa_status st = varlen_common(q, o, lse, cu_seqlens_q, B, total_q, H, H, gqa::kLatentV, causal, scale, &opt,
@@ -1096,7 +1098,6 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
     }
     const int max_e = varlen_max_entries(B, total_q, 128);
     if ((long)max_e * H >= (1L << 31) - 512) return GQA_ERR_UNSUPPORTED;     // the items are counted in an int
-    if (total_q == 0) return GQA_OK;
     const Rows rk{k->data, (long)k->token_stride, (long)k->head_stride, total_kv, H, gqa::kLatentNope},
         rv{v->data, (long)v->token_stride, (long)v->head_stride, total_kv, H, gqa::kLatentV},
         rp{k_pe->data, (long)k_pe->token_stride, 0, total_kv, 1, gqa::kLatentRope};
@@ -1194,6 +1195,7 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     if (!std::isfinite(scale) || (dtype != GQA_BF16 && dtype != GQA_FP16)) return GQA_ERR_INVALID_ARG;
     if (B > kLatentMaxB || !latent_rows_ok(total_q, H) || (long)num_pages * page_size >= (1L << 31))
         return GQA_ERR_UNSUPPORTED;
+    if (total_q == 0) return GQA_OK;                 // (empty tensors have no address)
     if (!q || !kv_cache || !cu_seqlens_q || !cache_seqlens || !block_table || !o) return GQA_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(kv_cache) || !aligned16(o)) return GQA_ERR_MISALIGNED;
     for (const void* p : {(const void*)cu_seqlens_q, (const void*)cache_seqlens, (const void*)block_table, (const void*)lse})
@@ -1202,7 +1204,6 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     const size_t need = parts.join + parts.ml + parts.o;
     if (!workspace || workspace_bytes < need) return GQA_ERR_WORKSPACE;
     if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return GQA_ERR_MISALIGNED;
-    if (total_q == 0) return GQA_OK;
     const long rows = (long)total_q * H, slots = (long)num_pages * page_size;
     const Span writes[] = {{o, rows * gqa::kLatentDim * 2}, {lse, rows * 4}, {workspace, (long)need}};
     const Span reads[] = {{q, rows * gqa::kLatentRow * 2}, {kv_cache, slots * gqa::kLatentRow * 2},

@@ -867,13 +867,14 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 }
 
 // Adds up the pieces of the row groups that were cut: o = sum_p w_p O_p / sum_p
-// w_p l_p with w_p = 2^(m_p - M).  Block (CTA of the team's first piece, JR rows of
-// it): a warp per row for the weights, then thread = dim, four rows at a time, so that
-// a piece is read 512 x 16 bytes at a time (four rows a block: 16 us where 128 heads
-// of 64 requests leave 36 MB of pieces).
-constexpr int JR = 16;
+// w_p l_p with w_p = 2^(m_p - M).  Block (CTA of the team's first piece, JR rows of it,
+// 128 dims): a warp per row for the weights, then thread = dim, U pieces at a time,
+// the first of them on their way while the weights are formed.  JR is small where a
+// group has few rows, because few groups of many pieces (one to four long requests)
+// would leave all the reading to a few SMs.
 template <int NR, bool F16>
-__global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
+__global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs a) {
+    constexpr int JR = NR == 64 ? 16 : 4, U = 32 / JR;
     griddep_wait();
     const int team = blockIdx.x / a.team, rank = blockIdx.x % a.team, r_first = blockIdx.y * JR;
     const int4 j = *reinterpret_cast<const int4*>(a.join + 4 * team);
@@ -884,51 +885,63 @@ __global__ void __launch_bounds__(512) latent_join_kernel(const LatentArgs a) {
     __shared__ float inv[JR];
     const int d = threadIdx.x, lane = d % 32, warp = d / 32;
     auto slot = [&](int p) { return 2 * ((team + p) * a.team + rank) + (p == 0 ? j.w : 0); };
-    {
-        const float2* ml = a.part_ml + r_first + warp;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (blockIdx.z * (NR / 4) + r_first / 4) * 128 + d;
+    float4 o[U][JR / 4];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int g = 0; g < JR / 4; ++g)
+                if (p0 + u < n) o[u][g] = src[(size_t)slot(p0 + u) * (NJ * NR / 4) * 128 + g * 128];
+    };
+    load(0);
+#pragma unroll
+    for (int r = warp; r < JR; r += 4) {
+        const float2* ml = a.part_ml + r_first + r;
         float M = -INFINITY, L = 0.f;
         for (int p = lane; p < n; p += 32) {
             const float m = ml[(size_t)slot(p) * NR].x;
-            w_s[p][warp] = m;
+            w_s[p][r] = m;
             M = fmaxf(M, m);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
         for (int p = lane; p < n; p += 32) {
             const float l = ml[(size_t)slot(p) * NR].y;
-            const float w = l == 0.f ? 0.f : fast_exp2(w_s[p][warp] - M);
-            w_s[p][warp] = w;
+            const float w = l == 0.f ? 0.f : fast_exp2(w_s[p][r] - M);
+            w_s[p][r] = w;
             L += w * l;
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
         if (lane == 0) {
-            inv[warp] = L != 0.f ? 1.f / L : 0.f;
-            if (r0 + warp < j.z && a.lse) a.lse[(size_t)j.y + r0 + warp] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+            inv[r] = L != 0.f ? 1.f / L : 0.f;
+            if (blockIdx.z == 0 && r0 + r < j.z && a.lse)
+                a.lse[(size_t)j.y + r0 + r] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
         }
     }
     __syncthreads();
     float4 acc[JR / 4];
 #pragma unroll
     for (int g = 0; g < JR / 4; ++g) acc[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-    const float4* src = reinterpret_cast<const float4*>(a.part_o) + ((d / 128) * (NR / 4) + r_first / 4) * 128 + d % 128;
-#pragma unroll 2
-    for (int p = 0; p < n; ++p) {
-        const float4* s = src + (size_t)slot(p) * (NJ * NR / 4) * 128;
-        float4 o[JR / 4];
+    for (int p = 0; p < n; p += U) {
 #pragma unroll
-        for (int g = 0; g < JR / 4; ++g) o[g] = s[g * 128];
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-        for (int g = 0; g < JR / 4; ++g) {
-            const float4 w = *reinterpret_cast<const float4*>(&w_s[p][4 * g]);
-            // a piece with no key for a row has not written its O
-            acc[g].x = w.x != 0.f ? fmaf(w.x, o[g].x, acc[g].x) : acc[g].x;
-            acc[g].y = w.y != 0.f ? fmaf(w.y, o[g].y, acc[g].y) : acc[g].y;
-            acc[g].z = w.z != 0.f ? fmaf(w.z, o[g].z, acc[g].z) : acc[g].z;
-            acc[g].w = w.w != 0.f ? fmaf(w.w, o[g].w, acc[g].w) : acc[g].w;
+            for (int g = 0; g < JR / 4; ++g) {
+                if (p + u < n) {
+                    const float4 w = *reinterpret_cast<const float4*>(&w_s[p + u][4 * g]);
+                    // a piece with no key for a row has not written its O
+                    acc[g].x = w.x != 0.f ? fmaf(w.x, o[u][g].x, acc[g].x) : acc[g].x;
+                    acc[g].y = w.y != 0.f ? fmaf(w.y, o[u][g].y, acc[g].y) : acc[g].y;
+                    acc[g].z = w.z != 0.f ? fmaf(w.z, o[u][g].z, acc[g].z) : acc[g].z;
+                    acc[g].w = w.w != 0.f ? fmaf(w.w, o[u][g].w, acc[g].w) : acc[g].w;
+                }
+            }
         }
+        load(p + U);
     }
-    uint16_t* out = static_cast<uint16_t*>(a.o) + ((size_t)j.y + r0) * DC + d;
+    uint16_t* out = static_cast<uint16_t*>(a.o) + ((size_t)j.y + r0) * DC + blockIdx.z * 128 + d;
 #pragma unroll
     for (int g = 0; g < JR / 4; ++g) {
         const float v[4] = {acc[g].x, acc[g].y, acc[g].z, acc[g].w};
@@ -950,8 +963,8 @@ cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_kv, const CU
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(ctas, NR / JR);
-    cfg.blockDim = dim3(512);
+    cfg.gridDim = dim3(ctas, NR == 64 ? 4 : NR / 4, NJ);
+    cfg.blockDim = dim3(128);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

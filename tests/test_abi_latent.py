@@ -88,7 +88,7 @@ def test_gather_argument_checks(lib):
     assert gather(lib, pages=1 << 27) == UNSUPPORTED
     for bad in (dict(cache=off(at(1), 8)), dict(out=off(at(4), 8)), dict(cu=off(at(2), 2)), dict(table=off(at(3), 2))):
         assert gather(lib, **bad) == MISALIGNED, bad
-    assert gather(lib, total=0) == 0
+    assert gather(lib, total=0) == 0 and gather(lib, total=0, out=None, cache=None) == 0
 
 
 # 2 requests, 10 queries and 40 keys of 4 heads
@@ -114,7 +114,7 @@ def test_varlen_argument_checks(lib):
     assert need > 0
     assert varlen(lib, n=need - 1) == WORKSPACE and varlen(lib, ws=None) == WORKSPACE
     assert varlen(lib, tq=(1 << 30) - 1, H=400, n=1 << 40) == UNSUPPORTED
-    assert varlen(lib, tq=0) == 0
+    assert varlen(lib, tq=0) == 0 and varlen(lib, tq=0, q=None, o=None, lse=None, ws=None, n=0) == 0
     for sizes in ((0, 10, 4), (2, -1, 4), (2, 10, 0), (2, 1 << 30, 4)):
         assert lib.attn_latent_varlen_workspace_size(*sizes) == 0, sizes
 
@@ -142,7 +142,7 @@ def test_paged_argument_checks(lib):
     for bad in (dict(o=off(at(1), 64)), dict(o=off(at(2), 64)), dict(lse=off(at(5), 4)), dict(ws=at(0)), dict(lse=off(at(6), 4)),
                 dict(o=off(at(8), 256)), dict(lse=off(at(3), 8)), dict(lse=at(4))):
         assert paged(lib, n=need, **bad) == INVALID, bad
-    assert paged(lib, tq=0) == 0
+    assert paged(lib, tq=0) == 0 and paged(lib, tq=0, q=None, o=None, lse=None, ws=None, n=0) == 0
     for sizes in ((0, 10, 4), (16385, 10, 4), (2, -1, 4), (2, 10, 0), (2, 1 << 25, 64), (2, 1 << 30, 1)):
         assert lib.attn_latent_paged_workspace_size(*sizes) == 0, sizes
 
