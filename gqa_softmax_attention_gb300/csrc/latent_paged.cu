@@ -418,11 +418,6 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     for (int k = 0; k < p.n && ok; ++k) {
                         groups(k + 2, pg, g2);
                         pages(k + 3, pg);
-                        if (rank == 0) {
-#pragma unroll
-                            for (int i = 0; i < NB; ++i)
-                                if (i < nbox && g2[i] != outside) tma_prefetch_4d(&tm_row, 0, 0, 0, g2[i]);
-                        }
 #pragma unroll
                         for (int u = 0; u < NU; ++u) {
                             if (!(ok = mbar_wait(kv_empty(ps), pp ^ 1, abort_flag))) break;
@@ -436,6 +431,11 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                 }
                             }
                             step(u);
+                        }
+                        if (rank == 0) {
+#pragma unroll
+                            for (int i = 0; i < NB; ++i)
+                                if (i < nbox && g2[i] != outside) tma_prefetch_4d(&tm_row, 0, 0, 0, g2[i]);
                         }
 #pragma unroll
                         for (int i = 0; i < NB; ++i) {
