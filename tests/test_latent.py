@@ -536,3 +536,120 @@ def test_expanded_blocks_without_a_partner(g):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
     for b, h, rows, ref in varlen_refs(c):
         check(o[rows, h], lse[rows, h], ref, "request %d head %d" % (b, h))
+
+
+# ---------------------------------------------------------------- odd calls
+
+def test_absorbed_many_requests(g):
+    """More requests than threads of a CTA, most of them short or without queries."""
+    gen = torch.Generator().manual_seed(30)
+    lens = [int(x) for x in torch.randint(0, 40, (900,), generator=gen)]
+    lens[17], lens[500] = 3000, 777
+    nq = [int(x) for x in torch.randint(0, 3, (900,), generator=gen)]
+    paged_check(g, paged_case(gen, nq, lens, 6, 16, torch.bfloat16))
+
+
+@pytest.mark.parametrize("H,ps", [(200, 256), (7, 1000), (64, 40), (33, 64)])
+def test_absorbed_head_counts_and_page_sizes(g, H, ps):
+    gen = torch.Generator().manual_seed(H)
+    paged_check(g, paged_case(gen, [1, 3, 2], [1500, 77, 640], H, ps, torch.float16))
+
+
+def test_absorbed_malformed_metadata(g):
+    """Lengths past the table's capacity are cut to it, negative ones count as none,
+    offsets are clamped into the packed rows: wrong input, but no access out of range."""
+    gen = torch.Generator().manual_seed(31)
+    c = paged_case(gen, [1, 1, 1], [256, 128, 64], 16, 64, torch.bfloat16)
+    c["cache"].nan_to_num_(0.25)
+    c["table"].clamp_(min=0)
+    c["lens"].copy_(i32([1 << 29, -5, 64]))
+    c["L"] = [256, 0, 64]
+    paged_check(g, c)
+    for cu in ([0, -3, 1 << 30, 2], [2, 1, 0, 3], [5, 6, 7, 8]):
+        g.attn_fwd_latent_paged(c["q"], c["cache"], i32(cu), c["lens"], c["table"], SCALE)
+        g.attn_fwd_latent_varlen(c["q"][..., :192].contiguous(), c["q"][..., :128], c["q"][..., 128:256],
+                                 c["q"][:, 0, 256:320], i32(cu), i32(cu[::-1]))
+        g.attn_latent_gather(c["cache"], i32(cu), c["table"], 50)
+    torch.cuda.synchronize()
+    g.gqa_device_error()
+
+
+def test_sliced_queries_and_two_streams_at_once(g):
+    """Queries that are a slice are copied; calls side by side on two streams do not meet."""
+    gen = torch.Generator().manual_seed(32)
+    c = paged_case(gen, [1] * 40, [int(x) for x in torch.randint(1, 5000, (40,), generator=gen)], 16, 64, torch.bfloat16)
+    e = varlen_case(gen, [300, 411], [300, 900], 8, torch.bfloat16)
+    wide = torch.cat([c["q"], c["q"]], 2)[..., 100:676]
+    args = (c["cache"], c["cu"], c["lens"], c["table"], SCALE)
+    o, lse = g.attn_fwd_latent_paged(c["q"], *args)
+    o2, lse2 = g.attn_fwd_latent_paged(wide, *args)
+    assert torch.equal(*(g.attn_fwd_latent_paged(x, *args)[0] for x in (wide, wide.contiguous()))) and o2.shape == o.shape
+    oe, le = g.attn_fwd_latent_varlen(e["q"], e["k"], e["v"], e["pe"], e["cq"], e["ck"])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for n in range(20):
+        with torch.cuda.stream(streams[n % 2]):
+            got.append(g.attn_fwd_latent_paged(c["q"], *args) if n % 4 < 2 else
+                       g.attn_fwd_latent_varlen(e["q"], e["k"], e["v"], e["pe"], e["cq"], e["ck"]))
+    torch.cuda.synchronize()
+    for n, (x, y) in enumerate(got):
+        assert torch.equal(x, o if n % 4 < 2 else oe) and torch.equal(y, lse if n % 4 < 2 else le), n
+    g.gqa_device_error()
+
+
+def test_one_workspace_for_calls_in_turn(g):
+    """A caller's workspace, larger than needed and full of NaN, used call after call."""
+    gen = torch.Generator().manual_seed(33)
+    cases = [paged_case(gen, [1] * 5, [3000, 10, 500, 1, 64], 16, 64, torch.bfloat16),
+             paged_case(gen, [4, 1], [700, 2000], 64, 16, torch.bfloat16)]
+    size = max(g.attn_latent_paged_workspace_size(len(c["nq"]), sum(c["nq"]), c["H"]) for c in cases)
+    ws = torch.full((size // 4 + 64,), math.nan, device="cuda")
+    for c in cases * 2:
+        paged_check(g, c, workspace=ws)
+
+
+def test_empty_calls(g):
+    """No query, no key, no token: shapes come back, nothing runs."""
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")
+    o, lse = g.attn_fwd_latent_paged(z(0, 16, ROW), z(4, 16, ROW), i32([0, 0]), i32([20]), i32([[0, 1]]), SCALE)
+    assert o.shape == (0, 16, C) and lse.shape == (0, 16)
+    o, lse = g.attn_fwd_latent_varlen(z(0, 4, 192), z(0, 4, 128), z(0, 4, 128), z(0, 64), i32([0, 0]), i32([0, 0]))
+    assert o.shape == (0, 4, V) and lse.shape == (0, 4)
+    o, lse = g.attn_fwd_latent_varlen(z(3, 4, 192), z(0, 4, 128), z(0, 4, 128), z(0, 64), i32([0, 3]), i32([0, 0]))
+    assert bool((o == 0).all()) and bool(torch.isneginf(lse).all())
+    assert g.attn_latent_gather(z(4, 16, ROW), i32([0, 0]), i32([[0]]), 0).shape == (0, ROW)
+    out = g.attn_latent_norm_rope_paged(z(0, 4, 64), z(0, ROW), g.rope_table(8, 64), i32([]), i32([]), z(4, 16, ROW))
+    assert out.shape == (0, 4, 64)
+
+
+def test_refusals(g):
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")
+    cs = g.rope_table(8, 64)
+    paged = dict(q=z(1, 4, ROW), kv_cache=z(4, 16, ROW), cu_seqlens_q=i32([0, 1]), cache_seqlens=i32([20]),
+                 block_table=i32([[0, 1]]), scale=SCALE)
+    for bad in (dict(q=z(1, 4, 512)), dict(q=z(1, 4, ROW, d=torch.float32)), dict(kv_cache=z(4, 16, ROW, d=torch.float16)),
+                dict(kv_cache=z(4, 16, 640)), dict(kv_cache=z(4, 32, ROW)[:, ::2]), dict(cu_seqlens_q=i32([0])),
+                dict(cache_seqlens=i32([20]).long()), dict(block_table=i32([0, 1])), dict(block_table=i32([[0, 1], [0, 1]])),
+                dict(scale=math.inf), dict(out=z(1, 4, ROW)), dict(lse=z(1, 4)), dict(workspace=z(16, d=torch.uint8))):
+        with pytest.raises(ValueError):
+            g.attn_fwd_latent_paged(**{**paged, **bad})
+    var = dict(q=z(2, 4, 192), k=z(3, 4, 128), v=z(3, 4, 128), k_pe=z(3, 64), cu_seqlens_q=i32([0, 2]),
+               cu_seqlens_kv=i32([0, 3]))
+    for bad in (dict(q=z(2, 4, 128)), dict(k=z(3, 2, 128)), dict(v=z(4, 4, 128)), dict(k_pe=z(3, 32)), dict(k_pe=z(3, 4, 64)),
+                dict(v=z(3, 4, 128, d=torch.float16)), dict(cu_seqlens_kv=i32([0, 1, 3])), dict(cu_seqlens_q=i32([0])),
+                dict(out=z(2, 4, 192)), dict(workspace=z(8, d=torch.uint8))):
+        with pytest.raises(ValueError):
+            g.attn_fwd_latent_varlen(**{**var, **bad})
+    app = dict(q_pe=z(2, 4, 64), kv=z(2, ROW), cos_sin=cs, positions=i32([0, 1]), slots=i32([0, 1]), kv_cache=z(4, 16, ROW))
+    for bad in (dict(q_pe=z(2, 4, 32)), dict(kv=z(3, ROW)), dict(kv=z(2, 512)), dict(cos_sin=g.rope_table(8, 32)),
+                dict(positions=i32([0])), dict(slots=i32([0, 1]).long()), dict(kv_cache=z(4, 16, ROW, d=torch.float16)),
+                dict(kv_weight=z(64)), dict(kv_weight=z(512, d=torch.float16)), dict(eps=-1.0),
+                dict(out=z(2, 4, 65)[..., 1:]), dict(out=z(2, 4, 64, d=torch.float16)), dict(kv_out=z(2, 640)[:, :ROW])):
+        with pytest.raises(ValueError):
+            g.attn_latent_norm_rope_paged(**{**app, **bad})
+    for bad in (dict(kv_cache=z(4, 16, 512)), dict(cu_seqlens_kv=i32([0])), dict(total_kv=-1), dict(total_kv=1 << 30),
+                dict(out=z(19, ROW))):
+        with pytest.raises(ValueError):
+            g.attn_latent_gather(**{**dict(kv_cache=z(4, 16, ROW), cu_seqlens_kv=i32([0, 20]), block_table=i32([[0, 1]]),
+                                          total_kv=20), **bad})
