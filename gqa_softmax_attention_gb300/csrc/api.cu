@@ -1071,8 +1071,20 @@ static bool make_rows_map(CUtensorMap* map, const Rows& r, int box_t, bool f16) 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// CTAs of an expanded call, and the bytes of its part slots: none where the query
+// blocks alone fill so many rounds of CTAs that no tail is cut.
+static int latent_varlen_grid(int B, int total_q, int H) {
+    const long n = sm_count() > 0 ? sm_count() : 148, items = (long)varlen_max_entries(B, total_q, 128) * H;
+    return (int)(items < n ? items : n);
+}
+static size_t latent_varlen_parts(int B, int total_q, int H) {
+    const long grid = latent_varlen_grid(B, total_q, H), least = ((long)total_q + 255) / 256 * H;
+    return least >= 8 * grid ? 0 : (size_t)grid * gqa::kLatentPartSlots * gqa::kLatentPartFloats * sizeof(float);
+}
+
 size_t attn_latent_varlen_workspace_size(int B, int total_q, int H) {
-    return total_q < kMaxSeq ? varlen_ws_bytes(B, total_q, H, H) : 0;
+    const size_t plan = total_q < kMaxSeq ? varlen_ws_bytes(B, total_q, H, H) : 0;
+    return plan == 0 ? 0 : (plan + 255) / 256 * 256 + latent_varlen_parts(B, total_q, H);
 }
 
 gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const gqa_head_rows* v,
@@ -1103,8 +1115,11 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
         rp{k_pe->data, (long)k_pe->token_stride, 0, total_kv, 1, gqa::kLatentRope};
     const long rows = (long)total_q * H;
     constexpr int dq = gqa::kLatentNope + gqa::kLatentRope;
+    const size_t plan = (varlen_ws_bytes(B, total_q, H, H) + 255) / 256 * 256, parts = latent_varlen_parts(B, total_q, H);
+    // parts of at least a few key tiles each: short calls are never cut
+    const bool cut = parts > 0 && workspace_bytes >= plan + parts && total_kv >= 8 * 128;
     const Span writes[] = {{o, rows * gqa::kLatentV * 2}, {lse, rows * 4},
-                           {workspace, (long)varlen_ws_bytes(B, total_q, H, H)}};
+                           {workspace, (long)(cut ? plan + parts : varlen_ws_bytes(B, total_q, H, H))}};
     const Span reads[] = {{q, rows * dq * 2}, rk.span(), rv.span(), rp.span(), {cu_seqlens_q, (B + 1L) * 4},
                           {cu_seqlens_kv, (B + 1L) * 4}};
     for (int i = 0; i < 3; ++i) {
@@ -1125,7 +1140,15 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
     if (gqa::launch_varlen_plan(cu_seqlens_q, cu_seqlens_kv, false, B, 128, 1, a.causal, total_q, total_kv,
                                 ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e, s, false, true) != cudaSuccess)
         return GQA_ERR_CUDA;
-    return gqa::launch_latent_varlen(tq, tk, tv, tp, a, (long)max_e * H, s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
+    // heads whose keys and values (512 bytes a token and head) take half of L2
+    const long per_head = total_kv > 0 ? (long)total_kv * 512 : 512;
+    a.head_group = (int)std::max(1L, std::min((long)H, (64L << 20) / per_head));
+    a.grid = latent_varlen_grid(B, total_q, H);
+    if (cut) {
+        a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
+        a.part_lse = a.part_o + (size_t)a.grid * gqa::kLatentPartSlots * 2 * 128 * gqa::kLatentV;
+    }
+    return gqa::launch_latent_varlen(tq, tk, tv, tp, a, s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 
 // Rows and offsets into them are ints on the device, with room for a team's rows past the last.

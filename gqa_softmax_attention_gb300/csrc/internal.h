@@ -56,6 +56,10 @@ struct PrefillArgs {
     float* part_o;            // [parts, 128, D], divided by the part's row sums
     float* part_lse;          // [parts, 128], base 2
     uint32_t ps_mul, ps_shift;   // n / page_size = (umulhi(n, ps_mul) + n) >> ps_shift for 0 <= n < 2^31
+    // expanded latent calls: heads whose keys stay in L2 together; persistent CTAs.
+    // part_o [2 grid, 2, 32, 128, 4] and part_lse [2 grid, 2, 128, 2] there hold the parts
+    // of cut items: O of four dims a step, maximum (base 2) and sum; nullptr: none is cut
+    int head_group, grid;
 };
 
 // Launches the tcgen05 prefill kernel.  The tensor maps describe q, k, v as
@@ -337,8 +341,11 @@ int latent_paged_take_device_error();
 // attn_fwd_latent_varlen): PrefillArgs with D = kLatentV, g = 1, qpb = 128.
 // tm_q {192, H, total_q}, tm_k / tm_v {128, H, total_kv} with {64, 1, 128}
 // boxes (tm_v: 64 rows), tm_pe {64, total_kv} with a {64, 128} box.
+// a.grid CTAs; with a.part_o set a second kernel joins the parts.
 cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                 const CUtensorMap& tm_pe, const PrefillArgs& a, long max_items, cudaStream_t stream);
+                                 const CUtensorMap& tm_pe, const PrefillArgs& a, cudaStream_t stream);
+constexpr int kLatentPartSlots = 2;          // part slots a CTA of the grid
+constexpr long kLatentPartFloats = 2L * 128 * (kLatentV + 2);   // of a slot: O, maximum and sum of two row blocks
 int latent_varlen_take_device_error();
 
 }  // namespace gqa

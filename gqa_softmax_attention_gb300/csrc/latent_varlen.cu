@@ -20,8 +20,9 @@
 //   warp 9      MMA issuer
 //   warps 0-7   softmax of the two tiles, one row per thread, and the output
 //   warps 10-11 zero the value rows past a request's end in its last tile
-// Items of one head follow one another, so that the row blocks of a request read
-// its keys from L2.
+// Items go by cost, the longest first, within groups of heads whose keys and values
+// fit L2 together.  What does not fill a last round of CTAs is cut along the keys
+// (Split) into FP32 parts that latent_varlen_join_kernel adds up.
 #include <cmath>
 
 #include "internal.h"
@@ -58,9 +59,84 @@ constexpr int NBAR = 4 + 2 * NS + 6 + 1 + 4 + 2;
 constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int OFF_INFO = OFF_MISC + 16;         // two item records: claimed item, tiles of Q0 and of Q1
 constexpr int REC = 4;
-constexpr int SMEM_BYTES = OFF_INFO + 2 * REC * 4 + 1024;
+constexpr int OFF_SPLIT = OFF_INFO + 2 * REC * 4;
+constexpr int SMEM_BYTES = OFF_SPLIT + 16 + 1024;
 constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + DV, TMEM_COLS = 512;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
+
+// Which items are cut.  With n_items = q grid + tail, the last `tail` items would keep
+// all but that many CTAs waiting for a whole item's time; they go in P parts each
+// instead (at least kPartTiles key tiles a part, at most two part slots a CTA).  P takes
+// the fewest tile times ceil(tail P / grid) (n / P + 2), 2 for a part's own start and end, if
+// that saves more than the joining costs (kJoinTiles); from kMaxRounds rounds on the
+// tail is short against the rest.
+constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 32;
+struct Split {
+    int n_entries, n_items, n0, P;       // items [n0, n_items) are cut
+    __device__ __forceinline__ int claims() const { return n0 + (n_items - n0) * P; }
+};
+
+struct Item {
+    int h, q0, qs, sq, ks, skv;     // head; first query of the item; first query / key row of the request and its counts
+    TileInfo t0, t1;
+    int lo, c0, c1;                 // this part's first key tile, and its tiles for either query tile
+    int part, parts;                // parts > 1: results go to part slot `slot`; parts 0: nothing to do
+    int slot;
+};
+
+// Item (w, part) of a claim; the whole of one where P is 1.
+__device__ __forceinline__ Item describe_item(const PrefillArgs& a, int n_entries, int w, int part, int P, int slot) {
+    Item it;
+    // entries by cost within a group of heads: the heads of an entry, then the next entry
+    const int hg = a.head_group, grp = w / (n_entries * hg), x = w - grp * n_entries * hg;
+    const int heads = min(hg, a.Hq - grp * hg);
+    const int4* e = reinterpret_cast<const int4*>(a.entries + (size_t)(x / heads) * 8);
+    const int4 e0 = e[0], e1 = e[1];
+    it.h = grp * hg + x % heads;
+    it.q0 = e0.y;
+    it.qs = e0.z;
+    it.sq = e0.w;
+    it.ks = e1.x;
+    it.skv = e1.y;
+    it.t0 = tile_info_n(it.q0, BM, it.sq, it.skv, a.causal, -1, -1);
+    it.t1 = tile_info_n(it.q0 + BM, BM, it.sq, it.skv, a.causal, -1, -1);
+    const int n = max(it.t0.n_tiles, it.t1.n_tiles);
+    const int len = P > 1 ? max(kPartTiles, (n + P - 1) / P) : max(n, 1);
+    it.lo = part * len;
+    it.c0 = max(0, min(it.t0.n_tiles - it.lo, len));
+    it.c1 = max(0, min(it.t1.n_tiles - it.lo, len));
+    it.part = part;
+    it.parts = part > 0 && it.lo >= n ? 0 : max(1, (n + len - 1) / len);
+    it.slot = slot;
+    return it;
+}
+__device__ __forceinline__ Item describe_claim(const PrefillArgs& a, const Split& s, int w) {
+    if (w < s.n0) return describe_item(a, s.n_entries, w, 0, 1, 0);
+    const int x = w - s.n0;
+    return describe_item(a, s.n_entries, s.n0 + x / s.P, x % s.P, s.P, x);
+}
+__device__ __forceinline__ Split find_split(const PrefillArgs& a) {
+    Split s;
+    s.n_entries = *a.n_entries;
+    s.n_items = s.n_entries * a.Hq;
+    s.n0 = s.n_items;
+    s.P = 1;
+    const int tail = s.n_items % a.grid;
+    if (a.part_o == nullptr || tail == 0 || s.n_items / a.grid >= kMaxRounds) return s;
+    const Item it = describe_item(a, s.n_entries, s.n_items - tail, 0, 1, 0);    // the longest of the tail, or near it
+    const int n = max(it.c0, it.c1);
+    const int most = min(min(kMaxParts, kLatentPartSlots * a.grid / tail), n / kPartTiles);
+    int best = 16 * (n + 2 - kJoinTiles);                   // sixteenths of a tile time
+    for (int p = 2; p <= most; ++p) {
+        const int cost = (tail * p + a.grid - 1) / a.grid * (16 * n / p + 32);
+        if (cost < best) {
+            best = cost;
+            s.P = p;
+            s.n0 = s.n_items - tail;
+        }
+    }
+    return s;
+}
 
 template <bool F16>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
@@ -69,33 +145,13 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                      const PrefillArgs a) {
     constexpr uint32_t IDESC_QK = make_idesc_16<F16>(BM, BN, false, false);
     constexpr uint32_t IDESC_PV = make_idesc_16<F16>(BM, DV, false, true);
+    griddep_launch_dependents();                 // the joining kernel may be scheduled (it waits for this grid)
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_u32(smem_raw);
     uint8_t* smem = smem_raw + ((1024 - (raw_base & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
     // through a shuffle, so that the compiler knows the roles' branches to be uniform
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
-
-    const int n_entries = *a.n_entries;
-    const long n_items = (long)n_entries * a.Hq;
-    struct Item {
-        int h, q0, qs, sq, ks, skv;     // head; first query of the item; first query / key row of the request and its counts
-        TileInfo t0, t1;
-    };
-    auto describe = [&](int w) {
-        Item it;
-        const int4* e = reinterpret_cast<const int4*>(a.entries + (size_t)(w % n_entries) * 8);
-        const int4 e0 = e[0], e1 = e[1];
-        it.h = w / n_entries;
-        it.q0 = e0.y;
-        it.qs = e0.z;
-        it.sq = e0.w;
-        it.ks = e1.x;
-        it.skv = e1.y;
-        it.t0 = tile_info_n(it.q0, BM, it.sq, it.skv, a.causal, -1, -1);
-        it.t1 = tile_info_n(it.q0 + BM, BM, it.sq, it.skv, a.causal, -1, -1);
-        return it;
-    };
 
     const uint32_t bar0 = sb + OFF_BAR;
     auto q_full = [&](int k) { return bar0 + 8u * k; };
@@ -133,6 +189,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
+    Split* split = reinterpret_cast<Split*>(smem + OFF_SPLIT);
+    if (threadIdx.x == 32 * WARP_LOAD) *split = find_split(a);
     if (warp == WARP_MMA) {
         tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish();
@@ -141,6 +199,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    const Split sp = *split;
 
     // As in prefill.cu each role ends by itself; the MMA warp frees TMEM once the
     // softmax warps have arrived on barrier 2.
@@ -158,13 +217,13 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 bool ok = true;
                 for (int r = 0; ok; ++r) {
                     const int w = atomicAdd(a.work, 1);
-                    const bool none = w >= n_items;
+                    const bool none = w >= sp.claims();
                     int c[2] = {0, 0};
                     Item it;
                     if (!none) {
-                        it = describe(w);
-                        c[0] = it.t0.n_tiles;
-                        c[1] = it.t1.n_tiles;
+                        it = describe_claim(a, sp, w);
+                        c[0] = it.c0;
+                        c[1] = it.c1;
                     }
                     ok = mbar_wait(info_empty(r & 1), ((r >> 1) & 1) ^ 1, abort_flag);
                     if (!ok) break;
@@ -187,7 +246,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     if (c[0] > 0) ok = load_q(0);
                     const int n = max(c[0], c[1]);
                     for (int j = 0; j < n && ok; ++j) {
-                        const int key = it.ks + j * BN;
+                        const int key = it.ks + (it.lo + j) * BN;
                         for (int x = 0; x < UNITS && ok; ++x, ++nu) {
                             const uint32_t f = full(nu % NS);
                             ok = mbar_wait(empty(nu % NS), parity_of(nu) ^ 1u, abort_flag);
@@ -331,7 +390,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (lane == 0) mbar_arrive(info_empty(r & 1));
                 if (w < 0) break;
                 if (n == 0) continue;
-                const Item it = describe(w);
+                const Item it = describe_claim(a, sp, w);
                 const uint32_t uv = u0 + (n - 1) * UNITS + KU;
                 u0 += n * UNITS;
                 if (!__all_sync(0xffffffffu, mbar_wait(v_landed, nl & 1, abort_flag))) break;
@@ -340,7 +399,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     // the MMA thread has seen the slot full; so does the writer here
                     if (!__all_sync(0xffffffffu, mbar_wait(full((uv + x) % NS), parity_of(uv + x), abort_flag)))
                         break;
-                    const int r0 = it.skv - (n - 1) * BN - x * 64;   // first row of the half past the end
+                    const int r0 = it.skv - (it.lo + n - 1) * BN - x * 64;   // first row of the half past the end
                     uint8_t* base = smem + (slot_addr(uv + x) - sb);
                     for (int y = max(r0, 0) * 16 + t; y < 64 * 16; y += 64) {
                         const int row = y / 16, sl = (y / 8) % 2, q = y % 8;
@@ -370,13 +429,14 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (lane == 0) mbar_arrive(info_empty(rr & 1));
             __syncwarp();
             if (!named_bar_and(3 + k, BM, ok) || w < 0) break;
-            const Item itm = describe(w);
+            const Item itm = describe_claim(a, sp, w);
             const TileInfo ti = k == 0 ? itm.t0 : itm.t1;
+            const int n_tiles = k == 0 ? itm.c0 : itm.c1;
             const int lim = (int)key_hi((long)ti.q0 + r + itm.skv - itm.sq, itm.skv, a.causal, -1);   // keys this row sees
             float m_ref = -INFINITY;     // reference max (log2 units, scaled)
             float l_run = 0.f;
-            for (int j = 0; j < ti.n_tiles; ++j) {
-                const int kbase = j * BN;
+            for (int j = 0; j < n_tiles; ++j) {
+                const int kbase = (itm.lo + j) * BN;
                 ok = __all_sync(0xffffffffu, mbar_wait(s_full(k), sf & 1, abort_flag));
                 ++sf;
                 if (!ok) break;
@@ -446,23 +506,39 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // ---- the tile's end (also after a wait gave up: all four warps pass the barrier below)
             // An item without a tile for this warpgroup has no phase of o_final: the
             // MMA thread could end it before the phase of the item before has been seen.
-            if (ok && ti.n_tiles > 0) {
+            if (ok && n_tiles > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(o_final(k), n_done & 1, abort_flag));
                 ++n_done;
                 if (ok) tc_fence_after();
             }
             const bool row_ok = r < ti.rows_valid;
             const size_t orow = (size_t)(itm.qs + ti.q0 + r) * a.Hq + itm.h;
-            const bool some = l_run != 0.f && ti.n_tiles > 0;    // 0: no key; NaN goes on
+            const bool some = l_run != 0.f && n_tiles > 0;       // 0: no key; NaN goes on
             const float inv = some ? 1.f / l_run : 0.f;
-            if (row_ok && a.lse && ok) a.lse[orow] = some ? (m_ref + log2f(l_run)) * kLn2 : -INFINITY;
+            if (row_ok && a.lse && ok && itm.parts == 1) a.lse[orow] = some ? (m_ref + log2f(l_run)) * kLn2 : -INFINITY;
             uint16_t* dst = static_cast<uint16_t*>(a.o) + orow * DV;
-            if (ti.rows_valid > 0 && ok) {
+            if (ti.rows_valid > 0 && ok && itm.parts > 1) {
+                // a part: O as it is, four dims a step, with the row's maximum and sum
+                const size_t at = (size_t)itm.slot * 2 + k;
+                reinterpret_cast<float2*>(a.part_lse)[at * BM + r] = some ? make_float2(m_ref, l_run) : make_float2(-INFINITY, 0.f);
+                if (n_tiles > 0) {
+                    float4* part = reinterpret_cast<float4*>(a.part_o) + at * (DV / 4) * BM + r;
+#pragma unroll 1
+                    for (int c = 0; c < DV; c += 32) {
+                        float o[32];
+                        __syncwarp();
+                        tmem_ld32(tmem + lane_addr + col_o + c, o);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            part[(c / 4 + e) * BM] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    }
+                }
+            } else if (ti.rows_valid > 0 && ok && itm.parts == 1) {
 #pragma unroll 1
                 for (int c = 0; c < DV; c += 32) {
                     float o[32];
                     __syncwarp();
-                    if (ti.n_tiles > 0) {
+                    if (n_tiles > 0) {
                         tmem_ld32(tmem + lane_addr + col_o + c, o);
                     } else {
 #pragma unroll
@@ -489,25 +565,76 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
+// Adds up the parts of cut items: o = sum_p w_p O_p / sum_p w_p l_p with w_p = 2^(m_p -
+// M).  Block (cut item, query tile; 32 of the dims), thread = row: each load covers four
+// dims of 32 rows, 512 bytes in a row.
+template <bool F16>
+__global__ void __launch_bounds__(BM) latent_varlen_join_kernel(const PrefillArgs a) {
+    griddep_wait();
+    const Split sp = find_split(a);
+    const int x = blockIdx.x / 2, k = blockIdx.x % 2, r = threadIdx.x;
+    if (x >= sp.n_items - sp.n0) return;
+    const Item it = describe_item(a, sp.n_entries, sp.n0 + x, 0, sp.P, x * sp.P);
+    const TileInfo ti = k == 0 ? it.t0 : it.t1;
+    if (it.parts <= 1 || r >= ti.rows_valid) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_lse) + ((size_t)it.slot * 2 + k) * BM + r;
+    const float4* src = reinterpret_cast<const float4*>(a.part_o) + (((size_t)it.slot * 2 + k) * (DV / 4) + blockIdx.y * 8) * BM + r;
+    float M = -INFINITY, L = 0.f;
+    for (int p = 0; p < it.parts; ++p) M = fmaxf(M, ml[(size_t)p * 2 * BM].x);
+    float4 acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int p = 0; p < it.parts; ++p) {
+        const float2 s = ml[(size_t)p * 2 * BM];
+        const float w = s.y == 0.f ? 0.f : fast_exp2(s.x - M);
+        L += w * s.y;
+        if (w == 0.f) continue;                    // a part without a key has not written its O
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 o = src[((size_t)p * 2 * (DV / 4) + e) * BM];
+            acc[e].x = fmaf(w, o.x, acc[e].x);
+            acc[e].y = fmaf(w, o.y, acc[e].y);
+            acc[e].z = fmaf(w, o.z, acc[e].z);
+            acc[e].w = fmaf(w, o.w, acc[e].w);
+        }
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    const size_t orow = (size_t)(it.qs + ti.q0 + r) * a.Hq + it.h;
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * DV + blockIdx.y * 32);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        dst[e] = make_uint4(pack2<F16>(acc[2 * e].x * inv, acc[2 * e].y * inv), pack2<F16>(acc[2 * e].z * inv, acc[2 * e].w * inv),
+                            pack2<F16>(acc[2 * e + 1].x * inv, acc[2 * e + 1].y * inv),
+                            pack2<F16>(acc[2 * e + 1].z * inv, acc[2 * e + 1].w * inv));
+    if (blockIdx.y == 0 && a.lse) a.lse[orow] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
 template <bool F16>
 cudaError_t launch_t(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v, const CUtensorMap& tm_pe,
-                     const PrefillArgs& a, long max_items, cudaStream_t stream) {
+                     const PrefillArgs& a, cudaStream_t stream) {
     static SmemLimit limit;
-    const cudaError_t e = limit.set(reinterpret_cast<const void*>(latent_varlen_kernel<F16>), SMEM_BYTES);
+    cudaError_t e = limit.set(reinterpret_cast<const void*>(latent_varlen_kernel<F16>), SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    const long sms = a.num_sms > 0 ? a.num_sms : 148;
-    const long grid = max_items < sms ? max_items : sms;    // persistent: one CTA per SM
-    if (grid <= 0) return cudaSuccess;
-    latent_varlen_kernel<F16><<<(unsigned)grid, NUM_THREADS, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, tm_pe, a);
-    return cudaGetLastError();
+    latent_varlen_kernel<F16><<<(unsigned)a.grid, NUM_THREADS, SMEM_BYTES, stream>>>(tm_q, tm_k, tm_v, tm_pe, a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || a.part_o == nullptr) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * a.grid, DV / 32);
+    cfg.blockDim = dim3(BM);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, latent_varlen_join_kernel<F16>, a);
 }
 
 }  // namespace
 
 cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
-                                 const CUtensorMap& tm_pe, const PrefillArgs& a, long max_items, cudaStream_t stream) {
-    return a.f16 ? launch_t<true>(tm_q, tm_k, tm_v, tm_pe, a, max_items, stream)
-                 : launch_t<false>(tm_q, tm_k, tm_v, tm_pe, a, max_items, stream);
+                                 const CUtensorMap& tm_pe, const PrefillArgs& a, cudaStream_t stream) {
+    return a.f16 ? launch_t<true>(tm_q, tm_k, tm_v, tm_pe, a, stream) : launch_t<false>(tm_q, tm_k, tm_v, tm_pe, a, stream);
 }
 
 int latent_varlen_take_device_error() {

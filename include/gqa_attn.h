@@ -558,7 +558,10 @@ gqa_status attn_latent_gather(const void* kv_cache, const int32_t* cu_seqlens_kv
  *   k, v  [total_kv, H, 128], strided (halves of one projection)
  *   k_pe  [total_kv, 64], strided (the end of latent rows; head_stride is not used)
  *   o     [total_q, H, 128], lse [total_q, H] or NULL
- *   workspace  attn_latent_varlen_workspace_size bytes, 16-byte aligned
+ *   workspace  attn_varlen_workspace_size(B, total_q, H, H) bytes, 16-byte aligned;
+ *         with attn_latent_varlen_workspace_size bytes the items that do not fill a last
+ *         round of CTAs are cut along the keys and joined (results agree within the
+ *         usual tolerance).  Calls sharing one must not overlap on the GPU
  * Data 16-byte aligned, strides multiples of 8 elements.  o, lse and the workspace
  * may overlap nothing that is read, nor one another.
  */

@@ -110,8 +110,9 @@ def test_varlen_argument_checks(lib):
                 dict(ck=off(at(5), 2)), dict(k=rows(off(at(2), 8), 1024, 256)), dict(v=rows(at(2), 1028, 256)),
                 dict(pe=rows(at(3), 580)), dict(ws=off(at(8), 8))):
         assert varlen(lib, **bad) == MISALIGNED, bad
-    need = lib.attn_latent_varlen_workspace_size(2, 10, 4)
-    assert need > 0
+    need = lib.attn_varlen_workspace_size(2, 10, 4, 4)      # the least; the rest is for cut items
+    assert 0 < need < lib.attn_latent_varlen_workspace_size(2, 10, 4)
+    assert lib.attn_latent_varlen_workspace_size(2, 1 << 20, 128) < 1 << 20      # many rounds: nothing is cut
     assert varlen(lib, n=need - 1) == WORKSPACE and varlen(lib, ws=None) == WORKSPACE
     assert varlen(lib, tq=(1 << 30) - 1, H=400, n=1 << 40) == UNSUPPORTED
     assert varlen(lib, tq=0) == 0 and varlen(lib, tq=0, q=None, o=None, lse=None, ws=None, n=0) == 0

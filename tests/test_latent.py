@@ -301,6 +301,48 @@ def test_expanded(g, nq, lens, H, dtype):
     varlen_check(g, c, causal=False)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("nq,lens,H", [
+    ([300], [5000], 3),                                       # six items, ten parts each
+    ([1], [9001], 1),                                         # one row
+    ([700, 3, 129], [3000, 2500, 1100], 20),                  # a tail behind whole rounds, shorter requests in it
+    ([200, 50], [100, 2000], 5),                              # rows without a key among cut items
+    ([2048, 1], [2048, 4000], 19),
+])
+def test_expanded_cut_along_the_keys(g, nq, lens, H, dtype):
+    c = varlen_case(torch.Generator().manual_seed(sum(lens) + H), nq, lens, H, DT[dtype])
+    o, lse = varlen_check(g, c)
+    varlen_check(g, c, causal=False)
+    # the least workspace: nothing is cut
+    ws = torch.empty(g.attn_varlen_workspace_size(len(nq), sum(nq), H, H), dtype=torch.uint8, device="cuda")
+    o2, lse2 = g.attn_fwd_latent_varlen(c["q"], c["k"], c["v"], c["pe"], c["cq"], c["ck"], workspace=ws)
+    for b, h, rows, ref in varlen_refs(c):
+        check(o2[rows, h], lse2[rows, h], ref, "uncut, request %d head %d" % (b, h))
+    o3, lse3 = g.attn_fwd_latent_varlen(c["q"], c["k"], c["v"], c["pe"], c["cq"], c["ck"])
+    assert torch.equal(o, o3) and torch.equal(lse, lse3)
+
+
+def test_expanded_in_a_graph(g):
+    """A captured call follows new offsets, lengths and values, cut or not."""
+    gen = torch.Generator().manual_seed(23)
+    c = varlen_case(gen, [200, 56], [3000, 1000], 4, torch.bfloat16)
+    args = (c["q"], c["k"], c["v"], c["pe"], c["cq"], c["ck"])
+    g.attn_fwd_latent_varlen(*args)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o, lse = g.attn_fwd_latent_varlen(*args)
+    for nq, lens in (([200, 56], [3000, 1000]), ([1, 255], [60, 3940]), ([256, 0], [500, 3500])):
+        c["nq"], c["L"] = nq, lens
+        c["cq"].copy_(i32(sums(nq)))
+        c["ck"].copy_(i32(sums(lens)))
+        c["q"].copy_(randn(gen, 256, 4, 192))
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, h, rows, ref in varlen_refs(c):
+            check(o[rows, h], lse[rows, h], ref, "request %d head %d" % (b, h))
+    g.gqa_device_error()
+
+
 def test_expanded_many_items(g):
     """More items than CTAs, requests of every length."""
     nq = [1, 513, 130, 7, 255, 384, 2, 900]
