@@ -823,12 +823,9 @@ def _result(name, out, shape, dtype, device):
     return out, _data(name, out, dtype, shape, device)
 
 
-def _workspace(workspace, need, device):
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+def _workspace(workspace, device):
     if not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != device:
         raise ValueError("workspace must be a contiguous tensor on %s" % device)
-    return workspace
 
 
 def attn_fwd_latent_varlen(q, k, v, k_pe, cu_seqlens_q, cu_seqlens_kv, causal=True, scale=None, out=None, lse=None,
@@ -841,7 +838,9 @@ def attn_fwd_latent_varlen(q, k, v, k_pe, cu_seqlens_q, cu_seqlens_kv, causal=Tr
     slices (halves of one projection, the end of latent rows: strides of multiples of
     8, other layouts are copied first).  cu_seqlens_q / cu_seqlens_kv and the mask as
     attn_fwd_varlen; scale None: 1/sqrt(192).
-    workspace: optional, attn_latent_varlen_workspace_size bytes.
+    workspace: optional, attn_latent_varlen_workspace_size bytes (with
+    attn_varlen_workspace_size(B, total_q, H, H) bytes at least, nothing is cut along
+    the keys to fill the GPU).
     Returns (o [total_q, H, 128], lse [total_q, H] float32).
     """
     _check_16_cuda("q", q, 3)
@@ -862,7 +861,13 @@ def attn_fwd_latent_varlen(q, k, v, k_pe, cu_seqlens_q, cu_seqlens_kv, causal=Tr
     out, po = _result("out", out, (total_q, H, LATENT_V), dt, dev)
     lse, pl = _result("lse", lse, (total_q, H), f32, dev)
     lib = _lib.load()
-    workspace = _workspace(workspace, lib.attn_latent_varlen_workspace_size(B, total_q, H), dev)
+    if workspace is None:
+        # short calls are never cut along the keys and need the plan's bytes alone
+        size = lib.attn_latent_varlen_workspace_size if total_kv >= 1024 else lib.attn_varlen_workspace_size
+        workspace = torch.empty(_on(dev, size, B, total_q, H, *((H,) if total_kv < 1024 else ())), dtype=torch.uint8,
+                                device=dev)
+    else:
+        _workspace(workspace, dev)
     st = _on(dev, lib.attn_fwd_latent_varlen, q.data_ptr(), ctypes.byref(rk), ctypes.byref(rv), ctypes.byref(rp), cq, ck,
              po, pl, B, total_q, total_kv, H, 1 if causal else 0, resolve_scale(scale, dq), _DTYPES[dt],
              workspace.data_ptr(), workspace.numel() * workspace.element_size(), _raw_stream(dev))
@@ -903,9 +908,9 @@ def attn_fwd_latent_paged(q, kv_cache, cu_seqlens_q, cache_seqlens, block_table,
     lse, pl = _result("lse", lse, (total_q, H), f32, dev)
     lib = _lib.load()
     if workspace is None:
-        workspace = _workspace(None, _on(dev, lib.attn_latent_paged_workspace_size, B, total_q, H), dev)
+        workspace = torch.empty(_on(dev, lib.attn_latent_paged_workspace_size, B, total_q, H), dtype=torch.uint8, device=dev)
     else:
-        _workspace(workspace, 0, dev)
+        _workspace(workspace, dev)
     st = _on(dev, lib.attn_fwd_latent_paged, q.data_ptr(), pc, cq, sl, bt, page_size, po, pl, B, total_q, H, num_pages,
              max_pages, 1 if causal else 0, float(scale), _DTYPES[dt], workspace.data_ptr(),
              workspace.numel() * workspace.element_size(), _raw_stream(dev))
@@ -915,7 +920,7 @@ def attn_fwd_latent_paged(q, kv_cache, cu_seqlens_q, cache_seqlens, block_table,
 
 
 def attn_latent_varlen_workspace_size(B, total_q, H):
-    """Workspace bytes of attn_fwd_latent_varlen."""
+    """Workspace bytes of attn_fwd_latent_varlen on the current device."""
     return int(_lib.load().attn_latent_varlen_workspace_size(B, total_q, H))
 
 

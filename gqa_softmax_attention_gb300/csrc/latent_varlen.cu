@@ -70,7 +70,7 @@ static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 // the fewest tile times ceil(tail P / grid) (n / P + 2), 2 for a part's own start and end, if
 // that saves more than the joining costs (kJoinTiles); from kMaxRounds rounds on the
 // tail is short against the rest.
-constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 32;
+constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 16;
 struct Split {
     int n_entries, n_items, n0, P;       // items [n0, n_items) are cut
     __device__ __forceinline__ int claims() const { return n0 + (n_items - n0) * P; }
@@ -190,7 +190,10 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         fence_mbar_init();
     }
     Split* split = reinterpret_cast<Split*>(smem + OFF_SPLIT);
-    if (threadIdx.x == 32 * WARP_LOAD) *split = find_split(a);
+    if (threadIdx.x == 32 * WARP_LOAD) {
+        *split = find_split(a);
+        if (blockIdx.x == 0 && a.part_o) a.work[2] = split->P;     // the header's last word, for the joining kernel
+    }
     if (warp == WARP_MMA) {
         tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish();
@@ -571,10 +574,12 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 template <bool F16>
 __global__ void __launch_bounds__(BM) latent_varlen_join_kernel(const PrefillArgs a) {
     griddep_wait();
-    const Split sp = find_split(a);
+    const int P = a.work[2];
+    if (P <= 1) return;
     const int x = blockIdx.x / 2, k = blockIdx.x % 2, r = threadIdx.x;
-    if (x >= sp.n_items - sp.n0) return;
-    const Item it = describe_item(a, sp.n_entries, sp.n0 + x, 0, sp.P, x * sp.P);
+    const int n_entries = *a.n_entries, n_items = n_entries * a.Hq, tail = n_items % a.grid;
+    if (x >= tail) return;
+    const Item it = describe_item(a, n_entries, n_items - tail + x, 0, P, x * P);
     const TileInfo ti = k == 0 ? it.t0 : it.t1;
     if (it.parts <= 1 || r >= ti.rows_valid) return;
     const float2* ml = reinterpret_cast<const float2*>(a.part_lse) + ((size_t)it.slot * 2 + k) * BM + r;

@@ -591,8 +591,8 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
                                  float scale, int dtype, void* workspace, size_t workspace_bytes,
                                  gqa_stream_t stream);
 
-/* Workspace bytes of the two attention calls (0 for sizes that they refuse); the
- * absorbed form's depends on the current device. */
+/* Workspace bytes of the two attention calls on the current device (0 for sizes that
+ * they refuse). */
 size_t attn_latent_varlen_workspace_size(int B, int total_q, int H);
 size_t attn_latent_paged_workspace_size(int B, int total_q, int H);
 
