@@ -1026,8 +1026,7 @@ gqa_status attn_latent_norm_rope_paged(const gqa_head_rows* q_pe, const gqa_head
     a.interleaved = rope->interleaved ? 1 : 0;
     a.T = T; a.H = H;
     a.num_slots = (long)num_pages * page_size;
-    return gqa::launch_latent_append(a, dtype == GQA_FP16, sm_count(), reinterpret_cast<cudaStream_t>(stream)) ==
-                   cudaSuccess
+    return gqa::launch_latent_append(a, dtype == GQA_FP16, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GQA_OK
                : GQA_ERR_CUDA;
 }

@@ -299,7 +299,7 @@ struct LatentAppendArgs {
     int max_pos, interleaved, T, H;
     long num_slots;
 };
-cudaError_t launch_latent_append(const LatentAppendArgs& a, bool f16, int num_sms, cudaStream_t stream);
+cudaError_t launch_latent_append(const LatentAppendArgs& a, bool f16, cudaStream_t stream);
 struct LatentGatherArgs {
     const void* cache;              // [num_pages, page_size, kLatentRow]
     const int32_t* cu;              // [B + 1]
