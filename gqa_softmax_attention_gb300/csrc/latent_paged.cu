@@ -46,6 +46,13 @@
 // that lies in one range is written out directly; of one that is cut, each
 // piece leaves O, maximum and sum in FP32, at most two pieces a team, and
 // latent_join_kernel adds them up.
+//
+// Measured (bf16, pages of 64, queries of one token): 64 requests of 1K to 16K keys
+// take 104 to 110 us with 16 heads (625 MB once: 85 to 90 % of the copy rate; in pages of one
+// token, gathered, 178) and 178 to 188 us with 128 heads (850 TFLOP/s).  What
+// bounds the latter is the chain of a tile's loads, S^T, softmax and O^T through a ring two tiles
+// deep, 2450 cycles a tile where its MMAs read operands for 1970.  Two requests of 300
+// to 700 keys take 11 us, replayed from a graph.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
