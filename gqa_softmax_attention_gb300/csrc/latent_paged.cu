@@ -623,6 +623,10 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     } else {
         // ------------------------------------------------------------ softmax warps 0-3
         constexpr int HC = NR / 2;               // rows (columns of S^T) of a thread
+        // A float16 P below 2^-14 rounds to a multiple of 2^-24.  The reference stands six
+        // binades below the maximum, so that a weight is off by 2^-31 of the strongest at most
+        // (from the maximum itself 16383 keys 26 binades below one would lose their share).
+        constexpr float kLead = F16 ? 6.f : 0.f, kMost = kRescaleThreshold + kLead;
         const int row = threadIdx.x;             // this thread's row, where rows are meant
         const int key = warp * 16 + lane % 16, c0 = (lane / 16) * HC;   // its key of a tile and first column
         const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
@@ -657,6 +661,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
             }
             named_bar_sync(kSmBar, 128);
+            bool unset = false;                  // this row has seen infinite scores alone so far
             float sums[HC];
 #pragma unroll
             for (int c = 0; c < HC; ++c) sums[c] = 0.f;
@@ -692,9 +697,9 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 float top = -INFINITY;
 #pragma unroll
                 for (int c = 0; c < HC; c += 2) top = fmax3(top, s[c], s[c + 1]);
-                // The first tile gives every row that sees a key its reference;
-                // a row that sees none there sees none in later tiles either.
-                const bool keep = named_bar_and(kSmBar, 128, ok && k > 0 && !(top > kRescaleThreshold));
+                // The first tile gives every row that sees a key its reference (unless all
+                // its scores are -inf); a row that sees none there sees none in later tiles.
+                const bool keep = named_bar_and(kSmBar, 128, ok && k > 0 && !unset && !(top > kMost));
                 if (!keep) {
                     // column maxima over the tile's keys
                     half_warp_columns<HC, true>(s, lane);
@@ -705,11 +710,13 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                         const float d = fmaxf(fmaxf(cross[row], cross[NR + row]), fmaxf(cross[2 * NR + row], cross[3 * NR + row]));
                         const float old = ref[row];
                         float f = 1.f;
-                        if (old == -INFINITY || d > kRescaleThreshold) {
-                            const float m = d - neg_ref[row];         // neg_ref is 0 while there is no reference
+                        if (old == -INFINITY || d > kMost) {
+                            const float m = d - neg_ref[row] - kLead;     // neg_ref is 0 while there is no reference
                             f = old == -INFINITY ? 0.f : fast_exp2(old - m);
                             ref[row] = m;
                             neg_ref[row] = m == -INFINITY ? 0.f : -m;
+                            // (no reference, and the row sees keys of the next tile)
+                            unset = m == -INFINITY && limit[row] > (p.lt0 + k + 1) * BN;
                         }
                         factor[row] = f;
                     }

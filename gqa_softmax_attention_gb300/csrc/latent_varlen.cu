@@ -429,6 +429,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const uint32_t lane_addr = (uint32_t)((warp % 4) * 32) << 16;
         const uint32_t col_s = k == 0 ? COL_S0 : COL_S1, col_o = k == 0 ? COL_O0 : COL_O1;
         const float sl = a.scale_log2;
+        // As in latent_paged.cu: a float16 P keeps 2^-31 of the strongest weight.
+        constexpr float kLead = F16 ? 6.f : 0.f;
         int sf = 0;                  // S tiles taken so far (s_full parity)
         int n_done = 0;              // items with a tile finished (o_final parity)
         bool ok = true;
@@ -495,8 +497,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     const float mx_raw = fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3]));
                     const float mx = fast ? mx_raw * sl : mx_raw;
                     if (mx > m_ref + kRescaleThreshold) {
-                        alpha = fast_exp2(m_ref - mx);
-                        m_ref = mx;
+                        alpha = fast_exp2(m_ref - (mx - kLead));
+                        m_ref = mx - kLead;
                     }
                     const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
                     uint32_t pk[BN / 2];

@@ -651,6 +651,77 @@ def test_one_workspace_for_calls_in_turn(g):
         paged_check(g, c, workspace=ws)
 
 
+# A weight 2^-26 of the strongest keeps its share: n of them before one strong key.  P is 2^-20 (six binades of
+# room), which float16 has exactly.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("form", ["absorbed", "expanded"])
+def test_many_weak_keys_behind_a_strong_one(g, form, dtype):
+    dt, scale = DT[dtype], 26 * math.log(2.0) / 256
+    if form == "absorbed":
+        B, L, H, ps = 160, 16384, 16, 64                    # all requests read the same pages
+        rows = torch.zeros(L, ROW, dtype=dt, device="cuda")
+        rows[1:, :C] = 1.0
+        rows[0, C] = 16.0
+        q = torch.zeros(B, H, ROW, dtype=dt, device="cuda")
+        q[..., C] = 16.0
+        table = torch.arange(L // ps, dtype=torch.int32, device="cuda").expand(B, -1).contiguous()
+        o, lse = g.attn_fwd_latent_paged(q, rows.view(L // ps, ps, ROW), i32(list(range(B + 1))), i32([L] * B), table,
+                                         scale)
+        q, k, v = q[0], rows, rows[:, :C]
+    else:
+        B, L, H = 1, 16384, 2
+        kk = torch.zeros(L, H, NOPE, dtype=dt, device="cuda")
+        vv = torch.ones(L, H, V, dtype=dt, device="cuda")
+        pe = torch.zeros(L, R, dtype=dt, device="cuda")
+        pe[0, 0], vv[0] = 16.0, 0.0
+        q = torch.zeros(1, H, NOPE + R, dtype=dt, device="cuda")
+        q[..., NOPE] = 16.0
+        ws = torch.empty(g.attn_varlen_workspace_size(1, 1, H, H), dtype=torch.uint8, device="cuda")   # keys uncut
+        o, lse = g.attn_fwd_latent_varlen(q, kk, vv, pe, i32([0, 1]), i32([0, L]), scale=scale, workspace=ws)
+        q, k, v = q[0], torch.cat([kk[:, 0], pe], 1), vv[:, 0]
+    torch.cuda.synchronize()
+    ref = attend(q, k, v, torch.full((H,), L, device="cuda"), scale)
+    for b in range(B):
+        check(o[b], lse[b], ref, "request %d" % b)
+
+
+# Rotated dims of -inf hide a key from queries that are positive there, whole tiles of keys too.
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_absorbed_keys_hidden_by_infinity(g, dtype):
+    gen = torch.Generator().manual_seed(31)
+    dt = DT[dtype]
+    lens, hidden, ps, H = [200, 64, 130, 20000], [70, 63, 129, 19000], 8, 40
+    c = paged_case(gen, [1] * 4, lens, H, ps, dt)
+    c["q"][..., C] = c["q"][..., C].abs() + 0.5
+    flat = c["cache"].flatten(0, 1)
+    places = []
+    for b, (n, x) in enumerate(zip(lens, hidden)):
+        t = torch.arange(n, device="cuda")
+        at = c["table"][b].long()[t // ps] * ps + t % ps
+        flat[at[:x], C] = -math.inf
+        places.append(at[x:])
+    o, lse = g.attn_fwd_latent_paged(c["q"], c["cache"], c["cu"], c["lens"], c["table"], SCALE)
+    torch.cuda.synchronize()
+    for b, at in enumerate(places):
+        rows = flat[at]
+        check(o[b], lse[b], attend(c["q"][b], rows, rows[:, :C], torch.full((H,), lens[b], device="cuda"), SCALE),
+              "request %d" % b)
+
+
+def test_expanded_keys_hidden_by_infinity(g):
+    gen = torch.Generator().manual_seed(32)
+    n, L, H, x = 20, 300, 3, 200
+    q = randn(gen, n, H, NOPE + R)
+    q[..., NOPE] = q[..., NOPE].abs() + 0.5
+    k, v, pe = randn(gen, L, H, NOPE), randn(gen, L, H, V), randn(gen, L, R)
+    pe[:x, 0] = -math.inf
+    o, lse = g.attn_fwd_latent_varlen(q, k, v, pe, i32([0, n]), i32([0, L]))
+    torch.cuda.synchronize()
+    at = torch.arange(n, device="cuda") + (L - n) - x
+    for h in range(H):
+        check(o[:, h], lse[:, h], attend(q[:, h], torch.cat([k[x:, h], pe[x:]], 1), v[x:, h], at, SCALE), "head %d" % h)
+
+
 def test_empty_calls(g):
     """No query, no key, no token: shapes come back, nothing runs."""
     z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")
