@@ -882,13 +882,14 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
 // Adds up the pieces of the row groups that were cut: o = sum_p w_p O_p / sum_p
 // w_p l_p with w_p = 2^(m_p - M).  Block (CTA of the team's first piece, JR rows of it,
-// 128 dims): a warp per row for the weights, then thread = dim, U pieces at a time,
-// the first of them on their way while the weights are formed.  JR is small where a
+// 128 dims): 128 / JR lanes per row for the weights, then thread = dim, U pieces at a
+// time, the first of them on their way while the weights are formed (with a warp per row
+// and four rows in turn the weights took 5 us of the kernel's 6).  JR is small where a
 // group has few rows, because few groups of many pieces (one to four long requests)
 // would leave all the reading to a few SMs.
 template <int NR, bool F16>
 __global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs a) {
-    constexpr int JR = NR == 64 ? 16 : 4, U = 32 / JR;
+    constexpr int JR = NR == 64 ? 16 : 4, U = 32 / JR, LR = 128 / JR;
     griddep_wait();
     const int team = blockIdx.x / a.team, rank = blockIdx.x % a.team, r_first = blockIdx.y * JR;
     const int4 j = *reinterpret_cast<const int4*>(a.join + 4 * team);
@@ -897,7 +898,7 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs a) {
     if (n <= 0 || r0 >= j.z) return;
     __shared__ float w_s[256][JR];                 // n <= teams <= 256
     __shared__ float inv[JR];
-    const int d = threadIdx.x, lane = d % 32, warp = d / 32;
+    const int d = threadIdx.x, lane = d % LR, r = d / LR;     // of the weights' row
     auto slot = [&](int p) { return 2 * ((team + p) * a.team + rank) + (p == 0 ? j.w : 0); };
     const float4* src = reinterpret_cast<const float4*>(a.part_o) + (blockIdx.z * (NR / 4) + r_first / 4) * 128 + d;
     float4 o[U][JR / 4];
@@ -908,31 +909,28 @@ __global__ void __launch_bounds__(128) latent_join_kernel(const LatentArgs a) {
             for (int g = 0; g < JR / 4; ++g)
                 if (p0 + u < n) o[u][g] = src[(size_t)slot(p0 + u) * (NJ * NR / 4) * 128 + g * 128];
     };
+    const float2* ml = a.part_ml + r_first + r;
+    const float2 first = lane < n ? ml[(size_t)slot(lane) * NR] : make_float2(-INFINITY, 0.f);
     load(0);
+    float M = first.x, L = 0.f;
+    for (int p = lane + LR; p < n; p += LR) {
+        w_s[p][r] = ml[(size_t)slot(p) * NR].x;
+        M = fmaxf(M, w_s[p][r]);
+    }
 #pragma unroll
-    for (int r = warp; r < JR; r += 4) {
-        const float2* ml = a.part_ml + r_first + r;
-        float M = -INFINITY, L = 0.f;
-        for (int p = lane; p < n; p += 32) {
-            const float m = ml[(size_t)slot(p) * NR].x;
-            w_s[p][r] = m;
-            M = fmaxf(M, m);
-        }
+    for (int x = LR / 2; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    for (int p = lane; p < n; p += LR) {
+        const float l = p == lane ? first.y : ml[(size_t)slot(p) * NR].y;
+        const float w = l == 0.f ? 0.f : fast_exp2((p == lane ? first.x : w_s[p][r]) - M);
+        w_s[p][r] = w;
+        L += w * l;
+    }
 #pragma unroll
-        for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-        for (int p = lane; p < n; p += 32) {
-            const float l = ml[(size_t)slot(p) * NR].y;
-            const float w = l == 0.f ? 0.f : fast_exp2(w_s[p][r] - M);
-            w_s[p][r] = w;
-            L += w * l;
-        }
-#pragma unroll
-        for (int x = 16; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-        if (lane == 0) {
-            inv[r] = L != 0.f ? 1.f / L : 0.f;
-            if (blockIdx.z == 0 && r0 + r < j.z && a.lse)
-                a.lse[(size_t)j.y + r0 + r] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
-        }
+    for (int x = LR / 2; x > 0; x >>= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+    if (lane == 0) {
+        inv[r] = L != 0.f ? 1.f / L : 0.f;
+        if (blockIdx.z == 0 && r0 + r < j.z && a.lse)
+            a.lse[(size_t)j.y + r0 + r] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
     }
     __syncthreads();
     float4 acc[JR / 4];
