@@ -49,7 +49,7 @@
 //
 // Measured (bf16, pages of 64, queries of one token): 64 requests of 1K to 16K keys
 // take 104 to 110 us with 16 heads (625 MB once: 85 to 90 % of the copy rate; in pages of one
-// token, gathered, 178) and 178 to 188 us with 128 heads (850 TFLOP/s).  What
+// token, gathered, 178) and 174 to 180 us with 128 heads (860 TFLOP/s).  What
 // bounds the latter is the chain of a tile's loads, S^T, softmax and O^T through a ring two tiles
 // deep, 2450 cycles a tile where its MMAs read operands for 1970.  Two requests of 300
 // to 700 keys take 11 us, replayed from a graph.
@@ -123,10 +123,13 @@ __device__ __forceinline__ void request_rows(const LatentArgs& a, int b, int& qs
 }
 
 // A row group counts kStartTiles tiles more than it has: a piece's start and end cost a
-// team about as much, and a range of many short row groups would take longer than
-// one of a single long one (64 requests of 1K to 16K keys, 128 heads: ranges of four
-// pieces ended 24 us after those of one, of 155).
-constexpr int kStartTiles = 2;
+// team about as much (4 us at 64 rows a CTA, 2.6 at 16, where a tile takes 1.2 and 1.4),
+// and a range of many short row groups would take longer than one of a single long one
+// (64 requests of 1K to 16K keys, 128 heads, none counted: ranges of four pieces ended
+// 24 us after those of one, of 155).  23 drafts and 9 steps of 40 heads: 73 us with 1, 68
+// with 2, 65 with 3, 62 to 66 with 4; 24 chunks of 4 queries by 64 heads 91, 86 and 87
+// with 2 to 4.
+constexpr int kStartTiles = 3;
 
 // A stretch of one row group's tiles, and the walk over those of a range.
 struct Piece {

@@ -512,9 +512,10 @@ gqa_status attn_qk_norm_rope_paged(const gqa_head_rows* q, const gqa_head_rows* 
  *   absorbed  attn_fwd_latent_paged over the cache itself: with the key projection W_k
  *             [128, 512] of a head, q = [W_k^T q_nope, q_pe], and the value
  *             projection applied to its output (decode steps, drafted tokens)
- * dtype (gqa_dtype) names the type of every 16-bit tensor of a call.  A key value
- * that is infinite or no number makes every query of a request that shares a row
- * block with one that sees it undefined, as in the other attention calls.
+ * dtype (gqa_dtype) names the type of every 16-bit tensor of a call.  A cached or key
+ * value that is no number, or an infinite one among the latents or values, makes every
+ * query of a request that shares a row block with one that sees it undefined, as in the
+ * other attention calls; an infinite key dim that makes a score -inf hides its key.
  */
 
 /*
