@@ -1177,10 +1177,9 @@ static LatentParts latent_parts(int B, int total_q, int H) {
     p.o = slots * gqa::kLatentRows * gqa::kLatentDim * sizeof(float);
     return p;
 }
-constexpr int kLatentMaxB = 16384;      // their tile counts are summed in shared memory
 
 size_t attn_latent_paged_workspace_size(int B, int total_q, int H) {
-    if (B <= 0 || B > kLatentMaxB || total_q < 0 || total_q >= kMaxSeq || H <= 0 || !latent_rows_ok(total_q, H)) return 0;
+    if (B <= 0 || B > gqa::kLatentMaxB || total_q < 0 || total_q >= kMaxSeq || H <= 0 || !latent_rows_ok(total_q, H)) return 0;
     const LatentParts p = latent_parts(B, total_q, H);
     return p.join + p.ml + p.o;
 }
@@ -1219,7 +1218,7 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     if (B <= 0 || total_q < 0 || H <= 0 || page_size <= 0 || num_pages <= 0 || max_pages <= 0) return GQA_ERR_INVALID_ARG;
     if (total_q >= kMaxSeq || (long)max_pages * page_size >= kMaxSeq) return GQA_ERR_INVALID_ARG;
     if (!std::isfinite(scale) || (dtype != GQA_BF16 && dtype != GQA_FP16)) return GQA_ERR_INVALID_ARG;
-    if (B > kLatentMaxB || !latent_rows_ok(total_q, H) || (long)num_pages * page_size >= (1L << 31))
+    if (B > gqa::kLatentMaxB || !latent_rows_ok(total_q, H) || (long)num_pages * page_size >= (1L << 31))
         return GQA_ERR_UNSUPPORTED;
     if (total_q == 0) return GQA_OK;                 // (empty tensors have no address)
     if (!q || !kv_cache || !cu_seqlens_q || !cache_seqlens || !block_table || !o) return GQA_ERR_INVALID_ARG;

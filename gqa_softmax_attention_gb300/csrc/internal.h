@@ -312,6 +312,7 @@ cudaError_t launch_latent_gather(const LatentGatherArgs& a, cudaStream_t stream)
 // Packed queries [total_q, H, kLatentRow] over a paged latent cache
 // (latent_paged.cu; see attn_fwd_latent_paged).
 constexpr int kLatentRows = 64;     // most (query, head) rows of a CTA
+constexpr int kLatentMaxB = 16384;  // most requests: their tiles are summed in shared memory, 8 bytes each
 struct LatentArgs {
     const int32_t* cu_q;            // [B + 1]
     const int32_t* lens;            // [B]

@@ -104,6 +104,7 @@ struct LCfg {
     // The shared dims' slot of a tile is free when its second slot of latents is: that one
     // was last used by a tile that came after the shared dims' last one, or with it.
     static_assert((NP == 4 && NT == 2) || (NP == 5 && NT == 3), "slots that come free together");
+    static_assert(kLatentMaxB * 8 <= NP * HALF, "prefix sums over the ring");
     static_assert(OFF_KV % 1024 == 0 && OFF_P % 1024 == 0, "swizzle atoms");
     static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };

@@ -582,6 +582,21 @@ def test_expanded_blocks_without_a_partner(g):
 
 # ---------------------------------------------------------------- odd calls
 
+@pytest.mark.parametrize("H", [8, 40])
+def test_absorbed_most_requests(g, H):
+    """16384 requests of one key: its latent, whatever the query.  One more is refused."""
+    gen = torch.Generator().manual_seed(29)
+    B, ps = 16384, 8
+    cache, q = randn(gen, 100, ps, ROW), randn(gen, 64, H, ROW).repeat(B // 64, 1, 1)
+    table = torch.randint(0, 100, (B, 1), generator=gen).int().cuda()
+    cu, lens = torch.arange(B + 1).int().cuda(), torch.ones(B, dtype=torch.int32, device="cuda")
+    o, _ = g.attn_fwd_latent_paged(q, cache, cu, lens, table, SCALE)
+    assert torch.equal(o, cache[table[:, 0].long(), 0, :C][:, None].expand(B, H, C))
+    with pytest.raises((ValueError, RuntimeError), match="unsupported"):
+        g.attn_fwd_latent_paged(q, cache, torch.arange(B + 2).int().cuda(), torch.ones(B + 1).int().cuda(),
+                                torch.zeros(B + 1, 1).int().cuda(), SCALE)
+
+
 def test_absorbed_many_requests(g):
     """More requests than threads of a CTA, most of them short or without queries."""
     gen = torch.Generator().manual_seed(30)
