@@ -611,16 +611,10 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                         kt += c_all;
                         vt += c_all;
                         if (ok) {
-                            mma_commit(o_final(0));
-                            mma_commit(o_final(1));
+                            if (c0 > 0) mma_commit(o_final(0));
+                            if (c1 > 0) mma_commit(o_final(1));
                         }
                     }
-                }
-                // one o_final phase per Q tile and item (also for a tile with no key):
-                // arrives when every MMA of the item has completed
-                if (lane == 0 && ok && c_all == 0) {
-                    mma_commit(o_final(0));
-                    mma_commit(o_final(1));
                 }
                 ok = __shfl_sync(0xffffffffu, ok, 0);
             }
@@ -686,7 +680,7 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
         const uint32_t stage = sb + C::OFF_STAGE + k * C::SUB_BYTES;   // this warpgroup's output box
         const float sl = a.scale_log2;
         int sf = 0;                  // S tiles taken so far (s_full parity)
-        int n_done = 0;              // items finished (o_final parity)
+        int n_done = 0;              // items with a visited tile finished (o_final parity)
         bool ok = true;
         for (int rr = 0;; ++rr) {
             // The item record: the first chunk's tile flags, the first visited
@@ -850,12 +844,16 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
             }
             // ---- epilogue of this Q tile: the last P V done.  It runs even after
             // a wait gave up, so that the warpgroup's named barriers below see
-            // all four warps.
-            if (ok) {
+            // all four warps.  o_final(k) has one phase for every item of which
+            // this Q tile visits a key tile (it arrives when every MMA of the
+            // tile has completed) and none for the others: that phase waits for
+            // no softmax, so the MMA thread could end it, and with it the
+            // barrier's parity, before the phase of the item before was seen.
+            if (ok && it > 0) {
                 ok = __all_sync(0xffffffffu, mbar_wait(o_final(k), n_done & 1, abort_flag));
+                ++n_done;
                 if (ok) tc_fence_after();
             }
-            ++n_done;
             const bool row_ok = PACKED ? (r < g * qpb && r / g < ti.rows_valid) : r < ti.rows_valid;
             // this row's place in o [.., D] and lse
             const size_t orow = PACKED ? (size_t)(itm.qs + row_q) * a.Hq + itm.hq + r % g
