@@ -479,7 +479,7 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 if (__all_sync(0xffffffffu, m_ref != -INFINITY)) {
                     uint32_t pk[BN / 2];
                     rs = exp_row<F16>(s, fa, m_ref, pk);
-                    if (!__any_sync(0xffffffffu, !(rs <= (F16 ? 65504.f : kSumLimit)))) {
+                    if (!__any_sync(0xffffffffu, !(rs <= sum_limit<F16>()))) {
                         tmem_st64(tmem + lane_addr + col_s, pk);
                         done = true;
                     }

@@ -35,11 +35,11 @@
 // max exceeds it by more than kRescaleThreshold (log2 units), so most tiles
 // touch no O at all.  Once every row of a warp has a reference, a tile is
 // exponentiated against it without taking its row max; only a row sum above
-// kSumLimit (2^32) sends the warp back to the scores in TMEM for the max.  The
-// result is exact either way: O and l are accumulated against the same
-// reference.  A rescale of O_k before PV of tile i needs PV of tile i-1
-// complete; that is implied by S_k of tile i having landed, since its commit
-// follows that PV in the MMA thread's order.
+// sum_limit (2^32; 65504, the largest float16, where P is one) sends the warp back
+// to the scores in TMEM for the max.  The result is exact either way: O and l are
+// accumulated against the same reference.  A rescale of O_k before PV of tile i
+// needs PV of tile i-1 complete; that is implied by S_k of tile i having landed,
+// since its commit follows that PV in the MMA thread's order.
 //
 // Key tiles holding no visible key (beyond the causal bound or fully padded)
 // are never loaded, and tiles past Q0's causal bound are skipped for Q0.
@@ -785,13 +785,13 @@ prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__
                 // Once every row of the warp has a reference max, the tile is
                 // exponentiated against it directly, with no row max: P and l
                 // stay exact relative to the reference, and fp32 / 16-bit P hold
-                // values up to the row-sum limit.  A row whose sum passes the
+                // values up to the row-sum limit (no P is larger than the sum).  A row whose sum passes the
                 // limit (or is not finite) sends the warp to the path below.
                 bool done = false;
                 if (__all_sync(0xffffffffu, m_ref != -INFINITY)) {
                     uint32_t pk[BN / 2];
                     rs = exp_row<F16>(s, fa, m_ref, pk);
-                    if (!__any_sync(0xffffffffu, !(rs <= kSumLimit))) {
+                    if (!__any_sync(0xffffffffu, !(rs <= sum_limit<F16>()))) {
                         tmem_st64(tmem + lane_addr + col_s, pk);   // P over the first 64 columns of S
                         done = true;
                     }
