@@ -14,8 +14,8 @@ namespace {
 // lengths into [0, kv_cap], so malformed metadata can give wrong results but
 // no access out of range; entries past max_entries are dropped.  The
 // requests are then ordered by estimated cost, heaviest first (a counting
-// sort over NBUCKET cost buckets), each request's blocks together and its
-// heaviest (last) block first.
+// sort over NBUCKET cost buckets, requests of one bucket in their own order),
+// each request's blocks together and its heaviest (last) block first.
 constexpr int NBUCKET = 2048;
 // SM time of one cached key of a decode step against one plan cost unit (see
 // the end of varlen_plan_kernel), as the two kernels run side by side: the
@@ -55,6 +55,7 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
     __shared__ unsigned long long pre_cost, dec_keys;   // listed blocks' cost; decode steps' cached keys
     __shared__ int base, most_tiles;                    // most key tiles that a block visits
     __shared__ int bucket[NBUCKET];
+    __shared__ int chain[NBUCKET], group_next[1024], group_sum[1024];   // step 3
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     // pairs (flag bit 2): an entry covers two consecutive row blocks
     const bool pairs = (paged & 4) != 0;
@@ -70,7 +71,10 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         pre_cost = 0;
         dec_keys = 0;
     }
-    for (int i = threadIdx.x; i < NBUCKET; i += 1024) bucket[i] = 0;
+    for (int i = threadIdx.x; i < NBUCKET; i += 1024) {
+        bucket[i] = 0;
+        chain[i] = -1;
+    }
     __syncthreads();
     // 1. entries in request order
     for (int b0 = 0; b0 < B; b0 += 1024) {
@@ -177,13 +181,59 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         bucket[c2] = start + n1;
     }
     __syncthreads();
-    // 3. each request reserves its range; then every block takes its place
-    for (int e = threadIdx.x; e < n; e += 1024) {
-        int4* src = reinterpret_cast<int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
-        const int4 e0 = src[0], e1 = src[1];
-        if (e0.y == 0) src[1].w = atomicAdd(&bucket[e1.z], min((e0.w + span - 1) / span, n - e));
+    // 3. each request reserves its range, within a bucket in the order of the
+    // requests; then every block takes its place.  (Ranges taken by atomics alone stood
+    // in whatever order the warps came: which items a call cuts along the keys, and so
+    // the last bits of their results, changed from run to run.)  1024 entries at a
+    // time: a warp's requests of one bucket form a group, its first lane's; the groups
+    // of a bucket are chained in any order, and each adds up those of lower threads.
+    for (int e_first = 0; e_first < n; e_first += 1024) {
+        const int e = e_first + threadIdx.x;
+        int key = -1, cnt = 0;
+        if (e < n) {
+            const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
+            const int4 e0 = src[0], e1 = src[1];
+            if (e0.y == 0) {
+                key = e1.z;
+                cnt = min((e0.w + span - 1) / span, n - e);
+            }
+        }
+        const unsigned same = __match_any_sync(0xffffffffu, key);
+        const int leader = __ffs(same) - 1;
+        int before, sum;                               // blocks of the group's lower lanes, of all
+        if (__all_sync(0xffffffffu, cnt <= 1)) {
+            before = __popc(same & ((1u << lane) - 1));
+            sum = __popc(same);
+        } else {
+            before = sum = 0;
+            for (unsigned rest = __ballot_sync(0xffffffffu, cnt > 0); rest != 0; rest &= rest - 1) {
+                const int l = __ffs(rest) - 1, c = __shfl_sync(0xffffffffu, cnt, l);
+                if ((same >> l) & 1) {
+                    sum += c;
+                    before += l < lane ? c : 0;
+                }
+            }
+        }
+        const bool leads = key >= 0 && lane == leader;
+        if (leads) {
+            group_sum[threadIdx.x] = sum;
+            group_next[threadIdx.x] = atomicExch(&chain[key], (int)threadIdx.x);
+        }
+        __syncthreads();
+        int start = 0;
+        if (leads) {
+            start = bucket[key];
+            for (int t = chain[key]; t >= 0; t = group_next[t]) start += t < (int)threadIdx.x ? group_sum[t] : 0;
+        }
+        start = __shfl_sync(0xffffffffu, start, leader);
+        if (key >= 0) tmp[(size_t)e * ot::ENTRY_INTS + 7] = start + before;
+        __syncthreads();
+        if (leads) {
+            atomicAdd(&bucket[key], sum);
+            chain[key] = -1;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     for (int e = threadIdx.x; e < n; e += 1024) {
         const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
         const int4 e0 = src[0], e1 = src[1];
