@@ -1073,7 +1073,8 @@ static bool make_rows_map(CUtensorMap* map, const Rows& r, int box_t, bool f16) 
 // CTAs of an expanded call, and the bytes of its part slots: none where the query
 // blocks alone fill so many rounds of CTAs that no tail is cut.
 static int latent_varlen_grid(int B, int total_q, int H) {
-    const long n = sm_count() > 0 ? sm_count() : 148, items = (long)varlen_max_entries(B, total_q, 128) * H;
+    const long n = std::min(sm_count() > 0 ? sm_count() : 148, gqa::kLatentMaxGrid);
+    const long items = (long)varlen_max_entries(B, total_q, 128) * H;
     return (int)(items < n ? items : n);
 }
 static size_t latent_varlen_parts(int B, int total_q, int H) {
@@ -1136,9 +1137,6 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
         return GQA_ERR_CUDA;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     int32_t* ws = static_cast<int32_t*>(workspace);
-    if (gqa::launch_varlen_plan(cu_seqlens_q, cu_seqlens_kv, false, B, 128, 1, a.causal, total_q, total_kv,
-                                ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e, s, false, true) != cudaSuccess)
-        return GQA_ERR_CUDA;
     // heads whose keys and values (512 bytes a token and head) take half of L2
     const long per_head = total_kv > 0 ? (long)total_kv * 512 : 512;
     a.head_group = (int)std::max(1L, std::min((long)H, (64L << 20) / per_head));
@@ -1147,6 +1145,10 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
         a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
         a.part_lse = a.part_o + (size_t)a.grid * gqa::kLatentPartSlots * 2 * 128 * gqa::kLatentV;
     }
+    if (gqa::launch_varlen_plan(cu_seqlens_q, cu_seqlens_kv, false, B, 128, 1, a.causal, total_q, total_kv,
+                                ws + 4 + (size_t)max_e * 8, ws + 4, ws, max_e, s, false, true, 0, false, 0, 1, -1, -1,
+                                {cut ? a.grid : 0, H, a.head_group}) != cudaSuccess)
+        return GQA_ERR_CUDA;
     return gqa::launch_latent_varlen(tq, tk, tv, tp, a, s) == cudaSuccess ? GQA_OK : GQA_ERR_CUDA;
 }
 

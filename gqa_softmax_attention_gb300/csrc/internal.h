@@ -109,12 +109,18 @@ __host__ __device__ constexpr bool cut_pays(long tiles, long blocks) { return ti
 // is no decode step); fp8: the caches are e4m3 bytes.  With split_grid (the
 // chunk kernel's CTAs) n_entries[3] receives in how many parts each block's
 // keys are cut so that few blocks over long caches still fill those CTAs; wl and
-// wr, the window, bound the key tiles that a block visits.
+// wr, the window, bound the key tiles that a block visits.  With tail.grid set
+// n_entries[2] and [3] receive the tiles of a part and the parts of the cut items of
+// an expanded latent call.
+struct TailSplit {
+    int grid;                 // persistent CTAs; 0: nothing is cut
+    int H, head_group;        // items: groups of head_group heads, in each every entry with all the group's heads
+};
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single = false, bool pairs = false,
                                int grid = 0, bool fp8 = false, int split_grid = 0, int Hkv = 1, int wl = -1,
-                               int wr = -1);
+                               int wr = -1, const TailSplit& tail = {0, 0, 0});
 // tm_q / tm_o: {D, Hq, total_q} with a {64, g, qpb} box.  Packed: tm_k / tm_v
 // {D, Hkv, total_kv} with {64, 1, 128} and {64, 1, 128 or 64 (D = 256)} boxes.
 // Paged: the caches as {64, 8, D / 64, pages * page_size / 8, Hkv} with
@@ -345,6 +351,7 @@ int latent_paged_take_device_error();
 // a.grid CTAs; with a.part_o set a second kernel joins the parts.
 cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_k, const CUtensorMap& tm_v,
                                  const CUtensorMap& tm_pe, const PrefillArgs& a, cudaStream_t stream);
+constexpr int kLatentMaxGrid = 1024;         // most CTAs: the plan kernel takes a thread for each item of a tail
 constexpr int kLatentPartSlots = 2;          // part slots a CTA of the grid
 constexpr long kLatentPartFloats = 2L * 128 * (kLatentV + 2);   // of a slot: O, maximum and sum of two row blocks
 int latent_varlen_take_device_error();

@@ -20,9 +20,10 @@
 //   warp 9      MMA issuer
 //   warps 0-7   softmax of the two tiles, one row per thread, and the output
 //   warps 10-11 zero the value rows past a request's end in its last tile
-// Items go by cost, the longest first, within groups of heads whose keys and values
-// fit L2 together.  What does not fill a last round of CTAs is cut along the keys
-// (Split) into FP32 parts that latent_varlen_join_kernel adds up.
+// Items go in the plan's order (requests by their whole cost, the heaviest first, each
+// one's blocks from the last, with the most keys, to the first) within groups of heads
+// whose keys and values fit L2 together.  What does not fill a last round of CTAs is cut
+// along the keys (Split) into FP32 parts that latent_varlen_join_kernel adds up.
 //
 // Measured (bf16): a chunk of 2048 tokens at the end of 16384 keys, 64 heads, 820 to 830
 // us (1.56 PFLOP/s of unmasked products; 881 without cut items), eight prompts of 300 to
@@ -67,19 +68,15 @@ constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
 constexpr int OFF_INFO = OFF_MISC + 16;         // two item records: claimed item, tiles of Q0 and of Q1
 constexpr int REC = 4;
 constexpr int OFF_SPLIT = OFF_INFO + 2 * REC * 4;
-constexpr int SMEM_BYTES = OFF_SPLIT + 16 + 1024;
+constexpr int SMEM_BYTES = OFF_SPLIT + 32 + 1024;
 constexpr uint32_t COL_S0 = 0, COL_S1 = 128, COL_O0 = 256, COL_O1 = 256 + DV, TMEM_COLS = 512;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 
-// Which items are cut.  With n_items = q grid + tail, the last `tail` items would keep
-// all but that many CTAs waiting for a whole item's time; they go in P parts each
-// instead (at least kPartTiles key tiles a part, at most two part slots a CTA).  P takes
-// the fewest tile times ceil(tail P / grid) (n / P + 2), 2 for a part's own start and end, if
-// that saves more than the joining costs (kJoinTiles); from kMaxRounds rounds on the
-// tail is short against the rest (a CTA's share of it is under an eighth).
-constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 16;
+// Items [n0, n_items), a last round of CTAs that is not full, are cut into up to P parts of
+// `len` key tiles at most (the plan kernel's choice, in the header of its list).
 struct Split {
-    int n_entries, n_items, n0, P;       // items [n0, n_items) are cut
+    int n_entries, n_items, n0;
+    int P, len;                          // P = 1: none is cut
     __device__ __forceinline__ int claims() const { return n0 + (n_items - n0) * P; }
 };
 
@@ -87,14 +84,14 @@ struct Item {
     int h, q0, qs, sq, ks, skv;     // head; first query of the item; first query / key row of the request and its counts
     TileInfo t0, t1;
     int lo, c0, c1;                 // this part's first key tile, and its tiles for either query tile
-    int part, parts;                // parts > 1: results go to part slot `slot`; parts 0: nothing to do
+    int parts;                      // > 1: results go to part slot `slot`; 0: nothing to do
     int slot;
 };
 
-// Item (w, part) of a claim; the whole of one where P is 1.
-__device__ __forceinline__ Item describe_item(const PrefillArgs& a, int n_entries, int w, int part, int P, int slot) {
+// Part `part` of item w, cut into equal parts of `len` key tiles at most (0: the whole of it).
+__device__ __forceinline__ Item describe_item(const PrefillArgs& a, int n_entries, int w, int part, int len, int slot) {
     Item it;
-    // entries by cost within a group of heads: the heads of an entry, then the next entry
+    // the plan's entries within a group of heads: the heads of an entry, then the next entry
     const int hg = a.head_group, grp = w / (n_entries * hg), x = w - grp * n_entries * hg;
     const int heads = min(hg, a.Hq - grp * hg);
     const int4* e = reinterpret_cast<const int4*>(a.entries + (size_t)(x / heads) * 8);
@@ -108,40 +105,36 @@ __device__ __forceinline__ Item describe_item(const PrefillArgs& a, int n_entrie
     it.t0 = tile_info_n(it.q0, BM, it.sq, it.skv, a.causal, -1, -1);
     it.t1 = tile_info_n(it.q0 + BM, BM, it.sq, it.skv, a.causal, -1, -1);
     const int n = max(it.t0.n_tiles, it.t1.n_tiles);
-    const int len = P > 1 ? max(kPartTiles, (n + P - 1) / P) : max(n, 1);
-    it.lo = part * len;
-    it.c0 = max(0, min(it.t0.n_tiles - it.lo, len));
-    it.c1 = max(0, min(it.t1.n_tiles - it.lo, len));
-    it.part = part;
-    it.parts = part > 0 && it.lo >= n ? 0 : max(1, (n + len - 1) / len);
+    int parts = 1, each = max(1, n);
+    if (len > 0) {
+        parts = max(1, (n + len - 1) / len);
+        each = max(1, (n + parts - 1) / parts);       // (parts of `each` are as many again)
+    }
+    it.lo = part * each;
+    it.c0 = max(0, min(it.t0.n_tiles - it.lo, each));
+    it.c1 = max(0, min(it.t1.n_tiles - it.lo, each));
+    it.parts = part < parts ? parts : 0;
     it.slot = slot;
     return it;
 }
 __device__ __forceinline__ Item describe_claim(const PrefillArgs& a, const Split& s, int w) {
-    if (w < s.n0) return describe_item(a, s.n_entries, w, 0, 1, 0);
-    const int x = w - s.n0;
-    return describe_item(a, s.n_entries, s.n0 + x / s.P, x % s.P, s.P, x);
+    // (one copy of describe_item a role: two made short calls 1 us and a long one 6 us of 740 slower)
+    const int x = w - s.n0, P = s.P;
+    int item = w, part = 0, len = 0;
+    if (x >= 0) {
+        item = s.n0 + x / P;
+        part = x - (item - s.n0) * P;
+        len = s.len;
+    }
+    return describe_item(a, s.n_entries, item, part, len, x);
 }
 __device__ __forceinline__ Split find_split(const PrefillArgs& a) {
     Split s;
     s.n_entries = *a.n_entries;
     s.n_items = s.n_entries * a.Hq;
-    s.n0 = s.n_items;
-    s.P = 1;
-    const int tail = s.n_items % a.grid;
-    if (a.part_o == nullptr || tail == 0 || s.n_items / a.grid >= kMaxRounds) return s;
-    const Item it = describe_item(a, s.n_entries, s.n_items - tail, 0, 1, 0);    // the longest of the tail, or near it
-    const int n = max(it.c0, it.c1);
-    const int most = min(min(kMaxParts, kLatentPartSlots * a.grid / tail), n / kPartTiles);
-    int best = 16 * (n + 2 - kJoinTiles);                   // sixteenths of a tile time
-    for (int p = 2; p <= most; ++p) {
-        const int cost = (tail * p + a.grid - 1) / a.grid * (16 * n / p + 32);
-        if (cost < best) {
-            best = cost;
-            s.P = p;
-            s.n0 = s.n_items - tail;
-        }
-    }
+    s.len = a.part_o ? a.n_entries[2] : 0;
+    s.P = a.part_o ? a.n_entries[3] : 1;
+    s.n0 = s.P > 1 ? s.n_items - s.n_items % a.grid : s.n_items;
     return s;
 }
 
@@ -196,11 +189,8 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         *abort_flag = 0;
         fence_mbar_init();
     }
-    Split* split = reinterpret_cast<Split*>(smem + OFF_SPLIT);
-    if (threadIdx.x == 32 * WARP_LOAD) {
-        *split = find_split(a);
-        if (blockIdx.x == 0 && a.part_o) a.work[2] = split->P;     // the header's last word, for the joining kernel
-    }
+    Split& sp = *reinterpret_cast<Split*>(smem + OFF_SPLIT);     // (in shared memory: a softmax thread has no registers to spare)
+    if (threadIdx.x == 32 * WARP_LOAD) sp = find_split(a);
     if (warp == WARP_MMA) {
         tmem_alloc(smem_u32(tmem_slot), TMEM_COLS);
         tmem_relinquish();
@@ -209,7 +199,6 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    const Split sp = *split;
 
     // As in prefill.cu each role ends by itself; the MMA warp frees TMEM once the
     // softmax warps have arrived on barrier 2.
@@ -589,12 +578,10 @@ latent_varlen_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 template <bool F16>
 __global__ void __launch_bounds__(BM) latent_varlen_join_kernel(const PrefillArgs a) {
     griddep_wait();
-    const int P = a.work[2];
-    if (P <= 1) return;
+    const Split sp = find_split(a);
     const int x = blockIdx.x / 2, k = blockIdx.x % 2, r = threadIdx.x;
-    const int n_entries = *a.n_entries, n_items = n_entries * a.Hq, tail = n_items % a.grid;
-    if (x >= tail) return;
-    const Item it = describe_item(a, n_entries, n_items - tail + x, 0, P, x * P);
+    if (x >= sp.n_items - sp.n0) return;
+    const Item it = describe_item(a, sp.n_entries, sp.n0 + x, 0, sp.len, x * sp.P);
     const TileInfo ti = k == 0 ? it.t0 : it.t1;
     if (it.parts <= 1 || r >= ti.rows_valid) return;
     const float2* ml = reinterpret_cast<const float2*>(a.part_lse) + ((size_t)it.slot * 2 + k) * BM + r;

@@ -46,11 +46,28 @@ __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb,
     return min(NBUCKET - 1, tiles * (nq * g >= 64 ? 2 : 3));
 }
 
+// Which items of an expanded latent call are cut along the keys.  With n_items = q grid
+// + tail, the last `tail` items would keep all but that many CTAs waiting for a whole
+// item's time; they are cut into up to P parts each instead, of at least kPartTiles key
+// tiles, shorter ones into fewer or none.  They are no alike, and the longest may be the
+// last of all: a few queries over a long context weigh less than a prompt as a whole and
+// come after its lightest blocks.  So the length goes by the longest of the tail.  Parts
+// taken one after the other by all CTAs end by (W - l) / grid + l, W the tile times
+// of all of them (2 more a part for its start and end) and l those of the longest
+// part; P takes the least of that, if it saves more than the joining costs
+// (kJoinTiles).  From kMaxRounds rounds on the tail is short against the rest (a CTA's
+// share of it is under an eighth).  (By the tail's first item alone, before: a 4096-token
+// prompt beside one query over 8192 keys, 12 heads, 122 us uncut, 87 in five parts; 20 heads
+// 169 and 132; three prompts of 3000 beside 16 queries over 12000 keys, 8 heads, 177 and 125.
+// A call of which nothing is cut pays 1 us for the choice.)
+constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 16;
+
 __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, const int32_t* kv, int paged,
                                                           int B, int qpb, int g, int causal, int total_q,
                                                           long kv_cap, int32_t* tmp, int32_t* entries,
                                                           int32_t* n_entries, int max_entries, int grid,
-                                                          double dec_per_key, int split_grid, int Hkv, int wl, int wr) {
+                                                          double dec_per_key, int split_grid, int Hkv, int wl, int wr,
+                                                          const TailSplit ts) {
     __shared__ int warp_sum[32];
     __shared__ unsigned long long pre_cost, dec_keys;   // listed blocks' cost; decode steps' cached keys
     __shared__ int base, most_tiles;                    // most key tiles that a block visits
@@ -246,6 +263,45 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         dst[0] = e0;
         dst[1] = make_int4(e1.x, e1.y, 0, 0);
     }
+    if (ts.grid > 0) {
+        const int n_items = n * ts.H, tail = n_items % ts.grid;      // tail < grid <= 1024
+        unsigned* best = reinterpret_cast<unsigned*>(&warp_sum[0]);  // a cost's bits, its P in the last five
+        int* longest = &warp_sum[1];
+        int* tiles = group_sum;                                      // of each item of the tail
+        const bool may = tail > 0 && n_items / ts.grid < kMaxRounds;
+        if (threadIdx.x == 0) {
+            *best = ~31u | 1u;
+            *longest = 0;
+        }
+        __syncthreads();                                             // (and every entry is in its place)
+        if (may && threadIdx.x < tail) {
+            const int w = n_items - tail + threadIdx.x, grp = w / (n * ts.head_group);
+            const int heads = min(ts.head_group, ts.H - grp * ts.head_group);
+            const int4* e = reinterpret_cast<const int4*>(entries + (size_t)((w - grp * n * ts.head_group) / heads) * ot::ENTRY_INTS);
+            const int4 e0 = e[0], e1 = e[1];
+            const int t = pf::tile_info_n(e0.y, span, e0.w, e1.y, causal, wl, wr).n_tiles;
+            tiles[threadIdx.x] = t;
+            atomicMax(longest, t);
+        }
+        __syncthreads();
+        const int t_max = *longest;
+        const int most = may ? min(min(kMaxParts, kLatentPartSlots * ts.grid / tail), t_max / kPartTiles) : 0;
+        if (most > 1 && warp < most) {
+            const int p = warp + 1, len = p > 1 ? max(kPartTiles, (t_max + p - 1) / p) : t_max;
+            float w = 0.f;
+            for (int x = lane; x < tail; x += 32) w += (float)(tiles[x] + 2 * max(1, (tiles[x] + len - 1) / len));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+            const float l = (float)(len + 2), cost = (w - l) / (float)ts.grid + l + (p > 1 ? (float)kJoinTiles : 0.f);
+            if (lane == 0) atomicMin(best, (__float_as_uint(cost) & ~31u) + p);      // (positive floats order as their bits)
+        }
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            const int p = (int)(*best & 31u);
+            n_entries[2] = p > 1 ? max(kPartTiles, (t_max + p - 1) / p) : 0;
+            n_entries[3] = p;
+        }
+    }
     if (threadIdx.x == 0) {
         n_entries[0] = n;
         n_entries[1] = 0;                              // the attention kernel's item counter
@@ -261,7 +317,7 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
             ge = (int)lrint((double)grid * tp / (tp + td));
             ge = min(grid, max(ge, min(grid, 8)));
         }
-        n_entries[2] = ge;
+        if (ts.grid == 0) n_entries[2] = ge;
         if (split_grid > 0) {
             // as many parts as leave every one a CTA, but no more than give the block
             // with the most visited tiles kPartTiles each (shorter blocks fill fewer
@@ -280,13 +336,13 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
 cudaError_t launch_varlen_plan(const int32_t* cu_q, const int32_t* kv, bool paged, int B, int qpb, int g, int causal,
                                int total_q, long kv_cap, int32_t* tmp, int32_t* entries, int32_t* n_entries,
                                int max_entries, cudaStream_t stream, bool skip_single, bool pairs, int grid,
-                               bool fp8, int split_grid, int Hkv, int wl, int wr) {
+                               bool fp8, int split_grid, int Hkv, int wl, int wr, const TailSplit& tail) {
     // flags: bit 0 paged (kv holds cache lengths), bit 1 skip single-query
     // requests, bit 2 pairs of row blocks
     const int flags = (paged ? 1 : 0) | (skip_single ? 2 : 0) | (pairs ? 4 : 0);
     varlen_plan_kernel<<<1, 1024, 0, stream>>>(cu_q, kv, flags, B, qpb, g, causal, total_q, kv_cap, tmp,
                                                entries, n_entries, max_entries, grid,
-                                               fp8 ? kDecPerKey8 : kDecPerKey, split_grid, Hkv, wl, wr);
+                                               fp8 ? kDecPerKey8 : kDecPerKey, split_grid, Hkv, wl, wr, tail);
     return cudaGetLastError();
 }
 

@@ -84,6 +84,30 @@ def test_requests_of_one_cost_keep_their_order(g, B):
     assert ws[16:16 + 32 * len(want)].view(torch.int32).view(-1, 8)[:, :2].tolist() == want
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("nq,lens,last", [
+    ([4096, 1], [4096, 8192], 1),              # a prompt, and one query at the end of a long context
+    ([2048, 1], [2048, 4000], 1),
+    ([1500, 1500, 16], [1500, 1500, 12000], 1),
+])
+def test_long_items_that_come_last_are_cut(g, nq, lens, last, dtype):
+    """A chunk of few queries over many keys weighs less than a prompt as a whole and comes
+    after it, the longest items of the call last.  As many heads as leave the tail those items and some
+    short ones before them."""
+    entries = sum(-(-n // 256) for n in nq)
+    group = (64 << 20) // (512 * sum(lens))                   # heads whose items follow one another
+    heads = [H for H in range(2, group + 1) if entries * H > sms() and last * H < entries * H % sms() <= sms() // 2]
+    H = heads[0] if heads else next(H for H in range(group, 1, -1) if last * H < entries * H % sms() <= sms() // 2)
+    c = varlen_case(torch.Generator().manual_seed(sum(lens)), nq, lens, H, DT[dtype])
+    o, lse, parts = call(g, c)
+    assert parts > 1
+    for b, h, rows, ref in varlen_refs(c):
+        if h in (0, H - 1):
+            check(o[rows, h], lse[rows, h], ref, "request %d head %d" % (b, h))
+    o2, lse2, _ = call(g, c)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
 def test_short_items_of_a_tail_stay_whole(g):
     """Nothing is cut where every item is short."""
     c = varlen_case(torch.Generator().manual_seed(4), [100] * 20, [100] * 20, 3, torch.bfloat16)
