@@ -1070,15 +1070,17 @@ static bool make_rows_map(CUtensorMap* map, const Rows& r, int box_t, bool f16) 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// CTAs of an expanded call, and the bytes of its part slots: none where the query
-// blocks alone fill so many rounds of CTAs that no tail is cut.
-static int latent_varlen_grid(int B, int total_q, int H) {
+// CTAs of an expanded call: no more than it has items, or parts where items may be cut (one
+// query over 9000 keys, one head: 61 us in two parts on the CTAs of two items, 35 in 15; 300 over
+// 5000, three heads, 49 and 36; 64 requests of 20 tokens, one head, pay 1 us of 18 for it).  And the bytes of its part slots: none where the query blocks alone fill
+// so many rounds of CTAs that no tail is cut.
+static int latent_varlen_grid(int B, int total_q, int H, bool cut) {
     const long n = std::min(sm_count() > 0 ? sm_count() : 148, gqa::kLatentMaxGrid);
-    const long items = (long)varlen_max_entries(B, total_q, 128) * H;
-    return (int)(items < n ? items : n);
+    const long claims = (long)varlen_max_entries(B, total_q, 128) * H * (cut ? gqa::kLatentMaxParts : 1);
+    return (int)(claims < n ? claims : n);
 }
 static size_t latent_varlen_parts(int B, int total_q, int H) {
-    const long grid = latent_varlen_grid(B, total_q, H), least = ((long)total_q + 255) / 256 * H;
+    const long grid = latent_varlen_grid(B, total_q, H, true), least = ((long)total_q + 255) / 256 * H;
     return least >= 8 * grid ? 0 : (size_t)grid * gqa::kLatentPartSlots * gqa::kLatentPartFloats * sizeof(float);
 }
 
@@ -1140,7 +1142,7 @@ gqa_status attn_fwd_latent_varlen(const void* q, const gqa_head_rows* k, const g
     // heads whose keys and values (512 bytes a token and head) take half of L2
     const long per_head = total_kv > 0 ? (long)total_kv * 512 : 512;
     a.head_group = (int)std::max(1L, std::min((long)H, (64L << 20) / per_head));
-    a.grid = latent_varlen_grid(B, total_q, H);
+    a.grid = latent_varlen_grid(B, total_q, H, cut);
     if (cut) {
         a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + plan);
         a.part_lse = a.part_o + (size_t)a.grid * gqa::kLatentPartSlots * 2 * 128 * gqa::kLatentV;

@@ -353,6 +353,7 @@ cudaError_t launch_latent_varlen(const CUtensorMap& tm_q, const CUtensorMap& tm_
                                  const CUtensorMap& tm_pe, const PrefillArgs& a, cudaStream_t stream);
 constexpr int kLatentMaxGrid = 1024;         // most CTAs: the plan kernel takes a thread for each item of a tail
 constexpr int kLatentPartSlots = 2;          // part slots a CTA of the grid
+constexpr int kLatentMaxParts = 16;          // most parts of an item
 constexpr long kLatentPartFloats = 2L * 128 * (kLatentV + 2);   // of a slot: O, maximum and sum of two row blocks
 int latent_varlen_take_device_error();
 

@@ -60,7 +60,7 @@ __device__ __forceinline__ int entry_cost(const int4 e0, const int4 e1, int qpb,
 // prompt beside one query over 8192 keys, 12 heads, 122 us uncut, 87 in five parts; 20 heads
 // 169 and 132; three prompts of 3000 beside 16 queries over 12000 keys, 8 heads, 177 and 125.
 // A call of which nothing is cut pays 1 us for the choice.)
-constexpr int kJoinTiles = 4, kMaxRounds = 8, kMaxParts = 16;
+constexpr int kJoinTiles = 4, kMaxRounds = 8;
 
 __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, const int32_t* kv, int paged,
                                                           int B, int qpb, int g, int causal, int total_q,
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         }
         __syncthreads();
         const int t_max = *longest;
-        const int most = may ? min(min(kMaxParts, kLatentPartSlots * ts.grid / tail), t_max / kPartTiles) : 0;
+        const int most = may ? min(min(kLatentMaxParts, kLatentPartSlots * ts.grid / tail), t_max / kPartTiles) : 0;
         if (most > 1 && warp < most) {
             const int p = warp + 1, len = p > 1 ? max(kPartTiles, (t_max + p - 1) / p) : t_max;
             float w = 0.f;

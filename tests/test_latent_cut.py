@@ -108,6 +108,17 @@ def test_long_items_that_come_last_are_cut(g, nq, lens, last, dtype):
     assert torch.equal(o, o2) and torch.equal(lse, lse2)
 
 
+@pytest.mark.parametrize("nq,lens,H,least", [([1], [9000], 1, 12), ([300], [5000], 3, 8), ([2, 1], [4000, 6000], 2, 8)])
+def test_few_items_are_cut_for_idle_sms(g, nq, lens, H, least):
+    """A call of fewer items than SMs takes more CTAs than it has items: as many parts as
+    pay, not as many as the items' own CTAs could hold."""
+    c = varlen_case(torch.Generator().manual_seed(sum(lens)), nq, lens, H, torch.bfloat16)
+    o, lse, parts = repeats(g, c, 5)
+    assert parts >= least
+    for b, h, rows, ref in varlen_refs(c):
+        check(o[rows, h], lse[rows, h], ref, "request %d head %d" % (b, h))
+
+
 def test_short_items_of_a_tail_stay_whole(g):
     """Nothing is cut where every item is short."""
     c = varlen_case(torch.Generator().manual_seed(4), [100] * 20, [100] * 20, 3, torch.bfloat16)
