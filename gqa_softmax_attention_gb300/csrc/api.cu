@@ -1259,10 +1259,14 @@ gqa_status attn_fwd_latent_paged(const void* q, const void* kv_cache, const int3
     a.causal = causal ? 1 : 0;
     a.f16 = dtype == GQA_FP16 ? 1 : 0;
     a.team = parts.team; a.teams = parts.teams;
-    // fewer tiles a team make the joining dearer than they save: 1, 2 and 8 tiles are
-    // within 2 us of one another for one request of 2000 keys and for eight of 200 to 500,
-    // but 8 take 32 us for forty of 200 to 900 keys (64 heads) where 2 take 27
-    a.min_tiles = 2;
+    // The least of a team's range, in places of the sequence, which a row group's three start
+    // tiles take as well: where a group starts, a range of two holds no key tile and the
+    // next one a single tile, so short calls are cut into pieces of one and two tiles.  That is
+    // what pays (us, captured, by 1, 2, 3, 4, 5 and 8 places): one request of 2000 keys, 16 heads
+    // 13.1, 11.7, 11.8, 12.9, 14.2, 15.3, 64 heads 21.7, 17.5, 16.7, 17.6, 19.0, 20.4; two of 300 and 700, 16
+    // heads 10.8, 10.5, 10.8, 12.4, 12.3, 14.1; eight of 200 to 500, 64 heads 15.4, 14.6, 15.9, 18.3, 18.0, 23.7;
+    // forty of 200 to 900, 64 heads 18.7, 18.8, 18.8, 20.0, 20.5, 24.1; 128 heads like 64.
+    a.min_places = 2;
     a.scale_log2 = (float)((double)scale * 1.4426950408889634074);
     page_divisor(page_size, &a.ps_mul, &a.ps_shift);
     CUtensorMap tq, tkv, tpe, trow;

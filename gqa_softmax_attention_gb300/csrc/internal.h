@@ -332,7 +332,7 @@ struct LatentArgs {
     int B, total_q, H, page_size, num_pages, max_pages, causal, f16;
     int nr;                         // rows of a CTA: 16, 32 or 64 (64 with gathered rows)
     int team, teams;                // CTAs that read the same keys for further rows; teams of the grid
-    int min_tiles;                  // least tiles of a team
+    int min_places;                 // least places of a team's range: key tiles, or start tiles of a row group
     int box_tokens;                 // tokens of a TMA box; 0: rows gathered with cp.async
     float scale_log2;
     uint32_t ps_mul, ps_shift;      // n / page_size as in PrefillArgs

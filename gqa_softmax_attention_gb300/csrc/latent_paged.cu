@@ -111,7 +111,7 @@ struct LCfg {
 
 // Where this team's range of the tile sequence starts.
 struct LRange {
-    long g0, n, per;        // first tile, tiles, tiles per team
+    long g0, n, per;        // first place, places, places per team (key and start tiles)
     int b, seg, off, pad;   // request and row group of the first one, and its place in that
 };
 
@@ -336,7 +336,7 @@ latent_paged_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             __syncthreads();
         }
         long per = (base + a.teams - 1) / a.teams;
-        if (per < a.min_tiles) per = a.min_tiles;
+        if (per < a.min_places) per = a.min_places;
         const long g0 = team * per, n = max(0L, min(per, base - g0));
         if (n > 0) {
             for (int b = threadIdx.x; b < a.B; b += C::THREADS) {
