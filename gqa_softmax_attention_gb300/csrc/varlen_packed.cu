@@ -70,7 +70,8 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
                                                           const TailSplit ts) {
     __shared__ int warp_sum[32];
     __shared__ unsigned long long pre_cost, dec_keys;   // listed blocks' cost; decode steps' cached keys
-    __shared__ int base, most_tiles;                    // most key tiles that a block visits
+    __shared__ unsigned base;                           // blocks of earlier requests (step 1)
+    __shared__ int most_tiles;                          // most key tiles that a block visits
     __shared__ int bucket[NBUCKET];
     __shared__ int chain[NBUCKET], group_next[1024], group_sum[1024];   // step 3
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -109,28 +110,33 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
             nrb = (sq + span - 1) / span;
             if ((paged & 2) && sq == 1) nrb = 0;      // a decode step, run by the split decode kernel
         }
-        int x = nrb;                                   // inclusive scan within the warp
+        // inclusive scan within the warp; sums stop at max_entries, where the list ends
+        // (malformed offsets can list the same rows again and again)
+        auto sum = [&](unsigned p, unsigned q) { return min(p + q, (unsigned)max_entries); };
+        unsigned x = min(nrb, max_entries);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
+            const unsigned y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x = sum(x, y);
         }
-        if (lane == 31) warp_sum[warp] = x;
+        if (lane == 31) warp_sum[warp] = (int)x;
         __syncthreads();
         if (warp == 0) {
-            int s = warp_sum[lane];
+            unsigned s = (unsigned)warp_sum[lane];
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, s, o);
-                if (lane >= o) s += y;
+                const unsigned y = __shfl_up_sync(0xffffffffu, s, o);
+                if (lane >= o) s = sum(s, y);
             }
-            warp_sum[lane] = s;
+            warp_sum[lane] = (int)s;
         }
         __syncthreads();
-        const int first = base + (warp > 0 ? warp_sum[warp - 1] : 0) + x - nrb;
+        const unsigned before = __shfl_up_sync(0xffffffffu, x, 1);
+        const unsigned first = sum(base, sum(warp > 0 ? (unsigned)warp_sum[warp - 1] : 0u, lane > 0 ? before : 0u));
         // the request's estimated cost: the sum of its blocks' costs
+        // (2047 units for every 128 queries pass 31 bits at 134 million: it stops far past the last bucket)
         int total = 0;
-        for (int k = 0; k < nrb; ++k) total += cost_of(b, k * span, qs, sq, ks, L);
+        for (int k = 0; k < nrb; ++k) total = min(total + cost_of(b, k * span, qs, sq, ks, L), 1 << 30);
         if (total > 0) atomicAdd(&pre_cost, (unsigned long long)total);
         if (split_grid > 0) {
             int most = 0;
@@ -143,17 +149,17 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         if ((paged & 2) && sq == 1 && b < B && L > 0) atomicAdd(&dec_keys, (unsigned long long)L);
         const int key = min(NBUCKET - 1, total / 16);
         for (int k = 0; k < nrb; ++k) {
-            const int e = first + k;
-            if (e >= max_entries) break;
+            const unsigned e = first + k;
+            if (e >= (unsigned)max_entries) break;
             int4* dst = reinterpret_cast<int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
             dst[0] = make_int4(b, k * span, qs, sq);
             dst[1] = make_int4(ks, L, key, 0);             // .w: the request's start once placed
         }
         __syncthreads();
-        if (threadIdx.x == 1023) base = first + nrb;
+        if (threadIdx.x == 1023) base = sum(first, min(nrb, max_entries));
         __syncthreads();
     }
-    const int n = min(base, max_entries);
+    const int n = (int)base;
     // 2. requests ordered by estimated cost, heaviest first (a counting sort of
     // their total costs), each request's blocks kept together and placed from
     // its last block (the most keys under a causal mask) to its first: the
