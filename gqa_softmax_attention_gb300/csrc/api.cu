@@ -1161,9 +1161,9 @@ static bool latent_rows_ok(int total_q, int H) { return (long)total_q * H < (1L 
 // same keys side by side (so that L2 serves the second): as many rows as a request
 // brings, on average, up to two CTAs of 64.  Columns that no row fills cost MMA cycles
 // and shared memory that the ring could have: with 16 heads, 64 requests of 1K to 16K
-// keys take 117, 118 and 129 us with 16, 32 and 64 rows a CTA, four of 31K 53, 64 and
-// 68.  Two CTAs against one: 128 heads, the same 64 requests, 184 against 216 us; 24
-// chunks of 8 queries by 16 heads 57 against 61, of 4 by 64 heads 95 against 99.
+// keys take 91, 95 and 100 us with 16, 32 and 64 rows a CTA, four of 31K 37, 39 and 51
+// (captured).  Two CTAs against one: 128 heads, the same 64 requests, 151 against 190 us;
+// 24 chunks of 8 queries by 16 heads 50 against 54, of 4 by 64 heads 85 against 89.
 struct LatentParts {
     int nr, team, teams;
     size_t join, ml, o;     // bytes
