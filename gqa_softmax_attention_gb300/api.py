@@ -886,7 +886,7 @@ def attn_fwd_latent_paged(q, kv_cache, cu_seqlens_q, cache_seqlens, block_table,
     (query tokens included) and block_table [B, max_pages] int32 CUDA tensors, as
     attn_fwd_paged; any page size (multiples of 8 move by TMA, others are gathered row
     by row).  scale: the multiplier of the scores, 1 / sqrt of the expanded head's
-    key dims by custom.
+    key dims by custom.  At most 16384 requests.
     workspace: optional, attn_latent_paged_workspace_size bytes.
     Returns (o [total_q, H, 512], the weighted sums of the latents, lse [total_q, H]
     float32).

@@ -48,11 +48,11 @@
 // latent_join_kernel adds them up.
 //
 // Measured (bf16, pages of 64, queries of one token): 64 requests of 1K to 16K keys
-// take 104 to 110 us with 16 heads (625 MB once: 85 to 90 % of the copy rate; in pages of one
-// token, gathered, 178) and 174 to 180 us with 128 heads (860 TFLOP/s).  What
-// bounds the latter is the chain of a tile's loads, S^T, softmax and O^T through a ring two tiles
-// deep, 2450 cycles a tile where its MMAs read operands for 1970.  Two requests of 300
-// to 700 keys take 11 us, replayed from a graph.
+// take 104 to 112 us with 16 heads (625 MB once: 83 to 90 % of the copy rate) and 171 to 185 us
+// with 128 heads (860 TFLOP/s), which the chain of a tile's loads, S^T, softmax and O^T through
+// a ring two tiles deep bounds: 2450 cycles a tile where its MMAs read operands for 1970.
+// Replayed from a graph: two requests of 300 to 700 keys 11 us; 64 of 1K to 16K, 16 heads, 91,
+// and 176 in pages of one token, gathered.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(NT) latent_append_kernel(const LatentAppendArg
 // A block takes GROWS rows of the packed result: a warp finds the rows' requests
 // and cache rows, then all threads copy 16 bytes at a time, every load of a
 // thread issued before its first store (16 requests, 134K rows: 51 us, 90 % of the
-// copy rate).
+// copy rate).  The search reads all offsets before the block's rows, 32 at a time: 1000
+// requests of 100 rows 5.8 TB/s, 4000 of 30 4.4, 16384 of 10 1.8.
 constexpr int GROWS = 32;
 constexpr int CHUNKS = kLatentRow * 2 / 16;    // 72
 constexpr int GT = 288;                        // GROWS * CHUNKS / GT = 8 chunks a thread

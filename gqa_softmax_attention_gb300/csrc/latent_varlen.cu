@@ -25,10 +25,10 @@
 // whose keys and values fit L2 together.  What does not fill a last round of CTAs is cut
 // along the keys (Split) into FP32 parts that latent_varlen_join_kernel adds up.
 //
-// Measured (bf16): a chunk of 2048 tokens at the end of 16384 keys, 64 heads, 820 to 830
-// us (1.56 PFLOP/s of unmasked products; 881 without cut items), eight prompts of 300 to
-// 4000 tokens, 32 heads, 455 (643 in the order of the requests), one of 4096, 20 heads, 97
-// (124 without cut items).  The tensor core is the bound, under the power cap (1.55 to 1.7
+// Measured (bf16): a chunk of 2048 tokens at the end of 16384 keys, 64 heads, 807 to 811
+// us (1.59 PFLOP/s of unmasked products), eight prompts of 300 to 4000 tokens, 32 heads,
+// 449, one of 4096, 20 heads, 87 replayed from a graph; a 4096-token prompt beside one query over
+// 8192 keys, 12 heads, 87 in five parts of its tail (122 uncut).  The tensor core is the bound, under the power cap (1.55 to 1.7
 // GHz in a loop of the long ones); short prompts lose to masked halves of diagonal tiles and
 // to row blocks that a request does not fill.
 #include <cmath>
