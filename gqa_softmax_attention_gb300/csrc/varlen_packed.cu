@@ -160,6 +160,18 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         __syncthreads();
     }
     const int n = (int)base;
+    // a thread's first entry stays in registers (fewer loads: most calls have no other)
+    int4 f0 = make_int4(0, 1, 0, 0), f1 = f0;
+    auto entry = [&](int e, int4& e0, int4& e1) {
+        const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
+        e0 = e < 1024 ? f0 : src[0];
+        e1 = e < 1024 ? f1 : src[1];
+    };
+    if (threadIdx.x < n) {
+        const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)threadIdx.x * ot::ENTRY_INTS);
+        f0 = src[0];
+        f1 = src[1];
+    }
     // 2. requests ordered by estimated cost, heaviest first (a counting sort of
     // their total costs), each request's blocks kept together and placed from
     // its last block (the most keys under a causal mask) to its first: the
@@ -167,8 +179,8 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
     // which stay in L2 while its blocks need them.  A request's first entry
     // (q0 = 0) stands for the whole request.
     for (int e = threadIdx.x; e < n; e += 1024) {
-        const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
-        const int4 e0 = src[0], e1 = src[1];
+        int4 e0, e1;
+        entry(e, e0, e1);
         // blocks of the request that made the list (all of them unless the
         // cap cut it short), so that the placed entries fill [0, n)
         if (e0.y == 0) atomicAdd(&bucket[e1.z], min((e0.w + span - 1) / span, n - e));
@@ -214,8 +226,8 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         const int e = e_first + threadIdx.x;
         int key = -1, cnt = 0;
         if (e < n) {
-            const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
-            const int4 e0 = src[0], e1 = src[1];
+            int4 e0, e1;
+            entry(e, e0, e1);
             if (e0.y == 0) {
                 key = e1.z;
                 cnt = min((e0.w + span - 1) / span, n - e);
@@ -251,6 +263,7 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         start = __shfl_sync(0xffffffffu, start, leader);
         if (key >= 0) tmp[(size_t)e * ot::ENTRY_INTS + 7] = start + before;
         __syncthreads();
+        if (e_first + 1024 >= n) break;
         if (leads) {
             atomicAdd(&bucket[key], sum);
             chain[key] = -1;
@@ -258,8 +271,8 @@ __global__ void __launch_bounds__(1024) varlen_plan_kernel(const int32_t* cu_q, 
         __syncthreads();
     }
     for (int e = threadIdx.x; e < n; e += 1024) {
-        const int4* src = reinterpret_cast<const int4*>(tmp + (size_t)e * ot::ENTRY_INTS);
-        const int4 e0 = src[0], e1 = src[1];
+        int4 e0, e1;
+        entry(e, e0, e1);
         const int k = e0.y / span;
         const int cnt = min((e0.w + span - 1) / span, n - (e - k));
         const int start = reinterpret_cast<const int4*>(tmp + (size_t)(e - k) * ot::ENTRY_INTS)[1].w;
